@@ -8,6 +8,7 @@ There is no CPU fallback: if the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -20,6 +21,7 @@ GQA_OK, GQA_ERR_INVALID_ARG, GQA_ERR_UNSUPPORTED, GQA_ERR_CUDA, GQA_ERR_TIMEOUT 
 
 #: Every symbol the header declares, with (restype, argtypes).
 _P, _I, _F, _SZ, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64
+_I64 = ctypes.c_int64
 SIGNATURES = {
     "gqa_status_str": (ctypes.c_char_p, [_I]),
     "gqa_version": (_I, []),
@@ -50,6 +52,18 @@ SIGNATURES = {
     "gqa_attn_prefill_chunk_default_parts": (_I, [_I, _I, _I, _I, _I]),
     "gqa_attn_prefill_chunk_split": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P,
                                           _P, _P, _P]),
+    "gqa_kv_append_fp8_block": (_I, [_P, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P,
+                                     _P]),
+    "gqa_kv_append_paged_fp8_block": (_I, [_P, _P, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                           _P, _P, _P, _P, _P]),
+    "gqa_kv_read_fp8_block": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "gqa_kv_read_paged_fp8_block": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                                         _P, _P, _P]),
+    "gqa_attn_decode_fp8_block": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I,
+                                       _P, _P, _P, _P]),
+    "gqa_attn_decode_paged_fp8_block": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                             _I, _I, _F, _I, _P, _P, _P, _P]),
+    "gqa_attn_decode_fp8_block_default_splits": (_I, [_I, _I, _I]),
     "gqa_last_device_error": (_I, [_P]),
     "gqa_trace_clear": (_I, []),
     "gqa_trace_read": (_I, [_P, _SZ]),
@@ -109,6 +123,24 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _on(device):
+    """A context with `device` current (no change where it is already)."""
+    import torch
+
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _keep(tensor, stream):
+    """Keeps a temporary's memory from reuse until `stream` (given by the caller) is past it."""
+    import torch
+
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+        tensor.record_stream(s)
 
 
 # ------------------------------------------------------- same-name entries --
@@ -242,6 +274,60 @@ def gqa_attn_prefill_chunk_split(q, k_cache, v_cache, seq_lens, B, T_q, S_max, H
     return load().gqa_attn_prefill_chunk_split(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seq_lens), B, T_q, S_max, H_q, H_kv, d, scale,
         int(window), int(n_part), _ptr(workspace), _ptr(out), _ptr(lse), _stream(stream))
+
+
+def gqa_kv_append_fp8_block(k_new, v_new, new_stride, n_new, seq_lens, B, T, S_max, H_kv, d, block,
+                            k_cache, v_cache, k_scale, v_scale, stream=None) -> int:
+    return load().gqa_kv_append_fp8_block(
+        _ptr(k_new), _ptr(v_new), new_stride, _ptr(n_new), _ptr(seq_lens), B, T, S_max, H_kv, d,
+        block, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _stream(stream))
+
+
+def gqa_kv_append_paged_fp8_block(k_new, v_new, new_stride, n_new, block_table, seq_lens, B, T,
+                                  num_pages, page_size, max_blocks, H_kv, d, block, k_pool, v_pool,
+                                  k_scale, v_scale, stream=None) -> int:
+    return load().gqa_kv_append_paged_fp8_block(
+        _ptr(k_new), _ptr(v_new), new_stride, _ptr(n_new), _ptr(block_table), _ptr(seq_lens), B, T,
+        num_pages, page_size, max_blocks, H_kv, d, block, _ptr(k_pool), _ptr(v_pool),
+        _ptr(k_scale), _ptr(v_scale), _stream(stream))
+
+
+def gqa_kv_read_fp8_block(k_cache, v_cache, k_scale, v_scale, seq_lens, B, S_max, H_kv, d, block,
+                          start, S_out, k_out, v_out, stream=None) -> int:
+    return load().gqa_kv_read_fp8_block(
+        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(seq_lens), B, S_max, H_kv,
+        d, block, start, S_out, _ptr(k_out), _ptr(v_out), _stream(stream))
+
+
+def gqa_kv_read_paged_fp8_block(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, B,
+                                num_pages, page_size, max_blocks, H_kv, d, block, start, S_out,
+                                k_out, v_out, stream=None) -> int:
+    return load().gqa_kv_read_paged_fp8_block(
+        _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
+        B, num_pages, page_size, max_blocks, H_kv, d, block, start, S_out, _ptr(k_out), _ptr(v_out),
+        _stream(stream))
+
+
+def gqa_attn_decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, seq_lens, B, T_q, S_max, H_q,
+                              H_kv, d, block, scale, n_split, workspace, out, lse,
+                              stream=None) -> int:
+    return load().gqa_attn_decode_fp8_block(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(seq_lens), B, T_q,
+        S_max, H_q, H_kv, d, block, scale, n_split, _ptr(workspace), _ptr(out), _ptr(lse),
+        _stream(stream))
+
+
+def gqa_attn_decode_paged_fp8_block(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, B,
+                                    T_q, num_pages, page_size, max_blocks, H_q, H_kv, d, block,
+                                    scale, n_split, workspace, out, lse, stream=None) -> int:
+    return load().gqa_attn_decode_paged_fp8_block(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+        _ptr(seq_lens), B, T_q, num_pages, page_size, max_blocks, H_q, H_kv, d, block, scale,
+        n_split, _ptr(workspace), _ptr(out), _ptr(lse), _stream(stream))
+
+
+def gqa_attn_decode_fp8_block_default_splits(B, H_kv, S_max) -> int:
+    return load().gqa_attn_decode_fp8_block_default_splits(B, H_kv, S_max)
 
 
 def gqa_trace_clear() -> int:
@@ -461,6 +547,193 @@ def decode_fp8(q, k8, v8, k_scale, v_scale, seq_lens, scale=None, n_split=None, 
         _check(gqa_attn_decode_combine(workspace, B, H_q, d, n_split, out, lse, stream),
                "gqa_attn_decode_combine")
     return out, lse
+
+
+def _need(ok, what):
+    if not ok:
+        raise GQAError(GQA_ERR_INVALID_ARG, what)
+
+
+def _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table, what):
+    """Checks the tensors of a block-scaled E4M3 cache; returns (B, S_max, H_kv, d)."""
+    import torch
+
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    _need(k8.dtype == u8 and v8.dtype == u8 and k8.dim() == 4 and k8.shape == v8.shape
+          and k8.is_contiguous() and v8.is_contiguous(),
+          f"{what}: the codes are dense uint8 [B, S_max, H_kv, d] or [num_pages, page_size, H_kv, d]")
+    units, per, H_kv, d = k8.shape
+    shape = (units, -(-per // block) if block > 0 else 0, H_kv)
+    _need(k_scale.dtype == f32 and v_scale.dtype == f32 and k_scale.shape == shape
+          and v_scale.shape == shape and k_scale.is_contiguous() and v_scale.is_contiguous(),
+          f"{what}: the scales are dense float32 {shape}")
+    dev = k8.device
+    _need(v8.device == dev and k_scale.device == dev and v_scale.device == dev
+          and seq_lens.device == dev and dev.type == "cuda",
+          f"{what}: the tensors are not on one CUDA device")
+    B = units
+    if block_table is not None:
+        _need(block_table.dtype == i32 and block_table.dim() == 2 and block_table.is_contiguous()
+              and block_table.device == dev, f"{what}: block_table is dense int32 [B, max_blocks]")
+        B, per = block_table.shape[0], block_table.shape[1] * per
+    _need(seq_lens.dtype == i32 and seq_lens.shape == (B,) and seq_lens.is_contiguous(),
+          f"{what}: seq_lens is dense int32 [B]")
+    return B, per, H_kv, d
+
+
+def kv_cache_fp8_block(units, per, H_kv, d, block, device="cuda"):
+    """An empty block-scaled E4M3 cache (k8, v8, k_scale, v_scale) of `units` sequences of `per`
+    positions, or of `units` pages of `per` tokens.  Nothing in it needs a value before tokens
+    are appended."""
+    import torch
+
+    def codes():
+        return torch.empty((units, per, H_kv, d), dtype=torch.uint8, device=device)
+
+    def scales():
+        return torch.empty((units, -(-per // block), H_kv), dtype=torch.float32, device=device)
+
+    return codes(), codes(), scales(), scales()
+
+
+def kv_append_fp8_block(k_new, v_new, k8, v8, k_scale, v_scale, seq_lens, block, n_new=None,
+                        block_table=None, stream=None):
+    """Quantise new tokens (bf16 [B, T, H_kv, d]; rows may be slices of wider ones) into a
+    block-scaled E4M3 cache; seq_lens are the lengths after the call, n_new [B] the valid rows
+    of each sequence (None: all T).  Paged when block_table is given."""
+    import torch
+
+    what = "kv_append_fp8_block"
+    B, S_max, H_kv, d = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table, what)
+    _need(k_new.dtype == torch.bfloat16 and v_new.dtype == torch.bfloat16 and k_new.dim() == 4
+          and k_new.shape == v_new.shape and k_new.shape[0] == B and k_new.shape[2:] == (H_kv, d)
+          and k_new.device == k8.device and v_new.device == k8.device,
+          f"{what}: the new rows are bfloat16 [B, T, H_kv, d] on the cache's device")
+    T = k_new.shape[1]
+    _need(n_new is None or (n_new.dtype == torch.int32 and n_new.shape == (B,)
+                            and n_new.is_contiguous() and n_new.device == k8.device),
+          f"{what}: n_new is dense int32 [B]")
+    if T == 0:
+        return
+    # the stride between tokens; a dimension of size 1 has none of its own
+    stride = k_new.stride(1) if T > 1 else k_new.stride(0) if B > 1 else H_kv * d
+    for x in (k_new, v_new):
+        sb, st, sh, sd = x.stride()
+        _need((d == 1 or sd == 1) and (H_kv == 1 or sh == d) and (T == 1 or st == stride)
+              and (B == 1 or sb == T * stride),
+              f"{what}: the rows of k_new and v_new are H_kv * d dense elements, one stride apart")
+    with _on(k8.device):
+        if block_table is None:
+            st = gqa_kv_append_fp8_block(k_new, v_new, stride, n_new, seq_lens, B, T, S_max, H_kv,
+                                         d, block, k8, v8, k_scale, v_scale, stream)
+        else:
+            P, page_size = k8.shape[:2]
+            st = gqa_kv_append_paged_fp8_block(k_new, v_new, stride, n_new, block_table, seq_lens,
+                                               B, T, P, page_size, block_table.shape[1], H_kv, d,
+                                               block, k8, v8, k_scale, v_scale, stream)
+    _check(st, "gqa_kv_append_fp8_block")
+
+
+def kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, start=0, k_out=None, v_out=None,
+                      block_table=None, stream=None):
+    """Tokens start.. of a block-scaled E4M3 cache as bf16 (k, v) [B, S_out, H_kv, d]; rows past
+    a sequence's end keep what k_out and v_out hold (new outputs, S_out = S_max - start: zeros)."""
+    import torch
+
+    what = "kv_read_fp8_block"
+    B, S_max, H_kv, d = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table, what)
+    if k_out is None:
+        k_out = torch.zeros((B, S_max - start, H_kv, d), dtype=torch.bfloat16, device=k8.device)
+    if v_out is None:
+        v_out = torch.zeros(k_out.shape, dtype=torch.bfloat16, device=k8.device)
+    _need(k_out.dtype == torch.bfloat16 and v_out.dtype == torch.bfloat16 and k_out.dim() == 4
+          and k_out.shape == v_out.shape and k_out.shape[0] == B and k_out.shape[2:] == (H_kv, d)
+          and k_out.is_contiguous() and v_out.is_contiguous() and k_out.device == k8.device
+          and v_out.device == k8.device,
+          f"{what}: k_out and v_out are dense bfloat16 [B, S_out, H_kv, d] on the cache's device")
+    S_out = k_out.shape[1]
+    with _on(k8.device):
+        if block_table is None:
+            st = gqa_kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, B, S_max, H_kv, d, block,
+                                       start, S_out, k_out, v_out, stream)
+        else:
+            P, page_size = k8.shape[:2]
+            st = gqa_kv_read_paged_fp8_block(k8, v8, k_scale, v_scale, block_table, seq_lens, B, P,
+                                             page_size, block_table.shape[1], H_kv, d, block,
+                                             start, S_out, k_out, v_out, stream)
+    _check(st, "gqa_kv_read_fp8_block")
+    return k_out, v_out
+
+
+def decode_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=None, n_split=None,
+                     workspace=None, out=None, lse=None, stream=None, block_table=None):
+    """Decode + combine over a block-scaled E4M3 cache (paged when block_table is given).
+
+    q [B, H_q, d] (out [B, H_q, d], lse [B, H_q]) or, for the last T_q positions of each
+    sequence, q [B, T_q, H_q, d] (out [B, T_q, H_q, d], lse [B, T_q, H_q])."""
+    import torch
+
+    what = "decode_fp8_block"
+    B, S_max, H_kv, d = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table, what)
+    dev, rows = k8.device, q.shape[:-1]
+    _need(q.dtype == torch.bfloat16 and q.dim() in (3, 4) and q.shape[0] == B and q.shape[-1] == d
+          and q.is_contiguous() and q.device == dev,
+          f"{what}: q is dense bfloat16 [B, H_q, d] or [B, T_q, H_q, d] on the cache's device")
+    T_q, H_q = (q.shape[1] if q.dim() == 4 else 1), q.shape[-2]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty(rows, dtype=torch.float32, device=dev)
+    _need(out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous()
+          and out.device == dev and lse.dtype == torch.float32 and lse.shape == rows
+          and lse.is_contiguous() and lse.device == dev,
+          f"{what}: out is dense bfloat16 like q, lse dense float32 like q without d")
+    with _on(dev):
+        if n_split is None:
+            n_split = gqa_attn_decode_fp8_block_default_splits(B, H_kv, S_max)
+        if n_split > 1:
+            if workspace is None:
+                workspace = decode_workspace(B * T_q, H_q, d, n_split, dev)
+                _keep(workspace, stream)
+            else:
+                _need(workspace.device == dev and workspace.is_contiguous()
+                      and workspace.numel() * workspace.element_size()
+                      >= gqa_attn_decode_workspace_bytes(B * T_q, H_q, d, n_split),
+                      f"{what}: the workspace is too small or not on the cache's device")
+        if block_table is None:
+            st = gqa_attn_decode_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, B, T_q, S_max,
+                                           H_q, H_kv, d, block, scale, n_split, workspace, out,
+                                           lse, stream)
+        else:
+            P, page_size = k8.shape[:2]
+            st = gqa_attn_decode_paged_fp8_block(q, k8, v8, k_scale, v_scale, block_table, seq_lens,
+                                                 B, T_q, P, page_size, block_table.shape[1], H_q,
+                                                 H_kv, d, block, scale, n_split, workspace, out,
+                                                 lse, stream)
+        _check(st, "gqa_attn_decode_fp8_block")
+        if n_split > 1:
+            _check(gqa_attn_decode_combine(workspace, B * T_q, H_q, d, n_split, out, lse, stream),
+                   "gqa_attn_decode_combine")
+    return out, lse
+
+
+def prefill_chunk_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=None, window=-1,
+                            out=None, lse=None, block_table=None, stream=None):
+    """A chunk of T_q queries ending each sequence (q [B, T_q, H_q, d], any T_q) over a
+    block-scaled E4M3 cache: the cache is read back as bf16 and prefill_chunk runs on it."""
+    import torch
+
+    B, S_max, H_kv, d = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table,
+                                     "prefill_chunk_fp8_block")
+    with _on(k8.device):
+        k = torch.empty((B, S_max, H_kv, d), dtype=torch.bfloat16, device=k8.device)
+        v = torch.empty_like(k)
+        _keep(k, stream)
+        _keep(v, stream)
+        kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, 0, k, v, block_table, stream)
+        return prefill_chunk(q, k, v, seq_lens, scale, window, out, lse, stream)
 
 
 def prefill_causal(q, k, v, scale=None, out=None, lse=None, stream=None):

@@ -543,6 +543,256 @@ gqa_status gqa_attn_decode_paged_fp8(const void* q, const void* k_pool, const vo
       gqa::launch_decode_fp8(p, tm_k, tm_v, tm_ks, tm_vs, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// Token rows of a block-scaled cache: row and key indices, also those of a tile
+// that runs past the end, stay within 32 bits.
+constexpr long long kMaxBlockRows = 0x7fffff00LL;
+
+// The layout of a block-scaled E4M3 cache: checks what the calls on it share and
+// fills the units of the parameter block (a unit is a sequence of a contiguous
+// cache, block_table null, or a page of a pool).
+gqa_status kv_block_layout(const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int32_t* block_table,
+                           const int32_t* seq_lens, int B, int S_max, bool paged, int num_pages,
+                           int page_size, int max_blocks, int H_kv, int d, int block,
+                           gqa::KvBlockParams* p) {
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !seq_lens) return GQA_ERR_INVALID_ARG;
+  if (B < 1 || B > 65535 || H_kv < 1 || H_kv > 32767) return GQA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(seq_lens, 4))
+    return GQA_ERR_INVALID_ARG;
+  if (!head_dim_ok(d)) return GQA_ERR_UNSUPPORTED;
+  if (block != 16 && block != 32 && block != 64 && block != 128) return GQA_ERR_UNSUPPORTED;
+  *p = gqa::KvBlockParams{};
+  if (paged) {
+    if (!block_table || !aligned(block_table, 4)) return GQA_ERR_INVALID_ARG;
+    if (num_pages < 1 || max_blocks < 1 || page_size < 1) return GQA_ERR_INVALID_ARG;
+    if (page_size < 16 || (page_size & (page_size - 1)) != 0) return GQA_ERR_UNSUPPORTED;
+    if (block > page_size) return GQA_ERR_INVALID_ARG;
+    if ((long long)max_blocks * page_size > kMaxBlockRows ||
+        (long long)num_pages * page_size > kMaxBlockRows)
+      return GQA_ERR_INVALID_ARG;
+    S_max = max_blocks * page_size;
+    p->units = num_pages;
+    p->per = page_size;
+    p->block_table = block_table;
+    p->max_blocks = max_blocks;
+    p->page_size = page_size;
+    p->num_pages = num_pages;
+  } else {
+    if (S_max < 1 || (long long)B * S_max > kMaxBlockRows) return GQA_ERR_INVALID_ARG;
+    p->units = B;
+    p->per = S_max;
+  }
+  p->per_blk = p->per / block + (p->per % block != 0);
+  p->B = B;
+  p->S_max = S_max;
+  p->H_kv = H_kv;
+  p->d = d;
+  p->block = block;
+  p->seq_lens = seq_lens;
+  p->k_cache = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+  p->v_cache = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+  p->k_scale = const_cast<float*>(k_scale);
+  p->v_scale = const_cast<float*>(v_scale);
+  return GQA_OK;
+}
+
+gqa_status run_kv_append(gqa::KvBlockParams* p, const void* k_new, const void* v_new,
+                         long long new_stride, const int32_t* n_new, int T, gqa_stream_t stream) {
+  if (!k_new || !v_new || T < 1) return GQA_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || (n_new && !aligned(n_new, 4)))
+    return GQA_ERR_INVALID_ARG;
+  if (new_stride < (long long)p->H_kv * p->d || new_stride % 8 != 0) return GQA_ERR_INVALID_ARG;
+  p->k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p->v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p->new_stride = new_stride;
+  p->n_new = n_new;
+  p->T = T;
+  const gqa_status st = error_word(&p->err);
+  if (st != GQA_OK) return st;
+  return cuda_status(gqa::launch_kv_append(*p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gqa_status run_kv_read(gqa::KvBlockParams* p, int start, int S_out, void* k_out, void* v_out,
+                       gqa_stream_t stream) {
+  if (!k_out || !v_out || start < 0 || S_out < 1) return GQA_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return GQA_ERR_INVALID_ARG;
+  if ((long long)start + S_out > 0x7fffffffLL) return GQA_ERR_INVALID_ARG;
+  p->start = start;
+  p->S_out = S_out;
+  p->k_out = static_cast<__nv_bfloat16*>(k_out);
+  p->v_out = static_cast<__nv_bfloat16*>(v_out);
+  const gqa_status st = error_word(&p->err);
+  if (st != GQA_OK) return st;
+  return cuda_status(
+      gqa::launch_kv_read(*p, num_sms_current_device(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int T_q, int H_q,
+                                float scale, int n_split, void* workspace, void* out, float* lse,
+                                gqa_stream_t stream) {
+  if (!q || !out || !lse || H_q < 1 || n_split < 1) return GQA_ERR_INVALID_ARG;
+  if (H_q % c.H_kv != 0 || H_q > 65535) return GQA_ERR_INVALID_ARG;
+  if (T_q < 1 || T_q > 64 || T_q > c.S_max) return GQA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return GQA_ERR_INVALID_ARG;
+  if ((long long)c.B * T_q > 65535) return GQA_ERR_INVALID_ARG;
+  const int G = H_q / c.H_kv;
+  if (G > 16 || T_q * G > kMaxMultiRows) return GQA_ERR_UNSUPPORTED;
+  if (n_split > 1 && !workspace) return GQA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+      (workspace && !aligned(workspace, 256)))
+    return GQA_ERR_INVALID_ARG;
+  // Codes as [rows][H_kv][d] bytes; boxes of up to 128 rows of one head, always
+  // 128 bytes wide: for d = 32 and 64 TMA fills the rest of each row with zeros.
+  const long long rows = (long long)c.units * c.per;
+  const int box_rows = c.block_table && c.page_size < 128 ? c.page_size : 128;
+  const uint64_t dims[3] = {(uint64_t)c.d, (uint64_t)c.H_kv, (uint64_t)rows};
+  const uint64_t strides[2] = {(uint64_t)c.d, (uint64_t)c.H_kv * c.d};
+  const uint32_t box[3] = {128u, 1u, (uint32_t)box_rows};
+  CUtensorMap tm_k, tm_v;
+  unsigned* err = nullptr;
+  gqa_status st = error_word(&err);
+  if (st != GQA_OK) return st;
+  if ((st = encode_map(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.k_cache, 3, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B)) != GQA_OK)
+    return st;
+  if ((st = encode_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.v_cache, 3, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B)) != GQA_OK)
+    return st;
+  auto log2i = [](int x) {
+    int l = 0;
+    while ((1 << l) < x) ++l;
+    return l;
+  };
+  gqa::DecodeBlockParams p{};
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.block_log2 = log2i(c.block);
+  p.page_log2 = c.block_table ? log2i(c.page_size) : 0;
+  p.per_blk = c.per_blk;
+  gqa::DecodeParams& dp = p.dec;
+  dp.q = static_cast<const __nv_bfloat16*>(q);
+  dp.seq_lens = c.seq_lens;
+  dp.B = c.B;
+  dp.S_max = c.S_max;
+  dp.H_q = H_q;
+  dp.H_kv = c.H_kv;
+  dp.G = G;
+  dp.d = c.d;
+  dp.T_q = T_q;
+  dp.n_rg = 1;
+  dp.n_split = n_split;
+  const long long per = ((long long)c.S_max + n_split - 1) / n_split;
+  dp.chunk = (int)((per + 127) / 128 * 128);  // (S_max is below 2^31 - 255)
+  dp.scale_log2 = scale * 1.4426950408889634f;
+  dp.ws_ml = static_cast<float2*>(workspace);
+  dp.ws_O = workspace ? reinterpret_cast<float*>(
+                            static_cast<char*>(workspace) +
+                            gqa::decode_ws_O_offset(c.B * T_q, H_q, n_split))
+                      : nullptr;
+  dp.out = static_cast<__nv_bfloat16*>(out);
+  dp.lse = lse;
+  dp.err = err;
+  dp.wait_ns = g_wait_ns.load();
+  dp.block_table = c.block_table;
+  dp.max_blocks = c.max_blocks;
+  dp.page_size = c.page_size;
+  dp.num_pages = c.num_pages;
+  return cuda_status(gqa::launch_decode_fp8_block(p, tm_k, tm_v, num_sms_current_device(),
+                                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+gqa_status gqa_kv_append_fp8_block(const void* k_new, const void* v_new, int64_t new_stride,
+                                   const int32_t* n_new, const int32_t* seq_lens, int B, int T,
+                                   int S_max, int H_kv, int d, int block, void* k_cache,
+                                   void* v_cache, float* k_scale, float* v_scale,
+                                   gqa_stream_t stream) {
+  gqa::KvBlockParams p;
+  const gqa_status st = kv_block_layout(k_cache, v_cache, k_scale, v_scale, nullptr, seq_lens, B,
+                                        S_max, false, 0, 0, 0, H_kv, d, block, &p);
+  if (st != GQA_OK) return st;
+  return run_kv_append(&p, k_new, v_new, new_stride, n_new, T, stream);
+}
+
+gqa_status gqa_kv_append_paged_fp8_block(const void* k_new, const void* v_new, int64_t new_stride,
+                                         const int32_t* n_new, const int32_t* block_table,
+                                         const int32_t* seq_lens, int B, int T, int num_pages,
+                                         int page_size, int max_blocks, int H_kv, int d, int block,
+                                         void* k_pool, void* v_pool, float* k_scale,
+                                         float* v_scale, gqa_stream_t stream) {
+  gqa::KvBlockParams p;
+  const gqa_status st = kv_block_layout(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, B,
+                                        0, true, num_pages, page_size, max_blocks, H_kv, d, block,
+                                        &p);
+  if (st != GQA_OK) return st;
+  return run_kv_append(&p, k_new, v_new, new_stride, n_new, T, stream);
+}
+
+gqa_status gqa_kv_read_fp8_block(const void* k_cache, const void* v_cache, const float* k_scale,
+                                 const float* v_scale, const int32_t* seq_lens, int B, int S_max,
+                                 int H_kv, int d, int block, int start, int S_out, void* k_out,
+                                 void* v_out, gqa_stream_t stream) {
+  gqa::KvBlockParams p;
+  const gqa_status st = kv_block_layout(k_cache, v_cache, k_scale, v_scale, nullptr, seq_lens, B,
+                                        S_max, false, 0, 0, 0, H_kv, d, block, &p);
+  if (st != GQA_OK) return st;
+  return run_kv_read(&p, start, S_out, k_out, v_out, stream);
+}
+
+gqa_status gqa_kv_read_paged_fp8_block(const void* k_pool, const void* v_pool,
+                                       const float* k_scale, const float* v_scale,
+                                       const int32_t* block_table, const int32_t* seq_lens, int B,
+                                       int num_pages, int page_size, int max_blocks, int H_kv,
+                                       int d, int block, int start, int S_out, void* k_out,
+                                       void* v_out, gqa_stream_t stream) {
+  gqa::KvBlockParams p;
+  const gqa_status st = kv_block_layout(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, B,
+                                        0, true, num_pages, page_size, max_blocks, H_kv, d, block,
+                                        &p);
+  if (st != GQA_OK) return st;
+  return run_kv_read(&p, start, S_out, k_out, v_out, stream);
+}
+
+gqa_status gqa_attn_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* seq_lens, int B, int T_q, int S_max, int H_q,
+                                     int H_kv, int d, int block, float scale, int n_split,
+                                     void* workspace, void* out, float* lse,
+                                     gqa_stream_t stream) {
+  gqa::KvBlockParams c;
+  const gqa_status st = kv_block_layout(k_cache, v_cache, k_scale, v_scale, nullptr, seq_lens, B,
+                                        S_max, false, 0, 0, 0, H_kv, d, block, &c);
+  if (st != GQA_OK) return st;
+  return run_decode_fp8_block(c, q, T_q, H_q, scale, n_split, workspace, out, lse, stream);
+}
+
+gqa_status gqa_attn_decode_paged_fp8_block(const void* q, const void* k_pool, const void* v_pool,
+                                           const float* k_scale, const float* v_scale,
+                                           const int32_t* block_table, const int32_t* seq_lens,
+                                           int B, int T_q, int num_pages, int page_size,
+                                           int max_blocks, int H_q, int H_kv, int d, int block,
+                                           float scale, int n_split, void* workspace, void* out,
+                                           float* lse, gqa_stream_t stream) {
+  gqa::KvBlockParams c;
+  const gqa_status st = kv_block_layout(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, B,
+                                        0, true, num_pages, page_size, max_blocks, H_kv, d, block,
+                                        &c);
+  if (st != GQA_OK) return st;
+  return run_decode_fp8_block(c, q, T_q, H_q, scale, n_split, workspace, out, lse, stream);
+}
+
+int gqa_attn_decode_fp8_block_default_splits(int B, int H_kv, int S_max) {
+  return gqa_attn_decode_default_splits(B, H_kv, S_max, -1);
+}
+
 gqa_status gqa_attn_decode_combine(const void* workspace, int B, int H_q, int d, int n_split,
                                    void* out, float* lse, gqa_stream_t stream) {
   if (!workspace || !out || !lse) return GQA_ERR_INVALID_ARG;

@@ -76,6 +76,36 @@ struct PrefillParams {
   float* ws_O;    // [rows][n_part][d]
 };
 
+// The block-scaled E4M3 cache (codes [units][per][H_kv][d], scales
+// [units][per_blk][H_kv] fp32): a unit is a sequence of a contiguous cache
+// (per = S_max) or a page of a pool (per = page_size, block_table set).
+struct KvBlockParams {
+  int B, S_max, H_kv, d, block;
+  int units, per, per_blk;  // per_blk = ceil(per / block)
+  const int32_t* seq_lens;  // [B]
+  const int32_t* block_table;
+  int max_blocks, page_size, num_pages;
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  // append: the last n_new[b] (or T) of seq_lens[b] tokens are rows 0.. of
+  // [B, T] rows, new_stride elements apart
+  const __nv_bfloat16 *k_new, *v_new;
+  long long new_stride;
+  const int32_t* n_new;
+  int T;
+  // read: tokens start.. of each sequence to [B, S_out, H_kv, d]
+  int start, S_out;
+  __nv_bfloat16 *k_out, *v_out;
+  unsigned* err;
+};
+
+// Decode over that cache: the rows of DecodeParams plus the scales.
+struct DecodeBlockParams {
+  DecodeParams dec;
+  const float *k_scale, *v_scale;
+  int block_log2, page_log2, per_blk;
+};
+
 // Byte offset of the O partials in a chunk-split prefill workspace.
 inline size_t prefill_ws_O_offset(size_t rows, int n_part) {
   return (rows * n_part * sizeof(float2) + 255) / 256 * 256;
@@ -112,6 +142,13 @@ cudaError_t launch_prefill_chunk(const PrefillParams& p, const CUtensorMap& tm_q
 cudaError_t launch_prefill_merge(const PrefillParams& p, cudaStream_t stream);
 // Trace build: zero the causal prefill's stamp records (no-op otherwise).
 cudaError_t prefill_trace_clear();
+cudaError_t launch_kv_append(const KvBlockParams& p, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvBlockParams& p, int num_sms, cudaStream_t stream);
+// Decode of T_q * G (<= 64) query rows per KV head over the block-scaled E4M3
+// cache; K/V boxes of min(page_size, 128) rows, 128 bytes wide; p.dec.chunk a
+// multiple of 128.  Same partial layout as launch_decode_split.
+cudaError_t launch_decode_fp8_block(const DecodeBlockParams& p, const CUtensorMap& tm_k,
+                                    const CUtensorMap& tm_v, int sms, cudaStream_t stream);
 cudaError_t launch_wait_selftest(unsigned* err, uint64_t limit_ns, cudaStream_t stream);
 
 // Layout of the decode workspace: byte offset of the O partials.

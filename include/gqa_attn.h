@@ -43,6 +43,10 @@
  * - An E4M3 cache with per-token scales: gqa_attn_decode_fp8 /
  *   gqa_attn_decode_paged_fp8 (+ combine) with 3x the default split count
  *   (15.8-16.3 us per step at 32K).
+ * - An E4M3 cache with a scale per block of tokens and KV head, filled by this
+ *   library: gqa_kv_append_fp8_block as tokens arrive, gqa_attn_decode_fp8_block
+ *   (+ combine) for the last one or few tokens, gqa_kv_read_fp8_block followed by
+ *   gqa_attn_prefill_chunk for the next chunk of a prompt (each also paged).
  * - A few new tokens per sequence (speculative verification, T_q <= 64):
  *   gqa_attn_decode_multi / gqa_attn_decode_paged_multi (+ combine with B * T_q
  *   rows); above 16 query rows per KV head at d = 128 they run on the tensor
@@ -436,6 +440,106 @@ gqa_status gqa_attn_decode_paged_multi(const void* q, const void* k_pool, const 
                                        int H_q, int H_kv, int d, float scale, int n_split,
                                        void* workspace, void* out, float* lse,
                                        gqa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The block-scaled E4M3 cache: writing, reading back, decode
+ * ------------------------------------------------------------------------
+ * Keys and values as E4M3 codes with one fp32 scale for every `block` consecutive
+ * tokens of a KV head, K and V apart (an E4M3 cache as in gqa_attn_decode_fp8,
+ * with scales that follow the heads and cover several tokens):
+ *   contiguous  k_cache, v_cache  device uint8 [B, S_max, H_kv, d]
+ *               k_scale, v_scale  device fp32  [B, ceil(S_max / block), H_kv]
+ *   paged       k_pool, v_pool    device uint8 [num_pages, page_size, H_kv, d]
+ *               k_scale, v_scale  device fp32  [num_pages, page_size / block, H_kv]
+ * The value held for token t, head h, element c is e4m3(code) * scale of t's block.
+ * block is 16, 32, 64 or 128, d is 32, 64 or 128 (GQA_ERR_UNSUPPORTED otherwise);
+ * pages as in gqa_attn_decode_paged, with block <= page_size.  A cache has at most
+ * 2^31 - 256 token rows (B * S_max, or num_pages * page_size).  Codes are 16-byte,
+ * scales 4-byte aligned.  seq_lens: device int32 [B].
+ *
+ * Append: quantises the last tokens of each sequence into the cache.
+ *   k_new, v_new  device bf16, rows (b * T + i) * new_stride of H_kv * d elements
+ *                 each: [B, T, H_kv, d] if new_stride = H_kv * d, or a slice of
+ *                 wider rows (a fused projection).  new_stride is in elements, a
+ *                 multiple of 8, at least H_kv * d.
+ *   n_new         device int32 [B] with 0 <= n_new[b] <= T, or NULL (every one T)
+ *   seq_lens      lengths AFTER the call: rows i < n_new[b] become tokens
+ *                 seq_lens[b] - n_new[b] + i.  n_new[b] <= seq_lens[b] <= S_max.
+ * With a the largest finite |x| of the new tokens of a block and head, their scale
+ * is the smallest power of two s >= 2^-100 with a / s <= 448.  A block whose first
+ * token is new takes it; a block that holds older tokens takes the larger of it
+ * and its present scale, and if that grows its older codes are rounded again:
+ * e4m3(code * old / s).  New codes are e4m3(x / s), to nearest even; infinities
+ * and NaN become the NaN code and do not enter the scale.  Nothing else is read or
+ * written: rows at or past seq_lens[b], rows i >= n_new[b] and the blocks before
+ * the first new token are left alone, and a block's contents past seq_lens[b] may
+ * be anything.  No atomics: the result does not depend on timing, and appending
+ * the same tokens in one call or in several differs only where a scale grew later
+ * (codes rounded twice below E4M3's normal range).  Two sequences must not share
+ * a page that is written (shared prefixes end at a page boundary), and calls that
+ * touch the same block must be ordered.  A bad length or count (checked on the
+ * device) leaves that sequence's cache untouched, an entry of the block table
+ * outside the pool leaves that block unwritten; both are reported through the
+ * error word (GQA_ERR_INVALID_ARG). */
+gqa_status gqa_kv_append_fp8_block(const void* k_new, const void* v_new, int64_t new_stride,
+                                   const int32_t* n_new, const int32_t* seq_lens, int B, int T,
+                                   int S_max, int H_kv, int d, int block, void* k_cache,
+                                   void* v_cache, float* k_scale, float* v_scale,
+                                   gqa_stream_t stream);
+gqa_status gqa_kv_append_paged_fp8_block(const void* k_new, const void* v_new, int64_t new_stride,
+                                         const int32_t* n_new, const int32_t* block_table,
+                                         const int32_t* seq_lens, int B, int T, int num_pages,
+                                         int page_size, int max_blocks, int H_kv, int d, int block,
+                                         void* k_pool, void* v_pool, float* k_scale,
+                                         float* v_scale, gqa_stream_t stream);
+
+/* Read back: tokens start .. start + S_out - 1 of each sequence as bf16,
+ *   k_out, v_out  device bf16 [B, S_out, H_kv, d] (16-byte aligned),
+ * row i = bf16(e4m3(code) * scale) of token start + i, rounded to nearest even
+ * (exact for power-of-two scales within bf16's range).  Rows of tokens at or past
+ * seq_lens[b] are left as they were; 0 <= seq_lens[b] <= S_max (a bad length, or a
+ * page index outside the pool, makes the rows concerned NaN and sets the error
+ * word).  With start = 0 and S_out = S_max the result is the cache that
+ * gqa_attn_prefill_chunk takes. */
+gqa_status gqa_kv_read_fp8_block(const void* k_cache, const void* v_cache, const float* k_scale,
+                                 const float* v_scale, const int32_t* seq_lens, int B, int S_max,
+                                 int H_kv, int d, int block, int start, int S_out, void* k_out,
+                                 void* v_out, gqa_stream_t stream);
+gqa_status gqa_kv_read_paged_fp8_block(const void* k_pool, const void* v_pool,
+                                       const float* k_scale, const float* v_scale,
+                                       const int32_t* block_table, const int32_t* seq_lens, int B,
+                                       int num_pages, int page_size, int max_blocks, int H_kv,
+                                       int d, int block, int start, int S_out, void* k_out,
+                                       void* v_out, gqa_stream_t stream);
+
+/* Decode of the last T_q positions of each sequence over that cache: queries,
+ * visibility, outputs, workspace and follow-up gqa_attn_decode_combine() are those
+ * of gqa_attn_decode_multi() (q and out bf16 [B, T_q, H_q, d], lse fp32
+ * [B, T_q, H_q]; 1 <= T_q <= seq_lens[b] <= S_max), with splits of
+ * ceil(S_max / n_split) keys rounded up to 128.  1 <= T_q <= 64, G = H_q / H_kv <=
+ * 16 and T_q * G <= 64 (GQA_ERR_UNSUPPORTED above); scale finite > 0.  Scales may
+ * be any finite fp32 numbers for keys; for values they must not be negative
+ * (NaN outputs), and one below 2^-100 counts as zero.  The codes are multiplied
+ * as they are, queries and weights as sums of two E4M3 terms (queries to 2^-21 of
+ * their row's largest magnitude, weights as bf16 would hold them).  A partial's m
+ * is a reference near the split's largest x_j + ln v_scale_j, not max_j x_j; l
+ * and O hold relative to it, so the merge is unchanged.  A query row with an
+ * infinity or NaN gives NaN.  Deterministic. */
+gqa_status gqa_attn_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* seq_lens, int B, int T_q, int S_max, int H_q,
+                                     int H_kv, int d, int block, float scale, int n_split,
+                                     void* workspace, void* out, float* lse, gqa_stream_t stream);
+gqa_status gqa_attn_decode_paged_fp8_block(const void* q, const void* k_pool, const void* v_pool,
+                                           const float* k_scale, const float* v_scale,
+                                           const int32_t* block_table, const int32_t* seq_lens,
+                                           int B, int T_q, int num_pages, int page_size,
+                                           int max_blocks, int H_q, int H_kv, int d, int block,
+                                           float scale, int n_split, void* workspace, void* out,
+                                           float* lse, gqa_stream_t stream);
+
+/* Split count for gqa_attn_decode_fp8_block on the current device.  Returns >= 1. */
+int gqa_attn_decode_fp8_block_default_splits(int B, int H_kv, int S_max);
 
 /* ------------------------------------------------------------------------
  * Decode with the merge inside thread-block clusters
