@@ -42,31 +42,61 @@
 namespace gqa {
 namespace {
 
-constexpr int kFbThreads = 192;
 constexpr int kFbKeys = 128;                // keys per tile
 constexpr uint32_t kFbTile = 128u * 128u;   // 128 rows of 128 bytes
 constexpr float kLoStep = 1.f / 32.f;       // weight of the low term
 constexpr float kPScaleLog2 = 8.f;          // P is held times 2^8
 constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100
 
-template <int R, int NS>
-struct FbLayout {
+// Compile-time shape of one variant.  R query rows (padded), NS slots per ring,
+// NT streams of tiles (stream s takes tiles s, s + NT, ..) and NG groups of rows:
+// the 4 NT NG softmax warps share the work of a tile by rows and alternate tiles.
+template <int R_, int NS_, int NT_, int NG_>
+struct FbShape {
+  static constexpr int R = R_, NS = NS_, NT = NT_, NG = NG_;
+  static constexpr int RW = R / NG;                 // rows of a warp
+  static constexpr int kWarps = 4 * NT * NG;        // softmax warps
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr uint32_t kRowP = 2 * R;          // bytes of a key's row of P
   static constexpr uint32_t kOffV = NS * kFbTile;
   static constexpr uint32_t kOffQ = 2 * NS * kFbTile;
   static constexpr uint32_t kOffP = kOffQ + 2 * R * 128;
-  static constexpr uint32_t kBytes = kOffP + 2 * R * 128 + 1024;  // + alignment slack
-  static constexpr uint32_t kCols = R == 8 ? 64 : R == 16 ? 128 : R == 32 ? 256 : 512;
-  static constexpr uint32_t kColO = 4 * R;  // S_0, S_1 (2R columns each), then O
-  static constexpr int kChunk = R < 16 ? R : 16;  // rows handled at once
-  static constexpr int kPerSM = 2 * (kBytes + 2048) <= 227 * 1024 ? 2 : 1;
+  static constexpr uint32_t kTileP = 128 * kRowP;
+  static constexpr uint32_t kBytes = kOffP + NT * kTileP + 1024;  // + alignment slack
+  // tensor memory: S_0, S_1, then NT accumulators, 2R columns each
+  static constexpr uint32_t kColO = 4 * R;
+  static constexpr uint32_t kUsed = (4 + 2 * NT) * R;
+  static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  // CTAs an SM holds: shared memory (4 KB of it for the static part and the
+  // driver's) and 16 warps' worth of threads at 100 registers
+  static constexpr int kPerSM = 2 * (kBytes + 4096) <= 227 * 1024 && kThreads <= 320 ? 2 : 1;
 };
 
 // Instruction descriptor of tcgen05.mma.kind::f8f6f4 with E4M3 operands and fp32
 // accumulation: bits 4-5 D format (1 = f32), 7-9 and 10-12 the A and B formats
-// (0 = E4M3), 15 A major (1 = MN), 17-22 N >> 3, 24-28 M >> 4.
-__host__ __device__ constexpr uint32_t instr_desc_e4m3_f32(int M, int N, bool a_mn_major) {
-  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
+// (0 = E4M3), 15 and 16 A and B major (1 = MN), 17-22 N >> 3, 24-28 M >> 4.
+__host__ __device__ constexpr uint32_t instr_desc_e4m3_f32(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Shared-memory descriptor of an MN-major 8-bit operand whose whole N extent is one
+// row of SPAN bytes (16, 32, 64 or 128), one row per k, swizzled over the row;
+// groups of 8 rows follow one another.  Layout field (bits 61-63): 0 none, 6 32-byte,
+// 4 64-byte, 2 128-byte swizzle.  Without a swizzle the leading offset strides the
+// groups, with one the stride offset does: both are given.
+// Offset of byte `at` in such an operand: 16-byte pieces of a row are swizzled.
+template <int SPAN>
+__device__ __forceinline__ uint32_t swz_row(uint32_t at) {
+  if constexpr (SPAN == 16) return at;
+  else return swizzle<SPAN>(at);
+}
+template <int SPAN>
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+  constexpr uint64_t layout = SPAN == 128 ? 2 : SPAN == 64 ? 4 : SPAN == 32 ? 6 : 0;
+  constexpr uint64_t stride = (8 * SPAN) >> 4;
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (stride << 16) | (stride << 32) |
+         (1ull << 46) | (layout << 61);
 }
 
 __device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -80,13 +110,7 @@ __device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
-// 8 or 16 consecutive 32-bit columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                 "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
+// 16 or 32 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -101,6 +125,10 @@ template <int N>
 __device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) {
+  tmem_ld32(taddr, r);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -119,31 +147,57 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t two) {
   const uint32_t h = e4m3x2_to_f16x2(two);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// Two f16 values to two E4M3 codes.
+__device__ __forceinline__ uint32_t pack_e4m3x2(uint32_t f16x2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(f16x2));
+  return r;
+}
+
+// Sums v[0..N-1] over the 32 lanes, N a power of two: each step halves the
+// values a lane holds.  Lane l ends with the total of value l >> (5 - log2 N)
+// (the steps take the lane bits from the highest down).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+  int off = 16;
+#pragma unroll
+  for (int n = N; n > 1; n >>= 1) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float send = up ? v[i] : v[i + n / 2], keep = up ? v[i + n / 2] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
+    off >>= 1;
+  }
+#pragma unroll
+  for (int o = 16 / N; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
 }
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-template <int R, int NS, bool PAGED>
-__global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
+template <typename Sh, bool PAGED>
+__global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     gqa_decode_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 const __grid_constant__ CUtensorMap tm_v,
                                 const DecodeBlockParams pb) {
-  using Lay = FbLayout<R, NS>;
-  constexpr int RC = Lay::kChunk;
-  constexpr int NC = R / RC;
+  constexpr int R = Sh::R, NS = Sh::NS, NT = Sh::NT, NG = Sh::NG, RW = Sh::RW;
   const DecodeParams& p = pb.dec;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  __shared__ __align__(8) uint64_t s_full[2], q_ready, p_ready, o_full, drain;
+  __shared__ __align__(8) uint64_t s_full[2], q_ready, p_ready[NT], o_full[NT], drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag, bad_page;
-  __shared__ float cq[R];                       // tau log2(e) 2^-k of each row's query
-  __shared__ int lim_sm[R];                     // keys below it are visible
-  __shared__ __align__(16) float red[2][R][4];  // maxima of the four warps, by tile parity
-  __shared__ float m_run[2][R];                 // running references, by tile parity
+  __shared__ __align__(16) float cq[R];         // tau log2(e) 2^-k of each row's query
+  __shared__ __align__(16) int lim_sm[R];       // keys below it are visible
+  // the four warps' maxima of each row, by the parity of the stream's turn: written
+  // again two turns later, past a barrier that follows every read (later: sums of l)
+  __shared__ __align__(16) float red[2][NT][R][4];
+  // each softmax warp's own copy of its rows' new references less 8, and factors
+  __shared__ __align__(16) float ref_sm[Sh::kWarps][RW], alpha_sm[Sh::kWarps][RW];
+  __shared__ float m_end[NT][R];                // final references
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -181,16 +235,18 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
     }
     mbar_init(smem_u32(&s_full[0]), 1);
     mbar_init(smem_u32(&s_full[1]), 1);
-    mbar_init(smem_u32(&q_ready), 4);
-    mbar_init(smem_u32(&p_ready), 4);
-    mbar_init(smem_u32(&o_full), 1);
+    mbar_init(smem_u32(&q_ready), Sh::kWarps);
+    for (int s = 0; s < NT; ++s) {
+      mbar_init(smem_u32(&p_ready[s]), 4 * NG);
+      mbar_init(smem_u32(&o_full[s]), 1);
+    }
     mbar_init(smem_u32(&drain), 1);
     abort_flag = 0;
     bad_page = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_base_sh), Lay::kCols);
+    tmem_alloc(smem_u32(&tmem_base_sh), Sh::kCols);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -227,11 +283,9 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
   const bool bad = L < p.T_q || L > p.S_max;  // (L >= T_q >= 1 otherwise)
   const int t_end = bad ? 0 : min(t0 + min(p.chunk, p.S_max - t0), L);
   const int n = t_end > t0 ? (t_end - t0 + kFbKeys - 1) / kFbKeys : 0;
-  if (threadIdx.x >= 64) {
-    for (int r = threadIdx.x - 64; r < R; r += 128) {
-      lim_sm[r] = r < rows ? min(t_end, L - p.T_q + 1 + r / G) : t_end;
-      m_run[0][r] = -INFINITY;
-    }
+  if (threadIdx.x < R) {
+    const int r = threadIdx.x;
+    lim_sm[r] = r < rows ? min(t_end, L - p.T_q + 1 + r / G) : t_end;
   }
   __syncthreads();
   tc_fence_after();
@@ -240,13 +294,13 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
     // A bad length: NaN outputs and the error bit.  An empty split: the merge
     // identity (-inf, 0); its O is not written.  (One split is never empty.)
     if (bad && threadIdx.x == 0 && split == 0 && kv == 0) atomicOr(p.err, kErrBadSeqLen);
-    for (int r = threadIdx.x; r < rows; r += kFbThreads)
+    for (int r = threadIdx.x; r < rows; r += Sh::kThreads)
       write_nan_or_ml(out_row(r), bad ? make_float2(NAN, NAN) : make_float2(-INFINITY, 0.f));
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
       tc_fence_after();
-      tmem_dealloc(tmem, Lay::kCols);
+      tmem_dealloc(tmem, Sh::kCols);
     }
     return;
   }
@@ -285,7 +339,7 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
       if (j >= NS && !wait_all(is_k ? &k_empty[slot] : &v_empty[slot], ((j / NS) - 1) & 1))
         return false;
       const uint32_t fb = smem_u32(is_k ? &k_full[slot] : &v_full[slot]);
-      const uint32_t dst = sb + (is_k ? 0u : Lay::kOffV) + slot * kFbTile;
+      const uint32_t dst = sb + (is_k ? 0u : Sh::kOffV) + slot * kFbTile;
       const CUtensorMap* map = is_k ? &tm_k : &tm_v;
       const int tok0 = t0 + j * kFbKeys;
       if constexpr (!PAGED) {
@@ -333,42 +387,43 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer --
-    constexpr uint32_t idS = instr_desc_e4m3_f32(128, 2 * R, false);
-    constexpr uint32_t idO = instr_desc_e4m3_f32(128, 2 * R, true);
-    const uint32_t qb = sb + Lay::kOffQ, ppb = sb + Lay::kOffP;
+    constexpr uint32_t idS = instr_desc_e4m3_f32(128, 2 * R, false, false);
+    constexpr uint32_t idO = instr_desc_e4m3_f32(128, 2 * R, true, true);
+    const uint32_t qb = sb + Sh::kOffQ, ppb = sb + Sh::kOffP;
     const int ksteps = D / 32;
-    auto issue_s = [&](int j) {  // S_j = K_j Q^T
+    auto issue_s = [&](int j) -> bool {  // S_j = K_j Q^T
+      if (!wait_all(&k_full[j % NS], (j / NS) & 1)) return false;
+      tc_fence_after();
       const uint32_t kb = sb + (j % NS) * kFbTile;
       for (int kk = 0; kk < ksteps; ++kk)
         tc_mma_f8_ss(tmem + 2 * R * (j & 1), smem_desc_sw128(kb + kk * 32, 16, 1024),
                      smem_desc_sw128(qb + kk * 32, 16, 1024), idS, kk > 0);
+      tc_commit(smem_u32(&s_full[j & 1]));
+      tc_commit(smem_u32(&k_empty[j % NS]));
+      return true;
     };
     auto finish = [&](int j) -> bool {  // O = V_j^T P_j, once both are there
+      const int s = j % NT;
       if (!wait_all(&v_full[j % NS], (j / NS) & 1)) return false;
-      if (!wait_all(&p_ready, j & 1)) return false;
+      if (!wait_all(&p_ready[s], (j / NT) & 1)) return false;
       tc_fence_after();
-      const uint32_t vb = sb + Lay::kOffV + (j % NS) * kFbTile;
+      const uint32_t vb = sb + Sh::kOffV + (j % NS) * kFbTile, pj = ppb + s * Sh::kTileP;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)  // 32 keys each: four groups of 8 rows of V
-        tc_mma_f8_ss(tmem + Lay::kColO, smem_desc_sw128(vb + kk * 4096, kFbTile, 1024),
-                     smem_desc_sw128(ppb + kk * 32, 16, 1024), idO, kk > 0);
-      tc_commit(smem_u32(&o_full));
+      for (int kk = 0; kk < 4; ++kk)  // 32 keys each: four groups of 8 rows of V and of P
+        tc_mma_f8_ss(tmem + Sh::kColO + 2 * R * s, smem_desc_sw128(vb + kk * 4096, kFbTile, 1024),
+                     smem_desc_mn<Sh::kRowP>(pj + kk * 32 * Sh::kRowP), idO, kk > 0);
+      tc_commit(smem_u32(&o_full[s]));
       tc_commit(smem_u32(&v_empty[j % NS]));
       return true;
     };
-    bool ok = wait_all(&q_ready, 0);
-    // Order S_0, S_1, O_0, S_2, O_1, ...: S_{j+1} runs while the softmax works on
-    // S_j.  S_j overwrites S_{j-2}, which was read before p_ready(j - 2).
+    // Order S_0, S_1, O_0, S_2, O_1, ...: the next S runs while the softmax works.
+    // S_{j+2} overwrites S_j, which was read before p_ready of tile j.
+    bool ok = wait_all(&q_ready, 0) && issue_s(0);
+    if (ok && n > 1) ok = issue_s(1);
     for (int j = 0; ok && j < n; ++j) {
-      ok = wait_all(&k_full[j % NS], (j / NS) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      issue_s(j);
-      tc_commit(smem_u32(&s_full[j & 1]));
-      tc_commit(smem_u32(&k_empty[j % NS]));
-      if (j > 0) ok = finish(j - 1);
+      ok = finish(j);
+      if (ok && j + 2 < n) ok = issue_s(j + 2);
     }
-    if (ok) finish(n - 1);
     // Every MMA issued here has completed before tensor memory is released.
     tc_commit(smem_u32(&drain));
     mbar_wait(smem_u32(&drain), 0, p.wait_ns, p.err);
@@ -378,10 +433,15 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
     const int quarter = warp & 3;                // tensor-memory lanes 32 * quarter ..
     const int kl = quarter * 32 + lane;          // key of a tile; later, row d of O^T
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const int sw = warp - 2, gi = sw >> 2;       // warp, and group of four
+    const int st = gi / NG, r0 = (gi % NG) * RW;  // stream of tiles, first row
+    // Column (and byte of P, and row of Q) of row r's high term; the low term's
+    // is RW further: a warp's 2 RW columns are neighbours.
+    auto col = [](int r) { return r / RW * 2 * RW + r % RW; };
 
     // Q as two E4M3 terms, one row per warp and turn: lane takes columns
     // 4 lane .. 4 lane + 3.
-    for (int r = quarter; r < R; r += 4) {
+    for (int r = sw; r < R; r += Sh::kWarps) {
       uint2 w = make_uint2(0u, 0u);
       if (r < rows && lane * 4 < D)
         w = *reinterpret_cast<const uint2*>(p.q + out_row(r) * D + lane * 4);
@@ -404,18 +464,18 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
         lo[2 * i] = (u - g.x) * 32.f;
         lo[2 * i + 1] = (v - g.y) * 32.f;
       }
-      const uint32_t at = (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-      st_shared_u32(sb + Lay::kOffQ + r * 128 + at, hi[0] | (hi[1] << 16));
-      st_shared_u32(sb + Lay::kOffQ + (R + r) * 128 + at,
+      const int nh = col(r), nl = nh + RW, c = lane >> 2, in = (lane & 3) * 4;
+      st_shared_u32(sb + Sh::kOffQ + nh * 128 + ((c ^ (nh & 7)) << 4) + in, hi[0] | (hi[1] << 16));
+      st_shared_u32(sb + Sh::kOffQ + nl * 128 + ((c ^ (nl & 7)) << 4) + in,
                     pack_e4m3x2(lo[0], lo[1]) | (pack_e4m3x2(lo[2], lo[3]) << 16));
       if (lane == 0) cq[r] = a >= 0x7f80u ? NAN : p.scale_log2 * __int_as_float((127 - k) << 23);
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&q_ready));
-    named_bar_sync(1, 128);  // cq
+    named_bar_sync(5, 32 * Sh::kWarps);  // cq
 
-    // Scales of this thread's key, one tile ahead; its page, two tiles ahead.
+    // Scales of this thread's key, one tile of the stream ahead; its page, two.
     auto page_of = [&](int j) -> int {
       const int tok = t0 + j * kFbKeys + kl;
       if (j >= n || tok >= t_end) return -1;
@@ -433,114 +493,153 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
       ks = pb.k_scale[i];
       vs = pb.v_scale[i];
     };
-    float acc[R], l[R];
+    float acc[RW], l[RW];
 #pragma unroll
-    for (int r = 0; r < R; ++r) acc[r] = l[r] = 0.f;
+    for (int i = 0; i < RW; ++i) acc[i] = l[i] = 0.f;
+    float m_mine = -INFINITY;  // running reference of row r0 + lane (lanes below RW)
     const int lim_lo = min(t_end, L - p.T_q + 1);  // keys below it: visible from every row
-    int unit1 = page_of(1);
+    int unit1 = page_of(st + NT);
     float ks, vs, ks1, vs1;
-    scale_of(0, page_of(0), ks, vs);
+    scale_of(st, page_of(st), ks, vs);
     bool alive = true;
+    const uint32_t tO = tmem + lane_base + Sh::kColO + 2 * R * st + 2 * r0;
+    const uint32_t prow = sb + Sh::kOffP + st * Sh::kTileP;
+    // acc = (acc + O) of the stream's last tile; O^T row d = kl
+    auto add_o = [&]() {
+      uint32_t o[2 * RW];
+      tmem_ld_cols(tO, o);
+      tmem_wait_ld();
+      reg_fence(o);
+#pragma unroll
+      for (int i = 0; i < RW; i += 2) {
+        float u, v;
+        ffma2(u, v, __uint_as_float(o[RW + i]), __uint_as_float(o[RW + i + 1]), kLoStep, kLoStep,
+              __uint_as_float(o[i]), __uint_as_float(o[i + 1]));
+        fadd2(acc[i], acc[i + 1], acc[i], acc[i + 1], u, v);
+      }
+    };
 
-    for (int j = 0; j < n; ++j) {
-      scale_of(j + 1, unit1, ks1, vs1);
-      unit1 = page_of(j + 2);
+    int turn = 0;  // tiles of this stream so far
+    for (int j = st; j < n; j += NT, ++turn) {
+      scale_of(j + NT, unit1, ks1, vs1);
+      unit1 = page_of(j + 2 * NT);
       // log2 vs and 1 / vs; scales below 2^-100 count as zero, negative ones are NaN
       const bool v_live = vs >= kMinVScale;
       const float lv = v_live ? __log2f(vs) : (vs >= 0.f ? -100.f : NAN);
-      const float ivs = v_live ? 1.f / vs : 1.f / kMinVScale;
+      const float ivs = v_live ? __frcp_rn(vs) : 1.f / kMinVScale;
+      const uint32_t p_mask = vs >= 0.f && !v_live ? 0u : 0xffffffffu;
       const int key = t0 + j * kFbKeys + kl;
-      const bool edge = t0 + (j + 1) * kFbKeys > lim_lo;
-      const uint32_t tS = tmem + lane_base + 2 * R * (j & 1);
       // (a warp whose wait failed keeps to the barriers of the others)
       alive = alive && wait_all(&s_full[j & 1], (j >> 1) & 1);
       tc_fence_after();
-      // y of RC rows from column c0 on
-      auto scores = [&](int c0, float (&y)[RC]) {
-        uint32_t sh[RC], sl[RC];
-        tmem_ld_cols(tS + c0, sh);
-        tmem_ld_cols(tS + R + c0, sl);
+      float y[RW];
+      if (alive) {
+        uint32_t s[2 * RW];
+        tmem_ld_cols(tmem + lane_base + 2 * R * (j & 1) + 2 * r0, s);
         tmem_wait_ld();
-        reg_fence(sh);
-        reg_fence(sl);
+        reg_fence(s);
 #pragma unroll
-        for (int i = 0; i < RC; ++i) {
-          const float s = fmaf(__uint_as_float(sl[i]), kLoStep, __uint_as_float(sh[i]));
-          y[i] = fmaf(s, cq[c0 + i] * ks, lv);
-          if (edge && key >= lim_sm[c0 + i]) y[i] = -INFINITY;
+        for (int i = 0; i < RW; i += 4) {
+          const float4 c4 = *reinterpret_cast<const float4*>(&cq[r0 + i]);
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+          for (int u = 0; u < 4; u += 2) {
+            float a0, a1, b0, b1;
+            ffma2(a0, a1, __uint_as_float(s[RW + i + u]), __uint_as_float(s[RW + i + u + 1]),
+                  kLoStep, kLoStep, __uint_as_float(s[i + u]), __uint_as_float(s[i + u + 1]));
+            fmul2(b0, b1, c[u], c[u + 1], ks, ks);
+            ffma2(y[i + u], y[i + u + 1], a0, a1, b0, b1, lv, lv);
+          }
         }
-      };
-      float y[RC];
+        if (t0 + (j + 1) * kFbKeys > lim_lo) {
 #pragma unroll
-      for (int c = 0; alive && c < NC; ++c) {
-        scores(c * RC, y);
-        float mine = 0.f;
+          for (int i = 0; i < RW; ++i)
+            if (key >= lim_sm[r0 + i]) y[i] = -INFINITY;
+        }
+        float mine = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < RC; ++i) {
+        for (int i = 0; i < RW; ++i) {
           const float m = warp_max(y[i]);
           if (lane == i) mine = m;
         }
-        if (lane < RC) red[j & 1][c * RC + lane][quarter] = mine;
+        if (lane < RW) red[turn & 1][st][r0 + lane][quarter] = mine;
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(1 + gi, 128);
+      // Lane i works out row r0 + i's new reference and factor for its warp.
+      bool grew = false;
+      if (lane < RW) {
+        const float4 mx = *reinterpret_cast<const float4*>(red[turn & 1][st][r0 + lane]);
+        const float m_new = fmax3(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w), m_mine);
+        const float ref = m_new == -INFINITY ? 0.f : m_new;  // no (-inf) - (-inf)
+        grew = m_new > m_mine;
+        ref_sm[sw][lane] = ref - kPScaleLog2;
+        alpha_sm[sw][lane] = ex2_approx(m_mine - ref);
+        m_mine = m_new;
+      }
+      const bool rescale = __any_sync(0xffffffffu, grew);
+      __syncwarp();  // ref_sm, alpha_sm
 
-      // O of the previous tile is complete: its P may be overwritten.
-      alive = alive && (j == 0 || wait_all(&o_full, (j - 1) & 1));
+      // The stream's previous O is complete: added, and its P may be overwritten.
+      alive = alive && (turn == 0 || wait_all(&o_full[st], (turn - 1) & 1));
       tc_fence_after();
+      if (alive) {
+        if (turn > 0) add_o();
+        if (rescale) {
 #pragma unroll
-      for (int c = 0; alive && c < NC; ++c) {
-        const int c0 = c * RC;
-        if (NC > 1) scores(c0, y);
-        uint32_t oh[RC], ol[RC];
-        if (j > 0) {
-          tmem_ld_cols(tmem + lane_base + Lay::kColO + c0, oh);
-          tmem_ld_cols(tmem + lane_base + Lay::kColO + R + c0, ol);
-          tmem_wait_ld();
-          reg_fence(oh);
-          reg_fence(ol);
-        } else {
-#pragma unroll
-          for (int i = 0; i < RC; ++i) oh[i] = ol[i] = 0u;
+          for (int i = 0; i < RW; i += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(&alpha_sm[sw][i]);
+            fmul2(acc[i], acc[i + 1], acc[i], acc[i + 1], a.x, a.y);
+            fmul2(acc[i + 2], acc[i + 3], acc[i + 2], acc[i + 3], a.z, a.w);
+            fmul2(l[i], l[i + 1], l[i], l[i + 1], a.x, a.y);
+            fmul2(l[i + 2], l[i + 3], l[i + 2], l[i + 3], a.z, a.w);
+          }
         }
-        float pr[RC];
+        // P as two E4M3 terms, rounded to f16 on the way (2^-12 of itself, and
+        // steps of 2^-24 below 2^-14, both below what the terms hold).
+        uint32_t hi[RW / 4], lo[RW / 4];
 #pragma unroll
-        for (int i = 0; i < RC; ++i) {
-          const int r = c0 + i;
-          const float4 mx = *reinterpret_cast<const float4*>(red[j & 1][r]);
-          const float m_old = m_run[j & 1][r];
-          const float m_new = fmax3(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w), m_old);
-          if (kl == r) m_run[(j + 1) & 1][r] = m_new;
-          const float ref = m_new == -INFINITY ? 0.f : m_new;  // no (-inf) - (-inf)
-          const float alpha = ex2_approx(m_old - ref);
-          acc[r] = (acc[r] + fmaf(__uint_as_float(ol[i]), kLoStep, __uint_as_float(oh[i]))) * alpha;
-          const float e = ex2_approx(y[i] - ref + kPScaleLog2);
-          l[r] = fmaf(e, ivs, l[r] * alpha);
-          pr[i] = v_live || lv != lv ? e : 0.f;
-        }
-        // P as two E4M3 terms: byte kl of rows r and R + r, 128-byte swizzled
-        // (8-row groups of 1024 bytes).
-        const uint32_t pbase = sb + Lay::kOffP + (kl & 15);
-        const int chunk = kl >> 4;
-#pragma unroll
-        for (int i = 0; i < RC; i += 2) {
-          const uint32_t hi = pack_e4m3x2(pr[i], pr[i + 1]);
-          const float2 g = unpack_e4m3x2(hi);
-          const uint32_t lo = pack_e4m3x2((pr[i] - g.x) * 32.f, (pr[i + 1] - g.y) * 32.f);
+        for (int i = 0; i < RW; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&ref_sm[sw][i]);
+          float e0, e1, e2, e3;
+          fadd2(e0, e1, y[i], y[i + 1], -f.x, -f.y);
+          fadd2(e2, e3, y[i + 2], y[i + 3], -f.z, -f.w);
+          e0 = ex2_approx(e0);
+          e1 = ex2_approx(e1);
+          e2 = ex2_approx(e2);
+          e3 = ex2_approx(e3);
+          ffma2(l[i], l[i + 1], e0, e1, ivs, ivs, l[i], l[i + 1]);
+          ffma2(l[i + 2], l[i + 3], e2, e3, ivs, ivs, l[i + 2], l[i + 3]);
+          uint32_t h[2], d[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const int r = c0 + i + u;
-            const uint32_t at = pbase + r * 128 + ((chunk ^ (r & 7)) << 4);
-            st_shared_u8(at, u ? hi >> 8 : hi);
-            st_shared_u8(at + R * 128, u ? lo >> 8 : lo);
+            const uint32_t x = pack_f16x2(u ? e2 : e0, u ? e3 : e1);
+            h[u] = pack_e4m3x2(x);
+            const uint32_t g = e4m3x2_to_f16x2(h[u]);
+            const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x),
+                                              *reinterpret_cast<const __half2*>(&g)),
+                                      __float2half2_rn(32.f));
+            d[u] = pack_e4m3x2(*reinterpret_cast<const uint32_t*>(&r));
           }
+          hi[i / 4] = (h[0] | (h[1] << 16)) & p_mask;
+          lo[i / 4] = (d[0] | (d[1] << 16)) & p_mask;
+        }
+        // This key's bytes of the warp's rows: 2 RW together, 16-byte pieces of a
+        // row of P, swizzled over the row.
+        const uint32_t at = kl * Sh::kRowP + 2 * r0;
+        if constexpr (RW == 8) {
+          st_shared_v4(prow + swz_row<Sh::kRowP>(at), hi[0], hi[1], lo[0], lo[1]);
+        } else {
+          st_shared_v4(prow + swz_row<Sh::kRowP>(at), hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(prow + swz_row<Sh::kRowP>(at + 16), lo[0], lo[1], lo[2], lo[3]);
         }
       }
       // Cache rows past the end of the split may hold anything (even NaN codes),
-      // and 0 * NaN would reach O: they are zeroed once the tile has landed.
-      if (t0 + (j + 1) * kFbKeys > t_end) {
+      // and 0 * NaN would reach O: they are zeroed once the tile has landed (by
+      // the stream's first row group).
+      if (t0 + (j + 1) * kFbKeys > t_end && r0 == 0) {
         alive = alive && wait_all(&v_full[j % NS], (j / NS) & 1);
         if (alive && key >= t_end) {
-          const uint32_t vrow = sb + Lay::kOffV + (j % NS) * kFbTile + kl * 128;
+          const uint32_t vrow = sb + Sh::kOffV + (j % NS) * kFbTile + kl * 128;
 #pragma unroll
           for (int c16 = 0; c16 < 8; ++c16) st_shared_v4(vrow + c16 * 16, 0u, 0u, 0u, 0u);
         }
@@ -548,12 +647,13 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (alive && lane == 0) mbar_arrive(smem_u32(&p_ready));
+      if (alive && lane == 0) mbar_arrive(smem_u32(&p_ready[st]));
       ks = ks1;
       vs = vs1;
     }
 
-    // The last O; l over the 128 keys' threads; then O / l and LSE, or the partial.
+    // The stream's last O, and l over the keys.
+    if (turn > 0) alive = alive && wait_all(&o_full[st], (turn - 1) & 1);
     bool page_ok = true;
     if (PAGED && alive) {
       // (a bad index is recorded before the arrive on the last V tile)
@@ -562,53 +662,61 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
       else
         alive = false;
     }
-    alive = alive && wait_all(&o_full, (n - 1) & 1);
-    if (alive) {
+    if (alive && turn > 0) {
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        uint32_t oh[RC], ol[RC];
-        tmem_ld_cols(tmem + lane_base + Lay::kColO + c * RC, oh);
-        tmem_ld_cols(tmem + lane_base + Lay::kColO + R + c * RC, ol);
-        tmem_wait_ld();
-        reg_fence(oh);
-        reg_fence(ol);
-#pragma unroll
-        for (int i = 0; i < RC; ++i)
-          acc[c * RC + i] += fmaf(__uint_as_float(ol[i]), kLoStep, __uint_as_float(oh[i]));
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float s = l[r];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) red[n & 1][r][quarter] = s;
-      }
+      add_o();
     }
-    // All four warps reach this barrier, also after a failed wait.
-    named_bar_sync(1, 128);
-    const bool failed = *abort_v != 0 || !alive || !page_ok;
-    constexpr float kUnscale = 1.f / 256.f;  // P carried 2^8
+    named_bar_sync(1 + gi, 128);  // the maxima have been read
+    {
+      const float s = warp_sums(l, lane);
+      if (lane % (32 / RW) == 0) red[0][st][r0 + lane / (32 / RW)][quarter] = s;
+      if (quarter == 0 && lane < RW) m_end[st][r0 + lane] = m_mine;
+    }
+    if (!alive || !page_ok) *abort_v = 1;
+    named_bar_sync(5, 32 * Sh::kWarps);
+    // Every S and O of the CTA is complete, so the K ring is free: the second
+    // stream's accumulators go through it to the first.
+    float* const part = reinterpret_cast<float*>(smem);  // [R][128]
+    if constexpr (NT == 2) {
+      if (st == 1) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r >= rows) break;
-      const size_t row = out_row(r);
-      const float4 ls = *reinterpret_cast<const float4*>(red[n & 1][r]);
-      const float lr = failed ? NAN : ((ls.x + ls.y) + (ls.z + ls.w)) * kUnscale;
-      const float o = acc[r] * kUnscale;
-      const float m = m_run[n & 1][r];
-      if (p.n_split == 1) {
-        if (kl < D && in_bounds(row * D + kl, 1, n_rows * D, p.err))
-          p.out[row * D + kl] = __float2bfloat16(failed ? NAN : o / lr);
-        if (kl == 0 && in_bounds(row, 1, n_rows, p.err))
-          p.lse[row] = failed ? NAN : (m + log2f(lr)) * kLn2;
-      } else {
-        const size_t idx = row * p.n_split + split;
-        if (kl < D && !failed && in_bounds(idx * D + kl, 1, n_rows * p.n_split * D, p.err))
-          p.ws_O[idx * D + kl] = o;
-        // m in natural-log units; a row with no visible key: (-inf, 0)
-        if (kl == 0 && in_bounds(idx, 1, n_rows * p.n_split, p.err))
-          p.ws_ml[idx] = failed ? make_float2(NAN, NAN) : make_float2(m * kLn2, lr);
+        for (int i = 0; i < RW; ++i) part[(r0 + i) * 128 + kl] = acc[i];
+      }
+      named_bar_sync(5, 32 * Sh::kWarps);
+    }
+    const bool failed = *abort_v != 0;
+    constexpr float kUnscale = 1.f / 256.f;  // P carried 2^8
+    if (st == 0) {
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        const int r = r0 + i;
+        if (r >= rows) break;
+        const size_t row = out_row(r);
+        const float4 ls = *reinterpret_cast<const float4*>(red[0][0][r]);
+        float m = m_end[0][r], lr = (ls.x + ls.y) + (ls.z + ls.w), o = acc[i];
+        if constexpr (NT == 2) {  // the merge of two partials
+          const float4 l2 = *reinterpret_cast<const float4*>(red[0][1][r]);
+          const float m1 = m_end[1][r], M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
+          const float a0 = ex2_approx(m - ref), a1 = ex2_approx(m1 - ref);
+          lr = lr * a0 + ((l2.x + l2.y) + (l2.z + l2.w)) * a1;
+          o = o * a0 + part[r * 128 + kl] * a1;
+          m = M;
+        }
+        lr = failed ? NAN : lr * kUnscale;
+        o *= kUnscale;
+        if (p.n_split == 1) {
+          if (kl < D && in_bounds(row * D + kl, 1, n_rows * D, p.err))
+            p.out[row * D + kl] = __float2bfloat16(failed ? NAN : o / lr);
+          if (kl == 0 && in_bounds(row, 1, n_rows, p.err))
+            p.lse[row] = failed ? NAN : (m + log2f(lr)) * kLn2;
+        } else {
+          const size_t idx = row * p.n_split + split;
+          if (kl < D && !failed && in_bounds(idx * D + kl, 1, n_rows * p.n_split * D, p.err))
+            p.ws_O[idx * D + kl] = o;
+          // m in natural-log units; a row with no visible key: (-inf, 0)
+          if (kl == 0 && in_bounds(idx, 1, n_rows * p.n_split, p.err))
+            p.ws_ml[idx] = failed ? make_float2(NAN, NAN) : make_float2(m * kLn2, lr);
+        }
       }
     }
   }
@@ -617,15 +725,15 @@ __global__ void __launch_bounds__(kFbThreads, FbLayout<R, NS>::kPerSM)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, Lay::kCols);
+    tmem_dealloc(tmem, Sh::kCols);
   }
 }
 
-template <int R, int NS, bool PAGED>
+template <typename Sh, bool PAGED>
 cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
                       const CUtensorMap& tm_v, bool prefetch, cudaStream_t stream) {
-  auto kern = gqa_decode_fp8_block_kernel<R, NS, PAGED>;
-  constexpr int smem = FbLayout<R, NS>::kBytes;
+  auto kern = gqa_decode_fp8_block_kernel<Sh, PAGED>;
+  constexpr int smem = Sh::kBytes;
   static unsigned char done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -639,7 +747,7 @@ cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
   p.dec.prefetch_tiles = prefetch ? 3 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.dec.n_split, p.dec.H_kv, p.dec.B);
-  cfg.blockDim = dim3(kFbThreads);
+  cfg.blockDim = dim3(Sh::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -651,18 +759,18 @@ cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int R, int DEEP, int SHALLOW>
+template <typename Deep, typename Shallow>
 cudaError_t launch_fb_r(const DecodeBlockParams& p, const CUtensorMap& tm_k,
                         const CUtensorMap& tm_v, int sms, cudaStream_t stream) {
   // One CTA per SM at most: a deep ring.  More CTAs than SMs: two shallow rings
   // on each SM, where they fit.
   const bool one_wave = (long long)p.dec.n_split * p.dec.H_kv * p.dec.B <= sms;
   const bool paged = p.dec.block_table != nullptr;
-  if (one_wave || DEEP == SHALLOW)
-    return paged ? launch_fb<R, DEEP, true>(p, tm_k, tm_v, one_wave, stream)
-                 : launch_fb<R, DEEP, false>(p, tm_k, tm_v, one_wave, stream);
-  return paged ? launch_fb<R, SHALLOW, true>(p, tm_k, tm_v, false, stream)
-               : launch_fb<R, SHALLOW, false>(p, tm_k, tm_v, false, stream);
+  if (one_wave)
+    return paged ? launch_fb<Deep, true>(p, tm_k, tm_v, true, stream)
+                 : launch_fb<Deep, false>(p, tm_k, tm_v, true, stream);
+  return paged ? launch_fb<Shallow, true>(p, tm_k, tm_v, false, stream)
+               : launch_fb<Shallow, false>(p, tm_k, tm_v, false, stream);
 }
 
 }  // namespace
@@ -671,10 +779,13 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockParams& p, const CUtensorMa
                                     const CUtensorMap& tm_v, int sms, cudaStream_t stream) {
   const int rows = p.dec.T_q * p.dec.G;
   if (rows < 1 || rows > 64 || p.dec.chunk % kFbKeys != 0) return cudaErrorInvalidValue;
-  if (rows <= 8) return launch_fb_r<8, 6, 3>(p, tm_k, tm_v, sms, stream);
-  if (rows <= 16) return launch_fb_r<16, 6, 3>(p, tm_k, tm_v, sms, stream);
-  if (rows <= 32) return launch_fb_r<32, 6, 6>(p, tm_k, tm_v, sms, stream);
-  return launch_fb_r<64, 5, 5>(p, tm_k, tm_v, sms, stream);
+  if (rows <= 8)
+    return launch_fb_r<FbShape<8, 6, 2, 1>, FbShape<8, 3, 2, 1>>(p, tm_k, tm_v, sms, stream);
+  if (rows <= 16)
+    return launch_fb_r<FbShape<16, 6, 2, 1>, FbShape<16, 3, 2, 1>>(p, tm_k, tm_v, sms, stream);
+  if (rows <= 32)
+    return launch_fb_r<FbShape<32, 5, 2, 2>, FbShape<32, 5, 2, 2>>(p, tm_k, tm_v, sms, stream);
+  return launch_fb_r<FbShape<64, 5, 1, 4>, FbShape<64, 5, 1, 4>>(p, tm_k, tm_v, sms, stream);
 }
 
 }  // namespace gqa
