@@ -8,7 +8,6 @@ There is no CPU fallback: if the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -123,15 +122,6 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
-
-
-def _on(device):
-    """A context with `device` current (no change where it is already)."""
-    import torch
-
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
 
 
 def _keep(tensor, stream):
@@ -549,36 +539,54 @@ def decode_fp8(q, k8, v8, k_scale, v_scale, seq_lens, scale=None, n_split=None, 
     return out, lse
 
 
-def _need(ok, what):
-    if not ok:
-        raise GQAError(GQA_ERR_INVALID_ARG, what)
+def _refuse(what, why):
+    raise GQAError(GQA_ERR_INVALID_ARG, f"{what}: {why}")
+
+
+def _raw_stream(device: int, stream) -> int:
+    """Handle of `stream`, by default the current stream of CUDA device `device` (without
+    the stream object that torch.cuda.current_stream() builds: 0.1 instead of 2.9 us)."""
+    if stream is None:
+        import torch
+
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _other_device(device: int) -> bool:
+    import torch
+
+    return device != torch.cuda.current_device()
 
 
 def _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table, what):
-    """Checks the tensors of a block-scaled E4M3 cache; returns (B, S_max, H_kv, d)."""
+    """Checks the tensors of a block-scaled E4M3 cache; returns its device and
+    (units, tokens per unit, H_kv, d, B, max_blocks)."""
     import torch
 
-    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
-    _need(k8.dtype == u8 and v8.dtype == u8 and k8.dim() == 4 and k8.shape == v8.shape
-          and k8.is_contiguous() and v8.is_contiguous(),
-          f"{what}: the codes are dense uint8 [B, S_max, H_kv, d] or [num_pages, page_size, H_kv, d]")
-    units, per, H_kv, d = k8.shape
-    shape = (units, -(-per // block) if block > 0 else 0, H_kv)
-    _need(k_scale.dtype == f32 and v_scale.dtype == f32 and k_scale.shape == shape
-          and v_scale.shape == shape and k_scale.is_contiguous() and v_scale.is_contiguous(),
-          f"{what}: the scales are dense float32 {shape}")
-    dev = k8.device
-    _need(v8.device == dev and k_scale.device == dev and v_scale.device == dev
-          and seq_lens.device == dev and dev.type == "cuda",
-          f"{what}: the tensors are not on one CUDA device")
-    B = units
+    dev, shape = k8.get_device(), k8.shape
+    if (dev < 0 or len(shape) != 4 or k8.dtype is not torch.uint8 or v8.dtype is not torch.uint8
+            or v8.shape != shape or v8.get_device() != dev or not k8.is_contiguous()
+            or not v8.is_contiguous()):
+        _refuse(what, "the codes are dense uint8 [B, S_max, H_kv, d] or [num_pages, page_size, H_kv,"
+                      " d], K and V on one CUDA device")
+    units, per, H_kv, d = shape
+    sshape = (units, -(-per // block) if block > 0 else 0, H_kv)
+    if (k_scale.shape != sshape or v_scale.shape != sshape or k_scale.dtype is not torch.float32
+            or v_scale.dtype is not torch.float32 or k_scale.get_device() != dev
+            or v_scale.get_device() != dev or not k_scale.is_contiguous()
+            or not v_scale.is_contiguous()):
+        _refuse(what, f"the scales are dense float32 {sshape} on the codes' device")
+    B, max_blocks = units, 0
     if block_table is not None:
-        _need(block_table.dtype == i32 and block_table.dim() == 2 and block_table.is_contiguous()
-              and block_table.device == dev, f"{what}: block_table is dense int32 [B, max_blocks]")
-        B, per = block_table.shape[0], block_table.shape[1] * per
-    _need(seq_lens.dtype == i32 and seq_lens.shape == (B,) and seq_lens.is_contiguous(),
-          f"{what}: seq_lens is dense int32 [B]")
-    return B, per, H_kv, d
+        if (block_table.dim() != 2 or block_table.dtype is not torch.int32
+                or block_table.get_device() != dev or not block_table.is_contiguous()):
+            _refuse(what, "block_table is dense int32 [B, max_blocks] on the codes' device")
+        B, max_blocks = block_table.shape
+    if (seq_lens.shape != (B,) or seq_lens.dtype is not torch.int32 or seq_lens.get_device() != dev
+            or not seq_lens.is_contiguous()):
+        _refuse(what, "seq_lens is dense int32 [B] on the codes' device")
+    return dev, units, per, H_kv, d, B, max_blocks
 
 
 def kv_cache_fp8_block(units, per, H_kv, d, block, device="cuda"):
@@ -604,34 +612,43 @@ def kv_append_fp8_block(k_new, v_new, k8, v8, k_scale, v_scale, seq_lens, block,
     import torch
 
     what = "kv_append_fp8_block"
-    B, S_max, H_kv, d = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table, what)
-    _need(k_new.dtype == torch.bfloat16 and v_new.dtype == torch.bfloat16 and k_new.dim() == 4
-          and k_new.shape == v_new.shape and k_new.shape[0] == B and k_new.shape[2:] == (H_kv, d)
-          and k_new.device == k8.device and v_new.device == k8.device,
-          f"{what}: the new rows are bfloat16 [B, T, H_kv, d] on the cache's device")
-    T = k_new.shape[1]
-    _need(n_new is None or (n_new.dtype == torch.int32 and n_new.shape == (B,)
-                            and n_new.is_contiguous() and n_new.device == k8.device),
-          f"{what}: n_new is dense int32 [B]")
+    dev, units, per, H_kv, d, B, max_blocks = _block_cache(k8, v8, k_scale, v_scale, seq_lens,
+                                                           block, block_table, what)
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return kv_append_fp8_block(k_new, v_new, k8, v8, k_scale, v_scale, seq_lens, block,
+                                       n_new, block_table, stream)
+    shape = k_new.shape
+    if (len(shape) != 4 or shape[0] != B or shape[2] != H_kv or shape[3] != d
+            or v_new.shape != shape or k_new.dtype is not torch.bfloat16
+            or v_new.dtype is not torch.bfloat16 or k_new.get_device() != dev
+            or v_new.get_device() != dev):
+        _refuse(what, "the new rows are bfloat16 [B, T, H_kv, d] on the cache's device")
+    if n_new is not None and (n_new.shape != (B,) or n_new.dtype is not torch.int32
+                              or n_new.get_device() != dev or not n_new.is_contiguous()):
+        _refuse(what, "n_new is dense int32 [B] on the cache's device")
+    T = shape[1]
     if T == 0:
         return
+    strides = k_new.stride()
     # the stride between tokens; a dimension of size 1 has none of its own
-    stride = k_new.stride(1) if T > 1 else k_new.stride(0) if B > 1 else H_kv * d
-    for x in (k_new, v_new):
-        sb, st, sh, sd = x.stride()
-        _need((d == 1 or sd == 1) and (H_kv == 1 or sh == d) and (T == 1 or st == stride)
-              and (B == 1 or sb == T * stride),
-              f"{what}: the rows of k_new and v_new are H_kv * d dense elements, one stride apart")
-    with _on(k8.device):
-        if block_table is None:
-            st = gqa_kv_append_fp8_block(k_new, v_new, stride, n_new, seq_lens, B, T, S_max, H_kv,
-                                         d, block, k8, v8, k_scale, v_scale, stream)
-        else:
-            P, page_size = k8.shape[:2]
-            st = gqa_kv_append_paged_fp8_block(k_new, v_new, stride, n_new, block_table, seq_lens,
-                                               B, T, P, page_size, block_table.shape[1], H_kv, d,
-                                               block, k8, v8, k_scale, v_scale, stream)
-    _check(st, "gqa_kv_append_fp8_block")
+    step = strides[1] if T > 1 else strides[0] if B > 1 else H_kv * d
+    for s in (strides, v_new.stride()):
+        if (s[3] != 1 or (s[2] != d and H_kv > 1) or (s[1] != step and T > 1)
+                or (s[0] != T * step and B > 1)):
+            _refuse(what, "the rows of k_new and v_new are H_kv * d dense elements, one stride apart")
+    if block_table is None:
+        st = load().gqa_kv_append_fp8_block(
+            k_new.data_ptr(), v_new.data_ptr(), step, None if n_new is None else n_new.data_ptr(),
+            seq_lens.data_ptr(), B, T, per, H_kv, d, block, k8.data_ptr(), v8.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), _raw_stream(dev, stream))
+    else:
+        st = load().gqa_kv_append_paged_fp8_block(
+            k_new.data_ptr(), v_new.data_ptr(), step, None if n_new is None else n_new.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), B, T, units, per, max_blocks, H_kv, d,
+            block, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            _raw_stream(dev, stream))
+    _check(st, what)
 
 
 def kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, start=0, k_out=None, v_out=None,
@@ -641,81 +658,95 @@ def kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, start=0, k_out=
     import torch
 
     what = "kv_read_fp8_block"
-    B, S_max, H_kv, d = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table, what)
+    dev, units, per, H_kv, d, B, max_blocks = _block_cache(k8, v8, k_scale, v_scale, seq_lens,
+                                                           block, block_table, what)
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, start, k_out, v_out,
+                                     block_table, stream)
     if k_out is None:
+        S_max = per if block_table is None else max_blocks * per
         k_out = torch.zeros((B, S_max - start, H_kv, d), dtype=torch.bfloat16, device=k8.device)
     if v_out is None:
         v_out = torch.zeros(k_out.shape, dtype=torch.bfloat16, device=k8.device)
-    _need(k_out.dtype == torch.bfloat16 and v_out.dtype == torch.bfloat16 and k_out.dim() == 4
-          and k_out.shape == v_out.shape and k_out.shape[0] == B and k_out.shape[2:] == (H_kv, d)
-          and k_out.is_contiguous() and v_out.is_contiguous() and k_out.device == k8.device
-          and v_out.device == k8.device,
-          f"{what}: k_out and v_out are dense bfloat16 [B, S_out, H_kv, d] on the cache's device")
-    S_out = k_out.shape[1]
-    with _on(k8.device):
-        if block_table is None:
-            st = gqa_kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, B, S_max, H_kv, d, block,
-                                       start, S_out, k_out, v_out, stream)
-        else:
-            P, page_size = k8.shape[:2]
-            st = gqa_kv_read_paged_fp8_block(k8, v8, k_scale, v_scale, block_table, seq_lens, B, P,
-                                             page_size, block_table.shape[1], H_kv, d, block,
-                                             start, S_out, k_out, v_out, stream)
-    _check(st, "gqa_kv_read_fp8_block")
+    shape = k_out.shape
+    if (len(shape) != 4 or shape[0] != B or shape[2] != H_kv or shape[3] != d
+            or v_out.shape != shape or k_out.dtype is not torch.bfloat16
+            or v_out.dtype is not torch.bfloat16 or k_out.get_device() != dev
+            or v_out.get_device() != dev or not k_out.is_contiguous() or not v_out.is_contiguous()):
+        _refuse(what, "k_out and v_out are dense bfloat16 [B, S_out, H_kv, d] on the cache's device")
+    if block_table is None:
+        st = load().gqa_kv_read_fp8_block(
+            k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            seq_lens.data_ptr(), B, per, H_kv, d, block, start, shape[1], k_out.data_ptr(),
+            v_out.data_ptr(), _raw_stream(dev, stream))
+    else:
+        st = load().gqa_kv_read_paged_fp8_block(
+            k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), B, units, per, max_blocks, H_kv, d, block,
+            start, shape[1], k_out.data_ptr(), v_out.data_ptr(), _raw_stream(dev, stream))
+    _check(st, what)
     return k_out, v_out
 
 
 def decode_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=None, n_split=None,
                      workspace=None, out=None, lse=None, stream=None, block_table=None):
-    """Decode + combine over a block-scaled E4M3 cache (paged when block_table is given).
+    """Decode over a block-scaled E4M3 cache (paged when block_table is given).
 
     q [B, H_q, d] (out [B, H_q, d], lse [B, H_q]) or, for the last T_q positions of each
     sequence, q [B, T_q, H_q, d] (out [B, T_q, H_q, d], lse [B, T_q, H_q])."""
     import torch
 
     what = "decode_fp8_block"
-    B, S_max, H_kv, d = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table, what)
-    dev, rows = k8.device, q.shape[:-1]
-    _need(q.dtype == torch.bfloat16 and q.dim() in (3, 4) and q.shape[0] == B and q.shape[-1] == d
-          and q.is_contiguous() and q.device == dev,
-          f"{what}: q is dense bfloat16 [B, H_q, d] or [B, T_q, H_q, d] on the cache's device")
-    T_q, H_q = (q.shape[1] if q.dim() == 4 else 1), q.shape[-2]
+    dev, units, per, H_kv, d, B, max_blocks = _block_cache(k8, v8, k_scale, v_scale, seq_lens,
+                                                           block, block_table, what)
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return decode_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale, n_split,
+                                    workspace, out, lse, stream, block_table)
+    shape = q.shape
+    multi = len(shape) == 4
+    if (not (multi or len(shape) == 3) or shape[0] != B or shape[-1] != d
+            or q.dtype is not torch.bfloat16 or q.get_device() != dev or not q.is_contiguous()):
+        _refuse(what, "q is dense bfloat16 [B, H_q, d] or [B, T_q, H_q, d] on the cache's device")
+    T_q, H_q = (shape[1] if multi else 1), shape[-2]
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q)
+    elif (out.shape != shape or out.dtype is not torch.bfloat16 or out.get_device() != dev
+          or not out.is_contiguous()):
+        _refuse(what, "out is dense bfloat16, of q's shape, on the cache's device")
     if lse is None:
-        lse = torch.empty(rows, dtype=torch.float32, device=dev)
-    _need(out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous()
-          and out.device == dev and lse.dtype == torch.float32 and lse.shape == rows
-          and lse.is_contiguous() and lse.device == dev,
-          f"{what}: out is dense bfloat16 like q, lse dense float32 like q without d")
-    with _on(dev):
-        if n_split is None:
-            n_split = gqa_attn_decode_fp8_block_default_splits(B, H_kv, S_max)
-        if n_split > 1:
-            if workspace is None:
-                workspace = decode_workspace(B * T_q, H_q, d, n_split, dev)
-                _keep(workspace, stream)
-            else:
-                _need(workspace.device == dev and workspace.is_contiguous()
-                      and workspace.numel() * workspace.element_size()
-                      >= gqa_attn_decode_workspace_bytes(B * T_q, H_q, d, n_split),
-                      f"{what}: the workspace is too small or not on the cache's device")
-        if block_table is None:
-            st = gqa_attn_decode_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, B, T_q, S_max,
-                                           H_q, H_kv, d, block, scale, n_split, workspace, out,
-                                           lse, stream)
-        else:
-            P, page_size = k8.shape[:2]
-            st = gqa_attn_decode_paged_fp8_block(q, k8, v8, k_scale, v_scale, block_table, seq_lens,
-                                                 B, T_q, P, page_size, block_table.shape[1], H_q,
-                                                 H_kv, d, block, scale, n_split, workspace, out,
-                                                 lse, stream)
-        _check(st, "gqa_attn_decode_fp8_block")
-        if n_split > 1:
-            _check(gqa_attn_decode_combine(workspace, B * T_q, H_q, d, n_split, out, lse, stream),
-                   "gqa_attn_decode_combine")
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    elif (lse.shape != shape[:-1] or lse.dtype is not torch.float32 or lse.get_device() != dev
+          or not lse.is_contiguous()):
+        _refuse(what, "lse is dense float32, of q's shape without d, on the cache's device")
+    lib = load()
+    S_max = per if block_table is None else max_blocks * per
+    if n_split is None:
+        n_split = lib.gqa_attn_decode_fp8_block_default_splits(B, H_kv, S_max)
+    ws = None
+    if n_split > 1:
+        need = lib.gqa_attn_decode_workspace_bytes(B * T_q, H_q, d, n_split)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            _keep(workspace, stream)
+        elif (workspace.get_device() != dev or not workspace.is_contiguous()
+              or workspace.numel() * workspace.element_size() < need):
+            _refuse(what, f"the workspace is {need} dense bytes on the cache's device")
+        ws = workspace.data_ptr()
+    if block_table is None:
+        st = lib.gqa_attn_decode_fp8_block(
+            q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            seq_lens.data_ptr(), B, T_q, per, H_q, H_kv, d, block, scale, n_split, ws,
+            out.data_ptr(), lse.data_ptr(), _raw_stream(dev, stream))
+    else:
+        st = lib.gqa_attn_decode_paged_fp8_block(
+            q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), B, T_q, units, per, max_blocks, H_q, H_kv,
+            d, block, scale, n_split, ws, out.data_ptr(), lse.data_ptr(), _raw_stream(dev, stream))
+    _check(st, what)
     return out, lse
 
 
@@ -725,9 +756,10 @@ def prefill_chunk_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=
     block-scaled E4M3 cache: the cache is read back as bf16 and prefill_chunk runs on it."""
     import torch
 
-    B, S_max, H_kv, d = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table,
-                                     "prefill_chunk_fp8_block")
-    with _on(k8.device):
+    dev, _, per, H_kv, d, B, max_blocks = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block,
+                                                       block_table, "prefill_chunk_fp8_block")
+    with torch.cuda.device(dev):
+        S_max = per if block_table is None else max_blocks * per
         k = torch.empty((B, S_max, H_kv, d), dtype=torch.bfloat16, device=k8.device)
         v = torch.empty_like(k)
         _keep(k, stream)

@@ -702,8 +702,20 @@ gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int 
   dp.max_blocks = c.max_blocks;
   dp.page_size = c.page_size;
   dp.num_pages = c.num_pages;
-  return cuda_status(gqa::launch_decode_fp8_block(p, tm_k, tm_v, num_sms_current_device(),
-                                                  reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = cuda_status(gqa::launch_decode_fp8_block(p, tm_k, tm_v, num_sms_current_device(), s));
+  if (st != GQA_OK || n_split == 1) return st;
+  gqa::CombineParams m;
+  m.ws_ml = dp.ws_ml;
+  m.ws_O = dp.ws_O;
+  m.B = c.B * T_q;
+  m.H_q = H_q;
+  m.d = c.d;
+  m.n_split = n_split;
+  m.out = dp.out;
+  m.lse = lse;
+  m.err = err;
+  return cuda_status(gqa::launch_decode_combine(m, s));
 }
 
 }  // namespace

@@ -45,7 +45,7 @@
  *   (15.8-16.3 us per step at 32K).
  * - An E4M3 cache with a scale per block of tokens and KV head, filled by this
  *   library: gqa_kv_append_fp8_block as tokens arrive, gqa_attn_decode_fp8_block
- *   (+ combine) for the last one or few tokens, gqa_kv_read_fp8_block followed by
+ *   for the last one or few tokens, gqa_kv_read_fp8_block followed by
  *   gqa_attn_prefill_chunk for the next chunk of a prompt (each also paged).
  * - A few new tokens per sequence (speculative verification, T_q <= 64):
  *   gqa_attn_decode_multi / gqa_attn_decode_paged_multi (+ combine with B * T_q
@@ -513,10 +513,12 @@ gqa_status gqa_kv_read_paged_fp8_block(const void* k_pool, const void* v_pool,
                                        void* v_out, gqa_stream_t stream);
 
 /* Decode of the last T_q positions of each sequence over that cache: queries,
- * visibility, outputs, workspace and follow-up gqa_attn_decode_combine() are those
- * of gqa_attn_decode_multi() (q and out bf16 [B, T_q, H_q, d], lse fp32
- * [B, T_q, H_q]; 1 <= T_q <= seq_lens[b] <= S_max), with splits of
- * ceil(S_max / n_split) keys rounded up to 128.  1 <= T_q <= 64, G = H_q / H_kv <=
+ * visibility, outputs and workspace are those of gqa_attn_decode_multi() (q and out
+ * bf16 [B, T_q, H_q, d], lse fp32 [B, T_q, H_q]; 1 <= T_q <= seq_lens[b] <= S_max),
+ * with splits of ceil(S_max / n_split) keys rounded up to 128.  With n_split > 1
+ * the partials go to `workspace` (gqa_attn_decode_workspace_bytes(B * T_q, H_q, d,
+ * n_split) bytes, 256-byte aligned, in gqa_attn_decode's layout) and a second
+ * launch merges them into out and lse: no gqa_attn_decode_combine() follows.  1 <= T_q <= 64, G = H_q / H_kv <=
  * 16 and T_q * G <= 64 (GQA_ERR_UNSUPPORTED above); scale finite > 0.  Scales may
  * be any finite fp32 numbers for keys; for values they must not be negative
  * (NaN outputs), and one below 2^-100 counts as zero.  The codes are multiplied
