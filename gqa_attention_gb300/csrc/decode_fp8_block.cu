@@ -3,40 +3,42 @@
 //
 // What it computes, for the T_q last positions of each sequence (row r of a KV
 // head is query t = r / G of head kv G + r % G and sees keys below L - T_q + 1 + t):
-//   x_j = tau ks_j (q . kc_j),  O = sum_j 2^.. softmax(x)_j vs_j vc_j,  LSE = ln sum_j e^x_j
+//   x_j = tau ks_j (q . kc_j),  O = sum_j softmax(x)_j vs_j vc_j,  LSE = ln sum_j e^x_j
 // with kc, vc the E4M3 values and ks_j, vs_j the scales of key j's block of
 // tokens.  One CTA per (split, KV head, sequence) leaves the partial (m, l, O)
 // of decode.cu's layout for the combine kernel, or writes O and LSE (one split).
 //
 // Keys sit in the M rows of the MMA, query rows in N:
 //   S_j = K_j Q^T   (M = 128 keys, N = 2R, K = d; both operands in shared memory)
-//   O^T = V_j^T P   (M = d, N = 2R, K = 128 keys; V^T is the MN-major view of V)
+//   O^T = V_j^T P   (M = d, N = 2R, K = 128 keys; V^T and P are MN-major views)
 // so that a thread owns one key: its scales are one register each, its exponents
 // R, and a padded row costs no softmax work.  With the rows in M, as decode_tc.cu
 // has them, 8 query rows would leave 120 of 128 lanes idle and one warp with all
 // 128 exponentials of each row.
 //
 // kind::f8f6f4 wants both operands in 8 bits, so Q and P are split in two E4M3
-// terms, side by side in N (rows 0..R-1 the high terms, R..2R-1 the low):
+// terms, side by side in N:
 //   q 2^k = hi + lo / 32.  bf16 carries 8 significant bits and E4M3 four, so the
 //     split is exact down to 2^-21 of the row's largest |q| (hi <= 256, so the
 //     remainder is at most 8 and 32 times it at most 256).
 //   p in (0, 256] = hi + lo / 32, within 2^-9 of p above 2^-6 as bf16 would be,
-//     with a smallest step of 2^-14: 2^-22 of the reference weight.
+//     with a smallest step of 2^-14.
 // The codes need no conversion, which is what bounds the mma.sync sweep over
 // E4M3 codes.
 //
-// The value scale rides on the exponent: y_j = x_j log2 e + log2 vs_j, P = 2^(y - m + 8)
-// with m the running maximum of y over the split, and l sums P / vs_j in fp32.  So
-// the range of P adapts to vs as well as to the scores.  m is a reference, not
-// the maximum of x; the merge of the partials holds for any reference.
+// The value scale rides on the exponent: y_j = x_j log2 e + log2 vs_j, P = 2^(y - m + 7)
+// with m a running reference within 1 of the largest y so far, and l sums
+// P / vs_j in fp32.  So the range of P adapts to vs as well as to the scores.  m is
+// moved only when some y exceeds it by more than 1 (P stays below 2^8): a tile
+// costs one barrier that ORs that condition, and the row maxima are worked out
+// only when it holds.  The merge of the partials holds for any reference.
 //
 // Each P V starts a fresh accumulator that the softmax threads (now thread = row
-// d of O^T) add to fp32 registers, rescaled by 2^(m_old - m_new): no
-// rescaling pass through tensor memory, and the sum over tiles is fp32.
+// d of O^T) add to fp32 registers, rescaled when m moved: no rescaling pass
+// through tensor memory, and the sum over tiles is fp32.
 //
-// Roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer (and tensor
-// memory), warps 2-5 Q split, softmax, accumulation and epilogue.
+// Roles (64 + 32 kWarps threads): warp 0 TMA producer, warp 1 MMA issuer (and
+// tensor memory), the others Q split, softmax, accumulation and epilogue.
 #include "tcgen05.cuh"
 
 namespace gqa {
@@ -45,7 +47,8 @@ namespace {
 constexpr int kFbKeys = 128;                // keys per tile
 constexpr uint32_t kFbTile = 128u * 128u;   // 128 rows of 128 bytes
 constexpr float kLoStep = 1.f / 32.f;       // weight of the low term
-constexpr float kPScaleLog2 = 8.f;          // P is held times 2^8
+constexpr float kPScaleLog2 = 7.f;          // P is held times 2^7
+constexpr float kPMaxLog2 = 8.f;            // and must not pass 2^8
 constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100
 
 // Compile-time shape of one variant.  R query rows (padded), NS slots per ring,
@@ -55,7 +58,9 @@ template <int R_, int NS_, int NT_, int NG_>
 struct FbShape {
   static constexpr int R = R_, NS = NS_, NT = NT_, NG = NG_;
   static constexpr int RW = R / NG;                 // rows of a warp
+  static constexpr int NSB = 2 * NT;                // S buffers
   static constexpr int kWarps = 4 * NT * NG;        // softmax warps
+  static constexpr int kRowsQ = R / kWarps;         // rows of Q a warp splits
   static constexpr int kThreads = 64 + 32 * kWarps;
   static constexpr uint32_t kRowP = 2 * R;          // bytes of a key's row of P
   static constexpr uint32_t kOffV = NS * kFbTile;
@@ -63,13 +68,16 @@ struct FbShape {
   static constexpr uint32_t kOffP = kOffQ + 2 * R * 128;
   static constexpr uint32_t kTileP = 128 * kRowP;
   static constexpr uint32_t kBytes = kOffP + NT * kTileP + 1024;  // + alignment slack
-  // tensor memory: S_0, S_1, then NT accumulators, 2R columns each
-  static constexpr uint32_t kColO = 4 * R;
-  static constexpr uint32_t kUsed = (4 + 2 * NT) * R;
-  static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  // tensor memory: the S buffers, then NT accumulators, 2R columns each
+  static constexpr uint32_t kColO = NSB * 2 * R;
+  static constexpr uint32_t kUsed = (NSB + NT) * 2 * R;
+  static constexpr uint32_t kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   // CTAs an SM holds: shared memory (4 KB of it for the static part and the
-  // driver's) and 16 warps' worth of threads at 100 registers
-  static constexpr int kPerSM = 2 * (kBytes + 4096) <= 227 * 1024 && kThreads <= 320 ? 2 : 1;
+  // driver's), tensor memory and 20 warps at 102 registers
+  static constexpr int kPerSM =
+      2 * (kBytes + 4096) <= 227 * 1024 && kThreads <= 320 && kCols <= 256 ? 2 : 1;
+  static_assert(kUsed <= 512 && kRowsQ >= 1, "tensor memory; a row of Q for every warp");
+  static_assert(NT * R * 512 <= 2 * NS * (int)kFbTile, "the accumulators reuse the rings");
 };
 
 // Instruction descriptor of tcgen05.mma.kind::f8f6f4 with E4M3 operands and fp32
@@ -85,18 +93,18 @@ __host__ __device__ constexpr uint32_t instr_desc_e4m3_f32(int M, int N, bool a_
 // groups of 8 rows follow one another.  Layout field (bits 61-63): 0 none, 6 32-byte,
 // 4 64-byte, 2 128-byte swizzle.  Without a swizzle the leading offset strides the
 // groups, with one the stride offset does: both are given.
-// Offset of byte `at` in such an operand: 16-byte pieces of a row are swizzled.
-template <int SPAN>
-__device__ __forceinline__ uint32_t swz_row(uint32_t at) {
-  if constexpr (SPAN == 16) return at;
-  else return swizzle<SPAN>(at);
-}
 template <int SPAN>
 __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
   constexpr uint64_t layout = SPAN == 128 ? 2 : SPAN == 64 ? 4 : SPAN == 32 ? 6 : 0;
   constexpr uint64_t stride = (8 * SPAN) >> 4;
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (stride << 16) | (stride << 32) |
          (1ull << 46) | (layout << 61);
+}
+// Offset of byte `at` in such an operand: 16-byte pieces of a row are swizzled.
+template <int SPAN>
+__device__ __forceinline__ uint32_t swz_row(uint32_t at) {
+  if constexpr (SPAN == 16) return at;
+  else return swizzle<SPAN>(at);
 }
 
 __device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -110,7 +118,7 @@ __device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
-// 16 or 32 consecutive 32-bit columns of this thread's lane.
+// 16 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -125,10 +133,6 @@ template <int N>
 __device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) {
-  tmem_ld32(taddr, r);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -174,6 +178,19 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
   for (int o = 16 / N; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
   return v[0];
 }
+// Barrier `id` over `count` threads that returns whether any of them gave true.
+__device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "bar.red.or.pred p, %1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return any != 0;
+}
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -183,20 +200,19 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     gqa_decode_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 const __grid_constant__ CUtensorMap tm_v,
                                 const DecodeBlockParams pb) {
-  constexpr int R = Sh::R, NS = Sh::NS, NT = Sh::NT, NG = Sh::NG, RW = Sh::RW;
+  constexpr int R = Sh::R, NS = Sh::NS, NT = Sh::NT, NG = Sh::NG, RW = Sh::RW, NSB = Sh::NSB;
   const DecodeParams& p = pb.dec;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  __shared__ __align__(8) uint64_t s_full[2], q_ready, p_ready[NT], o_full[NT], drain;
+  __shared__ __align__(8) uint64_t s_full[NSB], q_ready, p_ready[NT], o_full[NT], drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag, bad_page;
   __shared__ __align__(16) float cq[R];         // tau log2(e) 2^-k of each row's query
   __shared__ __align__(16) int lim_sm[R];       // keys below it are visible
-  // the four warps' maxima of each row, by the parity of the stream's turn: written
-  // again two turns later, past a barrier that follows every read (later: sums of l)
-  __shared__ __align__(16) float red[2][NT][R][4];
-  // each softmax warp's own copy of its rows' new references less 8, and factors
-  __shared__ __align__(16) float ref_sm[Sh::kWarps][RW], alpha_sm[Sh::kWarps][RW];
+  __shared__ uint32_t row_sm[R];                // row of out, lse and the workspace
+  __shared__ __align__(16) float red[NT][R][4]; // by stream: maxima (later sums) of four warps
+  // each softmax warp's own copy: its rows' changes of reference and factors
+  __shared__ __align__(16) float move_sm[Sh::kWarps][RW], alpha_sm[Sh::kWarps][RW];
   __shared__ float m_end[NT][R];                // final references
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -209,20 +225,14 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   const int t0 = static_cast<int>(min((long long)split * p.chunk, (long long)p.S_max));
   const int G = p.G, rows = p.T_q * G;  // <= R
   const int D = p.d;
-  auto out_row = [&](int r) -> size_t {
-    return ((size_t)b * p.T_q + r / G) * p.H_q + kv * G + r % G;
+  // r / G without an integer division, as in decode.cu
+  const float inv_g = 1.f / static_cast<float>(G);
+  auto query_of = [&](int r) { return static_cast<int>((static_cast<float>(r) + 0.5f) * inv_g); };
+  auto out_row = [&](int r) -> uint32_t {  // (B * T_q and H_q are below 2^16)
+    const int t = query_of(r);
+    return static_cast<uint32_t>(b * p.T_q + t) * p.H_q + kv * G + (r - t * G);
   };
   const size_t n_rows = (size_t)p.B * p.T_q * p.H_q;
-  // NaN outputs of a row (one split), or its partial (m, l) alone
-  auto write_nan_or_ml = [&](size_t row, float2 ml) {
-    if (p.n_split == 1) {
-      if (in_bounds(row * D, D, n_rows * D, p.err))
-        for (int c = 0; c < D; ++c) p.out[row * D + c] = __float2bfloat16(NAN);
-      if (in_bounds(row, 1, n_rows, p.err)) p.lse[row] = NAN;
-    } else if (in_bounds(row * p.n_split + split, 1, n_rows * p.n_split, p.err)) {
-      p.ws_ml[row * p.n_split + split] = ml;
-    }
-  };
 
   // Set-up that touches no global memory runs before the dependency wait.
   volatile int* abort_v = &abort_flag;
@@ -233,8 +243,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       mbar_init(smem_u32(&v_full[s]), 1);
       mbar_init(smem_u32(&v_empty[s]), 1);
     }
-    mbar_init(smem_u32(&s_full[0]), 1);
-    mbar_init(smem_u32(&s_full[1]), 1);
+    for (int s = 0; s < NSB; ++s) mbar_init(smem_u32(&s_full[s]), 1);
     mbar_init(smem_u32(&q_ready), Sh::kWarps);
     for (int s = 0; s < NT; ++s) {
       mbar_init(smem_u32(&p_ready[s]), 4 * NG);
@@ -277,31 +286,44 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       }
     }
   }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The softmax warps' rows of Q travel together with the length: row sw, sw +
+  // kWarps, ..; lane takes columns 4 lane .. 4 lane + 3.
+  const int sw = warp - 2;
+  uint2 qw[Sh::kRowsQ];
+  if (warp >= 2) {
+#pragma unroll
+    for (int i = 0; i < Sh::kRowsQ; ++i) {
+      const int r = sw + i * Sh::kWarps;
+      qw[i] = make_uint2(0u, 0u);
+      if (r < rows && lane * 4 < D)
+        qw[i] = *reinterpret_cast<const uint2*>(p.q + (size_t)out_row(r) * D + lane * 4);
+    }
+  }
   const int L = p.seq_lens[b];
   const bool bad = L < p.T_q || L > p.S_max;  // (L >= T_q >= 1 otherwise)
   const int t_end = bad ? 0 : min(t0 + min(p.chunk, p.S_max - t0), L);
   const int n = t_end > t0 ? (t_end - t0 + kFbKeys - 1) / kFbKeys : 0;
-  if (threadIdx.x < R) {
-    const int r = threadIdx.x;
-    lim_sm[r] = r < rows ? min(t_end, L - p.T_q + 1 + r / G) : t_end;
-  }
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
   if (bad || n == 0) {
     // A bad length: NaN outputs and the error bit.  An empty split: the merge
     // identity (-inf, 0); its O is not written.  (One split is never empty.)
     if (bad && threadIdx.x == 0 && split == 0 && kv == 0) atomicOr(p.err, kErrBadSeqLen);
-    for (int r = threadIdx.x; r < rows; r += Sh::kThreads)
-      write_nan_or_ml(out_row(r), bad ? make_float2(NAN, NAN) : make_float2(-INFINITY, 0.f));
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-      tc_fence_after();
-      tmem_dealloc(tmem, Sh::kCols);
+    for (int r = threadIdx.x; r < rows; r += Sh::kThreads) {
+      const size_t row = out_row(r);
+      if (p.n_split == 1) {
+        if (in_bounds(row * D, D, n_rows * D, p.err))
+          for (int c = 0; c < D; ++c) p.out[row * D + c] = __float2bfloat16(NAN);
+        if (in_bounds(row, 1, n_rows, p.err)) p.lse[row] = NAN;
+      } else if (in_bounds(row * p.n_split + split, 1, n_rows * p.n_split, p.err)) {
+        p.ws_ml[row * p.n_split + split] =
+            bad ? make_float2(NAN, NAN) : make_float2(-INFINITY, 0.f);
+      }
     }
+    if (warp == 1) tmem_dealloc(tmem, Sh::kCols);
     return;
   }
 
@@ -391,38 +413,49 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     constexpr uint32_t idO = instr_desc_e4m3_f32(128, 2 * R, true, true);
     const uint32_t qb = sb + Sh::kOffQ, ppb = sb + Sh::kOffP;
     const int ksteps = D / 32;
-    auto issue_s = [&](int j) -> bool {  // S_j = K_j Q^T
-      if (!wait_all(&k_full[j % NS], (j / NS) & 1)) return false;
-      tc_fence_after();
-      const uint32_t kb = sb + (j % NS) * kFbTile;
-      for (int kk = 0; kk < ksteps; ++kk)
-        tc_mma_f8_ss(tmem + 2 * R * (j & 1), smem_desc_sw128(kb + kk * 32, 16, 1024),
-                     smem_desc_sw128(qb + kk * 32, 16, 1024), idS, kk > 0);
-      tc_commit(smem_u32(&s_full[j & 1]));
-      tc_commit(smem_u32(&k_empty[j % NS]));
-      return true;
+    auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity));
     };
-    auto finish = [&](int j) -> bool {  // O = V_j^T P_j, once both are there
-      const int s = j % NT;
-      if (!wait_all(&v_full[j % NS], (j / NS) & 1)) return false;
-      if (!wait_all(&p_ready[s], (j / NT) & 1)) return false;
-      tc_fence_after();
-      const uint32_t vb = sb + Sh::kOffV + (j % NS) * kFbTile, pj = ppb + s * Sh::kTileP;
+    // Whatever can run runs: the next S once its K is there and its buffer free (S_j
+    // overwrites S_{j - NSB}, read before p_ready of that tile), else the next O
+    // once its V and P are there.  Nothing for too long: give up as a wait does.
+    bool ok = wait_all(&q_ready, 0);
+    int js = 0, jo = 0;
+    uint64_t idle_since = 0;
+    for (uint32_t spin = 0; ok && jo < n;) {
+      if (js < n && js < jo + NSB && ready(&k_full[js % NS], (js / NS) & 1)) {
+        tc_fence_after();
+        const uint32_t kb = sb + (js % NS) * kFbTile;
+        for (int kk = 0; kk < ksteps; ++kk)  // S = K Q^T
+          tc_mma_f8_ss(tmem + 2 * R * (js % NSB), smem_desc_sw128(kb + kk * 32, 16, 1024),
+                       smem_desc_sw128(qb + kk * 32, 16, 1024), idS, kk > 0);
+        tc_commit(smem_u32(&s_full[js % NSB]));
+        tc_commit(smem_u32(&k_empty[js % NS]));
+        ++js;
+        spin = 0;
+      } else if (jo < js && ready(&p_ready[jo % NT], (jo / NT) & 1) &&
+                 ready(&v_full[jo % NS], (jo / NS) & 1)) {
+        tc_fence_after();
+        const int s = jo % NT;
+        const uint32_t vb = sb + Sh::kOffV + (jo % NS) * kFbTile, pj = ppb + s * Sh::kTileP;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)  // 32 keys each: four groups of 8 rows of V and of P
-        tc_mma_f8_ss(tmem + Sh::kColO + 2 * R * s, smem_desc_sw128(vb + kk * 4096, kFbTile, 1024),
-                     smem_desc_mn<Sh::kRowP>(pj + kk * 32 * Sh::kRowP), idO, kk > 0);
-      tc_commit(smem_u32(&o_full[s]));
-      tc_commit(smem_u32(&v_empty[j % NS]));
-      return true;
-    };
-    // Order S_0, S_1, O_0, S_2, O_1, ...: the next S runs while the softmax works.
-    // S_{j+2} overwrites S_j, which was read before p_ready of tile j.
-    bool ok = wait_all(&q_ready, 0) && issue_s(0);
-    if (ok && n > 1) ok = issue_s(1);
-    for (int j = 0; ok && j < n; ++j) {
-      ok = finish(j);
-      if (ok && j + 2 < n) ok = issue_s(j + 2);
+        for (int kk = 0; kk < 4; ++kk)  // O = V^T P: 32 keys each, four groups of 8 rows
+          tc_mma_f8_ss(tmem + Sh::kColO + 2 * R * s, smem_desc_sw128(vb + kk * 4096, kFbTile, 1024),
+                       smem_desc_mn<Sh::kRowP>(pj + kk * 32 * Sh::kRowP), idO, kk > 0);
+        tc_commit(smem_u32(&o_full[s]));
+        tc_commit(smem_u32(&v_empty[jo % NS]));
+        ++jo;
+        spin = 0;
+      } else if (++spin % 64 == 0) {
+        const uint64_t now = globaltimer_ns();
+        if (spin == 64) idle_since = now;
+        const bool late = now - idle_since > p.wait_ns;
+        if (__any_sync(0xffffffffu, late || *abort_v != 0)) {
+          if (lane == 0 && *abort_v == 0) atomicOr(p.err, kErrTimeout);
+          *abort_v = 1;
+          ok = false;
+        }
+      }
     }
     // Every MMA issued here has completed before tensor memory is released.
     tc_commit(smem_u32(&drain));
@@ -433,18 +466,17 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     const int quarter = warp & 3;                // tensor-memory lanes 32 * quarter ..
     const int kl = quarter * 32 + lane;          // key of a tile; later, row d of O^T
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const int sw = warp - 2, gi = sw >> 2;       // warp, and group of four
+    const int gi = sw >> 2;                      // group of four warps
     const int st = gi / NG, r0 = (gi % NG) * RW;  // stream of tiles, first row
     // Column (and byte of P, and row of Q) of row r's high term; the low term's
-    // is RW further: a warp's 2 RW columns are neighbours.
-    auto col = [](int r) { return r / RW * 2 * RW + r % RW; };
+    // is 8 further: eight rows' 16 columns are neighbours.
+    auto col = [](int r) { return r / 8 * 16 + r % 8; };
 
-    // Q as two E4M3 terms, one row per warp and turn: lane takes columns
-    // 4 lane .. 4 lane + 3.
-    for (int r = sw; r < R; r += Sh::kWarps) {
-      uint2 w = make_uint2(0u, 0u);
-      if (r < rows && lane * 4 < D)
-        w = *reinterpret_cast<const uint2*>(p.q + out_row(r) * D + lane * 4);
+    // Q as two E4M3 terms.
+#pragma unroll
+    for (int i = 0; i < Sh::kRowsQ; ++i) {
+      const int r = sw + i * Sh::kWarps;
+      const uint2 w = qw[i];
       const float f[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                           __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
       // the exponent of the largest |q| (bf16 bits); an infinity or NaN makes the row NaN
@@ -457,23 +489,26 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       float lo[4];
       uint32_t hi[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float u = f[2 * i] * up, v = f[2 * i + 1] * up;
-        hi[i] = pack_e4m3x2(u, v);
-        const float2 g = unpack_e4m3x2(hi[i]);
-        lo[2 * i] = (u - g.x) * 32.f;
-        lo[2 * i + 1] = (v - g.y) * 32.f;
+      for (int e = 0; e < 2; ++e) {
+        const float u = f[2 * e] * up, v = f[2 * e + 1] * up;
+        hi[e] = pack_e4m3x2(u, v);
+        const float2 g = unpack_e4m3x2(hi[e]);
+        lo[2 * e] = (u - g.x) * 32.f;
+        lo[2 * e + 1] = (v - g.y) * 32.f;
       }
-      const int nh = col(r), nl = nh + RW, c = lane >> 2, in = (lane & 3) * 4;
+      const int nh = col(r), nl = nh + 8, c = lane >> 2, in = (lane & 3) * 4;
       st_shared_u32(sb + Sh::kOffQ + nh * 128 + ((c ^ (nh & 7)) << 4) + in, hi[0] | (hi[1] << 16));
       st_shared_u32(sb + Sh::kOffQ + nl * 128 + ((c ^ (nl & 7)) << 4) + in,
                     pack_e4m3x2(lo[0], lo[1]) | (pack_e4m3x2(lo[2], lo[3]) << 16));
-      if (lane == 0) cq[r] = a >= 0x7f80u ? NAN : p.scale_log2 * __int_as_float((127 - k) << 23);
+      if (lane == 0) {
+        cq[r] = a >= 0x7f80u ? NAN : p.scale_log2 * __int_as_float((127 - k) << 23);
+        lim_sm[r] = r < rows ? min(t_end, L - p.T_q + 1 + query_of(r)) : t_end;
+        row_sm[r] = out_row(r);
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&q_ready));
-    named_bar_sync(5, 32 * Sh::kWarps);  // cq
 
     // Scales of this thread's key, one tile of the stream ahead; its page, two.
     auto page_of = [&](int j) -> int {
@@ -493,31 +528,39 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       ks = pb.k_scale[i];
       vs = pb.v_scale[i];
     };
-    float acc[RW], l[RW];
-#pragma unroll
-    for (int i = 0; i < RW; ++i) acc[i] = l[i] = 0.f;
-    float m_mine = -INFINITY;  // running reference of row r0 + lane (lanes below RW)
-    const int lim_lo = min(t_end, L - p.T_q + 1);  // keys below it: visible from every row
     int unit1 = page_of(st + NT);
     float ks, vs, ks1, vs1;
     scale_of(st, page_of(st), ks, vs);
+    float acc[RW], l[RW], off[RW];  // off: 7 less the row's reference (0 while it has none)
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      acc[i] = l[i] = 0.f;
+      off[i] = kPScaleLog2;
+    }
+    float m_mine = -INFINITY;  // reference of row r0 + lane (lanes below RW)
+    bool unset = true;         // some row has no reference yet
+    const int lim_lo = min(t_end, L - p.T_q + 1);  // keys below it: visible from every row
     bool alive = true;
     const uint32_t tO = tmem + lane_base + Sh::kColO + 2 * R * st + 2 * r0;
     const uint32_t prow = sb + Sh::kOffP + st * Sh::kTileP;
-    // acc = (acc + O) of the stream's last tile; O^T row d = kl
+    // acc += O of the stream's last tile; O^T row d = kl
     auto add_o = [&]() {
-      uint32_t o[2 * RW];
-      tmem_ld_cols(tO, o);
-      tmem_wait_ld();
-      reg_fence(o);
 #pragma unroll
-      for (int i = 0; i < RW; i += 2) {
-        float u, v;
-        ffma2(u, v, __uint_as_float(o[RW + i]), __uint_as_float(o[RW + i + 1]), kLoStep, kLoStep,
-              __uint_as_float(o[i]), __uint_as_float(o[i + 1]));
-        fadd2(acc[i], acc[i + 1], acc[i], acc[i + 1], u, v);
+      for (int c = 0; c < RW; c += 8) {
+        uint32_t o[16];
+        tmem_ld_cols(tO + 2 * c, o);
+        tmem_wait_ld();
+        reg_fence(o);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          float u, v;
+          ffma2(u, v, __uint_as_float(o[8 + i]), __uint_as_float(o[8 + i + 1]), kLoStep, kLoStep,
+                __uint_as_float(o[i]), __uint_as_float(o[i + 1]));
+          fadd2(acc[c + i], acc[c + i + 1], acc[c + i], acc[c + i + 1], u, v);
+        }
       }
     };
+    named_bar_sync(5, 32 * Sh::kWarps);  // cq, lim_sm, row_sm
 
     int turn = 0;  // tiles of this stream so far
     for (int j = st; j < n; j += NT, ++turn) {
@@ -530,25 +573,31 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       const uint32_t p_mask = vs >= 0.f && !v_live ? 0u : 0xffffffffu;
       const int key = t0 + j * kFbKeys + kl;
       // (a warp whose wait failed keeps to the barriers of the others)
-      alive = alive && wait_all(&s_full[j & 1], (j >> 1) & 1);
+      alive = alive && wait_all(&s_full[j % NSB], (j / NSB) & 1);
       tc_fence_after();
-      float y[RW];
-      if (alive) {
-        uint32_t s[2 * RW];
-        tmem_ld_cols(tmem + lane_base + 2 * R * (j & 1) + 2 * r0, s);
-        tmem_wait_ld();
-        reg_fence(s);
+      float y[RW];  // exponents of P: y - m + 7
+      float top = -INFINITY;
+      {
 #pragma unroll
-        for (int i = 0; i < RW; i += 4) {
-          const float4 c4 = *reinterpret_cast<const float4*>(&cq[r0 + i]);
-          const float c[4] = {c4.x, c4.y, c4.z, c4.w};
+        for (int c0 = 0; c0 < RW; c0 += 8) {
+          uint32_t s[16];
+          tmem_ld_cols(tmem + lane_base + 2 * R * (j % NSB) + 2 * (r0 + c0), s);
+          tmem_wait_ld();
+          reg_fence(s);
 #pragma unroll
-          for (int u = 0; u < 4; u += 2) {
-            float a0, a1, b0, b1;
-            ffma2(a0, a1, __uint_as_float(s[RW + i + u]), __uint_as_float(s[RW + i + u + 1]),
-                  kLoStep, kLoStep, __uint_as_float(s[i + u]), __uint_as_float(s[i + u + 1]));
-            fmul2(b0, b1, c[u], c[u + 1], ks, ks);
-            ffma2(y[i + u], y[i + u + 1], a0, a1, b0, b1, lv, lv);
+          for (int i = 0; i < 8; i += 4) {
+            const float4 c4 = *reinterpret_cast<const float4*>(&cq[r0 + c0 + i]);
+            const float c[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+              const int e = i + u, r = c0 + e;
+              float a0, a1, b0, b1, d0, d1;
+              ffma2(a0, a1, __uint_as_float(s[8 + e]), __uint_as_float(s[9 + e]), kLoStep, kLoStep,
+                    __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+              fmul2(b0, b1, c[u], c[u + 1], ks, ks);
+              fadd2(d0, d1, off[r], off[r + 1], lv, lv);
+              ffma2(y[r], y[r + 1], a0, a1, b0, b1, d0, d1);
+            }
           }
         }
         if (t0 + (j + 1) * kFbKeys > lim_lo) {
@@ -556,82 +605,84 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
           for (int i = 0; i < RW; ++i)
             if (key >= lim_sm[r0 + i]) y[i] = -INFINITY;
         }
+#pragma unroll
+        for (int i = 0; i < RW; i += 2) top = fmax3(top, y[i], y[i + 1]);
+      }
+      const bool update = named_bar_any(1 + gi, 128, unset || top > kPMaxLog2);
+      if (update) {
+        // The rows' maxima over the 128 keys become references where they are
+        // larger; lane i works out row r0 + i for its warp.
         float mine = -INFINITY;
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
-          const float m = warp_max(y[i]);
+          const float m = warp_max(y[i]) - off[i];
           if (lane == i) mine = m;
         }
-        if (lane < RW) red[turn & 1][st][r0 + lane][quarter] = mine;
+        if (lane < RW) red[st][r0 + lane][quarter] = mine;
+        named_bar_sync(1 + gi, 128);
+        if (lane < RW) {
+          const float4 mx = *reinterpret_cast<const float4*>(red[st][r0 + lane]);
+          const float m_new = fmax3(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w), m_mine);
+          const float ref = m_new == -INFINITY ? 0.f : m_new;  // no (-inf) - (-inf)
+          move_sm[sw][lane] = (m_mine == -INFINITY ? 0.f : m_mine) - ref;
+          alpha_sm[sw][lane] = ex2_approx(m_mine - ref);
+          m_mine = m_new;
+        }
+        unset = __any_sync(0xffffffffu, lane < RW && m_mine == -INFINITY);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < RW; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&move_sm[sw][i]);
+          fadd2(off[i], off[i + 1], off[i], off[i + 1], f.x, f.y);
+          fadd2(off[i + 2], off[i + 3], off[i + 2], off[i + 3], f.z, f.w);
+          fadd2(y[i], y[i + 1], y[i], y[i + 1], f.x, f.y);
+          fadd2(y[i + 2], y[i + 3], y[i + 2], y[i + 3], f.z, f.w);
+        }
       }
-      named_bar_sync(1 + gi, 128);
-      // Lane i works out row r0 + i's new reference and factor for its warp.
-      bool grew = false;
-      if (lane < RW) {
-        const float4 mx = *reinterpret_cast<const float4*>(red[turn & 1][st][r0 + lane]);
-        const float m_new = fmax3(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w), m_mine);
-        const float ref = m_new == -INFINITY ? 0.f : m_new;  // no (-inf) - (-inf)
-        grew = m_new > m_mine;
-        ref_sm[sw][lane] = ref - kPScaleLog2;
-        alpha_sm[sw][lane] = ex2_approx(m_mine - ref);
-        m_mine = m_new;
-      }
-      const bool rescale = __any_sync(0xffffffffu, grew);
-      __syncwarp();  // ref_sm, alpha_sm
 
       // The stream's previous O is complete: added, and its P may be overwritten.
       alive = alive && (turn == 0 || wait_all(&o_full[st], (turn - 1) & 1));
       tc_fence_after();
-      if (alive) {
-        if (turn > 0) add_o();
-        if (rescale) {
-#pragma unroll
-          for (int i = 0; i < RW; i += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(&alpha_sm[sw][i]);
-            fmul2(acc[i], acc[i + 1], acc[i], acc[i + 1], a.x, a.y);
-            fmul2(acc[i + 2], acc[i + 3], acc[i + 2], acc[i + 3], a.z, a.w);
-            fmul2(l[i], l[i + 1], l[i], l[i + 1], a.x, a.y);
-            fmul2(l[i + 2], l[i + 3], l[i + 2], l[i + 3], a.z, a.w);
-          }
-        }
-        // P as two E4M3 terms, rounded to f16 on the way (2^-12 of itself, and
-        // steps of 2^-24 below 2^-14, both below what the terms hold).
-        uint32_t hi[RW / 4], lo[RW / 4];
+      if (turn > 0) add_o();
+      if (update) {
 #pragma unroll
         for (int i = 0; i < RW; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&ref_sm[sw][i]);
-          float e0, e1, e2, e3;
-          fadd2(e0, e1, y[i], y[i + 1], -f.x, -f.y);
-          fadd2(e2, e3, y[i + 2], y[i + 3], -f.z, -f.w);
-          e0 = ex2_approx(e0);
-          e1 = ex2_approx(e1);
-          e2 = ex2_approx(e2);
-          e3 = ex2_approx(e3);
-          ffma2(l[i], l[i + 1], e0, e1, ivs, ivs, l[i], l[i + 1]);
-          ffma2(l[i + 2], l[i + 3], e2, e3, ivs, ivs, l[i + 2], l[i + 3]);
+          const float4 a = *reinterpret_cast<const float4*>(&alpha_sm[sw][i]);
+          fmul2(acc[i], acc[i + 1], acc[i], acc[i + 1], a.x, a.y);
+          fmul2(acc[i + 2], acc[i + 3], acc[i + 2], acc[i + 3], a.z, a.w);
+          fmul2(l[i], l[i + 1], l[i], l[i + 1], a.x, a.y);
+          fmul2(l[i + 2], l[i + 3], l[i + 2], l[i + 3], a.z, a.w);
+        }
+      }
+      // P as two E4M3 terms, rounded to f16 on the way (2^-12 of itself, and
+      // steps of 2^-24 below 2^-14, both below what the terms hold).
+      // Eight rows' two terms are 16 bytes of this key's row of P, swizzled over it.
+#pragma unroll
+      for (int c0 = 0; c0 < RW; c0 += 8) {
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const int r = c0 + i;
+          const float e0 = ex2_approx(y[r]), e1 = ex2_approx(y[r + 1]);
+          const float e2 = ex2_approx(y[r + 2]), e3 = ex2_approx(y[r + 3]);
+          ffma2(l[r], l[r + 1], e0, e1, ivs, ivs, l[r], l[r + 1]);
+          ffma2(l[r + 2], l[r + 3], e2, e3, ivs, ivs, l[r + 2], l[r + 3]);
           uint32_t h[2], d[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const uint32_t x = pack_f16x2(u ? e2 : e0, u ? e3 : e1);
             h[u] = pack_e4m3x2(x);
             const uint32_t g = e4m3x2_to_f16x2(h[u]);
-            const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x),
+            const __half2 q = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x),
                                               *reinterpret_cast<const __half2*>(&g)),
                                       __float2half2_rn(32.f));
-            d[u] = pack_e4m3x2(*reinterpret_cast<const uint32_t*>(&r));
+            d[u] = pack_e4m3x2(*reinterpret_cast<const uint32_t*>(&q));
           }
           hi[i / 4] = (h[0] | (h[1] << 16)) & p_mask;
           lo[i / 4] = (d[0] | (d[1] << 16)) & p_mask;
         }
-        // This key's bytes of the warp's rows: 2 RW together, 16-byte pieces of a
-        // row of P, swizzled over the row.
-        const uint32_t at = kl * Sh::kRowP + 2 * r0;
-        if constexpr (RW == 8) {
-          st_shared_v4(prow + swz_row<Sh::kRowP>(at), hi[0], hi[1], lo[0], lo[1]);
-        } else {
-          st_shared_v4(prow + swz_row<Sh::kRowP>(at), hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(prow + swz_row<Sh::kRowP>(at + 16), lo[0], lo[1], lo[2], lo[3]);
-        }
+        st_shared_v4(prow + swz_row<Sh::kRowP>(kl * Sh::kRowP + 2 * (r0 + c0)), hi[0], hi[1], lo[0],
+                     lo[1]);
       }
       // Cache rows past the end of the split may hold anything (even NaN codes),
       // and 0 * NaN would reach O: they are zeroed once the tile has landed (by
@@ -662,61 +713,58 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       else
         alive = false;
     }
-    if (alive && turn > 0) {
-      tc_fence_after();
-      add_o();
-    }
-    named_bar_sync(1 + gi, 128);  // the maxima have been read
+    tc_fence_after();
+    if (turn > 0) add_o();
+    // (red was last read before the barrier of the stream's last tile, or in its
+    // update: one more barrier of the group)
+    named_bar_sync(1 + gi, 128);
     {
       const float s = warp_sums(l, lane);
-      if (lane % (32 / RW) == 0) red[0][st][r0 + lane / (32 / RW)][quarter] = s;
+      if (lane % (32 / RW) == 0) red[st][r0 + lane / (32 / RW)][quarter] = s;
       if (quarter == 0 && lane < RW) m_end[st][r0 + lane] = m_mine;
     }
     if (!alive || !page_ok) *abort_v = 1;
     named_bar_sync(5, 32 * Sh::kWarps);
-    // Every S and O of the CTA is complete, so the K ring is free: the second
-    // stream's accumulators go through it to the first.
-    float* const part = reinterpret_cast<float*>(smem);  // [R][128]
-    if constexpr (NT == 2) {
-      if (st == 1) {
+    // Every S and O of the CTA is complete, so the rings are free (or the CTA has
+    // failed and writes NaN): the accumulators go through them, so that a warp
+    // merges and stores whole rows.
+    float* const part = reinterpret_cast<float*>(smem);  // [NT][R][128]
 #pragma unroll
-        for (int i = 0; i < RW; ++i) part[(r0 + i) * 128 + kl] = acc[i];
-      }
-      named_bar_sync(5, 32 * Sh::kWarps);
-    }
+    for (int i = 0; i < RW; ++i) part[(st * R + r0 + i) * 128 + kl] = acc[i];
+    named_bar_sync(5, 32 * Sh::kWarps);
     const bool failed = *abort_v != 0;
-    constexpr float kUnscale = 1.f / 256.f;  // P carried 2^8
-    if (st == 0) {
-#pragma unroll
-      for (int i = 0; i < RW; ++i) {
-        const int r = r0 + i;
-        if (r >= rows) break;
-        const size_t row = out_row(r);
-        const float4 ls = *reinterpret_cast<const float4*>(red[0][0][r]);
-        float m = m_end[0][r], lr = (ls.x + ls.y) + (ls.z + ls.w), o = acc[i];
-        if constexpr (NT == 2) {  // the merge of two partials
-          const float4 l2 = *reinterpret_cast<const float4*>(red[0][1][r]);
-          const float m1 = m_end[1][r], M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
-          const float a0 = ex2_approx(m - ref), a1 = ex2_approx(m1 - ref);
-          lr = lr * a0 + ((l2.x + l2.y) + (l2.z + l2.w)) * a1;
-          o = o * a0 + part[r * 128 + kl] * a1;
-          m = M;
-        }
-        lr = failed ? NAN : lr * kUnscale;
-        o *= kUnscale;
-        if (p.n_split == 1) {
-          if (kl < D && in_bounds(row * D + kl, 1, n_rows * D, p.err))
-            p.out[row * D + kl] = __float2bfloat16(failed ? NAN : o / lr);
-          if (kl == 0 && in_bounds(row, 1, n_rows, p.err))
-            p.lse[row] = failed ? NAN : (m + log2f(lr)) * kLn2;
-        } else {
-          const size_t idx = row * p.n_split + split;
-          if (kl < D && !failed && in_bounds(idx * D + kl, 1, n_rows * p.n_split * D, p.err))
-            p.ws_O[idx * D + kl] = o;
-          // m in natural-log units; a row with no visible key: (-inf, 0)
-          if (kl == 0 && in_bounds(idx, 1, n_rows * p.n_split, p.err))
-            p.ws_ml[idx] = failed ? make_float2(NAN, NAN) : make_float2(m * kLn2, lr);
-        }
+    constexpr float kUnscale = 1.f / 128.f;  // P carried 2^7
+    for (int r = sw; r < rows; r += Sh::kWarps) {
+      const float4 ls = *reinterpret_cast<const float4*>(red[0][r]);
+      float m = m_end[0][r], lr = (ls.x + ls.y) + (ls.z + ls.w);
+      float4 o = *reinterpret_cast<const float4*>(part + r * 128 + lane * 4);
+      if constexpr (NT == 2) {  // the merge of two partials
+        const float4 l2 = *reinterpret_cast<const float4*>(red[1][r]);
+        const float m1 = m_end[1][r], M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
+        const float a0 = ex2_approx(m - ref), a1 = ex2_approx(m1 - ref);
+        const float4 o1 = *reinterpret_cast<const float4*>(part + (R + r) * 128 + lane * 4);
+        lr = lr * a0 + ((l2.x + l2.y) + (l2.z + l2.w)) * a1;
+        o = make_float4(o.x * a0 + o1.x * a1, o.y * a0 + o1.y * a1, o.z * a0 + o1.z * a1,
+                        o.w * a0 + o1.w * a1);
+        m = M;
+      }
+      const size_t row = row_sm[r];
+      if (p.n_split == 1) {
+        const float inv = failed ? NAN : 1.f / lr;
+        if (lane * 4 < D && in_bounds(row * D + lane * 4, 4, n_rows * D, p.err))
+          *reinterpret_cast<uint2*>(p.out + row * D + lane * 4) =
+              make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (lane == 0 && in_bounds(row, 1, n_rows, p.err))
+          p.lse[row] = failed ? NAN : (m + log2f(lr * kUnscale)) * kLn2;
+      } else {
+        const size_t idx = row * p.n_split + split;
+        if (lane * 4 < D && in_bounds(idx * D + lane * 4, 4, n_rows * p.n_split * D, p.err))
+          *reinterpret_cast<float4*>(p.ws_O + idx * D + lane * 4) =
+              make_float4(o.x * kUnscale, o.y * kUnscale, o.z * kUnscale, o.w * kUnscale);
+        // m in natural-log units; a row with no visible key: (-inf, 0)
+        if (lane == 0 && in_bounds(idx, 1, n_rows * p.n_split, p.err))
+          p.ws_ml[idx] =
+              failed ? make_float2(NAN, NAN) : make_float2(m * kLn2, lr * kUnscale);
       }
     }
   }
