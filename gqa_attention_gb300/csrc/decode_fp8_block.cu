@@ -37,8 +37,9 @@
 // d of O^T) add to fp32 registers, rescaled when m moved: no rescaling pass
 // through tensor memory, and the sum over tiles is fp32.
 //
-// Roles (64 + 32 kWarps threads): warp 0 TMA producer, warp 1 MMA issuer (and
-// tensor memory), the others Q split, softmax, accumulation and epilogue.
+// Roles (96 + 32 kWarps threads): warp 0 TMA producer, warp 1 issuer of S (and
+// tensor memory), warp 2 issuer of O, the others Q split, softmax, accumulation
+// and epilogue.
 #include "tcgen05.cuh"
 
 namespace gqa {
@@ -61,7 +62,7 @@ struct FbShape {
   static constexpr int NSB = 2 * NT;                // S buffers
   static constexpr int kWarps = 4 * NT * NG;        // softmax warps
   static constexpr int kRowsQ = R / kWarps;         // rows of Q a warp splits
-  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kThreads = 96 + 32 * kWarps;
   static constexpr uint32_t kRowP = 2 * R;          // bytes of a key's row of P
   static constexpr uint32_t kOffV = NS * kFbTile;
   static constexpr uint32_t kOffQ = 2 * NS * kFbTile;
@@ -73,9 +74,9 @@ struct FbShape {
   static constexpr uint32_t kUsed = (NSB + NT) * 2 * R;
   static constexpr uint32_t kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   // CTAs an SM holds: shared memory (4 KB of it for the static part and the
-  // driver's), tensor memory and 20 warps at 102 registers
+  // driver's), tensor memory and 22 warps at 88 registers
   static constexpr int kPerSM =
-      2 * (kBytes + 4096) <= 227 * 1024 && kThreads <= 320 && kCols <= 256 ? 2 : 1;
+      2 * (kBytes + 4096) <= 227 * 1024 && kThreads <= 352 && kCols <= 256 ? 2 : 1;
   static_assert(kUsed <= 512 && kRowsQ >= 1, "tensor memory; a row of Q for every warp");
   static_assert(NT * R * 512 <= 2 * NS * (int)kFbTile, "the accumulators reuse the rings");
 };
@@ -178,6 +179,24 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
   for (int o = 16 / N; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
   return v[0];
 }
+// Whether the phase of `bar` has completed, for the whole (converged) warp: one
+// elected lane waits (as long as the hardware lets it), since the lanes' tests of
+// one barrier run one after another, and a vote hands on what it has acquired.
+__device__ __forceinline__ bool warp_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred e, p, q;\n\t"
+      "setp.ne.u32 p, %1, %1;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "vote.sync.any.pred q, p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (ok) __syncwarp();
+  return ok != 0;
+}
 // Barrier `id` over `count` threads that returns whether any of them gave true.
 __device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
   uint32_t any;
@@ -204,7 +223,8 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   const DecodeParams& p = pb.dec;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  __shared__ __align__(8) uint64_t s_full[NSB], q_ready, p_ready[NT], o_full[NT], drain;
+  __shared__ __align__(8) uint64_t s_full[NSB], s_empty[NSB], q_ready, p_ready[NT], o_full[NT],
+      drain[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag, bad_page;
   __shared__ __align__(16) float cq[R];         // tau log2(e) 2^-k of each row's query
@@ -243,13 +263,17 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       mbar_init(smem_u32(&v_full[s]), 1);
       mbar_init(smem_u32(&v_empty[s]), 1);
     }
-    for (int s = 0; s < NSB; ++s) mbar_init(smem_u32(&s_full[s]), 1);
+    for (int s = 0; s < NSB; ++s) {
+      mbar_init(smem_u32(&s_full[s]), 1);
+      mbar_init(smem_u32(&s_empty[s]), 4 * NG);
+    }
     mbar_init(smem_u32(&q_ready), Sh::kWarps);
     for (int s = 0; s < NT; ++s) {
       mbar_init(smem_u32(&p_ready[s]), 4 * NG);
       mbar_init(smem_u32(&o_full[s]), 1);
     }
-    mbar_init(smem_u32(&drain), 1);
+    mbar_init(smem_u32(&drain[0]), 1);
+    mbar_init(smem_u32(&drain[1]), 1);
     abort_flag = 0;
     bad_page = 0;
     fence_barrier_init();
@@ -293,9 +317,9 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The softmax warps' rows of Q travel together with the length: row sw, sw +
   // kWarps, ..; lane takes columns 4 lane .. 4 lane + 3.
-  const int sw = warp - 2;
+  const int sw = warp - 3;
   uint2 qw[Sh::kRowsQ];
-  if (warp >= 2) {
+  if (warp >= 3) {
 #pragma unroll
     for (int i = 0; i < Sh::kRowsQ; ++i) {
       const int r = sw + i * Sh::kWarps;
@@ -327,15 +351,25 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     return;
   }
 
-  // A bounded wait that also gives up once another role has aborted, taken by
-  // every lane of a warp with one agreed result.
+  // A bounded wait of a whole warp that also gives up once another role has
+  // aborted.
   auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-    bool ok = mbar_try_wait(smem_u32(bar), parity);
-    if (!ok && !*abort_v) {
-      ok = mbar_wait(smem_u32(bar), parity, p.wait_ns, p.err);
-      if (!ok) *abort_v = 1;
+    const uint32_t addr = smem_u32(bar);
+    if (warp_try_wait(addr, parity)) return true;
+    const uint64_t since = globaltimer_ns();
+#pragma unroll 1
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i)
+        if (warp_try_wait(addr, parity)) return true;
+      const bool late = globaltimer_ns() - since > p.wait_ns;
+      if (__any_sync(0xffffffffu, late || *abort_v != 0)) {
+        if (lane == 0 && *abort_v == 0) atomicOr(p.err, kErrTimeout);
+        __syncwarp();
+        *abort_v = 1;
+        return false;
+      }
     }
-    return __all_sync(0xffffffffu, ok);
   };
 
   if (warp == 0) {
@@ -408,58 +442,53 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ----------------------------------------------------------- MMA issuer --
+    // ------------------------------------------------------------ S issuer --
+    // S_j = K_j Q^T into buffer j % NSB, once K_j is there and S_{j - NSB} was read.
     constexpr uint32_t idS = instr_desc_e4m3_f32(128, 2 * R, false, false);
-    constexpr uint32_t idO = instr_desc_e4m3_f32(128, 2 * R, true, true);
-    const uint32_t qb = sb + Sh::kOffQ, ppb = sb + Sh::kOffP;
+    const uint64_t dk = smem_desc_sw128(sb, 16, 1024);  // slot 0; an offset adds to the address
+    const uint64_t dq = smem_desc_sw128(sb + Sh::kOffQ, 16, 1024);
     const int ksteps = D / 32;
-    auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity));
-    };
-    // Whatever can run runs: the next S once its K is there and its buffer free (S_j
-    // overwrites S_{j - NSB}, read before p_ready of that tile), else the next O
-    // once its V and P are there.  Nothing for too long: give up as a wait does.
     bool ok = wait_all(&q_ready, 0);
-    int js = 0, jo = 0;
-    uint64_t idle_since = 0;
-    for (uint32_t spin = 0; ok && jo < n;) {
-      if (js < n && js < jo + NSB && ready(&k_full[js % NS], (js / NS) & 1)) {
-        tc_fence_after();
-        const uint32_t kb = sb + (js % NS) * kFbTile;
-        for (int kk = 0; kk < ksteps; ++kk)  // S = K Q^T
-          tc_mma_f8_ss(tmem + 2 * R * (js % NSB), smem_desc_sw128(kb + kk * 32, 16, 1024),
-                       smem_desc_sw128(qb + kk * 32, 16, 1024), idS, kk > 0);
-        tc_commit(smem_u32(&s_full[js % NSB]));
-        tc_commit(smem_u32(&k_empty[js % NS]));
-        ++js;
-        spin = 0;
-      } else if (jo < js && ready(&p_ready[jo % NT], (jo / NT) & 1) &&
-                 ready(&v_full[jo % NS], (jo / NS) & 1)) {
-        tc_fence_after();
-        const int s = jo % NT;
-        const uint32_t vb = sb + Sh::kOffV + (jo % NS) * kFbTile, pj = ppb + s * Sh::kTileP;
+    for (int j = 0; ok && j < n; ++j) {
+      ok = wait_all(&k_full[j % NS], (j / NS) & 1) &&
+           (j < NSB || wait_all(&s_empty[j % NSB], (j / NSB - 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t dkj = dk + (j % NS) * (kFbTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // O = V^T P: 32 keys each, four groups of 8 rows
-          tc_mma_f8_ss(tmem + Sh::kColO + 2 * R * s, smem_desc_sw128(vb + kk * 4096, kFbTile, 1024),
-                       smem_desc_mn<Sh::kRowP>(pj + kk * 32 * Sh::kRowP), idO, kk > 0);
-        tc_commit(smem_u32(&o_full[s]));
-        tc_commit(smem_u32(&v_empty[jo % NS]));
-        ++jo;
-        spin = 0;
-      } else if (++spin % 64 == 0) {
-        const uint64_t now = globaltimer_ns();
-        if (spin == 64) idle_since = now;
-        const bool late = now - idle_since > p.wait_ns;
-        if (__any_sync(0xffffffffu, late || *abort_v != 0)) {
-          if (lane == 0 && *abort_v == 0) atomicOr(p.err, kErrTimeout);
-          *abort_v = 1;
-          ok = false;
-        }
-      }
+      for (int kk = 0; kk < 4; ++kk)  // 32 columns of d each
+        if (kk < ksteps)
+          tc_mma_f8_ss(tmem + 2 * R * (j % NSB), dkj + kk * 2, dq + kk * 2, idS, kk > 0);
+      tc_commit(smem_u32(&s_full[j % NSB]));
+      tc_commit(smem_u32(&k_empty[j % NS]));
     }
     // Every MMA issued here has completed before tensor memory is released.
-    tc_commit(smem_u32(&drain));
-    mbar_wait(smem_u32(&drain), 0, p.wait_ns, p.err);
+    tc_commit(smem_u32(&drain[0]));
+    mbar_wait(smem_u32(&drain[0]), 0, p.wait_ns, p.err);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ O issuer --
+    // O = V_j^T P_j into accumulator j % NT, once both are there (P_j is written
+    // after the softmax has taken the accumulator's previous contents).
+    constexpr uint32_t idO = instr_desc_e4m3_f32(128, 2 * R, true, true);
+    const uint64_t dv = smem_desc_sw128(sb + Sh::kOffV, kFbTile, 1024);
+    const uint64_t dp = smem_desc_mn<Sh::kRowP>(sb + Sh::kOffP);
+    bool ok = true;
+    for (int j = 0; ok && j < n; ++j) {
+      const int s = j % NT;
+      ok = wait_all(&v_full[j % NS], (j / NS) & 1) && wait_all(&p_ready[s], (j / NT) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t dvj = dv + (j % NS) * (kFbTile >> 4), dpj = dp + s * (Sh::kTileP >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)  // 32 keys each: four groups of 8 rows
+        tc_mma_f8_ss(tmem + Sh::kColO + 2 * R * s, dvj + kk * (4096 >> 4),
+                     dpj + kk * (32 * Sh::kRowP >> 4), idO, kk > 0);
+      tc_commit(smem_u32(&o_full[s]));
+      tc_commit(smem_u32(&v_empty[j % NS]));
+    }
+    tc_commit(smem_u32(&drain[1]));
+    mbar_wait(smem_u32(&drain[1]), 0, p.wait_ns, p.err);
     __syncwarp();
   } else {
     // ------------------------------------------- softmax, accumulation, end --
@@ -510,7 +539,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&q_ready));
 
-    // Scales of this thread's key, one tile of the stream ahead; its page, two.
+    // Scales of this thread's key, loaded one tile of the stream ahead; its page, two.
     auto page_of = [&](int j) -> int {
       const int tok = t0 + j * kFbKeys + kl;
       if (j >= n || tok >= t_end) return -1;
@@ -529,7 +558,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       vs = pb.v_scale[i];
     };
     int unit1 = page_of(st + NT);
-    float ks, vs, ks1, vs1;
+    float ks, vs;
     scale_of(st, page_of(st), ks, vs);
     float acc[RW], l[RW], off[RW];  // off: 7 less the row's reference (0 while it has none)
 #pragma unroll
@@ -564,8 +593,6 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
 
     int turn = 0;  // tiles of this stream so far
     for (int j = st; j < n; j += NT, ++turn) {
-      scale_of(j + NT, unit1, ks1, vs1);
-      unit1 = page_of(j + 2 * NT);
       // log2 vs and 1 / vs; scales below 2^-100 count as zero, negative ones are NaN
       const bool v_live = vs >= kMinVScale;
       const float lv = v_live ? __log2f(vs) : (vs >= 0.f ? -100.f : NAN);
@@ -608,6 +635,12 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
 #pragma unroll
         for (int i = 0; i < RW; i += 2) top = fmax3(top, y[i], y[i + 1]);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (alive && lane == 0) mbar_arrive(smem_u32(&s_empty[j % NSB]));
+      // (into the registers just read for the last time)
+      scale_of(j + NT, unit1, ks, vs);
+      unit1 = page_of(j + 2 * NT);
       const bool update = named_bar_any(1 + gi, 128, unset || top > kPMaxLog2);
       if (update) {
         // The rows' maxima over the 128 keys become references where they are
@@ -699,8 +732,6 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       tc_fence_before();
       __syncwarp();
       if (alive && lane == 0) mbar_arrive(smem_u32(&p_ready[st]));
-      ks = ks1;
-      vs = vs1;
     }
 
     // The stream's last O, and l over the keys.
