@@ -588,6 +588,8 @@ gqa_status kv_block_layout(const void* k_cache, const void* v_cache, const float
     p->per = S_max;
   }
   p->per_blk = p->per / block + (p->per % block != 0);
+  while ((1 << p->block_log2) < block) ++p->block_log2;
+  while (paged && (1 << p->page_log2) < page_size) ++p->page_log2;
   p->B = B;
   p->S_max = S_max;
   p->H_kv = H_kv;
@@ -628,8 +630,7 @@ gqa_status run_kv_read(gqa::KvBlockParams* p, int start, int S_out, void* k_out,
   p->v_out = static_cast<__nv_bfloat16*>(v_out);
   const gqa_status st = error_word(&p->err);
   if (st != GQA_OK) return st;
-  return cuda_status(
-      gqa::launch_kv_read(*p, num_sms_current_device(), reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(gqa::launch_kv_read(*p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int T_q, int H_q,
@@ -663,16 +664,11 @@ gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int 
   if ((st = encode_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.v_cache, 3, dims, strides, box,
                        CU_TENSOR_MAP_SWIZZLE_128B)) != GQA_OK)
     return st;
-  auto log2i = [](int x) {
-    int l = 0;
-    while ((1 << l) < x) ++l;
-    return l;
-  };
   gqa::DecodeBlockParams p{};
   p.k_scale = c.k_scale;
   p.v_scale = c.v_scale;
-  p.block_log2 = log2i(c.block);
-  p.page_log2 = c.block_table ? log2i(c.page_size) : 0;
+  p.block_log2 = c.block_log2;
+  p.page_log2 = c.page_log2;
   p.per_blk = c.per_blk;
   gqa::DecodeParams& dp = p.dec;
   dp.q = static_cast<const __nv_bfloat16*>(q);

@@ -80,11 +80,11 @@ struct PrefillParams {
 // [units][per_blk][H_kv] fp32): a unit is a sequence of a contiguous cache
 // (per = S_max) or a page of a pool (per = page_size, block_table set).
 struct KvBlockParams {
-  int B, S_max, H_kv, d, block;
+  int B, S_max, H_kv, d, block, block_log2;
   int units, per, per_blk;  // per_blk = ceil(per / block)
   const int32_t* seq_lens;  // [B]
   const int32_t* block_table;
-  int max_blocks, page_size, num_pages;
+  int max_blocks, page_size, page_log2, num_pages;
   uint8_t *k_cache, *v_cache;
   float *k_scale, *v_scale;
   // append: the last n_new[b] (or T) of seq_lens[b] tokens are rows 0.. of
@@ -95,6 +95,7 @@ struct KvBlockParams {
   int T;
   // read: tokens start.. of each sequence to [B, S_out, H_kv, d]
   int start, S_out;
+  uint32_t row_magic;  // set by the launcher: 2^32 over a row's pieces, rounded up
   __nv_bfloat16 *k_out, *v_out;
   unsigned* err;
 };
@@ -143,7 +144,7 @@ cudaError_t launch_prefill_merge(const PrefillParams& p, cudaStream_t stream);
 // Trace build: zero the causal prefill's stamp records (no-op otherwise).
 cudaError_t prefill_trace_clear();
 cudaError_t launch_kv_append(const KvBlockParams& p, cudaStream_t stream);
-cudaError_t launch_kv_read(const KvBlockParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvBlockParams& p, cudaStream_t stream);
 // Decode of T_q * G (<= 64) query rows per KV head over the block-scaled E4M3
 // cache; K/V boxes of min(page_size, 128) rows, 128 bytes wide; p.dec.chunk a
 // multiple of 128.  Same partial layout as launch_decode_split.
