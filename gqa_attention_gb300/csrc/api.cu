@@ -647,12 +647,21 @@ gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int 
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       (workspace && !aligned(workspace, 256)))
     return GQA_ERR_INVALID_ARG;
-  // Codes as [rows][H_kv][d] bytes; boxes of up to 128 rows of one head, always
-  // 128 bytes wide: for d = 32 and 64 TMA fills the rest of each row with zeros.
+  // Codes as [rows][H_kv][d] bytes, boxes of up to 128 rows, always 128 bytes wide.
+  // For d = 32 and 64, a CTA takes the 4 or 2 heads that share 128 bytes of a row
+  // (rows of H_kv d bytes, zeros past them), as long as their query rows fit and
+  // the grid still fills the GPU: a tile then serves all of them.  Otherwise the
+  // box is one head and TMA fills the rest of each row with zeros.
+  const int pack = 128 / c.d, head_rows = (T_q * G + 7) / 8 * 8;
+  const long long packed_ctas = (long long)n_split * ((c.H_kv + pack - 1) / pack) * c.B;
+  const bool packed = pack > 1 && c.H_kv > 1 && pack * head_rows <= 64 &&
+                      packed_ctas >= num_sms_current_device();
   const long long rows = (long long)c.units * c.per;
   const int box_rows = c.block_table && c.page_size < 128 ? c.page_size : 128;
-  const uint64_t dims[3] = {(uint64_t)c.d, (uint64_t)c.H_kv, (uint64_t)rows};
-  const uint64_t strides[2] = {(uint64_t)c.d, (uint64_t)c.H_kv * c.d};
+  const uint64_t width = (uint64_t)c.H_kv * c.d;
+  const uint64_t dims[3] = {packed ? width : (uint64_t)c.d, packed ? 1u : (uint64_t)c.H_kv,
+                            (uint64_t)rows};
+  const uint64_t strides[2] = {packed ? width : (uint64_t)c.d, width};
   const uint32_t box[3] = {128u, 1u, (uint32_t)box_rows};
   CUtensorMap tm_k, tm_v;
   unsigned* err = nullptr;
@@ -670,6 +679,8 @@ gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int 
   p.block_log2 = c.block_log2;
   p.page_log2 = c.page_log2;
   p.per_blk = c.per_blk;
+  p.heads = packed ? pack : 1;
+  p.head_rows = head_rows;
   gqa::DecodeParams& dp = p.dec;
   dp.q = static_cast<const __nv_bfloat16*>(q);
   dp.seq_lens = c.seq_lens;

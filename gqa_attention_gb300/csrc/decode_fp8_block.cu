@@ -37,9 +37,9 @@
 // d of O^T) add to fp32 registers, rescaled when m moved: no rescaling pass
 // through tensor memory, and the sum over tiles is fp32.
 //
-// Roles (96 + 32 kWarps threads): warp 0 TMA producer, warp 1 issuer of S (and
-// tensor memory), warp 2 issuer of O, the others Q split, softmax, accumulation
-// and epilogue.
+// Roles (128 + 32 kWarps threads): warps 0 and 3 TMA producers of K and V, warp 1
+// issuer of S (and tensor memory), warp 2 issuer of O, the others Q split, softmax,
+// accumulation and epilogue.
 #include "tcgen05.cuh"
 
 namespace gqa {
@@ -62,7 +62,7 @@ struct FbShape {
   static constexpr int NSB = 2 * NT;                // S buffers
   static constexpr int kWarps = 4 * NT * NG;        // softmax warps
   static constexpr int kRowsQ = R / kWarps;         // rows of Q a warp splits
-  static constexpr int kThreads = 96 + 32 * kWarps;
+  static constexpr int kThreads = 128 + 32 * kWarps;
   static constexpr uint32_t kRowP = 2 * R;          // bytes of a key's row of P
   static constexpr uint32_t kOffV = NS * kFbTile;
   static constexpr uint32_t kOffQ = 2 * NS * kFbTile;
@@ -74,9 +74,9 @@ struct FbShape {
   static constexpr uint32_t kUsed = (NSB + NT) * 2 * R;
   static constexpr uint32_t kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   // CTAs an SM holds: shared memory (4 KB of it for the static part and the
-  // driver's), tensor memory and 22 warps at 88 registers
+  // driver's), tensor memory and 24 warps at 80 registers
   static constexpr int kPerSM =
-      2 * (kBytes + 4096) <= 227 * 1024 && kThreads <= 352 && kCols <= 256 ? 2 : 1;
+      2 * (kBytes + 4096) <= 227 * 1024 && kThreads <= 384 && kCols <= 256 ? 2 : 1;
   static_assert(kUsed <= 512 && kRowsQ >= 1, "tensor memory; a row of Q for every warp");
   static_assert(NT * R * 512 <= 2 * NS * (int)kFbTile, "the accumulators reuse the rings");
 };
@@ -197,6 +197,22 @@ __device__ __forceinline__ bool warp_try_wait(uint32_t bar, uint32_t parity) {
   if (ok) __syncwarp();
   return ok != 0;
 }
+// One elected lane of the (converged) warp arms a barrier, or issues a copy.
+__device__ __forceinline__ void expect_tx_elect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_elect(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                  int c0, int c1, int c2, uint64_t pol) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(pol)
+      : "memory");
+}
 // Barrier `id` over `count` threads that returns whether any of them gave true.
 __device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
   uint32_t any;
@@ -239,20 +255,37 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x, kv = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x, b = blockIdx.z;
+  // KV heads hc blockIdx.y + 0 .. hc - 1 share the 128-byte rows of a tile (hc = 128 / d
+  // packed heads, or 1).  Head hl has the query rows r = hl rp + q, q < T_q * G.
+  const int hc = pb.heads, rp = pb.head_rows, kv0 = blockIdx.y * hc;
   // first key of the split (rows of a cache are below 2^31 - 256, so keys of a
   // tile past its end still fit)
   const int t0 = static_cast<int>(min((long long)split * p.chunk, (long long)p.S_max));
-  const int G = p.G, rows = p.T_q * G;  // <= R
+  const int G = p.G, rows = p.T_q * G;  // of a head
   const int D = p.d;
+  // Head of row r (rows past the last head's count as its padding).
+  auto head_of = [&](int r) {
+    return hc == 1 ? 0 : min(hc - 1, (r >= rp) + (r >= 2 * rp) + (r >= 3 * rp));
+  };
+  auto live_row = [&](int r) {
+    const int hl = head_of(r);
+    return r - hl * rp < rows && kv0 + hl < p.H_kv;
+  };
   // r / G without an integer division, as in decode.cu
   const float inv_g = 1.f / static_cast<float>(G);
-  auto query_of = [&](int r) { return static_cast<int>((static_cast<float>(r) + 0.5f) * inv_g); };
-  auto out_row = [&](int r) -> uint32_t {  // (B * T_q and H_q are below 2^16)
-    const int t = query_of(r);
-    return static_cast<uint32_t>(b * p.T_q + t) * p.H_q + kv * G + (r - t * G);
+  auto query_of = [&](int r) {
+    return static_cast<int>((static_cast<float>(r - head_of(r) * rp) + 0.5f) * inv_g);
+  };
+  auto out_row = [&](int r) -> uint32_t {  // of a live row (B * T_q and H_q are below 2^16)
+    const int hl = head_of(r), t = query_of(r);
+    return static_cast<uint32_t>(b * p.T_q + t) * p.H_q + (kv0 + hl) * G + (r - hl * rp - t * G);
   };
   const size_t n_rows = (size_t)p.B * p.T_q * p.H_q;
+
+  // Tile coordinates: packed heads are 128 bytes of the whole row of H_kv d codes,
+  // a head by itself is an index (the map then fills its 128-byte rows with zeros).
+  const int tx = hc == 1 ? 0 : static_cast<int>(blockIdx.y) * 128, ty = hc == 1 ? kv0 : 0;
 
   // Set-up that touches no global memory runs before the dependency wait.
   volatile int* abort_v = &abort_flag;
@@ -305,8 +338,8 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
         row = pg * p.page_size + (tk & (p.page_size - 1));
       }
       if (ok) {
-        tma_prefetch_l2_3d(&tm_k, 0, kv, row);
-        tma_prefetch_l2_3d(&tm_v, 0, kv, row);
+        tma_prefetch_l2_3d(&tm_k, tx, ty, row);
+        tma_prefetch_l2_3d(&tm_v, tx, ty, row);
       }
     }
   }
@@ -317,14 +350,14 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The softmax warps' rows of Q travel together with the length: row sw, sw +
   // kWarps, ..; lane takes columns 4 lane .. 4 lane + 3.
-  const int sw = warp - 3;
+  const int sw = warp - 4;
   uint2 qw[Sh::kRowsQ];
-  if (warp >= 3) {
+  if (warp >= 4) {
 #pragma unroll
     for (int i = 0; i < Sh::kRowsQ; ++i) {
       const int r = sw + i * Sh::kWarps;
       qw[i] = make_uint2(0u, 0u);
-      if (r < rows && lane * 4 < D)
+      if (lane * 4 < D && live_row(r))
         qw[i] = *reinterpret_cast<const uint2*>(p.q + (size_t)out_row(r) * D + lane * 4);
     }
   }
@@ -335,8 +368,9 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   if (bad || n == 0) {
     // A bad length: NaN outputs and the error bit.  An empty split: the merge
     // identity (-inf, 0); its O is not written.  (One split is never empty.)
-    if (bad && threadIdx.x == 0 && split == 0 && kv == 0) atomicOr(p.err, kErrBadSeqLen);
-    for (int r = threadIdx.x; r < rows; r += Sh::kThreads) {
+    if (bad && threadIdx.x == 0 && split == 0 && kv0 == 0) atomicOr(p.err, kErrBadSeqLen);
+    for (int r = threadIdx.x; r < R; r += Sh::kThreads) {
+      if (!live_row(r)) continue;
       const size_t row = out_row(r);
       if (p.n_split == 1) {
         if (in_bounds(row * D, D, n_rows * D, p.err))
@@ -372,82 +406,84 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     }
   };
 
-  if (warp == 0) {
-    // ----------------------------------------------------------- TMA producer --
-    // The whole warp runs the loop so that a tile's page indices are read in
-    // parallel, one box per lane; lane 0 arms each barrier before any copy.
-    if (lane == 0) {
-      tma_prefetch_map(&tm_k);
-      tma_prefetch_map(&tm_v);
-    }
+  if (warp == 0 || warp == 3) {
+    // ---------------------------------------------- TMA producers of K and V --
+    const bool is_k = warp == 0;
+    const CUtensorMap* const map = is_k ? &tm_k : &tm_v;
+    uint64_t* const full = is_k ? k_full : v_full;
+    uint64_t* const empty = is_k ? k_empty : v_empty;
+    const uint32_t ring = sb + (is_k ? 0u : Sh::kOffV);
+    if (lane == 0) tma_prefetch_map(map);
     const int h = PAGED ? min(p.page_size, kFbKeys) : kFbKeys;
-    const int nb = kFbKeys / h;  // <= 8 (page_size >= 16)
-    int issued_k = 0, issued_v = 0;
-    auto fetch = [&](int j) -> int {  // this lane's page of tile j, -1 for none
-      const int tok = t0 + j * kFbKeys + lane * h;
-      if (!PAGED || lane >= nb || j >= n || tok >= t_end) return -1;
-      const int pg = p.block_table[(size_t)b * p.max_blocks + (tok >> pb.page_log2)];
-      return pg >= 0 && pg < p.num_pages ? pg : -2;  // -2: outside the pool
+    const int nb = kFbKeys / h;  // boxes of a tile, <= 8 (page_size >= 16)
+    // Rows of 32 boxes at a time, one per lane, their pages loaded a round before
+    // they are used (a round is 4 to 32 tiles).  A box past the end of the split, or
+    // of a page outside the pool, reads rows past the pool, which TMA fills with
+    // zeros, so that every tile receives its bytes; a bad index is recorded before
+    // the barrier of any of its boxes is armed.
+    auto fetch = [&](int tile) -> int {  // this lane's page, -1 for none
+      const int tok = t0 + tile * kFbKeys + lane * h;
+      return PAGED && tok < t_end
+                 ? p.block_table[(size_t)b * p.max_blocks + (tok >> pb.page_log2)] : -1;
+    };
+    auto row_of = [&](int tile, int pg) -> int {
+      const int tok = t0 + tile * kFbKeys + lane * h;
+      const bool in = pg >= 0 && pg < p.num_pages;
+      if (__any_sync(0xffffffffu, tok < t_end && !in) && lane == 0) {
+        if (!*reinterpret_cast<volatile int*>(&bad_page)) atomicOr(p.err, kErrBadPage);
+        *reinterpret_cast<volatile int*>(&bad_page) = 1;
+      }
+      __syncwarp();
+      return tok < t_end && in ? pg * p.page_size + (tok & (p.page_size - 1))
+                               : p.num_pages * p.page_size;
     };
     const uint64_t pol = l2_policy_evict_first();  // every tile is read once
-    auto issue = [&](bool is_k, int j, int pg) -> bool {
-      const int slot = j % NS;
-      if (j >= NS && !wait_all(is_k ? &k_empty[slot] : &v_empty[slot], ((j / NS) - 1) & 1))
-        return false;
-      const uint32_t fb = smem_u32(is_k ? &k_full[slot] : &v_full[slot]);
-      const uint32_t dst = sb + (is_k ? 0u : Sh::kOffV) + slot * kFbTile;
-      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
-      const int tok0 = t0 + j * kFbKeys;
-      if constexpr (!PAGED) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(fb, kFbTile);
-          tma_load_3d(dst, map, fb, 0, kv, b * p.S_max + tok0, pol);
-        }
-      } else {
-        // A box wholly past the end of the split reads rows past the pool,
-        // which TMA fills with zeros, so that every tile receives its bytes; a
-        // bad page index is recorded before lane 0's arrive releases it.
-        const bool wrong = pg == -2;
-        const int row = pg >= 0 ? pg * p.page_size + ((tok0 + lane * h) & (p.page_size - 1))
-                                : p.num_pages * p.page_size;
-        if (__any_sync(0xffffffffu, wrong) && lane == 0) {
-          if (!*reinterpret_cast<volatile int*>(&bad_page)) atomicOr(p.err, kErrBadPage);
-          *reinterpret_cast<volatile int*>(&bad_page) = 1;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(fb, kFbTile);
-        __syncwarp();
-        if (lane < nb) tma_load_3d(dst + lane * h * 128, map, fb, 0, kv, row, pol);
+    int pages = fetch(32 / nb), rows_l = PAGED ? row_of(0, fetch(0)) : 0, at = 0, slot = 0;
+    uint32_t parity = 0;  // of the slot's present use
+    int issued = 0;
+    for (int j = 0; j < n; ++j) {
+      if (PAGED && at == 32) {  // a round has passed
+        rows_l = row_of(j, pages);
+        pages = fetch(j + 32 / nb);
+        at = 0;
       }
-      return true;
-    };
-    int pg0 = fetch(0), pg1 = fetch(1);
-    bool ok = true;
-    for (int j = 0; ok && j < n; ++j) {
-      const int pg2 = fetch(j + 2);
-      ok = issue(true, j, pg0);
-      if (ok) issued_k = j + 1;
-      ok = ok && issue(false, j, pg0);
-      if (ok) issued_v = j + 1;
-      pg0 = pg1;
-      pg1 = pg2;
+      if (j >= NS && !wait_all(&empty[slot], parity ^ 1)) break;
+      const uint32_t fb = smem_u32(&full[slot]), dst = ring + slot * kFbTile;
+      // The whole warp runs the copies and one elected lane issues them, which keeps
+      // their operands uniform (box i from lane i took a diverged warp's branches:
+      // 16-token pages of a 64 x 4K batch 37.6 instead of 33.1 us).
+      expect_tx_elect(fb, kFbTile);
+      if constexpr (!PAGED) {
+        tma_load_3d_elect(dst, map, fb, tx, ty, b * p.S_max + t0 + j * kFbKeys, pol);
+      } else {
+        for (int i = 0; i < nb; ++i)
+          tma_load_3d_elect(dst + i * h * 128, map, fb, tx, ty,
+                            __shfl_sync(0xffffffffu, rows_l, at + i), pol);
+      }
+      issued = j + 1;
+      at += nb;
+      if (++slot == NS) {
+        slot = 0;
+        parity ^= 1;
+      }
     }
     if (lane == 0) {
       // The next kernel may be scheduled; it waits for this grid before it reads.
       asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       // No copy may still target shared memory when the CTA exits.
-      for (int j = max(0, issued_k - NS); j < issued_k; ++j)
-        mbar_wait(smem_u32(&k_full[j % NS]), (j / NS) & 1, p.wait_ns, p.err);
-      for (int j = max(0, issued_v - NS); j < issued_v; ++j)
-        mbar_wait(smem_u32(&v_full[j % NS]), (j / NS) & 1, p.wait_ns, p.err);
+      for (int j = max(0, issued - NS); j < issued; ++j)
+        mbar_wait(smem_u32(&full[j % NS]), (j / NS) & 1, p.wait_ns, p.err);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ S issuer --
     // S_j = K_j Q^T into buffer j % NSB, once K_j is there and S_{j - NSB} was read.
-    constexpr uint32_t idS = instr_desc_e4m3_f32(128, 2 * R, false, false);
+    // Packed heads: head hl's columns of K against its rows of Q, into its columns.
     const uint64_t dk = smem_desc_sw128(sb, 16, 1024);  // slot 0; an offset adds to the address
     const uint64_t dq = smem_desc_sw128(sb + Sh::kOffQ, 16, 1024);
-    const int ksteps = D / 32;
+    const int ksteps = D / 32;  // of a head: 32 columns of d each
+    const uint32_t id = instr_desc_e4m3_f32(128, hc == 1 ? 2 * R : 2 * rp, false, false);
+    const uint32_t id_last = instr_desc_e4m3_f32(128, 2 * (R - (hc - 1) * rp), false, false);
     bool ok = wait_all(&q_ready, 0);
     for (int j = 0; ok && j < n; ++j) {
       ok = wait_all(&k_full[j % NS], (j / NS) & 1) &&
@@ -455,10 +491,19 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       if (!ok) break;
       tc_fence_after();
       const uint64_t dkj = dk + (j % NS) * (kFbTile >> 4);
+      if (hc == 1) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)  // 32 columns of d each
-        if (kk < ksteps)
-          tc_mma_f8_ss(tmem + 2 * R * (j % NSB), dkj + kk * 2, dq + kk * 2, idS, kk > 0);
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < ksteps)
+            tc_mma_f8_ss(tmem + 2 * R * (j % NSB), dkj + kk * 2, dq + kk * 2, id, kk > 0);
+      } else {
+#pragma unroll 1
+        for (int hl = 0; hl < hc; ++hl)
+          for (int kk = 0; kk < ksteps; ++kk)
+            tc_mma_f8_ss(tmem + 2 * R * (j % NSB) + hl * 2 * rp, dkj + (hl * ksteps + kk) * 2,
+                         dq + hl * (2 * rp * 128 >> 4) + kk * 2, hl == hc - 1 ? id_last : id,
+                         kk > 0);
+      }
       tc_commit(smem_u32(&s_full[j % NSB]));
       tc_commit(smem_u32(&k_empty[j % NS]));
     }
@@ -531,15 +576,21 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
                     pack_e4m3x2(lo[0], lo[1]) | (pack_e4m3x2(lo[2], lo[3]) << 16));
       if (lane == 0) {
         cq[r] = a >= 0x7f80u ? NAN : p.scale_log2 * __int_as_float((127 - k) << 23);
-        lim_sm[r] = r < rows ? min(t_end, L - p.T_q + 1 + query_of(r)) : t_end;
-        row_sm[r] = out_row(r);
+        const bool live = live_row(r);
+        lim_sm[r] = live ? min(t_end, L - p.T_q + 1 + query_of(r)) : t_end;
+        row_sm[r] = live ? out_row(r) : 0xffffffffu;  // (no row of an output: H_q is below 2^16)
       }
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&q_ready));
 
-    // Scales of this thread's key, loaded one tile of the stream ahead; its page, two.
+    // Scales of this thread's key for each eight rows (one head's), loaded one tile
+    // of the stream ahead; its page, two.
+    constexpr int RU = RW / 8;
+    int kv_of[RU];
+#pragma unroll
+    for (int c = 0; c < RU; ++c) kv_of[c] = min(kv0 + head_of(r0 + 8 * c), p.H_kv - 1);
     auto page_of = [&](int j) -> int {
       const int tok = t0 + j * kFbKeys + kl;
       if (j >= n || tok >= t_end) return -1;
@@ -547,19 +598,22 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       const int pg = p.block_table[(size_t)b * p.max_blocks + (tok >> pb.page_log2)];
       return pg >= 0 && pg < p.num_pages ? pg : -1;
     };
-    auto scale_of = [&](int j, int unit, float& ks, float& vs) {
-      ks = 1.f;
-      vs = 1.f;
+    float ks[RU], vs[RU];
+    auto load_scales = [&](int j, int unit) {
+#pragma unroll
+      for (int c = 0; c < RU; ++c) ks[c] = vs[c] = 1.f;
       if (unit < 0) return;
       const int tok = t0 + j * kFbKeys + kl;
       const int at = PAGED ? tok & (p.page_size - 1) : tok;
-      const size_t i = ((size_t)unit * pb.per_blk + (at >> pb.block_log2)) * p.H_kv + kv;
-      ks = pb.k_scale[i];
-      vs = pb.v_scale[i];
+      const size_t i = ((size_t)unit * pb.per_blk + (at >> pb.block_log2)) * p.H_kv;
+#pragma unroll
+      for (int c = 0; c < RU; ++c) {
+        ks[c] = pb.k_scale[i + kv_of[c]];
+        vs[c] = pb.v_scale[i + kv_of[c]];
+      }
     };
     int unit1 = page_of(st + NT);
-    float ks, vs;
-    scale_of(st, page_of(st), ks, vs);
+    load_scales(st, page_of(st));
     float acc[RW], l[RW], off[RW];  // off: 7 less the row's reference (0 while it has none)
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
@@ -594,10 +648,15 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     int turn = 0;  // tiles of this stream so far
     for (int j = st; j < n; j += NT, ++turn) {
       // log2 vs and 1 / vs; scales below 2^-100 count as zero, negative ones are NaN
-      const bool v_live = vs >= kMinVScale;
-      const float lv = v_live ? __log2f(vs) : (vs >= 0.f ? -100.f : NAN);
-      const float ivs = v_live ? __frcp_rn(vs) : 1.f / kMinVScale;
-      const uint32_t p_mask = vs >= 0.f && !v_live ? 0u : 0xffffffffu;
+      float lv[RU], ivs[RU];
+      uint32_t p_mask[RU];
+#pragma unroll
+      for (int c = 0; c < RU; ++c) {
+        const bool v_live = vs[c] >= kMinVScale;
+        lv[c] = v_live ? __log2f(vs[c]) : (vs[c] >= 0.f ? -100.f : NAN);
+        ivs[c] = v_live ? __frcp_rn(vs[c]) : 1.f / kMinVScale;
+        p_mask[c] = vs[c] >= 0.f && !v_live ? 0u : 0xffffffffu;
+      }
       const int key = t0 + j * kFbKeys + kl;
       // (a warp whose wait failed keeps to the barriers of the others)
       alive = alive && wait_all(&s_full[j % NSB], (j / NSB) & 1);
@@ -621,8 +680,8 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
               float a0, a1, b0, b1, d0, d1;
               ffma2(a0, a1, __uint_as_float(s[8 + e]), __uint_as_float(s[9 + e]), kLoStep, kLoStep,
                     __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-              fmul2(b0, b1, c[u], c[u + 1], ks, ks);
-              fadd2(d0, d1, off[r], off[r + 1], lv, lv);
+              fmul2(b0, b1, c[u], c[u + 1], ks[c0 / 8], ks[c0 / 8]);
+              fadd2(d0, d1, off[r], off[r + 1], lv[c0 / 8], lv[c0 / 8]);
               ffma2(y[r], y[r + 1], a0, a1, b0, b1, d0, d1);
             }
           }
@@ -639,7 +698,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       __syncwarp();
       if (alive && lane == 0) mbar_arrive(smem_u32(&s_empty[j % NSB]));
       // (into the registers just read for the last time)
-      scale_of(j + NT, unit1, ks, vs);
+      load_scales(j + NT, unit1);
       unit1 = page_of(j + 2 * NT);
       const bool update = named_bar_any(1 + gi, 128, unset || top > kPMaxLog2);
       if (update) {
@@ -698,8 +757,9 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
           const int r = c0 + i;
           const float e0 = ex2_approx(y[r]), e1 = ex2_approx(y[r + 1]);
           const float e2 = ex2_approx(y[r + 2]), e3 = ex2_approx(y[r + 3]);
-          ffma2(l[r], l[r + 1], e0, e1, ivs, ivs, l[r], l[r + 1]);
-          ffma2(l[r + 2], l[r + 3], e2, e3, ivs, ivs, l[r + 2], l[r + 3]);
+          const float iv = ivs[c0 / 8];
+          ffma2(l[r], l[r + 1], e0, e1, iv, iv, l[r], l[r + 1]);
+          ffma2(l[r + 2], l[r + 3], e2, e3, iv, iv, l[r + 2], l[r + 3]);
           uint32_t h[2], d[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -711,8 +771,8 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
                                       __float2half2_rn(32.f));
             d[u] = pack_e4m3x2(*reinterpret_cast<const uint32_t*>(&q));
           }
-          hi[i / 4] = (h[0] | (h[1] << 16)) & p_mask;
-          lo[i / 4] = (d[0] | (d[1] << 16)) & p_mask;
+          hi[i / 4] = (h[0] | (h[1] << 16)) & p_mask[c0 / 8];
+          lo[i / 4] = (d[0] | (d[1] << 16)) & p_mask[c0 / 8];
         }
         st_shared_v4(prow + swz_row<Sh::kRowP>(kl * Sh::kRowP + 2 * (r0 + c0)), hi[0], hi[1], lo[0],
                      lo[1]);
@@ -765,15 +825,18 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     named_bar_sync(5, 32 * Sh::kWarps);
     const bool failed = *abort_v != 0;
     constexpr float kUnscale = 1.f / 128.f;  // P carried 2^7
-    for (int r = sw; r < rows; r += Sh::kWarps) {
+    for (int r = sw; r < R; r += Sh::kWarps) {
+      if (row_sm[r] == 0xffffffffu) continue;
+      // (head hl's O lies in rows hl D .. of O^T)
+      const int at = r * 128 + min(head_of(r) * D + lane * 4, 124);
       const float4 ls = *reinterpret_cast<const float4*>(red[0][r]);
       float m = m_end[0][r], lr = (ls.x + ls.y) + (ls.z + ls.w);
-      float4 o = *reinterpret_cast<const float4*>(part + r * 128 + lane * 4);
+      float4 o = *reinterpret_cast<const float4*>(part + at);
       if constexpr (NT == 2) {  // the merge of two partials
         const float4 l2 = *reinterpret_cast<const float4*>(red[1][r]);
         const float m1 = m_end[1][r], M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
         const float a0 = ex2_approx(m - ref), a1 = ex2_approx(m1 - ref);
-        const float4 o1 = *reinterpret_cast<const float4*>(part + (R + r) * 128 + lane * 4);
+        const float4 o1 = *reinterpret_cast<const float4*>(part + R * 128 + at);
         lr = lr * a0 + ((l2.x + l2.y) + (l2.z + l2.w)) * a1;
         o = make_float4(o.x * a0 + o1.x * a1, o.y * a0 + o1.y * a1, o.z * a0 + o1.z * a1,
                         o.w * a0 + o1.w * a1);
@@ -825,7 +888,7 @@ cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
   DecodeBlockParams p = p_in;
   p.dec.prefetch_tiles = prefetch ? 3 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.dec.n_split, p.dec.H_kv, p.dec.B);
+  cfg.gridDim = dim3(p.dec.n_split, (p.dec.H_kv + p.heads - 1) / p.heads, p.dec.B);
   cfg.blockDim = dim3(Sh::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -843,7 +906,8 @@ cudaError_t launch_fb_r(const DecodeBlockParams& p, const CUtensorMap& tm_k,
                         const CUtensorMap& tm_v, int sms, cudaStream_t stream) {
   // One CTA per SM at most: a deep ring.  More CTAs than SMs: two shallow rings
   // on each SM, where they fit.
-  const bool one_wave = (long long)p.dec.n_split * p.dec.H_kv * p.dec.B <= sms;
+  const int groups = (p.dec.H_kv + p.heads - 1) / p.heads;
+  const bool one_wave = (long long)p.dec.n_split * groups * p.dec.B <= sms;
   const bool paged = p.dec.block_table != nullptr;
   if (one_wave)
     return paged ? launch_fb<Deep, true>(p, tm_k, tm_v, true, stream)
@@ -856,12 +920,12 @@ cudaError_t launch_fb_r(const DecodeBlockParams& p, const CUtensorMap& tm_k,
 
 cudaError_t launch_decode_fp8_block(const DecodeBlockParams& p, const CUtensorMap& tm_k,
                                     const CUtensorMap& tm_v, int sms, cudaStream_t stream) {
-  const int rows = p.dec.T_q * p.dec.G;
+  const int rows = p.heads == 1 ? p.dec.T_q * p.dec.G : p.heads * p.head_rows;
   if (rows < 1 || rows > 64 || p.dec.chunk % kFbKeys != 0) return cudaErrorInvalidValue;
   if (rows <= 8)
     return launch_fb_r<FbShape<8, 6, 2, 1>, FbShape<8, 3, 2, 1>>(p, tm_k, tm_v, sms, stream);
   if (rows <= 16)
-    return launch_fb_r<FbShape<16, 6, 2, 1>, FbShape<16, 3, 2, 1>>(p, tm_k, tm_v, sms, stream);
+    return launch_fb_r<FbShape<16, 6, 2, 2>, FbShape<16, 6, 2, 2>>(p, tm_k, tm_v, sms, stream);
   if (rows <= 32)
     return launch_fb_r<FbShape<32, 5, 2, 2>, FbShape<32, 5, 2, 2>>(p, tm_k, tm_v, sms, stream);
   return launch_fb_r<FbShape<64, 5, 1, 4>, FbShape<64, 5, 1, 4>>(p, tm_k, tm_v, sms, stream);

@@ -105,6 +105,10 @@ struct DecodeBlockParams {
   DecodeParams dec;
   const float *k_scale, *v_scale;
   int block_log2, page_log2, per_blk;
+  // KV heads of a CTA: 1 (the map's middle dimension is the head), or 128 / d
+  // packed ones (the map's rows are whole tokens, 128 bytes wide); then each has
+  // head_rows = T_q * G rounded up to 8 of the CTA's query rows.
+  int heads, head_rows;
 };
 
 // Byte offset of the O partials in a chunk-split prefill workspace.
@@ -145,9 +149,9 @@ cudaError_t launch_prefill_merge(const PrefillParams& p, cudaStream_t stream);
 cudaError_t prefill_trace_clear();
 cudaError_t launch_kv_append(const KvBlockParams& p, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvBlockParams& p, cudaStream_t stream);
-// Decode of T_q * G (<= 64) query rows per KV head over the block-scaled E4M3
-// cache; K/V boxes of min(page_size, 128) rows, 128 bytes wide; p.dec.chunk a
-// multiple of 128.  Same partial layout as launch_decode_split.
+// Decode of T_q * G (<= 64) query rows per KV head (all packed heads together
+// <= 64) over the block-scaled E4M3 cache; K/V boxes of min(page_size, 128) rows,
+// 128 bytes wide; p.dec.chunk a multiple of 128.  Same partial layout as launch_decode_split.
 cudaError_t launch_decode_fp8_block(const DecodeBlockParams& p, const CUtensorMap& tm_k,
                                     const CUtensorMap& tm_v, int sms, cudaStream_t stream);
 cudaError_t launch_wait_selftest(unsigned* err, uint64_t limit_ns, cudaStream_t stream);

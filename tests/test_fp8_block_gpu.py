@@ -517,3 +517,33 @@ def test_helpers_refuse():
     with pytest.raises(g.GQAError):
         g.kv_read_fp8_block(*args, k_out=torch.empty(2, 4, 2, 64, device=DEV))
     g.kv_append_fp8_block(k[:, :0], v[:, :0], *args)  # no rows: nothing to do
+
+
+# ------------------------------------------------- heads that share a tile ---
+@pytest.mark.parametrize("d,H", [(64, 2), (64, 5), (32, 3), (32, 4), (32, 6)])
+@pytest.mark.parametrize("T_q,G", [(1, 1), (1, 6), (3, 5), (1, 16), (2, 16)])
+@pytest.mark.parametrize("page", [0, 32])
+def test_decode_grids_that_fill_the_gpu(d, H, T_q, G, page):
+    """With d = 32 and 64 and a grid as large as the GPU, a CTA takes the heads that share 128
+    bytes of a row (also where the last group is not full, or their rows do not fit)."""
+    c = Cache(2, 900, H, d, 16, page, seed=d + H + T_q + G)
+    k, v = c.rows(900)
+    c.append(k, v, [900, 130 + T_q])
+    check_decode(c, T_q, G, 90, what=f"d={d} H={H} T_q={T_q} G={G}")
+
+
+def test_decode_heads_that_share_a_tile_stay_apart():
+    """NaN in one head's keys and values leaves the neighbours in the tile finite."""
+    c = Cache(1, 400, 4, 32, 16, 0, seed=61)
+    k, v = c.rows(400)
+    k[0, 7, 1, 3] = float("nan")
+    v[0, 300, 2, 5] = float("inf")
+    c.append(k, v, [400])
+    q = torch.randn(1, 1, 12, 32, generator=c.gen).to(torch.bfloat16)
+    out, lse = g.decode_fp8_block(q.to(DEV), *c.args(), c.lens(), 16, n_split=200)
+    nan = out[0, 0].isnan().cpu()
+    want = torch.zeros(12, 32, dtype=torch.bool)
+    want[3:6] = True
+    want[6:9, 5] = True
+    assert torch.equal(nan, want)
+    assert lse[0, 0].isnan().cpu().tolist() == [False] * 3 + [True] * 3 + [False] * 6
