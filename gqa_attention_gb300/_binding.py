@@ -62,7 +62,7 @@ SIGNATURES = {
                                        _P, _P, _P, _P]),
     "gqa_attn_decode_paged_fp8_block": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
                                              _I, _I, _F, _I, _P, _P, _P, _P]),
-    "gqa_attn_decode_fp8_block_default_splits": (_I, [_I, _I, _I]),
+    "gqa_attn_decode_fp8_block_default_splits": (_I, [_I, _I, _I, _I, _I]),
     "gqa_last_device_error": (_I, [_P]),
     "gqa_trace_clear": (_I, []),
     "gqa_trace_read": (_I, [_P, _SZ]),
@@ -122,15 +122,6 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
-
-
-def _keep(tensor, stream):
-    """Keeps a temporary's memory from reuse until `stream` (given by the caller) is past it."""
-    import torch
-
-    if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
-        tensor.record_stream(s)
 
 
 # ------------------------------------------------------- same-name entries --
@@ -316,8 +307,8 @@ def gqa_attn_decode_paged_fp8_block(q, k_pool, v_pool, k_scale, v_scale, block_t
         n_split, _ptr(workspace), _ptr(out), _ptr(lse), _stream(stream))
 
 
-def gqa_attn_decode_fp8_block_default_splits(B, H_kv, S_max) -> int:
-    return load().gqa_attn_decode_fp8_block_default_splits(B, H_kv, S_max)
+def gqa_attn_decode_fp8_block_default_splits(B, T_q, H_q, H_kv, S_max) -> int:
+    return load().gqa_attn_decode_fp8_block_default_splits(B, T_q, H_q, H_kv, S_max)
 
 
 def gqa_trace_clear() -> int:
@@ -539,54 +530,26 @@ def decode_fp8(q, k8, v8, k_scale, v_scale, seq_lens, scale=None, n_split=None, 
     return out, lse
 
 
-def _refuse(what, why):
-    raise GQAError(GQA_ERR_INVALID_ARG, f"{what}: {why}")
+_ext = None
 
 
-def _raw_stream(device: int, stream) -> int:
-    """Handle of `stream`, by default the current stream of CUDA device `device` (without
-    the stream object that torch.cuda.current_stream() builds: 0.1 instead of 2.9 us)."""
-    if stream is None:
-        import torch
+def _torch_binding():
+    """The C++ module that checks and passes on the tensors of the block-scaled cache's helpers
+    (the same checks in Python take longer than most of their kernels), and the handle of the
+    loaded library, which it calls."""
+    global _ext
+    lib = load()
+    if _ext is None:
+        import torch  # noqa: F401  (its libraries first)
 
-        return torch._C._cuda_getCurrentRawStream(device)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        if not os.path.exists(os.path.join(PKG, "_torch_binding.so")):
+            from . import build as _build  # compile in-tree; raises if the compiler fails
+            _build.build_torch_binding()
+        from . import _torch_binding as ext
 
-
-def _other_device(device: int) -> bool:
-    import torch
-
-    return device != torch.cuda.current_device()
-
-
-def _block_cache(k8, v8, k_scale, v_scale, seq_lens, block, block_table, what):
-    """Checks the tensors of a block-scaled E4M3 cache; returns its device and
-    (units, tokens per unit, H_kv, d, B, max_blocks)."""
-    import torch
-
-    dev, shape = k8.get_device(), k8.shape
-    if (dev < 0 or len(shape) != 4 or k8.dtype is not torch.uint8 or v8.dtype is not torch.uint8
-            or v8.shape != shape or v8.get_device() != dev or not k8.is_contiguous()
-            or not v8.is_contiguous()):
-        _refuse(what, "the codes are dense uint8 [B, S_max, H_kv, d] or [num_pages, page_size, H_kv,"
-                      " d], K and V on one CUDA device")
-    units, per, H_kv, d = shape
-    sshape = (units, -(-per // block) if block > 0 else 0, H_kv)
-    if (k_scale.shape != sshape or v_scale.shape != sshape or k_scale.dtype is not torch.float32
-            or v_scale.dtype is not torch.float32 or k_scale.get_device() != dev
-            or v_scale.get_device() != dev or not k_scale.is_contiguous()
-            or not v_scale.is_contiguous()):
-        _refuse(what, f"the scales are dense float32 {sshape} on the codes' device")
-    B, max_blocks = units, 0
-    if block_table is not None:
-        if (block_table.dim() != 2 or block_table.dtype is not torch.int32
-                or block_table.get_device() != dev or not block_table.is_contiguous()):
-            _refuse(what, "block_table is dense int32 [B, max_blocks] on the codes' device")
-        B, max_blocks = block_table.shape
-    if (seq_lens.shape != (B,) or seq_lens.dtype is not torch.int32 or seq_lens.get_device() != dev
-            or not seq_lens.is_contiguous()):
-        _refuse(what, "seq_lens is dense int32 [B] on the codes' device")
-    return dev, units, per, H_kv, d, B, max_blocks
+        ext.init(GQAError)
+        _ext = ext
+    return _ext, lib._handle
 
 
 def kv_cache_fp8_block(units, per, H_kv, d, block, device="cuda"):
@@ -609,84 +572,18 @@ def kv_append_fp8_block(k_new, v_new, k8, v8, k_scale, v_scale, seq_lens, block,
     """Quantise new tokens (bf16 [B, T, H_kv, d]; rows may be slices of wider ones) into a
     block-scaled E4M3 cache; seq_lens are the lengths after the call, n_new [B] the valid rows
     of each sequence (None: all T).  Paged when block_table is given."""
-    import torch
-
-    what = "kv_append_fp8_block"
-    dev, units, per, H_kv, d, B, max_blocks = _block_cache(k8, v8, k_scale, v_scale, seq_lens,
-                                                           block, block_table, what)
-    if _other_device(dev):
-        with torch.cuda.device(dev):
-            return kv_append_fp8_block(k_new, v_new, k8, v8, k_scale, v_scale, seq_lens, block,
-                                       n_new, block_table, stream)
-    shape = k_new.shape
-    if (len(shape) != 4 or shape[0] != B or shape[2] != H_kv or shape[3] != d
-            or v_new.shape != shape or k_new.dtype is not torch.bfloat16
-            or v_new.dtype is not torch.bfloat16 or k_new.get_device() != dev
-            or v_new.get_device() != dev):
-        _refuse(what, "the new rows are bfloat16 [B, T, H_kv, d] on the cache's device")
-    if n_new is not None and (n_new.shape != (B,) or n_new.dtype is not torch.int32
-                              or n_new.get_device() != dev or not n_new.is_contiguous()):
-        _refuse(what, "n_new is dense int32 [B] on the cache's device")
-    T = shape[1]
-    if T == 0:
-        return
-    strides = k_new.stride()
-    # the stride between tokens; a dimension of size 1 has none of its own
-    step = strides[1] if T > 1 else strides[0] if B > 1 else H_kv * d
-    for s in (strides, v_new.stride()):
-        if (s[3] != 1 or (s[2] != d and H_kv > 1) or (s[1] != step and T > 1)
-                or (s[0] != T * step and B > 1)):
-            _refuse(what, "the rows of k_new and v_new are H_kv * d dense elements, one stride apart")
-    if block_table is None:
-        st = load().gqa_kv_append_fp8_block(
-            k_new.data_ptr(), v_new.data_ptr(), step, None if n_new is None else n_new.data_ptr(),
-            seq_lens.data_ptr(), B, T, per, H_kv, d, block, k8.data_ptr(), v8.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), _raw_stream(dev, stream))
-    else:
-        st = load().gqa_kv_append_paged_fp8_block(
-            k_new.data_ptr(), v_new.data_ptr(), step, None if n_new is None else n_new.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), B, T, units, per, max_blocks, H_kv, d,
-            block, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            _raw_stream(dev, stream))
-    _check(st, what)
+    ext, lib = _torch_binding()
+    ext.append(lib, k8, v8, k_scale, v_scale, seq_lens, block, block_table, stream, k_new, v_new,
+               n_new)
 
 
 def kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, start=0, k_out=None, v_out=None,
                       block_table=None, stream=None):
     """Tokens start.. of a block-scaled E4M3 cache as bf16 (k, v) [B, S_out, H_kv, d]; rows past
     a sequence's end keep what k_out and v_out hold (new outputs, S_out = S_max - start: zeros)."""
-    import torch
-
-    what = "kv_read_fp8_block"
-    dev, units, per, H_kv, d, B, max_blocks = _block_cache(k8, v8, k_scale, v_scale, seq_lens,
-                                                           block, block_table, what)
-    if _other_device(dev):
-        with torch.cuda.device(dev):
-            return kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, start, k_out, v_out,
-                                     block_table, stream)
-    if k_out is None:
-        S_max = per if block_table is None else max_blocks * per
-        k_out = torch.zeros((B, S_max - start, H_kv, d), dtype=torch.bfloat16, device=k8.device)
-    if v_out is None:
-        v_out = torch.zeros(k_out.shape, dtype=torch.bfloat16, device=k8.device)
-    shape = k_out.shape
-    if (len(shape) != 4 or shape[0] != B or shape[2] != H_kv or shape[3] != d
-            or v_out.shape != shape or k_out.dtype is not torch.bfloat16
-            or v_out.dtype is not torch.bfloat16 or k_out.get_device() != dev
-            or v_out.get_device() != dev or not k_out.is_contiguous() or not v_out.is_contiguous()):
-        _refuse(what, "k_out and v_out are dense bfloat16 [B, S_out, H_kv, d] on the cache's device")
-    if block_table is None:
-        st = load().gqa_kv_read_fp8_block(
-            k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            seq_lens.data_ptr(), B, per, H_kv, d, block, start, shape[1], k_out.data_ptr(),
-            v_out.data_ptr(), _raw_stream(dev, stream))
-    else:
-        st = load().gqa_kv_read_paged_fp8_block(
-            k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), B, units, per, max_blocks, H_kv, d, block,
-            start, shape[1], k_out.data_ptr(), v_out.data_ptr(), _raw_stream(dev, stream))
-    _check(st, what)
-    return k_out, v_out
+    ext, lib = _torch_binding()
+    return ext.read(lib, k8, v8, k_scale, v_scale, seq_lens, block, block_table, stream, start,
+                    k_out, v_out)
 
 
 def decode_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=None, n_split=None,
@@ -695,59 +592,9 @@ def decode_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=None, n
 
     q [B, H_q, d] (out [B, H_q, d], lse [B, H_q]) or, for the last T_q positions of each
     sequence, q [B, T_q, H_q, d] (out [B, T_q, H_q, d], lse [B, T_q, H_q])."""
-    import torch
-
-    what = "decode_fp8_block"
-    dev, units, per, H_kv, d, B, max_blocks = _block_cache(k8, v8, k_scale, v_scale, seq_lens,
-                                                           block, block_table, what)
-    if _other_device(dev):
-        with torch.cuda.device(dev):
-            return decode_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale, n_split,
-                                    workspace, out, lse, stream, block_table)
-    shape = q.shape
-    multi = len(shape) == 4
-    if (not (multi or len(shape) == 3) or shape[0] != B or shape[-1] != d
-            or q.dtype is not torch.bfloat16 or q.get_device() != dev or not q.is_contiguous()):
-        _refuse(what, "q is dense bfloat16 [B, H_q, d] or [B, T_q, H_q, d] on the cache's device")
-    T_q, H_q = (shape[1] if multi else 1), shape[-2]
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.empty_like(q)
-    elif (out.shape != shape or out.dtype is not torch.bfloat16 or out.get_device() != dev
-          or not out.is_contiguous()):
-        _refuse(what, "out is dense bfloat16, of q's shape, on the cache's device")
-    if lse is None:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    elif (lse.shape != shape[:-1] or lse.dtype is not torch.float32 or lse.get_device() != dev
-          or not lse.is_contiguous()):
-        _refuse(what, "lse is dense float32, of q's shape without d, on the cache's device")
-    lib = load()
-    S_max = per if block_table is None else max_blocks * per
-    if n_split is None:
-        n_split = lib.gqa_attn_decode_fp8_block_default_splits(B, H_kv, S_max)
-    ws = None
-    if n_split > 1:
-        need = lib.gqa_attn_decode_workspace_bytes(B * T_q, H_q, d, n_split)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            _keep(workspace, stream)
-        elif (workspace.get_device() != dev or not workspace.is_contiguous()
-              or workspace.numel() * workspace.element_size() < need):
-            _refuse(what, f"the workspace is {need} dense bytes on the cache's device")
-        ws = workspace.data_ptr()
-    if block_table is None:
-        st = lib.gqa_attn_decode_fp8_block(
-            q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            seq_lens.data_ptr(), B, T_q, per, H_q, H_kv, d, block, scale, n_split, ws,
-            out.data_ptr(), lse.data_ptr(), _raw_stream(dev, stream))
-    else:
-        st = lib.gqa_attn_decode_paged_fp8_block(
-            q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), B, T_q, units, per, max_blocks, H_q, H_kv,
-            d, block, scale, n_split, ws, out.data_ptr(), lse.data_ptr(), _raw_stream(dev, stream))
-    _check(st, what)
-    return out, lse
+    ext, lib = _torch_binding()
+    return ext.decode(lib, k8, v8, k_scale, v_scale, seq_lens, block, block_table, stream, q, scale,
+                      n_split, workspace, out, lse)
 
 
 def prefill_chunk_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=None, window=-1,
@@ -756,15 +603,25 @@ def prefill_chunk_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=
     block-scaled E4M3 cache: the cache is read back as bf16 and prefill_chunk runs on it."""
     import torch
 
-    dev, _, per, H_kv, d, B, max_blocks = _block_cache(k8, v8, k_scale, v_scale, seq_lens, block,
-                                                       block_table, "prefill_chunk_fp8_block")
-    with torch.cuda.device(dev):
-        S_max = per if block_table is None else max_blocks * per
-        k = torch.empty((B, S_max, H_kv, d), dtype=torch.bfloat16, device=k8.device)
+    if q.dim() != 4 or q.dtype is not torch.bfloat16 or q.device != k8.device \
+            or not q.is_contiguous() or not q.is_cuda:
+        raise GQAError(GQA_ERR_INVALID_ARG, "prefill_chunk_fp8_block: q is dense bfloat16 "
+                       "[B, T_q, H_q, d] on the cache's device")
+    with torch.cuda.device(q.device):
+        B, per, H_kv, d = k8.shape
+        if block_table is not None:
+            B, per = block_table.shape[0], block_table.shape[1] * per
+        k = torch.empty((B, per, H_kv, d), dtype=torch.bfloat16, device=q.device)
         v = torch.empty_like(k)
-        _keep(k, stream)
-        _keep(v, stream)
+        if stream is not None:  # the temporaries outlive the call on a stream of the caller's
+            s = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(stream)
+            k.record_stream(s)
+            v.record_stream(s)
         kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, 0, k, v, block_table, stream)
+        if q.shape[0] != B or q.shape[3] != d:
+            raise GQAError(GQA_ERR_INVALID_ARG, "prefill_chunk_fp8_block: q's B or d is not the "
+                           "cache's")
         return prefill_chunk(q, k, v, seq_lens, scale, window, out, lse, stream)
 
 

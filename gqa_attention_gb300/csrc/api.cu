@@ -808,8 +808,22 @@ gqa_status gqa_attn_decode_paged_fp8_block(const void* q, const void* k_pool, co
   return run_decode_fp8_block(c, q, T_q, H_q, scale, n_split, workspace, out, lse, stream);
 }
 
-int gqa_attn_decode_fp8_block_default_splits(int B, int H_kv, int S_max) {
-  return gqa_attn_decode_default_splits(B, H_kv, S_max, -1);
+int gqa_attn_decode_fp8_block_default_splits(int B, int T_q, int H_q, int H_kv, int S_max) {
+  if (B < 1 || T_q < 1 || H_q < 1 || H_kv < 1 || S_max < 1 || H_q % H_kv != 0) return 1;
+  if (S_max <= 1024) return 1;  // (as gqa_attn_decode_default_splits: one launch)
+  const long long groups = (long long)B * H_kv;
+  long long n = num_sms_current_device() / groups;
+  // Up to 16 query rows a split streams at the HBM rate, and a multiple of four
+  // splits measured best (Llama3-70B heads, 16 against 19 splits: 15.6 / 16.2 us at
+  // 32K, 8.5 / 9.1 at 8K; two sequences, 8 against 9: 24.5 / 25.5); more rows are
+  // bound by the softmax and want every SM (8 tokens: 40.3 / 37.6 us).
+  if (T_q * (H_q / H_kv) <= 16 && n > 4) n -= n % 4;
+  const long long most = ((long long)S_max + 255) / 256;  // at least two tiles each
+  const long long fill = ((long long)S_max + 8191) / 8192;
+  if (n > most) n = most;
+  if (n < fill) n = fill;
+  if (n < 1) n = 1;
+  return (int)n;
 }
 
 gqa_status gqa_attn_decode_combine(const void* workspace, int B, int H_q, int d, int n_split,

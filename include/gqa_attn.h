@@ -540,8 +540,10 @@ gqa_status gqa_attn_decode_paged_fp8_block(const void* q, const void* k_pool, co
                                            float scale, int n_split, void* workspace, void* out,
                                            float* lse, gqa_stream_t stream);
 
-/* Split count for gqa_attn_decode_fp8_block on the current device.  Returns >= 1. */
-int gqa_attn_decode_fp8_block_default_splits(int B, int H_kv, int S_max);
+/* Split count for gqa_attn_decode_fp8_block on the current device: 1 for S_max <=
+ * 1024, otherwise at most one CTA per SM, with splits of at least 256 tokens and
+ * at most 8192.  Returns >= 1 (1 for invalid input). */
+int gqa_attn_decode_fp8_block_default_splits(int B, int T_q, int H_q, int H_kv, int S_max);
 
 /* ------------------------------------------------------------------------
  * Decode with the merge inside thread-block clusters

@@ -118,9 +118,12 @@ def test_decode_refusals(paged):
 
 
 def test_default_splits_cover_the_cache():
-    for B, H, S in [(1, 8, 32768), (1, 2, 1024), (64, 4, 4001), (8, 8, 131072)]:
-        n = g.gqa_attn_decode_fp8_block_default_splits(B, H, S)
-        assert 1 <= n <= max(1, -(-S // 128))
+    for B, T_q, H, S in [(1, 1, 8, 32768), (1, 8, 8, 32768), (1, 1, 2, 1024), (64, 1, 4, 4001),
+                         (8, 1, 8, 131072)]:
+        n = g.gqa_attn_decode_fp8_block_default_splits(B, T_q, 8 * H, H, S)
+        assert -(-S // 8192) <= n <= max(1, -(-S // 256))
+    assert g.gqa_attn_decode_fp8_block_default_splits(1, 1, 9, 8, 4096) == 1
+    assert g.gqa_attn_decode_fp8_block_default_splits(0, 1, 8, 8, 4096) == 1
 
 
 def test_helpers_refuse_cpu_tensors_and_wrong_layouts():
