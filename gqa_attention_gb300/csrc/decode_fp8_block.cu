@@ -50,7 +50,7 @@ constexpr uint32_t kFbTile = 128u * 128u;   // 128 rows of 128 bytes
 constexpr float kLoStep = 1.f / 32.f;       // weight of the low term
 constexpr float kPScaleLog2 = 7.f;          // P is held times 2^7
 constexpr float kPMaxLog2 = 8.f;            // and must not pass 2^8
-constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100
+constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100: smaller ones count as zero
 
 // Compile-time shape of one variant.  R query rows (padded), NS slots per ring,
 // NT streams of tiles (stream s takes tiles s, s + NT, ..) and NG groups of rows:
@@ -230,6 +230,25 @@ __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// The terms of a block's scales: the key scale; log2 of the value scale and its
+// inverse (value scales below 2^-100 count as zero: a log2 of -100, and the weights'
+// bytes masked away; negative ones are NaN).
+struct __align__(16) ScaleTerms {
+  float ks, lv, ivs;
+  uint32_t p_mask;
+};
+__device__ __forceinline__ ScaleTerms scale_terms(float ks, float vs) {
+  ScaleTerms s;
+  const bool live = vs >= kMinVScale;
+  s.ks = ks;
+  float lg;  // (to 2^-22; exact for powers of two)
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(vs));
+  s.lv = live ? lg : (vs >= 0.f ? -100.f : NAN);
+  s.ivs = ex2_approx(-s.lv);  // 1 / vs, of the same logarithm
+  s.p_mask = vs >= 0.f && !live ? 0u : 0xffffffffu;
+  return s;
+}
+
 template <typename Sh, bool PAGED>
 __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     gqa_decode_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -250,6 +269,10 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   // each softmax warp's own copy: its rows' changes of reference and factors
   __shared__ __align__(16) float move_sm[Sh::kWarps][RW], alpha_sm[Sh::kWarps][RW];
   __shared__ float m_end[NT][R];                // final references
+  // what the softmax needs of the scales, a ring by tile, head and block of tokens of
+  // the tile (the S buffers' barriers cover it)
+  constexpr int kScRing = 128;
+  __shared__ ScaleTerms sc_sm[kScRing];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -297,7 +320,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       mbar_init(smem_u32(&v_empty[s]), 1);
     }
     for (int s = 0; s < NSB; ++s) {
-      mbar_init(smem_u32(&s_full[s]), 1);
+      mbar_init(smem_u32(&s_full[s]), 2);  // the product, and the scales' terms
       mbar_init(smem_u32(&s_empty[s]), 4 * NG);
     }
     mbar_init(smem_u32(&q_ready), Sh::kWarps);
@@ -484,6 +507,33 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     const int ksteps = D / 32;  // of a head: 32 columns of d each
     const uint32_t id = instr_desc_e4m3_f32(128, hc == 1 ? 2 * R : 2 * rp, false, false);
     const uint32_t id_last = instr_desc_e4m3_f32(128, 2 * (R - (hc - 1) * rp), false, false);
+    // The scales' terms of 32 / (hc nsub) tiles at a time, one block of a head per lane:
+    // lane is tile, then head, then block of the tile.  Pages are loaded two rounds
+    // ahead, scales one (a round for each tile would take this warp longer than
+    // a tile).
+    const int sub_log2 = 7 - pb.block_log2, nsub = 1 << sub_log2;
+    const int per_tile = hc << sub_log2;  // <= 32
+    const int sc_round = 32 / per_tile;
+    const int sc_tile = lane / per_tile, sc_head = lane % per_tile >> sub_log2;
+    const size_t sc_kv = min(kv0 + sc_head, p.H_kv - 1);
+    auto sc_tok = [&](int tile) {
+      return t0 + (tile + sc_tile) * kFbKeys + ((lane & (nsub - 1)) << pb.block_log2);
+    };
+    auto sc_unit = [&](int tile) -> int {  // its page (or sequence), -1 for none
+      const int tok = sc_tok(tile);
+      if (sc_tile >= sc_round || tile + sc_tile >= n || tok >= t_end) return -1;
+      if (!PAGED) return b;
+      const int pg = p.block_table[(size_t)b * p.max_blocks + (tok >> pb.page_log2)];
+      return pg >= 0 && pg < p.num_pages ? pg : -1;
+    };
+    auto sc_load = [&](int tile, int unit) -> float2 {
+      if (unit < 0) return make_float2(1.f, 1.f);
+      const int tok = sc_tok(tile), in = PAGED ? tok & (p.page_size - 1) : tok;
+      const size_t i = ((size_t)unit * pb.per_blk + (in >> pb.block_log2)) * p.H_kv + sc_kv;
+      return make_float2(pb.k_scale[i], pb.v_scale[i]);
+    };
+    float2 scales = sc_load(0, sc_unit(0));
+    int sc_u = sc_unit(sc_round), sc_left = 0;
     bool ok = wait_all(&q_ready, 0);
     for (int j = 0; ok && j < n; ++j) {
       ok = wait_all(&k_full[j % NS], (j / NS) & 1) &&
@@ -506,6 +556,18 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       }
       tc_commit(smem_u32(&s_full[j % NSB]));
       tc_commit(smem_u32(&k_empty[j % NS]));
+      if (sc_left == 0) {
+        // A round of terms into its place of the ring.  What lay there belongs to
+        // tiles before j - 3 rounds, at least NSB before j: whoever emptied S_{j - NSB}
+        // had read them.
+        if (sc_tile < sc_round) sc_sm[(j * per_tile + lane) % kScRing] = scale_terms(scales.x, scales.y);
+        scales = sc_load(j + sc_round, sc_u);
+        sc_u = sc_unit(j + 2 * sc_round);
+        sc_left = sc_round;
+        __syncwarp();
+      }
+      --sc_left;
+      if (lane == 0) mbar_arrive(smem_u32(&s_full[j % NSB]));
     }
     // Every MMA issued here has completed before tensor memory is released.
     tc_commit(smem_u32(&drain[0]));
@@ -585,35 +647,13 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&q_ready));
 
-    // Scales of this thread's key for each eight rows (one head's), loaded one tile
-    // of the stream ahead; its page, two.
+    // The scales' terms of this thread's key for each eight rows (one head's).
     constexpr int RU = RW / 8;
-    int kv_of[RU];
+    const int sub_log2 = 7 - pb.block_log2;
+    int sc_at[RU];
 #pragma unroll
-    for (int c = 0; c < RU; ++c) kv_of[c] = min(kv0 + head_of(r0 + 8 * c), p.H_kv - 1);
-    auto page_of = [&](int j) -> int {
-      const int tok = t0 + j * kFbKeys + kl;
-      if (j >= n || tok >= t_end) return -1;
-      if (!PAGED) return b;
-      const int pg = p.block_table[(size_t)b * p.max_blocks + (tok >> pb.page_log2)];
-      return pg >= 0 && pg < p.num_pages ? pg : -1;
-    };
-    float ks[RU], vs[RU];
-    auto load_scales = [&](int j, int unit) {
-#pragma unroll
-      for (int c = 0; c < RU; ++c) ks[c] = vs[c] = 1.f;
-      if (unit < 0) return;
-      const int tok = t0 + j * kFbKeys + kl;
-      const int at = PAGED ? tok & (p.page_size - 1) : tok;
-      const size_t i = ((size_t)unit * pb.per_blk + (at >> pb.block_log2)) * p.H_kv;
-#pragma unroll
-      for (int c = 0; c < RU; ++c) {
-        ks[c] = pb.k_scale[i + kv_of[c]];
-        vs[c] = pb.v_scale[i + kv_of[c]];
-      }
-    };
-    int unit1 = page_of(st + NT);
-    load_scales(st, page_of(st));
+    for (int c = 0; c < RU; ++c)
+      sc_at[c] = (head_of(r0 + 8 * c) << sub_log2) + (kl >> pb.block_log2);
     float acc[RW], l[RW], off[RW];  // off: 7 less the row's reference (0 while it has none)
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
@@ -647,20 +687,13 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
 
     int turn = 0;  // tiles of this stream so far
     for (int j = st; j < n; j += NT, ++turn) {
-      // log2 vs and 1 / vs; scales below 2^-100 count as zero, negative ones are NaN
-      float lv[RU], ivs[RU];
-      uint32_t p_mask[RU];
-#pragma unroll
-      for (int c = 0; c < RU; ++c) {
-        const bool v_live = vs[c] >= kMinVScale;
-        lv[c] = v_live ? __log2f(vs[c]) : (vs[c] >= 0.f ? -100.f : NAN);
-        ivs[c] = v_live ? __frcp_rn(vs[c]) : 1.f / kMinVScale;
-        p_mask[c] = vs[c] >= 0.f && !v_live ? 0u : 0xffffffffu;
-      }
       const int key = t0 + j * kFbKeys + kl;
       // (a warp whose wait failed keeps to the barriers of the others)
       alive = alive && wait_all(&s_full[j % NSB], (j / NSB) & 1);
       tc_fence_after();
+      ScaleTerms sc[RU];
+#pragma unroll
+      for (int c = 0; c < RU; ++c) sc[c] = sc_sm[((j * hc << sub_log2) + sc_at[c]) % kScRing];
       float y[RW];  // exponents of P: y - m + 7
       float top = -INFINITY;
       {
@@ -680,8 +713,8 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
               float a0, a1, b0, b1, d0, d1;
               ffma2(a0, a1, __uint_as_float(s[8 + e]), __uint_as_float(s[9 + e]), kLoStep, kLoStep,
                     __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-              fmul2(b0, b1, c[u], c[u + 1], ks[c0 / 8], ks[c0 / 8]);
-              fadd2(d0, d1, off[r], off[r + 1], lv[c0 / 8], lv[c0 / 8]);
+              fmul2(b0, b1, c[u], c[u + 1], sc[c0 / 8].ks, sc[c0 / 8].ks);
+              fadd2(d0, d1, off[r], off[r + 1], sc[c0 / 8].lv, sc[c0 / 8].lv);
               ffma2(y[r], y[r + 1], a0, a1, b0, b1, d0, d1);
             }
           }
@@ -697,9 +730,6 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       tc_fence_before();
       __syncwarp();
       if (alive && lane == 0) mbar_arrive(smem_u32(&s_empty[j % NSB]));
-      // (into the registers just read for the last time)
-      load_scales(j + NT, unit1);
-      unit1 = page_of(j + 2 * NT);
       const bool update = named_bar_any(1 + gi, 128, unset || top > kPMaxLog2);
       if (update) {
         // The rows' maxima over the 128 keys become references where they are
@@ -757,7 +787,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
           const int r = c0 + i;
           const float e0 = ex2_approx(y[r]), e1 = ex2_approx(y[r + 1]);
           const float e2 = ex2_approx(y[r + 2]), e3 = ex2_approx(y[r + 3]);
-          const float iv = ivs[c0 / 8];
+          const float iv = sc[c0 / 8].ivs;
           ffma2(l[r], l[r + 1], e0, e1, iv, iv, l[r], l[r + 1]);
           ffma2(l[r + 2], l[r + 3], e2, e3, iv, iv, l[r + 2], l[r + 3]);
           uint32_t h[2], d[2];
@@ -771,8 +801,8 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
                                       __float2half2_rn(32.f));
             d[u] = pack_e4m3x2(*reinterpret_cast<const uint32_t*>(&q));
           }
-          hi[i / 4] = (h[0] | (h[1] << 16)) & p_mask[c0 / 8];
-          lo[i / 4] = (d[0] | (d[1] << 16)) & p_mask[c0 / 8];
+          hi[i / 4] = (h[0] | (h[1] << 16)) & sc[c0 / 8].p_mask;
+          lo[i / 4] = (d[0] | (d[1] << 16)) & sc[c0 / 8].p_mask;
         }
         st_shared_v4(prow + swz_row<Sh::kRowP>(kl * Sh::kRowP + 2 * (r0 + c0)), hi[0], hi[1], lo[0],
                      lo[1]);
@@ -798,7 +828,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     if (turn > 0) alive = alive && wait_all(&o_full[st], (turn - 1) & 1);
     bool page_ok = true;
     if (PAGED && alive) {
-      // (a bad index is recorded before the arrive on the last V tile)
+      // (a bad index is recorded before the barrier of the last V tile is armed)
       if (wait_all(&v_full[(n - 1) % NS], ((n - 1) / NS) & 1))
         page_ok = *reinterpret_cast<volatile int*>(&bad_page) == 0;
       else
