@@ -33,9 +33,7 @@
 // costs one barrier that ORs that condition, and the row maxima are worked out
 // only when it holds.  The merge of the partials holds for any reference.
 //
-// Each P V starts a fresh accumulator that the softmax threads (now thread = row
-// d of O^T) add to fp32 registers, rescaled when m moved: no rescaling pass
-// through tensor memory, and the sum over tiles is fp32.
+// O^T stays in tensor memory and is rescaled there when m moves (thread = row d).
 //
 // Roles (128 + 32 kWarps threads): warps 0 and 3 TMA producers of K and V, warp 1
 // issuer of S (and tensor memory), warp 2 issuer of O, the others Q split, softmax,
@@ -59,7 +57,7 @@ template <int R_, int NS_, int NT_, int NG_>
 struct FbShape {
   static constexpr int R = R_, NS = NS_, NT = NT_, NG = NG_;
   static constexpr int RW = R / NG;                 // rows of a warp
-  static constexpr int NSB = 2 * NT;                // S buffers
+  static constexpr int NSB = R < 64 ? 2 * NT : NT;  // S buffers (tensor memory has 512 columns)
   static constexpr int kWarps = 4 * NT * NG;        // softmax warps
   static constexpr int kRowsQ = R / kWarps;         // rows of Q a warp splits
   static constexpr int kThreads = 128 + 32 * kWarps;
@@ -108,15 +106,27 @@ __device__ __forceinline__ uint32_t swz_row(uint32_t at) {
   else return swizzle<SPAN>(at);
 }
 
-__device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// Issued by one lane (the caller's): D[tmem] (+)= A[smem] * B[smem], and the arrival
+// on `bar` once everything this lane has issued is complete.
+__device__ __forceinline__ void tc_mma_f8_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
       : "memory");
+}
+__device__ __forceinline__ void tc_commit_one(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 
 // 16 consecutive 32-bit columns of this thread's lane.
@@ -128,6 +138,9 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) 
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[16]) {
+  tmem_st16(taddr, r);
 }
 // Orders later uses of registers written by tmem_ld_cols after tmem_wait_ld.
 template <int N>
@@ -268,11 +281,13 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   __shared__ __align__(16) float red[NT][R][4]; // by stream: maxima (later sums) of four warps
   // each softmax warp's own copy: its rows' changes of reference and factors
   __shared__ __align__(16) float move_sm[Sh::kWarps][RW], alpha_sm[Sh::kWarps][RW];
+  __shared__ __align__(16) float off_sm[Sh::kWarps][RW];  // 7 less each row's reference
   __shared__ float m_end[NT][R];                // final references
-  // what the softmax needs of the scales, a ring by tile, head and block of tokens of
-  // the tile (the S buffers' barriers cover it)
-  constexpr int kScRing = 128;
+  // What the softmax needs of the scales: a ring of 8 rounds of 32 terms, by tile, head
+  // and block of tokens of the tile.
+  constexpr int kScRounds = 8, kScRing = 32 * kScRounds;
   __shared__ ScaleTerms sc_sm[kScRing];
+  __shared__ __align__(8) uint64_t sc_full[kScRounds];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -320,7 +335,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       mbar_init(smem_u32(&v_empty[s]), 1);
     }
     for (int s = 0; s < NSB; ++s) {
-      mbar_init(smem_u32(&s_full[s]), 2);  // the product, and the scales' terms
+      mbar_init(smem_u32(&s_full[s]), 1);
       mbar_init(smem_u32(&s_empty[s]), 4 * NG);
     }
     mbar_init(smem_u32(&q_ready), Sh::kWarps);
@@ -328,6 +343,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       mbar_init(smem_u32(&p_ready[s]), 4 * NG);
       mbar_init(smem_u32(&o_full[s]), 1);
     }
+    for (int s = 0; s < kScRounds; ++s) mbar_init(smem_u32(&sc_full[s]), 1);
     mbar_init(smem_u32(&drain[0]), 1);
     mbar_init(smem_u32(&drain[1]), 1);
     abort_flag = 0;
@@ -429,6 +445,30 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     }
   };
 
+  // The same for the one lane that runs an issuer.
+  auto wait_one = [&](uint64_t* bar, uint32_t parity) -> bool {
+    const uint32_t addr = smem_u32(bar);
+    if (mbar_try_wait(addr, parity)) return true;
+    const uint64_t since = globaltimer_ns();
+#pragma unroll 1
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(addr, parity)) return true;
+      if (*abort_v != 0) return false;
+      if (globaltimer_ns() - since > p.wait_ns) {
+        atomicOr(p.err, kErrTimeout);
+        *abort_v = 1;
+        return false;
+      }
+    }
+  };
+  // Rounds of the scales' terms: per_tile of them belong to a tile (a power of two),
+  // so a round covers 1 << round_log2 tiles.
+  const int sub_log2 = 7 - pb.block_log2;
+  const int per_tile_log2 = sub_log2 + (hc == 1 ? 0 : hc == 2 ? 1 : 2);
+  const int round_log2 = 5 - per_tile_log2;
+
   if (warp == 0 || warp == 3) {
     // ---------------------------------------------- TMA producers of K and V --
     const bool is_k = warp == 0;
@@ -460,6 +500,31 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       return tok < t_end && in ? pg * p.page_size + (tok & (p.page_size - 1))
                                : p.num_pages * p.page_size;
     };
+    // V's producer works out the scales' terms of a round at a time, one per lane: lane
+    // is tile, then head, then block of the tile.  Pages are loaded two rounds
+    // ahead, scales one (terms of one tile at a time take a warp longer than a tile).
+    const int sc_tile = lane >> per_tile_log2;
+    const int sc_in = lane & ((1 << per_tile_log2) - 1);
+    const size_t sc_kv = min(kv0 + (sc_in >> sub_log2), p.H_kv - 1);
+    auto sc_tok = [&](int tile) {
+      return t0 + (tile + sc_tile) * kFbKeys + ((sc_in & ((1 << sub_log2) - 1)) << pb.block_log2);
+    };
+    auto sc_unit = [&](int tile) -> int {  // its page (or sequence), -1 for none
+      if (is_k || tile + sc_tile >= n) return -1;
+      const int tok = sc_tok(tile);
+      if (tok >= t_end) return -1;
+      if (!PAGED) return b;
+      const int pg = p.block_table[(size_t)b * p.max_blocks + (tok >> pb.page_log2)];
+      return pg >= 0 && pg < p.num_pages ? pg : -1;
+    };
+    auto sc_load = [&](int tile, int unit) -> float2 {
+      if (unit < 0) return make_float2(1.f, 1.f);
+      const int tok = sc_tok(tile), in = PAGED ? tok & (p.page_size - 1) : tok;
+      const size_t i = ((size_t)unit * pb.per_blk + (in >> pb.block_log2)) * p.H_kv + sc_kv;
+      return make_float2(pb.k_scale[i], pb.v_scale[i]);
+    };
+    float2 scales = sc_load(0, sc_unit(0));
+    int sc_u = sc_unit(1 << round_log2);
     const uint64_t pol = l2_policy_evict_first();  // every tile is read once
     int pages = fetch(32 / nb), rows_l = PAGED ? row_of(0, fetch(0)) : 0, at = 0, slot = 0;
     uint32_t parity = 0;  // of the slot's present use
@@ -484,6 +549,16 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
                             __shfl_sync(0xffffffffu, rows_l, at + i), pol);
       }
       issued = j + 1;
+      if (!is_k && (j & ((1 << round_log2) - 1)) == 0) {
+        // A round of terms.  What lies in its place belongs to tiles before j - 7
+        // rounds, which the softmax is done with: V's slot of tile j - NS is empty.
+        const int round = j >> round_log2;
+        sc_sm[(round % kScRounds) * 32 + lane] = scale_terms(scales.x, scales.y);
+        scales = sc_load(j + (1 << round_log2), sc_u);
+        sc_u = sc_unit(j + (2 << round_log2));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sc_full[round % kScRounds]));
+      }
       at += nb;
       if (++slot == NS) {
         slot = 0;
@@ -507,95 +582,79 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     const int ksteps = D / 32;  // of a head: 32 columns of d each
     const uint32_t id = instr_desc_e4m3_f32(128, hc == 1 ? 2 * R : 2 * rp, false, false);
     const uint32_t id_last = instr_desc_e4m3_f32(128, 2 * (R - (hc - 1) * rp), false, false);
-    // The scales' terms of 32 / (hc nsub) tiles at a time, one block of a head per lane:
-    // lane is tile, then head, then block of the tile.  Pages are loaded two rounds
-    // ahead, scales one (a round for each tile would take this warp longer than
-    // a tile).
-    const int sub_log2 = 7 - pb.block_log2, nsub = 1 << sub_log2;
-    const int per_tile = hc << sub_log2;  // <= 32
-    const int sc_round = 32 / per_tile;
-    const int sc_tile = lane / per_tile, sc_head = lane % per_tile >> sub_log2;
-    const size_t sc_kv = min(kv0 + sc_head, p.H_kv - 1);
-    auto sc_tok = [&](int tile) {
-      return t0 + (tile + sc_tile) * kFbKeys + ((lane & (nsub - 1)) << pb.block_log2);
-    };
-    auto sc_unit = [&](int tile) -> int {  // its page (or sequence), -1 for none
-      const int tok = sc_tok(tile);
-      if (sc_tile >= sc_round || tile + sc_tile >= n || tok >= t_end) return -1;
-      if (!PAGED) return b;
-      const int pg = p.block_table[(size_t)b * p.max_blocks + (tok >> pb.page_log2)];
-      return pg >= 0 && pg < p.num_pages ? pg : -1;
-    };
-    auto sc_load = [&](int tile, int unit) -> float2 {
-      if (unit < 0) return make_float2(1.f, 1.f);
-      const int tok = sc_tok(tile), in = PAGED ? tok & (p.page_size - 1) : tok;
-      const size_t i = ((size_t)unit * pb.per_blk + (in >> pb.block_log2)) * p.H_kv + sc_kv;
-      return make_float2(pb.k_scale[i], pb.v_scale[i]);
-    };
-    float2 scales = sc_load(0, sc_unit(0));
-    int sc_u = sc_unit(sc_round), sc_left = 0;
-    bool ok = wait_all(&q_ready, 0);
-    for (int j = 0; ok && j < n; ++j) {
-      ok = wait_all(&k_full[j % NS], (j / NS) & 1) &&
-           (j < NSB || wait_all(&s_empty[j % NSB], (j / NSB - 1) & 1));
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t dkj = dk + (j % NS) * (kFbTile >> 4);
-      if (hc == 1) {
+    if (elect_one()) {
+      bool ok = wait_one(&q_ready, 0);
+      int slot = 0, buf = 0;
+      uint32_t parity = 0, bparity = 0;
+      for (int j = 0; ok && j < n; ++j) {
+        ok = wait_one(&k_full[slot], parity) &&
+             (j < NSB || wait_one(&s_empty[buf], bparity ^ 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t dkj = dk + slot * (kFbTile >> 4);
+        const uint32_t ts = tmem + 2 * R * buf;
+        if (hc == 1) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (kk < ksteps)
-            tc_mma_f8_ss(tmem + 2 * R * (j % NSB), dkj + kk * 2, dq + kk * 2, id, kk > 0);
-      } else {
+          for (int kk = 0; kk < 4; ++kk)
+            if (kk < ksteps) tc_mma_f8_one(ts, dkj + kk * 2, dq + kk * 2, id, kk > 0);
+        } else {
 #pragma unroll 1
-        for (int hl = 0; hl < hc; ++hl)
-          for (int kk = 0; kk < ksteps; ++kk)
-            tc_mma_f8_ss(tmem + 2 * R * (j % NSB) + hl * 2 * rp, dkj + (hl * ksteps + kk) * 2,
-                         dq + hl * (2 * rp * 128 >> 4) + kk * 2, hl == hc - 1 ? id_last : id,
-                         kk > 0);
+          for (int hl = 0; hl < hc; ++hl)
+            for (int kk = 0; kk < ksteps; ++kk)
+              tc_mma_f8_one(ts + hl * 2 * rp, dkj + (hl * ksteps + kk) * 2,
+                            dq + hl * (2 * rp * 128 >> 4) + kk * 2, hl == hc - 1 ? id_last : id,
+                            kk > 0);
+        }
+        tc_commit_one(smem_u32(&s_full[buf]));
+        tc_commit_one(smem_u32(&k_empty[slot]));
+        if (++slot == NS) {
+          slot = 0;
+          parity ^= 1;
+        }
+        if (++buf == NSB) {
+          buf = 0;
+          bparity ^= 1;
+        }
       }
-      tc_commit(smem_u32(&s_full[j % NSB]));
-      tc_commit(smem_u32(&k_empty[j % NS]));
-      if (sc_left == 0) {
-        // A round of terms into its place of the ring.  What lay there belongs to
-        // tiles before j - 3 rounds, at least NSB before j: whoever emptied S_{j - NSB}
-        // had read them.
-        if (sc_tile < sc_round) sc_sm[(j * per_tile + lane) % kScRing] = scale_terms(scales.x, scales.y);
-        scales = sc_load(j + sc_round, sc_u);
-        sc_u = sc_unit(j + 2 * sc_round);
-        sc_left = sc_round;
-        __syncwarp();
-      }
-      --sc_left;
-      if (lane == 0) mbar_arrive(smem_u32(&s_full[j % NSB]));
+      // Every MMA issued here has completed before tensor memory is released.
+      tc_commit_one(smem_u32(&drain[0]));
+      mbar_wait(smem_u32(&drain[0]), 0, p.wait_ns, p.err);
     }
-    // Every MMA issued here has completed before tensor memory is released.
-    tc_commit(smem_u32(&drain[0]));
-    mbar_wait(smem_u32(&drain[0]), 0, p.wait_ns, p.err);
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ O issuer --
-    // O = V_j^T P_j into accumulator j % NT, once both are there (P_j is written
-    // after the softmax has taken the accumulator's previous contents).
+    // O^T (+)= V_j^T P_j in accumulator j % NT, once both are there (P_j is written
+    // after the softmax has rescaled the accumulator, where it does).
     constexpr uint32_t idO = instr_desc_e4m3_f32(128, 2 * R, true, true);
     const uint64_t dv = smem_desc_sw128(sb + Sh::kOffV, kFbTile, 1024);
     const uint64_t dp = smem_desc_mn<Sh::kRowP>(sb + Sh::kOffP);
-    bool ok = true;
-    for (int j = 0; ok && j < n; ++j) {
-      const int s = j % NT;
-      ok = wait_all(&v_full[j % NS], (j / NS) & 1) && wait_all(&p_ready[s], (j / NT) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t dvj = dv + (j % NS) * (kFbTile >> 4), dpj = dp + s * (Sh::kTileP >> 4);
+    if (elect_one()) {
+      bool ok = true;
+      int slot = 0, s = 0;
+      uint32_t parity = 0, sparity = 0;
+      for (int j = 0; ok && j < n; ++j) {
+        ok = wait_one(&v_full[slot], parity) && wait_one(&p_ready[s], sparity);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t dvj = dv + slot * (kFbTile >> 4), dpj = dp + s * (Sh::kTileP >> 4);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)  // 32 keys each: four groups of 8 rows
-        tc_mma_f8_ss(tmem + Sh::kColO + 2 * R * s, dvj + kk * (4096 >> 4),
-                     dpj + kk * (32 * Sh::kRowP >> 4), idO, kk > 0);
-      tc_commit(smem_u32(&o_full[s]));
-      tc_commit(smem_u32(&v_empty[j % NS]));
+        for (int kk = 0; kk < 4; ++kk)  // 32 keys each: four groups of 8 rows
+          tc_mma_f8_one(tmem + Sh::kColO + 2 * R * s, dvj + kk * (4096 >> 4),
+                        dpj + kk * (32 * Sh::kRowP >> 4), idO, kk > 0 || j >= NT);
+        tc_commit_one(smem_u32(&o_full[s]));
+        tc_commit_one(smem_u32(&v_empty[slot]));
+        if (++slot == NS) {
+          slot = 0;
+          parity ^= 1;
+        }
+        if (++s == NT) {
+          s = 0;
+          sparity ^= 1;
+        }
+      }
+      tc_commit_one(smem_u32(&drain[1]));
+      mbar_wait(smem_u32(&drain[1]), 0, p.wait_ns, p.err);
     }
-    tc_commit(smem_u32(&drain[1]));
-    mbar_wait(smem_u32(&drain[1]), 0, p.wait_ns, p.err);
     __syncwarp();
   } else {
     // ------------------------------------------- softmax, accumulation, end --
@@ -647,53 +706,36 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&q_ready));
 
-    // The scales' terms of this thread's key for each eight rows (one head's).
+    // Where the scales' terms of this thread's key lie among a tile's, for each eight
+    // rows (one head's).
     constexpr int RU = RW / 8;
-    const int sub_log2 = 7 - pb.block_log2;
     int sc_at[RU];
 #pragma unroll
     for (int c = 0; c < RU; ++c)
       sc_at[c] = (head_of(r0 + 8 * c) << sub_log2) + (kl >> pb.block_log2);
-    float acc[RW], l[RW], off[RW];  // off: 7 less the row's reference (0 while it has none)
+    float l[RW];
 #pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      acc[i] = l[i] = 0.f;
-      off[i] = kPScaleLog2;
-    }
+    for (int i = 0; i < RW; ++i) l[i] = 0.f;
     float m_mine = -INFINITY;  // reference of row r0 + lane (lanes below RW)
+    if (lane < RW) off_sm[sw][lane] = kPScaleLog2;  // (0 for a row without one)
     bool unset = true;         // some row has no reference yet
     const int lim_lo = min(t_end, L - p.T_q + 1);  // keys below it: visible from every row
     bool alive = true;
     const uint32_t tO = tmem + lane_base + Sh::kColO + 2 * R * st + 2 * r0;
     const uint32_t prow = sb + Sh::kOffP + st * Sh::kTileP;
-    // acc += O of the stream's last tile; O^T row d = kl
-    auto add_o = [&]() {
-#pragma unroll
-      for (int c = 0; c < RW; c += 8) {
-        uint32_t o[16];
-        tmem_ld_cols(tO + 2 * c, o);
-        tmem_wait_ld();
-        reg_fence(o);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          float u, v;
-          ffma2(u, v, __uint_as_float(o[8 + i]), __uint_as_float(o[8 + i + 1]), kLoStep, kLoStep,
-                __uint_as_float(o[i]), __uint_as_float(o[i + 1]));
-          fadd2(acc[c + i], acc[c + i + 1], acc[c + i], acc[c + i + 1], u, v);
-        }
-      }
-    };
     named_bar_sync(5, 32 * Sh::kWarps);  // cq, lim_sm, row_sm
 
     int turn = 0;  // tiles of this stream so far
     for (int j = st; j < n; j += NT, ++turn) {
       const int key = t0 + j * kFbKeys + kl;
       // (a warp whose wait failed keeps to the barriers of the others)
+      if ((j & ((1 << round_log2) - 1)) < NT) {  // the stream's first tile of a round
+        const int round = j >> round_log2;
+        alive = alive && wait_all(&sc_full[round % kScRounds], (round / kScRounds) & 1);
+      }
       alive = alive && wait_all(&s_full[j % NSB], (j / NSB) & 1);
       tc_fence_after();
-      ScaleTerms sc[RU];
-#pragma unroll
-      for (int c = 0; c < RU; ++c) sc[c] = sc_sm[((j * hc << sub_log2) + sc_at[c]) % kScRing];
+      const ScaleTerms* const sc = sc_sm + (j << per_tile_log2) % kScRing;
       float y[RW];  // exponents of P: y - m + 7
       float top = -INFINITY;
       {
@@ -703,18 +745,20 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
           tmem_ld_cols(tmem + lane_base + 2 * R * (j % NSB) + 2 * (r0 + c0), s);
           tmem_wait_ld();
           reg_fence(s);
+          const float2 kl2 = *reinterpret_cast<const float2*>(&sc[sc_at[c0 / 8]]);  // ks, lv
 #pragma unroll
           for (int i = 0; i < 8; i += 4) {
             const float4 c4 = *reinterpret_cast<const float4*>(&cq[r0 + c0 + i]);
-            const float c[4] = {c4.x, c4.y, c4.z, c4.w};
+            const float4 f4 = *reinterpret_cast<const float4*>(&off_sm[sw][c0 + i]);
+            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
             for (int u = 0; u < 4; u += 2) {
               const int e = i + u, r = c0 + e;
               float a0, a1, b0, b1, d0, d1;
               ffma2(a0, a1, __uint_as_float(s[8 + e]), __uint_as_float(s[9 + e]), kLoStep, kLoStep,
                     __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-              fmul2(b0, b1, c[u], c[u + 1], sc[c0 / 8].ks, sc[c0 / 8].ks);
-              fadd2(d0, d1, off[r], off[r + 1], sc[c0 / 8].lv, sc[c0 / 8].lv);
+              fmul2(b0, b1, c[u], c[u + 1], kl2.x, kl2.x);
+              fadd2(d0, d1, f[u], f[u + 1], kl2.y, kl2.y);
               ffma2(y[r], y[r + 1], a0, a1, b0, b1, d0, d1);
             }
           }
@@ -737,10 +781,10 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
         float mine = -INFINITY;
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
-          const float m = warp_max(y[i]) - off[i];
+          const float m = warp_max(y[i]);
           if (lane == i) mine = m;
         }
-        if (lane < RW) red[st][r0 + lane][quarter] = mine;
+        if (lane < RW) red[st][r0 + lane][quarter] = mine - off_sm[sw][lane];
         named_bar_sync(1 + gi, 128);
         if (lane < RW) {
           const float4 mx = *reinterpret_cast<const float4*>(red[st][r0 + lane]);
@@ -748,6 +792,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
           const float ref = m_new == -INFINITY ? 0.f : m_new;  // no (-inf) - (-inf)
           move_sm[sw][lane] = (m_mine == -INFINITY ? 0.f : m_mine) - ref;
           alpha_sm[sw][lane] = ex2_approx(m_mine - ref);
+          off_sm[sw][lane] = kPScaleLog2 - ref;
           m_mine = m_new;
         }
         unset = __any_sync(0xffffffffu, lane < RW && m_mine == -INFINITY);
@@ -755,26 +800,34 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
 #pragma unroll
         for (int i = 0; i < RW; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&move_sm[sw][i]);
-          fadd2(off[i], off[i + 1], off[i], off[i + 1], f.x, f.y);
-          fadd2(off[i + 2], off[i + 3], off[i + 2], off[i + 3], f.z, f.w);
+          const float4 a = *reinterpret_cast<const float4*>(&alpha_sm[sw][i]);
           fadd2(y[i], y[i + 1], y[i], y[i + 1], f.x, f.y);
           fadd2(y[i + 2], y[i + 3], y[i + 2], y[i + 3], f.z, f.w);
-        }
-      }
-
-      // The stream's previous O is complete: added, and its P may be overwritten.
-      alive = alive && (turn == 0 || wait_all(&o_full[st], (turn - 1) & 1));
-      tc_fence_after();
-      if (turn > 0) add_o();
-      if (update) {
-#pragma unroll
-        for (int i = 0; i < RW; i += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(&alpha_sm[sw][i]);
-          fmul2(acc[i], acc[i + 1], acc[i], acc[i + 1], a.x, a.y);
-          fmul2(acc[i + 2], acc[i + 3], acc[i + 2], acc[i + 3], a.z, a.w);
           fmul2(l[i], l[i + 1], l[i], l[i + 1], a.x, a.y);
           fmul2(l[i + 2], l[i + 3], l[i + 2], l[i + 3], a.z, a.w);
         }
+      }
+
+      // The stream's previous O is complete: its P may be overwritten, and O rescaled
+      // (row d = kl of O^T, both terms' columns).
+      alive = alive && (turn == 0 || wait_all(&o_full[st], (turn - 1) & 1));
+      tc_fence_after();
+      if (update && turn > 0) {
+#pragma unroll 1
+        for (int c = 0; c < RW; c += 8) {
+          uint32_t o[16];
+          tmem_ld_cols(tO + 2 * c, o);
+          tmem_wait_ld();
+          reg_fence(o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float a = alpha_sm[sw][c + i];
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+            o[8 + i] = __float_as_uint(__uint_as_float(o[8 + i]) * a);
+          }
+          tmem_st_cols(tO + 2 * c, o);
+        }
+        tmem_wait_st();
       }
       // P as two E4M3 terms, rounded to f16 on the way (2^-12 of itself, and
       // steps of 2^-24 below 2^-14, both below what the terms hold).
@@ -782,12 +835,13 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
 #pragma unroll
       for (int c0 = 0; c0 < RW; c0 += 8) {
         uint32_t hi[2], lo[2];
+        const float iv = sc[sc_at[c0 / 8]].ivs;
+        const uint32_t mask = sc[sc_at[c0 / 8]].p_mask;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
           const int r = c0 + i;
           const float e0 = ex2_approx(y[r]), e1 = ex2_approx(y[r + 1]);
           const float e2 = ex2_approx(y[r + 2]), e3 = ex2_approx(y[r + 3]);
-          const float iv = sc[c0 / 8].ivs;
           ffma2(l[r], l[r + 1], e0, e1, iv, iv, l[r], l[r + 1]);
           ffma2(l[r + 2], l[r + 3], e2, e3, iv, iv, l[r + 2], l[r + 3]);
           uint32_t h[2], d[2];
@@ -801,8 +855,8 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
                                       __float2half2_rn(32.f));
             d[u] = pack_e4m3x2(*reinterpret_cast<const uint32_t*>(&q));
           }
-          hi[i / 4] = (h[0] | (h[1] << 16)) & sc[c0 / 8].p_mask;
-          lo[i / 4] = (d[0] | (d[1] << 16)) & sc[c0 / 8].p_mask;
+          hi[i / 4] = (h[0] | (h[1] << 16)) & mask;
+          lo[i / 4] = (d[0] | (d[1] << 16)) & mask;
         }
         st_shared_v4(prow + swz_row<Sh::kRowP>(kl * Sh::kRowP + 2 * (r0 + c0)), hi[0], hi[1], lo[0],
                      lo[1]);
@@ -824,7 +878,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       if (alive && lane == 0) mbar_arrive(smem_u32(&p_ready[st]));
     }
 
-    // The stream's last O, and l over the keys.
+    // The stream's O, and l over the keys.
     if (turn > 0) alive = alive && wait_all(&o_full[st], (turn - 1) & 1);
     bool page_ok = true;
     if (PAGED && alive) {
@@ -835,7 +889,6 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
         alive = false;
     }
     tc_fence_after();
-    if (turn > 0) add_o();
     // (red was last read before the barrier of the stream's last tile, or in its
     // update: one more barrier of the group)
     named_bar_sync(1 + gi, 128);
@@ -847,11 +900,22 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     if (!alive || !page_ok) *abort_v = 1;
     named_bar_sync(5, 32 * Sh::kWarps);
     // Every S and O of the CTA is complete, so the rings are free (or the CTA has
-    // failed and writes NaN): the accumulators go through them, so that a warp
-    // merges and stores whole rows.
+    // failed and writes NaN): O goes through them, so that a warp merges and stores
+    // whole rows.
     float* const part = reinterpret_cast<float*>(smem);  // [NT][R][128]
+#pragma unroll 1
+    for (int c = 0; c < RW; c += 8) {
+      uint32_t o[16] = {};
+      if (turn > 0) {
+        tmem_ld_cols(tO + 2 * c, o);
+        tmem_wait_ld();
+        reg_fence(o);
+      }
 #pragma unroll
-    for (int i = 0; i < RW; ++i) part[(st * R + r0 + i) * 128 + kl] = acc[i];
+      for (int i = 0; i < 8; ++i)
+        part[(st * R + r0 + c + i) * 128 + kl] =
+            fmaf(__uint_as_float(o[8 + i]), kLoStep, __uint_as_float(o[i]));
+    }
     named_bar_sync(5, 32 * Sh::kWarps);
     const bool failed = *abort_v != 0;
     constexpr float kUnscale = 1.f / 128.f;  // P carried 2^7
@@ -958,7 +1022,7 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockParams& p, const CUtensorMa
     return launch_fb_r<FbShape<16, 6, 2, 2>, FbShape<16, 6, 2, 2>>(p, tm_k, tm_v, sms, stream);
   if (rows <= 32)
     return launch_fb_r<FbShape<32, 5, 2, 2>, FbShape<32, 5, 2, 2>>(p, tm_k, tm_v, sms, stream);
-  return launch_fb_r<FbShape<64, 5, 1, 4>, FbShape<64, 5, 1, 4>>(p, tm_k, tm_v, sms, stream);
+  return launch_fb_r<FbShape<64, 5, 2, 2>, FbShape<64, 5, 2, 2>>(p, tm_k, tm_v, sms, stream);
 }
 
 }  // namespace gqa
