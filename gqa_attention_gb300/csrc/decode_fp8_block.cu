@@ -57,7 +57,7 @@ template <int R_, int NS_, int NT_, int NG_>
 struct FbShape {
   static constexpr int R = R_, NS = NS_, NT = NT_, NG = NG_;
   static constexpr int RW = R / NG;                 // rows of a warp
-  static constexpr int NSB = R < 64 ? 2 * NT : NT;  // S buffers (tensor memory has 512 columns)
+  static constexpr int NSB = 2 * NT;                // S buffers
   static constexpr int kWarps = 4 * NT * NG;        // softmax warps
   static constexpr int kRowsQ = R / kWarps;         // rows of Q a warp splits
   static constexpr int kThreads = 128 + 32 * kWarps;
@@ -1022,7 +1022,7 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockParams& p, const CUtensorMa
     return launch_fb_r<FbShape<16, 6, 2, 2>, FbShape<16, 6, 2, 2>>(p, tm_k, tm_v, sms, stream);
   if (rows <= 32)
     return launch_fb_r<FbShape<32, 5, 2, 2>, FbShape<32, 5, 2, 2>>(p, tm_k, tm_v, sms, stream);
-  return launch_fb_r<FbShape<64, 5, 2, 2>, FbShape<64, 5, 2, 2>>(p, tm_k, tm_v, sms, stream);
+  return launch_fb_r<FbShape<64, 5, 1, 4>, FbShape<64, 5, 1, 4>>(p, tm_k, tm_v, sms, stream);
 }
 
 }  // namespace gqa
