@@ -278,11 +278,13 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   __shared__ __align__(16) float cq[R];         // tau log2(e) 2^-k of each row's query
   __shared__ __align__(16) int lim_sm[R];       // keys below it are visible
   __shared__ uint32_t row_sm[R];                // row of out, lse and the workspace
-  __shared__ __align__(16) float red[NT][R][4]; // by stream: maxima (later sums) of four warps
+  __shared__ __align__(16) float red[NT][R][4]; // by stream: maxima of four warps
   // each softmax warp's own copy: its rows' changes of reference and factors
   __shared__ __align__(16) float move_sm[Sh::kWarps][RW], alpha_sm[Sh::kWarps][RW];
   __shared__ __align__(16) float off_sm[Sh::kWarps][RW];  // 7 less each row's reference
-  __shared__ float m_end[NT][R];                // final references
+  // final sums of l (of four warps) and references
+  __shared__ __align__(16) float l_end[NT][R][4];
+  __shared__ float m_end[NT][R];
   // What the softmax needs of the scales: a ring of 8 rounds of 32 terms, by tile, head
   // and block of tokens of the tile.
   constexpr int kScRounds = 8, kScRing = 32 * kScRounds;
@@ -544,6 +546,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       if constexpr (!PAGED) {
         tma_load_3d_elect(dst, map, fb, tx, ty, b * p.S_max + t0 + j * kFbKeys, pol);
       } else {
+#pragma unroll 1
         for (int i = 0; i < nb; ++i)
           tma_load_3d_elect(dst + i * h * 128, map, fb, tx, ty,
                             __shfl_sync(0xffffffffu, rows_l, at + i), pol);
@@ -878,30 +881,23 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       if (alive && lane == 0) mbar_arrive(smem_u32(&p_ready[st]));
     }
 
-    // The stream's O, and l over the keys.
-    if (turn > 0) alive = alive && wait_all(&o_full[st], (turn - 1) & 1);
-    bool page_ok = true;
-    if (PAGED && alive) {
-      // (a bad index is recorded before the barrier of the last V tile is armed)
-      if (wait_all(&v_full[(n - 1) % NS], ((n - 1) / NS) & 1))
-        page_ok = *reinterpret_cast<volatile int*>(&bad_page) == 0;
-      else
-        alive = false;
-    }
-    tc_fence_after();
-    // (red was last read before the barrier of the stream's last tile, or in its
-    // update: one more barrier of the group)
-    named_bar_sync(1 + gi, 128);
+    // l over the keys, while the last O is worked out; then the stream's O.  It goes
+    // through the K ring, so that a warp merges and stores whole rows: free once the
+    // last S is complete (or the CTA has failed and writes NaN).
     {
       const float s = warp_sums(l, lane);
-      if (lane % (32 / RW) == 0) red[st][r0 + lane / (32 / RW)][quarter] = s;
+      if (lane % (32 / RW) == 0) l_end[st][r0 + lane / (32 / RW)][quarter] = s;
       if (quarter == 0 && lane < RW) m_end[st][r0 + lane] = m_mine;
     }
-    if (!alive || !page_ok) *abort_v = 1;
-    named_bar_sync(5, 32 * Sh::kWarps);
-    // Every S and O of the CTA is complete, so the rings are free (or the CTA has
-    // failed and writes NaN): O goes through them, so that a warp merges and stores
-    // whole rows.
+    alive = alive && wait_all(&s_full[(n - 1) % NSB], ((n - 1) / NSB) & 1) &&
+            (turn == 0 || wait_all(&o_full[st], (turn - 1) & 1));
+    if (PAGED && alive) {
+      // (a bad index is recorded before the barrier of the last V tile is armed)
+      alive = wait_all(&v_full[(n - 1) % NS], ((n - 1) / NS) & 1) &&
+              *reinterpret_cast<volatile int*>(&bad_page) == 0;
+    }
+    if (!alive) *abort_v = 1;
+    tc_fence_after();
     float* const part = reinterpret_cast<float*>(smem);  // [NT][R][128]
 #pragma unroll 1
     for (int c = 0; c < RW; c += 8) {
@@ -923,11 +919,11 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       if (row_sm[r] == 0xffffffffu) continue;
       // (head hl's O lies in rows hl D .. of O^T)
       const int at = r * 128 + min(head_of(r) * D + lane * 4, 124);
-      const float4 ls = *reinterpret_cast<const float4*>(red[0][r]);
+      const float4 ls = *reinterpret_cast<const float4*>(l_end[0][r]);
       float m = m_end[0][r], lr = (ls.x + ls.y) + (ls.z + ls.w);
       float4 o = *reinterpret_cast<const float4*>(part + at);
       if constexpr (NT == 2) {  // the merge of two partials
-        const float4 l2 = *reinterpret_cast<const float4*>(red[1][r]);
+        const float4 l2 = *reinterpret_cast<const float4*>(l_end[1][r]);
         const float m1 = m_end[1][r], M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
         const float a0 = ex2_approx(m - ref), a1 = ex2_approx(m1 - ref);
         const float4 o1 = *reinterpret_cast<const float4*>(part + R * 128 + at);
