@@ -607,21 +607,19 @@ def prefill_chunk_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=
             or not q.is_contiguous() or not q.is_cuda:
         raise GQAError(GQA_ERR_INVALID_ARG, "prefill_chunk_fp8_block: q is dense bfloat16 "
                        "[B, T_q, H_q, d] on the cache's device")
-    with torch.cuda.device(q.device):
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, q.device)
+    # (what the call allocates belongs to its stream; stream(None) changes nothing)
+    with torch.cuda.device(q.device), torch.cuda.stream(stream):
         B, per, H_kv, d = k8.shape
         if block_table is not None:
             B, per = block_table.shape[0], block_table.shape[1] * per
-        k = torch.empty((B, per, H_kv, d), dtype=torch.bfloat16, device=q.device)
-        v = torch.empty_like(k)
-        if stream is not None:  # the temporaries outlive the call on a stream of the caller's
-            s = stream if isinstance(stream, torch.cuda.Stream) else \
-                torch.cuda.ExternalStream(stream)
-            k.record_stream(s)
-            v.record_stream(s)
-        kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, 0, k, v, block_table, stream)
         if q.shape[0] != B or q.shape[3] != d:
             raise GQAError(GQA_ERR_INVALID_ARG, "prefill_chunk_fp8_block: q's B or d is not the "
                            "cache's")
+        k = torch.empty((B, per, H_kv, d), dtype=torch.bfloat16, device=q.device)
+        v = torch.empty_like(k)
+        kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, 0, k, v, block_table, stream)
         return prefill_chunk(q, k, v, seq_lens, scale, window, out, lse, stream)
 
 

@@ -547,9 +547,9 @@ gqa_status gqa_attn_decode_paged_fp8(const void* q, const void* k_pool, const vo
 
 namespace {
 
-// Token rows of a block-scaled cache: row and key indices, also those of a tile
-// that runs past the end, stay within 32 bits.
-constexpr long long kMaxBlockRows = 0x7fffff00LL;
+// Token rows of a block-scaled cache: row and key indices, also those that a kernel
+// works out up to 2^15 keys past the end before it compares them, stay within 32 bits.
+constexpr long long kMaxBlockRows = 0x7fff0000LL;
 
 // The layout of a block-scaled E4M3 cache: checks what the calls on it share and
 // fills the units of the parameter block (a unit is a sequence of a contiguous
@@ -647,15 +647,19 @@ gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int 
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       (workspace && !aligned(workspace, 256)))
     return GQA_ERR_INVALID_ARG;
-  // Codes as [rows][H_kv][d] bytes, boxes of up to 128 rows, always 128 bytes wide.
-  // For d = 32 and 64, a CTA takes the 4 or 2 heads that share 128 bytes of a row
-  // (rows of H_kv d bytes, zeros past them), as long as their query rows fit and
-  // the grid still fills the GPU: a tile then serves all of them.  Otherwise the
-  // box is one head and TMA fills the rest of each row with zeros.
-  const int pack = 128 / c.d, head_rows = (T_q * G + 7) / 8 * 8;
-  const long long packed_ctas = (long long)n_split * ((c.H_kv + pack - 1) / pack) * c.B;
-  const bool packed = pack > 1 && c.H_kv > 1 && pack * head_rows <= 64 &&
-                      packed_ctas >= num_sms_current_device();
+  // Codes as [rows][H_kv][d] bytes, boxes of up to 128 rows, always 128 bytes wide: one
+  // head, and TMA fills the rest of each row with zeros.  A tile's cost is nearly
+  // the same for every d, so for d = 32 a CTA takes the four heads that share 128
+  // bytes of a row, where their query rows fit and the heads by themselves are more
+  // CTAs than two on each SM: 4K tokens, 8 KV heads of 8 rows, batch 64, 33.8 instead of
+  // 44.7 us (of 16 rows 50 instead of 76); a smaller grid is better kept as it is
+  // (batch 32 22.4 us, packed 32.5; of 16 rows 38.9 and 49.9).  Groups that are not full
+  // lose (2 heads 44.6 us, packed 63.6), and so do the pairs of d = 64 (48.7, packed
+  // 50.9; ragged lengths 34.8 and 38.1).
+  const int head_rows = (T_q * G + 7) / 8 * 8;
+  const long long head_ctas = (long long)n_split * c.H_kv * c.B;
+  const bool packed = c.d == 32 && c.H_kv % 4 == 0 && 4 * head_rows <= 64 &&
+                      head_ctas > 2LL * num_sms_current_device();
   const long long rows = (long long)c.units * c.per;
   const int box_rows = c.block_table && c.page_size < 128 ? c.page_size : 128;
   const uint64_t width = (uint64_t)c.H_kv * c.d;
@@ -679,7 +683,7 @@ gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int 
   p.block_log2 = c.block_log2;
   p.page_log2 = c.page_log2;
   p.per_blk = c.per_blk;
-  p.heads = packed ? pack : 1;
+  p.heads = packed ? 4 : 1;
   p.head_rows = head_rows;
   gqa::DecodeParams& dp = p.dec;
   dp.q = static_cast<const __nv_bfloat16*>(q);
@@ -694,7 +698,7 @@ gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int 
   dp.n_rg = 1;
   dp.n_split = n_split;
   const long long per = ((long long)c.S_max + n_split - 1) / n_split;
-  dp.chunk = (int)((per + 127) / 128 * 128);  // (S_max is below 2^31 - 255)
+  dp.chunk = (int)((per + 127) / 128 * 128);  // (S_max is below 2^31 - 2^15)
   dp.scale_log2 = scale * 1.4426950408889634f;
   dp.ws_ml = static_cast<float2*>(workspace);
   dp.ws_O = workspace ? reinterpret_cast<float*>(

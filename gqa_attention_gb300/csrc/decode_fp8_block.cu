@@ -71,10 +71,10 @@ struct FbShape {
   static constexpr uint32_t kColO = NSB * 2 * R;
   static constexpr uint32_t kUsed = (NSB + NT) * 2 * R;
   static constexpr uint32_t kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  // CTAs an SM holds: shared memory (4 KB of it for the static part and the
+  // CTAs an SM holds: shared memory (8 KB of it for the static part and the
   // driver's), tensor memory and 24 warps at 80 registers
   static constexpr int kPerSM =
-      2 * (kBytes + 4096) <= 227 * 1024 && kThreads <= 384 && kCols <= 256 ? 2 : 1;
+      2 * (kBytes + 8192) <= 228 * 1024 && kThreads <= 384 && kCols <= 256 ? 2 : 1;
   static_assert(kUsed <= 512 && kRowsQ >= 1, "tensor memory; a row of Q for every warp");
   static_assert(NT * R * 512 <= 2 * NS * (int)kFbTile, "the accumulators reuse the rings");
 };
@@ -274,7 +274,10 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   __shared__ __align__(8) uint64_t s_full[NSB], s_empty[NSB], q_ready, p_ready[NT], o_full[NT],
       drain[2];
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_flag, bad_page;
+  __shared__ int abort_flag, bad_page, nan_seen;
+  // NaN codes in V of the keys that only some queries see (at most T_q - 1 <= 63), a
+  // bit for each byte of the row
+  __shared__ __align__(16) uint32_t nan_v[64][4];
   __shared__ __align__(16) float cq[R];         // tau log2(e) 2^-k of each row's query
   __shared__ __align__(16) int lim_sm[R];       // keys below it are visible
   __shared__ uint32_t row_sm[R];                // row of out, lse and the workspace
@@ -296,8 +299,8 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, b = blockIdx.z;
-  // KV heads hc blockIdx.y + 0 .. hc - 1 share the 128-byte rows of a tile (hc = 128 / d
-  // packed heads, or 1).  Head hl has the query rows r = hl rp + q, q < T_q * G.
+  // KV heads hc blockIdx.y + 0 .. hc - 1 share the 128-byte rows of a tile (hc = 4 packed
+  // heads of d = 32, or 1).  Head hl has the query rows r = hl rp + q, q < T_q * G.
   const int hc = pb.heads, rp = pb.head_rows, kv0 = blockIdx.y * hc;
   // first key of the split (rows of a cache are below 2^31 - 256, so keys of a
   // tile past its end still fit)
@@ -306,11 +309,10 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   const int D = p.d;
   // Head of row r (rows past the last head's count as its padding).
   auto head_of = [&](int r) {
-    return hc == 1 ? 0 : min(hc - 1, (r >= rp) + (r >= 2 * rp) + (r >= 3 * rp));
+    return hc == 1 ? 0 : (r >= rp) + (r >= 2 * rp) + (r >= 3 * rp);
   };
   auto live_row = [&](int r) {
-    const int hl = head_of(r);
-    return r - hl * rp < rows && kv0 + hl < p.H_kv;
+    return r - head_of(r) * rp < rows;
   };
   // r / G without an integer division, as in decode.cu
   const float inv_g = 1.f / static_cast<float>(G);
@@ -350,6 +352,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     mbar_init(smem_u32(&drain[1]), 1);
     abort_flag = 0;
     bad_page = 0;
+    nan_seen = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   // Rounds of the scales' terms: per_tile of them belong to a tile (a power of two),
   // so a round covers 1 << round_log2 tiles.
   const int sub_log2 = 7 - pb.block_log2;
-  const int per_tile_log2 = sub_log2 + (hc == 1 ? 0 : hc == 2 ? 1 : 2);
+  const int per_tile_log2 = sub_log2 + (hc == 1 ? 0 : 2);
   const int round_log2 = 5 - per_tile_log2;
 
   if (warp == 0 || warp == 3) {
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     // ahead, scales one (terms of one tile at a time take a warp longer than a tile).
     const int sc_tile = lane >> per_tile_log2;
     const int sc_in = lane & ((1 << per_tile_log2) - 1);
-    const size_t sc_kv = min(kv0 + (sc_in >> sub_log2), p.H_kv - 1);
+    const int sc_kv = kv0 + (sc_in >> sub_log2);
     auto sc_tok = [&](int tile) {
       return t0 + (tile + sc_tile) * kFbKeys + ((sc_in & ((1 << sub_log2) - 1)) << pb.block_log2);
     };
@@ -602,11 +605,9 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
             if (kk < ksteps) tc_mma_f8_one(ts, dkj + kk * 2, dq + kk * 2, id, kk > 0);
         } else {
 #pragma unroll 1
-          for (int hl = 0; hl < hc; ++hl)
-            for (int kk = 0; kk < ksteps; ++kk)
-              tc_mma_f8_one(ts + hl * 2 * rp, dkj + (hl * ksteps + kk) * 2,
-                            dq + hl * (2 * rp * 128 >> 4) + kk * 2, hl == hc - 1 ? id_last : id,
-                            kk > 0);
+          for (int hl = 0; hl < 4; ++hl)
+            tc_mma_f8_one(ts + hl * 2 * rp, dkj + hl * 2, dq + hl * (2 * rp * 128 >> 4),
+                          hl == 3 ? id_last : id, false);
         }
         tc_commit_one(smem_u32(&s_full[buf]));
         tc_commit_one(smem_u32(&k_empty[slot]));
@@ -866,13 +867,40 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       }
       // Cache rows past the end of the split may hold anything (even NaN codes),
       // and 0 * NaN would reach O: they are zeroed once the tile has landed (by
-      // the stream's first row group).
-      if (t0 + (j + 1) * kFbKeys > t_end && r0 == 0) {
+      // the stream's first row group).  So are the NaN codes of keys that only the
+      // later queries see; the end of the kernel puts them into those queries' rows.
+      if (t0 + (j + 1) * kFbKeys > lim_lo && r0 == 0) {
         alive = alive && wait_all(&v_full[j % NS], (j / NS) & 1);
-        if (alive && key >= t_end) {
-          const uint32_t vrow = sb + Sh::kOffV + (j % NS) * kFbTile + kl * 128;
+        if (alive && key >= lim_lo) {
+          uint4* const vrow = reinterpret_cast<uint4*>(smem + Sh::kOffV + (j % NS) * kFbTile + kl * 128);
+          const bool past = key >= t_end;
+          uint32_t any = 0;
+#pragma unroll 1
+          for (int c = 0; c < 4 && !past; ++c) {  // 32 bytes: two swizzled pieces
+            uint32_t bits = 0;
 #pragma unroll
-          for (int c16 = 0; c16 < 8; ++c16) st_shared_v4(vrow + c16 * 16, 0u, 0u, 0u, 0u);
+            for (int h = 0; h < 2; ++h) {
+              uint4* const at = vrow + ((2 * c + h) ^ (kl & 7));
+              const uint4 w = *at;
+              uint32_t x[4] = {w.x, w.y, w.z, w.w}, here = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t is = __vcmpeq4(x[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                x[i] &= ~is;
+                // a bit of each byte of the mask, added up in the top byte
+                here |= ((is & 0x08040201u) * 0x01010101u >> 24 & 15u) << (4 * i);
+              }
+              if (here != 0) *at = make_uint4(x[0], x[1], x[2], x[3]);
+              bits |= here << (16 * h);
+            }
+            nan_v[key - (L - p.T_q + 1)][c] = bits;
+            any |= bits;
+          }
+          if (any != 0) *reinterpret_cast<volatile int*>(&nan_seen) = 1;
+          if (past) {
+#pragma unroll
+            for (int c16 = 0; c16 < 8; ++c16) vrow[c16] = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
       }
       fence_proxy_async_smem();
@@ -932,6 +960,17 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
                         o.w * a0 + o1.w * a1);
         m = M;
       }
+      if (*reinterpret_cast<volatile int*>(&nan_seen) != 0) {
+        const int dim = at - r * 128;  // of four
+        uint32_t bits = 0;
+        for (int key = max(t0, lim_lo); key < lim_sm[r]; ++key)
+          bits |= nan_v[key - (L - p.T_q + 1)][dim / 32];
+        bits >>= dim % 32;
+        if (bits & 1u) o.x = NAN;
+        if (bits & 2u) o.y = NAN;
+        if (bits & 4u) o.z = NAN;
+        if (bits & 8u) o.w = NAN;
+      }
       const size_t row = row_sm[r];
       if (p.n_split == 1) {
         const float inv = failed ? NAN : 1.f / lr;
@@ -978,7 +1017,7 @@ cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
   DecodeBlockParams p = p_in;
   p.dec.prefetch_tiles = prefetch ? 3 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.dec.n_split, (p.dec.H_kv + p.heads - 1) / p.heads, p.dec.B);
+  cfg.gridDim = dim3(p.dec.n_split, p.dec.H_kv / p.heads, p.dec.B);
   cfg.blockDim = dim3(Sh::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -996,8 +1035,7 @@ cudaError_t launch_fb_r(const DecodeBlockParams& p, const CUtensorMap& tm_k,
                         const CUtensorMap& tm_v, int sms, cudaStream_t stream) {
   // One CTA per SM at most: a deep ring.  More CTAs than SMs: two shallow rings
   // on each SM, where they fit.
-  const int groups = (p.dec.H_kv + p.heads - 1) / p.heads;
-  const bool one_wave = (long long)p.dec.n_split * groups * p.dec.B <= sms;
+  const bool one_wave = (long long)p.dec.n_split * (p.dec.H_kv / p.heads) * p.dec.B <= sms;
   const bool paged = p.dec.block_table != nullptr;
   if (one_wave)
     return paged ? launch_fb<Deep, true>(p, tm_k, tm_v, true, stream)

@@ -105,9 +105,9 @@ struct DecodeBlockParams {
   DecodeParams dec;
   const float *k_scale, *v_scale;
   int block_log2, page_log2, per_blk;
-  // KV heads of a CTA: 1 (the map's middle dimension is the head), or 128 / d
-  // packed ones (the map's rows are whole tokens, 128 bytes wide); then each has
-  // head_rows = T_q * G rounded up to 8 of the CTA's query rows.
+  // KV heads of a CTA: 1 (the map's middle dimension is the head), or 4 packed ones
+  // of d = 32 (the map's rows are whole tokens; H_kv is a multiple of 4); then each
+  // has head_rows = T_q * G rounded up to 8 of the CTA's query rows.
   int heads, head_rows;
 };
 

@@ -151,10 +151,19 @@ Cache cache(PyObject* const* a, PyObject* block, PyObject* table, const char* ca
   return c;
 }
 
-// The stream of a call: given, or the current one of the device.
+// The stream of a call: given, or the current one of the device.  What a call
+// allocates belongs to that stream (torch's allocator orders reuse by it).
 struct Stream {
   gqa_stream_t raw;
   bool given;
+};
+struct AllocateOn {
+  AllocateOn(const Stream& s, c10::DeviceIndex dev) {
+    if (s.given)
+      guard.reset_stream(
+          c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(s.raw), dev));
+  }
+  c10::cuda::OptionalCUDAStreamGuard guard;
 };
 Stream stream_of(PyObject* o, c10::DeviceIndex dev) {
   if (o == Py_None)
@@ -240,6 +249,8 @@ PyObject* read_(PyObject* const* a) {
   const int start = as_int(a[9], call);
   std::optional<at::Tensor> k = maybe_tensor(a[10], call), v = maybe_tensor(a[11], call);
   const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, c.dev));
+  const Stream s = stream_of(a[8], c.dev);
+  const AllocateOn on(s, c.dev);
   if (!k) {
     need(start >= 0 && start < c.s_max(), call, "start lies in the cache");
     k = at::zeros({c.B, c.s_max() - start, c.H, c.d}, c.k8.options().dtype(at::kBFloat16));
@@ -249,7 +260,6 @@ PyObject* read_(PyObject* const* a) {
            v->sizes() == k->sizes() && dense(*k, at::kBFloat16, c.dev) &&
            dense(*v, at::kBFloat16, c.dev),
        call, "k_out and v_out are dense bfloat16 [B, S_out, H_kv, d] on the cache's device");
-  const Stream s = stream_of(a[8], c.dev);
   const float *ks = static_cast<const float*>(c.ks.data_ptr()),
               *vs = static_cast<const float*>(c.vs.data_ptr());
   const int32_t* lens = static_cast<const int32_t*>(c.lens.data_ptr());
@@ -287,21 +297,16 @@ PyObject* decode_(PyObject* const* a) {
        "out is dense bfloat16, of q's shape, on the cache's device");
   need(!lse || (lse->sizes() == rows && dense(*lse, at::kFloat, c.dev)), call,
        "lse is dense float32, of q's shape without d, on the cache's device");
+  const Stream s = stream_of(a[8], c.dev);
+  const AllocateOn on(s, c.dev);
   if (!out) out = at::empty(q.sizes(), q.options());
   if (!lse) lse = at::empty(rows, q.options().dtype(at::kFloat));
-  const Stream s = stream_of(a[8], c.dev);
   const int n_split = a[11] == Py_None ? lib.default_splits(c.B, T_q, H_q, c.H, c.s_max())
                                        : as_int(a[11], call);
   if (n_split > 1) {
     const int64_t bytes = static_cast<int64_t>(
         lib.workspace_bytes(as_dim(int64_t(c.B) * T_q, call), H_q, c.d, n_split));
-    if (!ws) {
-      ws = at::empty({bytes}, q.options().dtype(at::kByte));
-      // (kept from reuse until a stream that is not torch's current one is past it)
-      if (s.given)
-        ws->record_stream(c10::cuda::getStreamFromExternal(
-            reinterpret_cast<cudaStream_t>(s.raw), c.dev));
-    }
+    if (!ws) ws = at::empty({bytes}, q.options().dtype(at::kByte));
     need(ws->is_cuda() && ws->get_device() == c.dev && ws->is_contiguous() &&
              static_cast<int64_t>(ws->nbytes()) >= bytes,
          call, "the workspace is too small, or not dense on the cache's device");

@@ -454,7 +454,7 @@ gqa_status gqa_attn_decode_paged_multi(const void* q, const void* k_pool, const 
  * The value held for token t, head h, element c is e4m3(code) * scale of t's block.
  * block is 16, 32, 64 or 128, d is 32, 64 or 128 (GQA_ERR_UNSUPPORTED otherwise);
  * pages as in gqa_attn_decode_paged, with block <= page_size.  A cache has at most
- * 2^31 - 256 token rows (B * S_max, or num_pages * page_size).  Codes are 16-byte,
+ * 2^31 - 2^16 token rows (B * S_max, or num_pages * page_size).  Codes are 16-byte,
  * scales 4-byte aligned.  seq_lens: device int32 [B].
  *
  * Append: quantises the last tokens of each sequence into the cache.
@@ -518,15 +518,16 @@ gqa_status gqa_kv_read_paged_fp8_block(const void* k_pool, const void* v_pool,
  * with splits of ceil(S_max / n_split) keys rounded up to 128.  With n_split > 1
  * the partials go to `workspace` (gqa_attn_decode_workspace_bytes(B * T_q, H_q, d,
  * n_split) bytes, 256-byte aligned, in gqa_attn_decode's layout) and a second
- * launch merges them into out and lse: no gqa_attn_decode_combine() follows.  1 <= T_q <= 64, G = H_q / H_kv <=
- * 16 and T_q * G <= 64 (GQA_ERR_UNSUPPORTED above); scale finite > 0.  Scales may
+ * launch merges them into out and lse: no gqa_attn_decode_combine() follows.
+ * 1 <= T_q <= 64, G = H_q / H_kv <= 16 and T_q * G <= 64 (GQA_ERR_UNSUPPORTED above); scale finite > 0.  Scales may
  * be any finite fp32 numbers for keys; for values they must not be negative
  * (NaN outputs), and one below 2^-100 counts as zero.  The codes are multiplied
  * as they are, queries and weights as sums of two E4M3 terms (queries to 2^-21 of
  * their row's largest magnitude, weights as bf16 would hold them).  A partial's m
  * is a reference near the split's largest x_j + ln v_scale_j, not max_j x_j; l
  * and O hold relative to it, so the merge is unchanged.  A query row with an
- * infinity or NaN gives NaN.  Deterministic. */
+ * infinity or NaN gives NaN; NaN codes and scales reach the rows that see their
+ * tokens and no others.  Deterministic. */
 gqa_status gqa_attn_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
                                      const float* k_scale, const float* v_scale,
                                      const int32_t* seq_lens, int B, int T_q, int S_max, int H_q,

@@ -524,8 +524,8 @@ def test_helpers_refuse():
 @pytest.mark.parametrize("T_q,G", [(1, 1), (1, 6), (3, 5), (1, 16), (2, 16)])
 @pytest.mark.parametrize("page", [0, 32])
 def test_decode_grids_that_fill_the_gpu(d, H, T_q, G, page):
-    """With d = 32 and 64 and a grid as large as the GPU, a CTA takes the heads that share 128
-    bytes of a row (also where the last group is not full, or their rows do not fit)."""
+    """With d = 32, a multiple of four heads and a grid larger than the GPU holds at once, a CTA
+    takes four heads (unless their rows do not fit)."""
     c = Cache(2, 900, H, d, 16, page, seed=d + H + T_q + G)
     k, v = c.rows(900)
     c.append(k, v, [900, 130 + T_q])
