@@ -35,9 +35,9 @@
 //
 // O^T stays in tensor memory and is rescaled there when m moves (thread = row d).
 //
-// Roles (128 + 32 kWarps threads): warps 0 and 3 TMA producers of K and V, warp 1
-// issuer of S (and tensor memory), warp 2 issuer of O, the others Q split, softmax,
-// accumulation and epilogue.
+// Roles: warps 0 and 3 TMA producers of K and V (and two more at the end, for small
+// pages), warp 1 issuer of S (and tensor memory), warp 2 issuer of O, the others Q
+// split, softmax, rescaling and epilogue.
 #include "tcgen05.cuh"
 
 namespace gqa {
@@ -50,6 +50,16 @@ constexpr float kPScaleLog2 = 7.f;          // P is held times 2^7
 constexpr float kPMaxLog2 = 8.f;            // and must not pass 2^8
 constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100: smaller ones count as zero
 
+// How the codes of a tile are loaded: one box of a contiguous cache, a box for each
+// page, or, for pages of 16 tokens and up to 32 query rows, such boxes by two warps each
+// for K and V.  A warp takes about 150 cycles to issue a box, so the eight of a tile
+// take longer than its softmax: batch 16 of 4K to 60K tokens, two queries, 249 us with
+// one warp, 215 with two; 64 x 4K, d = 64, 28.4 and 26.9.  At 32 tokens the four boxes fit
+// (23.8 us, and 24.7 with the registers of two more warps), as they do beside 64
+// rows' softmax (32K, eight queries: 31.6 and 34.4).
+enum class Load { kTile, kPages, kSmallPages };
+constexpr int kSmallPage = 16;
+
 // Compile-time shape of one variant.  R query rows (padded), NS slots per ring,
 // NT streams of tiles (stream s takes tiles s, s + NT, ..) and NG groups of rows:
 // the 4 NT NG softmax warps share the work of a tile by rows and alternate tiles.
@@ -60,7 +70,9 @@ struct FbShape {
   static constexpr int NSB = 2 * NT;                // S buffers
   static constexpr int kWarps = 4 * NT * NG;        // softmax warps
   static constexpr int kRowsQ = R / kWarps;         // rows of Q a warp splits
-  static constexpr int kThreads = 128 + 32 * kWarps;
+  static constexpr int threads(Load load) {
+    return 128 + 32 * kWarps + (load == Load::kSmallPages ? 64 : 0);
+  }
   static constexpr uint32_t kRowP = 2 * R;          // bytes of a key's row of P
   static constexpr uint32_t kOffV = NS * kFbTile;
   static constexpr uint32_t kOffQ = 2 * NS * kFbTile;
@@ -72,9 +84,9 @@ struct FbShape {
   static constexpr uint32_t kUsed = (NSB + NT) * 2 * R;
   static constexpr uint32_t kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   // CTAs an SM holds: shared memory (8 KB of it for the static part and the
-  // driver's), tensor memory and 24 warps at 80 registers
+  // driver's), tensor memory and 24 warps at 80 registers (28 at 72)
   static constexpr int kPerSM =
-      2 * (kBytes + 8192) <= 228 * 1024 && kThreads <= 384 && kCols <= 256 ? 2 : 1;
+      2 * (kBytes + 8192) <= 228 * 1024 && threads(Load::kPages) <= 384 && kCols <= 256 ? 2 : 1;
   static_assert(kUsed <= 512 && kRowsQ >= 1, "tensor memory; a row of Q for every warp");
   static_assert(NT * R * 512 <= 2 * NS * (int)kFbTile, "the accumulators reuse the rings");
 };
@@ -262,12 +274,13 @@ __device__ __forceinline__ ScaleTerms scale_terms(float ks, float vs) {
   return s;
 }
 
-template <typename Sh, bool PAGED>
-__global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
+template <typename Sh, Load LOAD>
+__global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
     gqa_decode_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 const __grid_constant__ CUtensorMap tm_v,
                                 const DecodeBlockParams pb) {
   constexpr int R = Sh::R, NS = Sh::NS, NT = Sh::NT, NG = Sh::NG, RW = Sh::RW, NSB = Sh::NSB;
+  constexpr bool PAGED = LOAD != Load::kTile;
   const DecodeParams& p = pb.dec;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
@@ -396,7 +409,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   // kWarps, ..; lane takes columns 4 lane .. 4 lane + 3.
   const int sw = warp - 4;
   uint2 qw[Sh::kRowsQ];
-  if (warp >= 4) {
+  if (sw >= 0 && sw < Sh::kWarps) {
 #pragma unroll
     for (int i = 0; i < Sh::kRowsQ; ++i) {
       const int r = sw + i * Sh::kWarps;
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     // A bad length: NaN outputs and the error bit.  An empty split: the merge
     // identity (-inf, 0); its O is not written.  (One split is never empty.)
     if (bad && threadIdx.x == 0 && split == 0 && kv0 == 0) atomicOr(p.err, kErrBadSeqLen);
-    for (int r = threadIdx.x; r < R; r += Sh::kThreads) {
+    for (int r = threadIdx.x; r < R; r += Sh::threads(LOAD)) {
       if (!live_row(r)) continue;
       const size_t row = out_row(r);
       if (p.n_split == 1) {
@@ -474,9 +487,11 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   const int per_tile_log2 = sub_log2 + (hc == 1 ? 0 : 2);
   const int round_log2 = 5 - per_tile_log2;
 
-  if (warp == 0 || warp == 3) {
+  constexpr int kSecond = 4 + Sh::kWarps;  // second producers, of small pages
+  if (warp == 0 || warp == 3 || (LOAD == Load::kSmallPages && warp >= kSecond)) {
     // ---------------------------------------------- TMA producers of K and V --
-    const bool is_k = warp == 0;
+    const bool is_k = warp == 0 || warp == kSecond;
+    const bool second = LOAD == Load::kSmallPages && warp >= kSecond;
     const CUtensorMap* const map = is_k ? &tm_k : &tm_v;
     uint64_t* const full = is_k ? k_full : v_full;
     uint64_t* const empty = is_k ? k_empty : v_empty;
@@ -515,7 +530,7 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       return t0 + (tile + sc_tile) * kFbKeys + ((sc_in & ((1 << sub_log2) - 1)) << pb.block_log2);
     };
     auto sc_unit = [&](int tile) -> int {  // its page (or sequence), -1 for none
-      if (is_k || tile + sc_tile >= n) return -1;
+      if (is_k || second || tile + sc_tile >= n) return -1;
       const int tok = sc_tok(tile);
       if (tok >= t_end) return -1;
       if (!PAGED) return b;
@@ -531,6 +546,8 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
     float2 scales = sc_load(0, sc_unit(0));
     int sc_u = sc_unit(1 << round_log2);
     const uint64_t pol = l2_policy_evict_first();  // every tile is read once
+    const int box0 = second ? nb / 2 : 0;
+    const int box1 = LOAD == Load::kSmallPages && !second ? nb / 2 : nb;
     int pages = fetch(32 / nb), rows_l = PAGED ? row_of(0, fetch(0)) : 0, at = 0, slot = 0;
     uint32_t parity = 0;  // of the slot's present use
     int issued = 0;
@@ -545,17 +562,18 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
       // The whole warp runs the copies and one elected lane issues them, which keeps
       // their operands uniform (box i from lane i took a diverged warp's branches:
       // 16-token pages of a 64 x 4K batch 37.6 instead of 33.1 us).
-      expect_tx_elect(fb, kFbTile);
+      // The first of two producers arms the barrier; bytes may arrive before that.
+      if (!second) expect_tx_elect(fb, kFbTile);
       if constexpr (!PAGED) {
         tma_load_3d_elect(dst, map, fb, tx, ty, b * p.S_max + t0 + j * kFbKeys, pol);
       } else {
 #pragma unroll 1
-        for (int i = 0; i < nb; ++i)
+        for (int i = box0; i < box1; ++i)
           tma_load_3d_elect(dst + i * h * 128, map, fb, tx, ty,
                             __shfl_sync(0xffffffffu, rows_l, at + i), pol);
       }
       issued = j + 1;
-      if (!is_k && (j & ((1 << round_log2) - 1)) == 0) {
+      if (!is_k && !second && (j & ((1 << round_log2) - 1)) == 0) {
         // A round of terms.  What lies in its place belongs to tiles before j - 7
         // rounds, which the softmax is done with: V's slot of tile j - NS is empty.
         const int round = j >> round_log2;
@@ -1000,10 +1018,10 @@ __global__ void __launch_bounds__(Sh::kThreads, Sh::kPerSM)
   }
 }
 
-template <typename Sh, bool PAGED>
+template <typename Sh, Load LOAD>
 cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
                       const CUtensorMap& tm_v, bool prefetch, cudaStream_t stream) {
-  auto kern = gqa_decode_fp8_block_kernel<Sh, PAGED>;
+  auto kern = gqa_decode_fp8_block_kernel<Sh, LOAD>;
   constexpr int smem = Sh::kBytes;
   static unsigned char done[64];
   int dev = 0;
@@ -1018,7 +1036,7 @@ cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
   p.dec.prefetch_tiles = prefetch ? 3 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.dec.n_split, p.dec.H_kv / p.heads, p.dec.B);
-  cfg.blockDim = dim3(Sh::kThreads);
+  cfg.blockDim = dim3(Sh::threads(LOAD));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1036,12 +1054,16 @@ cudaError_t launch_fb_r(const DecodeBlockParams& p, const CUtensorMap& tm_k,
   // One CTA per SM at most: a deep ring.  More CTAs than SMs: two shallow rings
   // on each SM, where they fit.
   const bool one_wave = (long long)p.dec.n_split * (p.dec.H_kv / p.heads) * p.dec.B <= sms;
-  const bool paged = p.dec.block_table != nullptr;
-  if (one_wave)
-    return paged ? launch_fb<Deep, true>(p, tm_k, tm_v, true, stream)
-                 : launch_fb<Deep, false>(p, tm_k, tm_v, true, stream);
-  return paged ? launch_fb<Shallow, true>(p, tm_k, tm_v, false, stream)
-               : launch_fb<Shallow, false>(p, tm_k, tm_v, false, stream);
+  if (p.dec.block_table == nullptr)
+    return one_wave ? launch_fb<Deep, Load::kTile>(p, tm_k, tm_v, true, stream)
+                    : launch_fb<Shallow, Load::kTile>(p, tm_k, tm_v, false, stream);
+  if constexpr (Deep::R <= 32) {
+    if (p.dec.page_size == kSmallPage)
+      return one_wave ? launch_fb<Deep, Load::kSmallPages>(p, tm_k, tm_v, true, stream)
+                      : launch_fb<Shallow, Load::kSmallPages>(p, tm_k, tm_v, false, stream);
+  }
+  return one_wave ? launch_fb<Deep, Load::kPages>(p, tm_k, tm_v, true, stream)
+                  : launch_fb<Shallow, Load::kPages>(p, tm_k, tm_v, false, stream);
 }
 
 }  // namespace
