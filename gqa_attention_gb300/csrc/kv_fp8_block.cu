@@ -10,8 +10,10 @@
 // re-encoding of older codes are exact before their one rounding.
 #include <algorithm>
 
+
 #include "common.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace gqa {
 namespace {
@@ -47,13 +49,25 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
 // rounding, so they are read once.  Neighbouring CTAs take the heads of one block
 // of tokens, whose pieces of a row lie together, in the new rows (strided by a
 // fused projection's width) and in the cache.
+//
+// Bound by HBM for prompts (each new value read once, each code written once): 32K
+// tokens of 8 heads of 128, blocks of 64, 201 MB in 33.1 us, 6.08 TB/s.  That took
+// few instructions per value: rows by added strides and 32-bit comparisons, the
+// product on fp32 pairs, and the two rare cases (a scale that grew over older
+// codes, a present scale that is no power of two) in loops of their own; with all of it
+// in one loop 84% of the issue slots were in use and the same prompt took 37.1 us (8
+// prompts of 256 to 1K tokens 5.8 us, now 4.4).  Eight vectors a thread, where the
+// block has them, halve a thread's share of the set-up (four: 33.9 us).  Single tokens
+// are bound by a chain of latencies (length, page, new row and scale, block maximum,
+// store): 1.8 us for one sequence, 3.1 for 128.
 template <int D, int BLK>
 struct AppendShape {
   static constexpr int kVecRow = D / 8;            // 16-byte vectors of a bf16 row
   static constexpr int kVecs = BLK * kVecRow;      // of the whole block
-  static constexpr int kThreads = kVecs <= 256 ? 64 : kVecs <= 512 ? 128 : 256;
-  static constexpr int kPer = kVecs / kThreads;    // per thread: 4, or 8 for the largest block
-  static constexpr int kCtas = (kPer <= 4 ? 2048 : 1024) / kThreads;  // of an SM
+  static constexpr int kThreads = kVecs <= 512 ? 64 : kVecs <= 1024 ? 128 : 256;
+  static constexpr int kPer = kVecs / kThreads;    // per thread: 1, 2, 4 or 8
+  static constexpr int kStep = kThreads / kVecRow; // rows between a thread's vectors
+  static constexpr int kCtas = (kPer <= 4 ? 1536 : 1024) / kThreads;  // of an SM
 };
 
 template <int D, int BLK, bool PAGED>
@@ -79,14 +93,18 @@ __global__ void __launch_bounds__(AppendShape<D, BLK>::kThreads, AppendShape<D, 
   // The new rows first: they do not depend on where the block lies.
   const __nv_bfloat16* const src = (is_v ? p.v_new : p.k_new) + (size_t)b * p.T * p.new_stride +
                                    (size_t)kv * D;
+  const int r0 = threadIdx.x / Sh::kVecRow, c = threadIdx.x % Sh::kVecRow;
+  const int i0 = t0 + r0 - first_new;  // new row of the thread's first vector (negative: an older row)
   uint4 x[Sh::kPer];
+  {
+    const __nv_bfloat16* px = src + (long long)i0 * p.new_stride + c * 8;
+    const long long step = Sh::kStep * p.new_stride;
 #pragma unroll
-  for (int j = 0; j < Sh::kPer; ++j) {
-    const int e = threadIdx.x + j * Sh::kThreads;
-    const int t = t0 + e / Sh::kVecRow, c = e % Sh::kVecRow;
-    x[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (t >= first_new && t < L)
-      x[j] = *reinterpret_cast<const uint4*>(src + (size_t)(t - first_new) * p.new_stride + c * 8);
+    for (int j = 0; j < Sh::kPer; ++j, px += step) {
+      x[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (static_cast<unsigned>(i0 + j * Sh::kStep) < static_cast<unsigned>(n))
+        x[j] = *reinterpret_cast<const uint4*>(px);
+    }
   }
   int unit = b, at = t0;
   if constexpr (PAGED) {
@@ -145,50 +163,76 @@ __global__ void __launch_bounds__(AppendShape<D, BLK>::kThreads, AppendShape<D, 
   const int e_new = scale_exp(amax);
   const float s_new = pow2f(e_new);
   const float s = has_old && s_old >= s_new ? s_old : s_new;
-  // x / s: a product where s is a power of two, as it is unless the caller filled
-  // the scales with others
-  const bool exact_inv = s == s_new || (__float_as_uint(s) & 0x7fffffu) == 0u;
-  const float inv = s == s_new ? pow2f(-e_new) : 1.f / s;
-
+  const size_t code0 = ((row0 + r0) * p.H_kv + kv) * D + c * 8;  // of the first vector
+  const size_t code_step = (size_t)Sh::kStep * p.H_kv * D;
+  auto store = [&](int j, const uint32_t (&q)[4]) {
+    const size_t code = code0 + j * code_step;
+    if (in_bounds(code, 8, extent, p.err))
+      *reinterpret_cast<uint2*>(cache + code) =
+          make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+  };
+  if (has_old && s > s_old) {
+    // The older rows, under a scale that grew: their codes are rounded again.
+    const float ratio = s_old / s;
 #pragma unroll
-  for (int j = 0; j < Sh::kPer; ++j) {
-    const int e = threadIdx.x + j * Sh::kThreads;
-    const int t = t0 + e / Sh::kVecRow, c = e % Sh::kVecRow;
-    const size_t code = ((row0 + e / Sh::kVecRow) * p.H_kv + kv) * D + c * 8;
-    uint2* const dst = reinterpret_cast<uint2*>(cache + code);
-    uint32_t q[4];
-    if (t >= first_new && t < L) {
-      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
-        q[i] = exact_inv ? e4m3x2(lo * inv, hi * inv) : e4m3x2(lo / s, hi / s);
-      }
-    } else if (t < first_new && s > s_old) {
-      // An older row under a scale that grew: its codes are rounded again.
-      const float ratio = s_old / s;
-      const uint2 old = *dst;
+    for (int j = 0; j < Sh::kPer; ++j) {
+      if (i0 + j * Sh::kStep >= 0) continue;
+      const uint2 old = *reinterpret_cast<const uint2*>(cache + code0 + j * code_step);
       const uint32_t w[4] = {old.x & 0xffffu, old.x >> 16, old.y & 0xffffu, old.y >> 16};
+      uint32_t q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = e4m3x2_to_float2(w[i]);
         q[i] = e4m3x2(f.x * ratio, f.y * ratio);
       }
-    } else {
-      continue;
+      store(j, q);
     }
-    if (in_bounds(code, 8, extent, p.err))
-      *dst = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+  }
+  // x / s: a product where s is a power of two, as it is unless the caller filled
+  // the scales with others.
+  if (s == s_new || (__float_as_uint(s) & 0x7fffffu) == 0u) {
+    const float inv = s == s_new ? pow2f(-e_new) : 1.f / s;
+#pragma unroll
+    for (int j = 0; j < Sh::kPer; ++j) {
+      if (static_cast<unsigned>(i0 + j * Sh::kStep) >= static_cast<unsigned>(n)) continue;
+      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        fmul2(lo, hi, __uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u), inv, inv);
+        q[i] = e4m3x2(lo, hi);
+      }
+      store(j, q);
+    }
+  } else {
+#pragma unroll 1
+    for (int j = 0; j < Sh::kPer; ++j) {
+      if (static_cast<unsigned>(i0 + j * Sh::kStep) >= static_cast<unsigned>(n)) continue;
+      uint4 v = x[0];
+#pragma unroll
+      for (int k = 1; k < Sh::kPer; ++k)
+        if (j == k) v = x[k];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        q[i] = e4m3x2(__uint_as_float(w[i] << 16) / s, __uint_as_float(w[i] & 0xffff0000u) / s);
+      store(j, q);
+    }
   }
   if (threadIdx.x == 0 && in_bounds(sidx, 1, (size_t)p.units * p.per_blk * p.H_kv, p.err))
     scales[sidx] = s;
 }
 
 // ------------------------------------------------------------------ read ----
-// A thread turns pieces of 8 codes (an 8-byte load) into 8 bf16 values (a 16-byte
+// A thread turns pieces of 16 codes (a 16-byte load) into 16 bf16 values (a 32-byte
 // store), kReadPer of them in flight; consecutive threads take consecutive pieces
 // of a token's H_kv x D codes, which lie together in the cache and in the output.
-constexpr int kReadThreads = 256, kReadPer = 4;
+// Bound by HBM: 32K tokens of 8 heads of 128 in pages of 64, 201 MB in 32.0 us, 6.3
+// TB/s (pieces of 8 codes: 35.2 us with 78% of the issue slots in use; one piece in
+// flight 33.2, four 32.0).
+constexpr int kReadThreads = 256, kReadPer = 2;
 constexpr int kReadChunk = kReadThreads * kReadPer;  // pieces of a CTA
 
 template <bool PAGED>
@@ -202,18 +246,21 @@ __global__ void __launch_bounds__(kReadThreads) gqa_kv_read_kernel(const KvBlock
   const int L = p.seq_lens[b];
   const bool bad = L < 0 || L > p.S_max;
   if (bad && blockIdx.x == 0 && is_v == 0 && threadIdx.x == 0) atomicOr(p.err, kErrBadSeqLen);
-  const uint32_t row_vecs = p.H_kv * p.d / 8;  // pieces of a token
+  const uint32_t row_vecs = p.H_kv * p.d / 16;  // pieces of a token
   const int rows = bad ? p.S_out : min(p.S_out, L - p.start);  // (rows past L are left alone)
   const long long first = (long long)blockIdx.x * kReadChunk;
   const int i0 = static_cast<int>(first / row_vecs);
+  if (i0 >= rows) return;
   const uint32_t w0 = static_cast<uint32_t>(first - (long long)i0 * row_vecs);
   const size_t extent = (size_t)p.B * p.S_out * p.H_kv * p.d;
-  const int head_shift = p.d == 128 ? 4 : p.d == 64 ? 3 : 2;  // pieces of a head
+  const int head_shift = p.d == 128 ? 3 : p.d == 64 ? 2 : 1;  // pieces of a head
+  // piece u of this thread in the output, and in a sequence of a contiguous cache
+  const size_t dst0 = ((size_t)b * p.S_out * row_vecs + first + threadIdx.x) * 16;
+  const size_t src0 = (((size_t)b * p.per + p.start) * row_vecs + first + threadIdx.x) * 16;
 
-  uint2 w[kReadPer];
-  float s[kReadPer];
-  int row[kReadPer];  // of the output; -1: none, -2 - row: NaN
-  uint32_t piece[kReadPer];
+  uint4 w[kReadPer];
+  float s[kReadPer];  // (NaN for a row that cannot be read)
+  bool live[kReadPer];
 #pragma unroll
   for (int u = 0; u < kReadPer; ++u) {
     // piece w0 + threadIdx.x + u * 256 from row i0 on: its row by a multiplication
@@ -221,45 +268,48 @@ __global__ void __launch_bounds__(kReadThreads) gqa_kv_read_kernel(const KvBlock
     // where a row is longer than the chunk
     const uint32_t x = w0 + threadIdx.x + u * kReadThreads;
     const uint32_t q = row_vecs > kReadChunk ? (x >= row_vecs ? 1u : 0u) : __umulhi(x, p.row_magic);
-    piece[u] = x - q * row_vecs;
+    const uint32_t piece = x - q * row_vecs;
     const int i = i0 + static_cast<int>(q);
-    row[u] = i < rows ? i : -1;
-    w[u] = make_uint2(0u, 0u);
-    s[u] = 0.f;
-    if (row[u] < 0) continue;
+    live[u] = i < rows;
+    w[u] = make_uint4(0u, 0u, 0u, 0u);
+    s[u] = NAN;
+    if (!live[u] || bad) continue;
     int unit = b, at = p.start + i;
-    bool ok = !bad;
+    size_t src = src0 + u * kReadThreads * 16;
     if constexpr (PAGED) {
-      if (ok) {
-        unit = p.block_table[(size_t)b * p.max_blocks + (at >> p.page_log2)];
-        at &= p.page_size - 1;
-        if (unit < 0 || unit >= p.num_pages) {
-          ok = false;
-          atomicOr(p.err, kErrBadPage);
-        }
+      unit = p.block_table[(size_t)b * p.max_blocks + (at >> p.page_log2)];
+      at &= p.page_size - 1;
+      if (unit < 0 || unit >= p.num_pages) {
+        atomicOr(p.err, kErrBadPage);
+        continue;
       }
+      src = (((size_t)unit * p.per + at) * row_vecs + piece) * 16;
     }
-    if (!ok) {
-      row[u] = -2 - i;
-      continue;
-    }
-    w[u] = *reinterpret_cast<const uint2*>(
-        cache + (((size_t)unit * p.per + at) * row_vecs + piece[u]) * 8);
+    w[u] = *reinterpret_cast<const uint4*>(cache + src);
     s[u] = scales[((size_t)unit * p.per_blk + (at >> p.block_log2)) * p.H_kv +
-                  (piece[u] >> head_shift)];
+                  (piece >> head_shift)];
   }
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
 #pragma unroll
   for (int u = 0; u < kReadPer; ++u) {
-    if (row[u] == -1) continue;
-    const bool nan = row[u] < 0;
-    const float2 f0 = e4m3x2_to_float2(w[u].x), f1 = e4m3x2_to_float2(w[u].x >> 16);
-    const float2 f2 = e4m3x2_to_float2(w[u].y), f3 = e4m3x2_to_float2(w[u].y >> 16);
-    uint4 o = make_uint4(pack_bf16x2(f0.x * s[u], f0.y * s[u]), pack_bf16x2(f1.x * s[u], f1.y * s[u]),
-                         pack_bf16x2(f2.x * s[u], f2.y * s[u]), pack_bf16x2(f3.x * s[u], f3.y * s[u]));
-    if (nan) o = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-    const int i = nan ? -2 - row[u] : row[u];
-    const size_t dst = (((size_t)b * p.S_out + i) * row_vecs + piece[u]) * 8;
-    if (in_bounds(dst, 8, extent, p.err)) *reinterpret_cast<uint4*>(out + dst) = o;
+    if (!live[u]) continue;
+    const uint32_t c[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = e4m3x2_to_float2(i & 1 ? c[i / 2] >> 16 : c[i / 2]);
+      float lo, hi;
+      fmul2(lo, hi, f.x, f.y, s[u], s[u]);
+      o[i] = pack_bf16x2(lo, hi);
+    }
+    const size_t dst = dst0 + u * kReadThreads * 16;
+    if (!in_bounds(dst, 16, extent, p.err)) continue;
+    if (wide) {
+      st_global_v8(out + dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+    } else {
+      *reinterpret_cast<uint4*>(out + dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(out + dst + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
   }
 }
 
@@ -314,7 +364,7 @@ cudaError_t launch_kv_append(const KvBlockParams& p, cudaStream_t stream) {
 
 cudaError_t launch_kv_read(const KvBlockParams& p_in, cudaStream_t stream) {
   KvBlockParams p = p_in;
-  const int row_vecs = p.H_kv * p.d / 8;
+  const int row_vecs = p.H_kv * p.d / 16;
   p.row_magic = static_cast<uint32_t>((0x100000000ull + row_vecs - 1) / row_vecs);
   const long long chunks = ((long long)p.S_out * row_vecs + kReadChunk - 1) / kReadChunk;
   if (chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
