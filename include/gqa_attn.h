@@ -542,8 +542,9 @@ gqa_status gqa_attn_decode_paged_fp8_block(const void* q, const void* k_pool, co
                                            float* lse, gqa_stream_t stream);
 
 /* Split count for gqa_attn_decode_fp8_block on the current device: 1 for S_max <=
- * 1024, otherwise at most one CTA per SM, with splits of at least 256 tokens and
- * at most 8192.  Returns >= 1 (1 for invalid input). */
+ * 1024, otherwise at most one CTA per SM with splits of at least 256 tokens, or more
+ * where they would hold over 8192 tokens each (4096 for several sequences of over
+ * 32768).  Returns >= 1 (1 for invalid input). */
 int gqa_attn_decode_fp8_block_default_splits(int B, int T_q, int H_q, int H_kv, int S_max);
 
 /* ------------------------------------------------------------------------
