@@ -814,22 +814,42 @@ gqa_status gqa_attn_decode_paged_fp8_block(const void* q, const void* k_pool, co
 
 int gqa_attn_decode_fp8_block_default_splits(int B, int T_q, int H_q, int H_kv, int S_max) {
   if (B < 1 || T_q < 1 || H_q < 1 || H_kv < 1 || S_max < 1 || H_q % H_kv != 0) return 1;
-  if (S_max <= 1024) return 1;  // (as gqa_attn_decode_default_splits: one launch)
   const long long groups = (long long)B * H_kv;
+  const int rows = (int)std::min<long long>((long long)T_q * (H_q / H_kv), 1 << 20);
   long long n = num_sms_current_device() / groups;
-  // Up to 16 query rows a split streams at the HBM rate, and a multiple of four
-  // splits measured best (Llama3-70B heads, 16 against 19 splits: 15.6 / 16.2 us at
-  // 32K, 8.5 / 9.1 at 8K; two sequences, 8 against 9: 24.5 / 25.5); more rows are
-  // bound by the softmax and want every SM (8 tokens: 40.3 / 37.6 us).
-  if (T_q * (H_q / H_kv) <= 16 && n > 4) n -= n % 4;
-  const long long most = ((long long)S_max + 255) / 256;  // at least two tiles each
-  // several long sequences are seldom equally long: finer splits even them out (the
-  // ragged batch of eight up to 128K: 266 us at 8192 tokens a split, 261 at 4096)
-  const int longest = B > 1 && S_max > 32768 ? 4096 : 8192;
+  // Up to 1024 tokens one launch, as gqa_attn_decode_default_splits, but for more than 32
+  // rows: a tile of theirs takes 1.8 us, the merge 2.5 (512 tokens, 64 rows: 13.0 us in
+  // one split, 11.1 in four).
+  const long long tiles = ((long long)S_max + 127) / 128;
+  if (S_max <= 1024) return rows > 32 && n >= 4 && tiles >= 4 ? (int)std::min(n, tiles) : 1;
+  // Up to 16 query rows a split streams at the HBM rate, and from eight on a multiple
+  // of four splits measured best (Llama3-70B heads, 16 against 19 splits: 7.2 / 8.1 us at
+  // 4K, 10.1 / 10.4 at 16K; two sequences, 8 against 9: 8.1 / 8.6); more rows are bound
+  // by the softmax and want every SM (8 tokens at 32K, 16 / 19: 40.3 / 37.6 us).
+  if (rows <= 16 && n >= 8) n -= n % 4;
+  n = std::max(1LL, std::min(n, (tiles + 1) / 2));  // at least two tiles each
+  // Grids that fill the GPU without splits are split all the same where sequences are
+  // long, since several are seldom equally long (8 x 100 to 10K: 24.6 us in three splits,
+  // 22.4 in four; 8 x 10K 31.5 and 32.3).  With more than 8 rows an SM holds one CTA
+  // instead of two, and what a second wave of them costs weighs more (16 x 16K, 32 rows: 87
+  // us in one split, 106 in two), so they are split later.  Of the counts from there on,
+  // the one whose last wave leaves the fewest SMs idle is taken (64 rows, 24 x 24K, 4 KV heads:
+  // 178 us in three splits, 220 in one, 240 in two).
+  const int longest = rows > 8 ? 32768 : B > 1 && S_max > 8192 ? 4096 : 8192;
   const long long fill = ((long long)S_max + longest - 1) / longest;
-  if (n > most) n = most;
-  if (n < fill) n = fill;
-  if (n < 1) n = 1;
+  const long long least = std::max(n, fill);
+  long long last = fill > n ? fill + fill / 2 : n;
+  if (rows > 8) last = std::max(last, std::min(3LL, tiles / 20));
+  const long long sms = num_sms_current_device();
+  double best = 0;
+  for (long long c = least; c <= last; ++c) {
+    const long long ctas = c * groups, wave = rows > 8 || ctas <= sms ? sms : 2 * sms;
+    const double used = (double)ctas / (double)((ctas + wave - 1) / wave * wave);
+    if (used > best + 0.01) {
+      best = used;
+      n = c;
+    }
+  }
   return (int)n;
 }
 

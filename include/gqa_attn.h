@@ -541,10 +541,11 @@ gqa_status gqa_attn_decode_paged_fp8_block(const void* q, const void* k_pool, co
                                            float scale, int n_split, void* workspace, void* out,
                                            float* lse, gqa_stream_t stream);
 
-/* Split count for gqa_attn_decode_fp8_block on the current device: 1 for S_max <=
- * 1024, otherwise at most one CTA per SM with splits of at least 256 tokens, or more
- * where they would hold over 8192 tokens each (4096 for several sequences of over
- * 32768).  Returns >= 1 (1 for invalid input). */
+/* Split count for gqa_attn_decode_fp8_block on the current device: 1 for S_max <= 1024 (up
+ * to S_max / 128 for more than 32 query rows), otherwise at most one CTA per SM with
+ * splits of at least 256 tokens, or more CTAs where a split would hold over 8192 tokens
+ * (4096 for several sequences; 32768 for more than 8 query rows).  Returns >= 1 (1 for
+ * invalid input). */
 int gqa_attn_decode_fp8_block_default_splits(int B, int T_q, int H_q, int H_kv, int S_max);
 
 /* ------------------------------------------------------------------------
