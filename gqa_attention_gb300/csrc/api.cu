@@ -633,6 +633,20 @@ gqa_status run_kv_read(gqa::KvBlockParams* p, int start, int S_out, void* k_out,
   return cuda_status(gqa::launch_kv_read(*p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Pieces of a batch that the kernel cuts by its lengths, for each of `groups` groups of
+// heads; 0: splits are even ones of S_max.  For more than 16 query rows, which are bound by
+// the softmax, so that an SM without work is lost (fewer are bound by HBM, and ragged
+// batches within 10% either way), where that leaves at least two pieces a sequence and
+// pieces of 16 tiles on average.  64 rows, 8 sequences, 8 KV heads: 100 to 10K tokens 65.8 us in
+// even splits, 48.8 cut by the lengths; 100 to 33K 167 and 115; all of 10K 65.5 and 69.2,
+// since the cut takes the lengths' round trip before the first load.  One sequence, and few
+// pieces each (16 sequences: 104 and 104 us, all of 10K 104 and 120), are split evenly.
+int length_pieces(int B, long long groups, int rows, int S_max) {
+  const long long sms = num_sms_current_device(), pieces = sms / groups;
+  const long long tiles = ((long long)S_max + 127) / 128;
+  return rows > 16 && B > 1 && pieces >= 2LL * B && tiles * B * groups >= 16 * sms ? (int)pieces : 0;
+}
+
 gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int T_q, int H_q,
                                 float scale, int n_split, void* workspace, void* out, float* lse,
                                 gqa_stream_t stream) {
@@ -685,6 +699,9 @@ gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int 
   p.per_blk = c.per_blk;
   p.heads = packed ? 4 : 1;
   p.head_rows = head_rows;
+  p.pieces = n_split == 1 ? 0
+                          : length_pieces(c.B, c.H_kv / p.heads, packed ? 4 * head_rows : T_q * G,
+                                          c.S_max);
   gqa::DecodeParams& dp = p.dec;
   dp.q = static_cast<const __nv_bfloat16*>(q);
   dp.seq_lens = c.seq_lens;
@@ -817,6 +834,9 @@ int gqa_attn_decode_fp8_block_default_splits(int B, int T_q, int H_q, int H_kv, 
   const long long groups = (long long)B * H_kv;
   const int rows = (int)std::min<long long>((long long)T_q * (H_q / H_kv), 1 << 20);
   long long n = num_sms_current_device() / groups;
+  // Cut by the lengths: room for twice as many pieces of a sequence as they have on average.
+  const int pieces = length_pieces(B, H_kv, rows, S_max);
+  if (pieces > 0) return 2 * ((pieces + B - 1) / B);
   // Up to 1024 tokens one launch, as gqa_attn_decode_default_splits, but for more than 32
   // rows: a tile of theirs takes 1.8 us, the merge 2.5 (512 tokens, 64 rows: 13.0 us in
   // one split, 11.1 in four).

@@ -55,6 +55,61 @@ constexpr float kPScaleLog2 = 7.f;          // P is held times 2^7
 constexpr float kPMaxLog2 = 8.f;            // and must not pass 2^8
 constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100: smaller ones count as zero
 
+// A CTA's share of a batch whose splits follow the sequences' lengths: piece `split` of
+// `count` of sequence b, each of `tiles` tiles (b < 0: none).
+struct Piece {
+  int b, split, count, tiles;
+};
+// The batch is cut into pieces of as many tiles as are needed for at most `pieces` of them
+// (and n_split of a sequence; every sequence has one, also one of a bad length), and
+// this CTA takes piece blockIdx.x in the order of the sequences.  One warp; every
+// warp of the grid finds the same cut.
+__device__ __forceinline__ Piece find_piece(const DecodeParams& p, int pieces, int lane) {
+  auto tiles_of = [&](int s) {
+    const int L = p.seq_lens[s];
+    return L < p.T_q || L > p.S_max ? 0 : (L + kFbKeys - 1) / kFbKeys;
+  };
+  int total = 0, most = 1;
+  for (int s = lane; s < p.B; s += 32) {
+    const int t = tiles_of(s);
+    total += t;
+    most = max(most, t);
+  }
+  // (fewer than 2^24 tiles of one sequence, and at most 2^7 sequences)
+  const long long all = static_cast<long long>(__reduce_add_sync(0xffffffffu, total >> 12)) * 4096 +
+                        __reduce_add_sync(0xffffffffu, total & 4095);
+  most = __reduce_max_sync(0xffffffffu, most);
+  int lo = static_cast<int>(max((all + pieces - 1) / pieces, (most + p.n_split - 1LL) / p.n_split));
+  lo = max(lo, 1);
+  // sum of ceil(t / c) <= all / c + B
+  int hi = static_cast<int>(min((long long)most, max((long long)lo, all / (pieces - p.B) + 1)));
+  while (lo < hi) {
+    const int c = (lo + hi) / 2;
+    int need = 0;
+    for (int s = lane; s < p.B; s += 32) need += max(1, (tiles_of(s) + c - 1) / c);
+    if (static_cast<int>(__reduce_add_sync(0xffffffffu, need)) <= pieces) hi = c;
+    else lo = c + 1;
+  }
+  int left = blockIdx.x;
+  for (int s0 = 0; s0 < p.B; s0 += 32) {
+    const int mine = s0 + lane < p.B ? max(1, (tiles_of(s0 + lane) + hi - 1) / hi) : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, upto > left);
+    if (past != 0) {
+      const int who = __ffs(past) - 1;
+      const int count = __shfl_sync(0xffffffffu, mine, who);
+      return {s0 + who, left - (__shfl_sync(0xffffffffu, upto, who) - count), count, hi};
+    }
+    left -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return {-1, 0, 0, hi};
+}
+
 // How the codes of a tile are loaded: one box of a contiguous cache, a box for each
 // page, or, for pages of 16 tokens and up to 32 query rows, such boxes by two warps each
 // for K and V.  A warp takes about 150 cycles to issue a box, so the eight of a tile
@@ -316,13 +371,13 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x, b = blockIdx.z;
+  int split = blockIdx.x, b = blockIdx.z, chunk = p.chunk;
   // KV heads hc blockIdx.y + 0 .. hc - 1 share the 128-byte rows of a tile (hc = 4 packed
   // heads of d = 32, or 1).  Head hl has the query rows r = hl rp + q, q < T_q * G.
   const int hc = pb.heads, rp = pb.head_rows, kv0 = blockIdx.y * hc;
   // first key of the split (rows of a cache are below 2^31 - 256, so keys of a
   // tile past its end still fit)
-  const int t0 = static_cast<int>(min((long long)split * p.chunk, (long long)p.S_max));
+  int t0 = static_cast<int>(min((long long)split * chunk, (long long)p.S_max));
   const int G = p.G, rows = p.T_q * G;  // of a head
   const int D = p.d;
   // Head of row r (rows past the last head's count as its padding).
@@ -388,7 +443,7 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
     int L_hint;
     asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(L_hint) : "l"(p.seq_lens + b));
     const int tk = t0 + i * kFbKeys + sub * h;
-    if (i < p.prefetch_tiles && tk < min(min(p.S_max, L_hint), t0 + min(p.chunk, p.S_max - t0))) {
+    if (i < p.prefetch_tiles && tk < min(min(p.S_max, L_hint), t0 + min(chunk, p.S_max - t0))) {
       int row = b * p.S_max + tk;
       bool ok = true;
       if constexpr (PAGED) {
@@ -410,6 +465,25 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
   const uint32_t tmem = tmem_base_sh;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  bool none = false;  // (a CTA past the batch's last piece)
+  if (R > 16 && pb.pieces > 0) {
+    const Piece mine = find_piece(p, pb.pieces, lane);
+    none = mine.b < 0;
+    b = max(mine.b, 0);
+    split = mine.split;
+    chunk = mine.tiles * kFbKeys;
+    t0 = split * chunk;
+    // the slots of the workspace that the sequence has no pieces for: the merge identity
+    if (!none && split == mine.count - 1) {
+      const int spare = p.n_split - mine.count;
+      for (int i = threadIdx.x; i < R * spare; i += Sh::threads(LOAD)) {
+        const int r = i / spare;
+        const size_t at = (size_t)out_row(live_row(r) ? r : 0) * p.n_split + mine.count + i % spare;
+        if (live_row(r) && in_bounds(at, 1, n_rows * p.n_split, p.err))
+          p.ws_ml[at] = make_float2(-INFINITY, 0.f);
+      }
+    }
+  }
   // The softmax warps' rows of Q travel together with the length: row sw, sw +
   // kWarps, ..; lane takes columns 4 lane .. 4 lane + 3.
   const int sw = warp - 4;
@@ -425,14 +499,14 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
   }
   const int L = p.seq_lens[b];
   const bool bad = L < p.T_q || L > p.S_max;  // (L >= T_q >= 1 otherwise)
-  const int t_end = bad ? 0 : min(t0 + min(p.chunk, p.S_max - t0), L);
+  const int t_end = bad || none ? 0 : min(t0 + min(chunk, p.S_max - t0), L);
   const int n = t_end > t0 ? (t_end - t0 + kFbKeys - 1) / kFbKeys : 0;
   if (bad || n == 0) {
     // A bad length: NaN outputs and the error bit.  An empty split: the merge
     // identity (-inf, 0); its O is not written.  (One split is never empty.)
     if (bad && threadIdx.x == 0 && split == 0 && kv0 == 0) atomicOr(p.err, kErrBadSeqLen);
     for (int r = threadIdx.x; r < R; r += Sh::threads(LOAD)) {
-      if (!live_row(r)) continue;
+      if (none || !live_row(r)) continue;
       const size_t row = out_row(r);
       if (p.n_split == 1) {
         if (in_bounds(row * D, D, n_rows * D, p.err))
@@ -1038,9 +1112,10 @@ cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
     if (dev >= 0 && dev < 64) done[dev] = 1;
   }
   DecodeBlockParams p = p_in;
-  p.dec.prefetch_tiles = prefetch ? 3 : 0;
+  p.dec.prefetch_tiles = prefetch && p.pieces == 0 ? 3 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.dec.n_split, p.dec.H_kv / p.heads, p.dec.B);
+  cfg.gridDim = p.pieces > 0 ? dim3(p.pieces, p.dec.H_kv / p.heads)
+                             : dim3(p.dec.n_split, p.dec.H_kv / p.heads, p.dec.B);
   cfg.blockDim = dim3(Sh::threads(LOAD));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1059,7 +1134,8 @@ cudaError_t launch_fb_r(const DecodeBlockParams& p, const CUtensorMap& tm_k,
   // One CTA per SM at most: a deep ring, and the first tiles prefetched into L2 while
   // the previous kernel ends.  More CTAs than SMs: two shallow rings on each SM (8 rows;
   // the larger shapes hold one CTA per SM either way).
-  const bool one_wave = (long long)p.dec.n_split * (p.dec.H_kv / p.heads) * p.dec.B <= sms;
+  const long long per_group = p.pieces > 0 ? p.pieces : (long long)p.dec.n_split * p.dec.B;
+  const bool one_wave = per_group * (p.dec.H_kv / p.heads) <= sms;
   if (p.dec.block_table == nullptr)
     return one_wave ? launch_fb<Deep, Load::kTile>(p, tm_k, tm_v, true, stream)
                     : launch_fb<Shallow, Load::kTile>(p, tm_k, tm_v, false, stream);
@@ -1078,6 +1154,7 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockParams& p, const CUtensorMa
                                     const CUtensorMap& tm_v, int sms, cudaStream_t stream) {
   const int rows = p.heads == 1 ? p.dec.T_q * p.dec.G : p.heads * p.head_rows;
   if (rows < 1 || rows > 64 || p.dec.chunk % kFbKeys != 0) return cudaErrorInvalidValue;
+  if (p.pieces > 0 && (rows <= 16 || p.pieces < 2 * p.dec.B)) return cudaErrorInvalidValue;
   if (rows <= 8)
     return launch_fb_r<FbShape<8, 6, 2, 1>, FbShape<8, 3, 2, 1>>(p, tm_k, tm_v, sms, stream);
   if (rows <= 16)

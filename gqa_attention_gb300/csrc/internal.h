@@ -109,6 +109,10 @@ struct DecodeBlockParams {
   // of d = 32 (the map's rows are whole tokens; H_kv is a multiple of 4); then each
   // has head_rows = T_q * G rounded up to 8 of the CTA's query rows.
   int heads, head_rows;
+  // Splits by the lengths (more than 16 query rows): the batch of B <= pieces / 2 sequences is
+  // cut into at most `pieces` pieces of equal numbers of tiles, at most n_split of a
+  // sequence, and grid x is the piece.  0: split x of sequence z has dec.chunk keys.
+  int pieces;
 };
 
 // Byte offset of the O partials in a chunk-split prefill workspace.

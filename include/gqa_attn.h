@@ -515,7 +515,11 @@ gqa_status gqa_kv_read_paged_fp8_block(const void* k_pool, const void* v_pool,
 /* Decode of the last T_q positions of each sequence over that cache: queries,
  * visibility, outputs and workspace are those of gqa_attn_decode_multi() (q and out
  * bf16 [B, T_q, H_q, d], lse fp32 [B, T_q, H_q]; 1 <= T_q <= seq_lens[b] <= S_max),
- * with splits of ceil(S_max / n_split) keys rounded up to 128.  With n_split > 1
+ * with splits of ceil(S_max / n_split) keys rounded up to 128; or, for batches with
+ * more than 16 query rows per KV head (T_q * G) and n_split > 1 whose sequences have
+ * two SMs each or more and work for them, at most n_split splits of a sequence, cut on the device
+ * so that the batch's lengths fill the GPU (a sequence's splits, and so the rounding
+ * of its outputs, then depend on the other lengths too).  With n_split > 1
  * the partials go to `workspace` (gqa_attn_decode_workspace_bytes(B * T_q, H_q, d,
  * n_split) bytes, 256-byte aligned, in gqa_attn_decode's layout) and a second
  * launch merges them into out and lse: no gqa_attn_decode_combine() follows.
@@ -544,8 +548,9 @@ gqa_status gqa_attn_decode_paged_fp8_block(const void* q, const void* k_pool, co
 /* Split count for gqa_attn_decode_fp8_block on the current device: 1 for S_max <= 1024 (up
  * to S_max / 128 for more than 32 query rows), otherwise at most one CTA per SM with
  * splits of at least 256 tokens, or more CTAs where a split would hold over 8192 tokens
- * (4096 for several sequences; 32768 for more than 8 query rows).  Returns >= 1 (1 for
- * invalid input). */
+ * (4096 for several sequences; 32768 for more than 8 query rows).  Where the splits are
+ * cut by the lengths, twice their number per sequence.  Returns >= 1 (1 for invalid
+ * input). */
 int gqa_attn_decode_fp8_block_default_splits(int B, int T_q, int H_q, int H_kv, int S_max);
 
 /* ------------------------------------------------------------------------

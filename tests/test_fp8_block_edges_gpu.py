@@ -246,6 +246,66 @@ def test_results_on_a_stream_of_the_callers(kind):
             assert torch.equal(x, y)
 
 
+# ------------------------------------------------------- splits cut by the lengths --
+@pytest.mark.parametrize("T_q,G", [(4, 8), (8, 8), (17, 1), (3, 7)])
+@pytest.mark.parametrize("page", [0, 128])
+def test_splits_cut_by_the_lengths(T_q, G, page):
+    """Ragged batches of many query rows: one long sequence and short ones, equal ones, all of
+    the shortest length, a bad length among good ones, with room for few or many splits."""
+    B, H, d, S = 6, 2, 64, 26000  # 12 of 152 SMs' groups, 204 tiles
+    c = Cache(B, S, H, d, 128, page, seed=T_q + G)
+    k, v = c.rows(9000)
+    c.append(k, v, [9000, T_q, 128, 4000, 127 + T_q, 1000])
+    for n_split in (2, 5, 24, None):
+        out, lse = check_decode(c, T_q, G, n_split, what=f"{n_split}")
+    q = torch.randn(B, T_q, H * G, d, generator=c.gen).to(torch.bfloat16).to(DEV)
+
+    def run(lens, n_split=None):
+        return g.decode_fp8_block(q, *c.args(), torch.tensor(lens, dtype=torch.int32, device=DEV), 128,
+                                  n_split=n_split, block_table=c.table)
+
+    good = run(c.len)
+    for bad in (S + 200, T_q - 1, -1):
+        out, lse = run([c.len[0], bad, *c.len[2:]])
+        assert g.gqa_last_device_error() == g.GQA_ERR_INVALID_ARG
+        assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
+        for x, y in ((out, good[0]), (lse, good[1])):
+            # the others: the same sums in another cut, each within (2^-8 + 2^-9) of values
+            # below 1.3, whose difference is below 2^-6
+            rest = [0, 2, 3, 4, 5]
+            assert bool(((x[rest] - y[rest]).abs().float() <= 2.0 ** -6).all())
+    again = run(c.len)
+    assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+    for lens in ([T_q] * B, [9000, T_q, T_q, 4000, T_q, 640], [min(n, 64 + 40 * T_q) for n in c.len]):
+        c.len = [max(T_q, min(n, m)) for n, m in zip(lens, (9000, T_q, 128, 4000, 127 + T_q, 1000))]
+        for n_split in (3, None):
+            check_decode(c, T_q, G, n_split, q=q.cpu(), what=f"{c.len}")
+
+
+def test_splits_cut_by_the_lengths_follow_a_captured_step():
+    """The cut is made on the device: a captured call replayed with other lengths."""
+    B, H, d, S, T_q, G = 4, 4, 32, 20000, 5, 4  # 16 groups of heads, 157 tiles
+    c = Cache(B, S, H, d, 64, 0, seed=71)
+    k, v = c.rows(6000)
+    c.append(k, v, [6000, 3000, 700, T_q])
+    q = torch.randn(B, T_q, H * G, d, generator=c.gen).to(torch.bfloat16)
+    qd, lens = q.to(DEV), c.lens()
+    out, lse = g.decode_fp8_block(qd, *c.args(), lens, 64)
+    ws = g.decode_workspace(B * T_q, H * G, d, 16)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        g.decode_fp8_block(qd, *c.args(), lens, 64, n_split=16, workspace=ws, out=out, lse=lse)
+    for new in ([6000, 3000, 700, T_q], [T_q, 3000, 64, T_q], [5999, 129, 128, T_q]):
+        c.len = new
+        lens.copy_(c.lens())
+        graph.replay()
+        torch.cuda.synchronize()
+        o, l, to, tl = c.expect(q, 1 / math.sqrt(d))
+        assert (np.abs(out.double().cpu().numpy() - o) <= to).all()
+        assert (np.abs(lse.double().cpu().numpy() - l) <= tl).all()
+
+
 # -------------------------------------------------------- the bounds-checking build --
 @pytest.fixture(scope="module")
 def checking(tmp_path_factory):
