@@ -37,7 +37,7 @@
 //
 // What bounds it (device time with the merge, 8 KV heads of 128, 32K tokens): 8 query rows
 // 14.6 us for 67 MB, the tiles at HBM's rate after about 5 us of start and merge; 16
-// rows 16.3, 32 rows 20.3, 64 rows 30.4, the softmax of R weights a key in two terms.
+// rows 16.3, 32 rows 20.3, 64 rows 30.8, the softmax of R weights a key in two terms.
 // One CTA takes 0.35 us a tile with 8 rows, 1.8 us with 64.
 //
 // Roles: warps 0 and 3 TMA producers of K and V (and two more at the end, for small

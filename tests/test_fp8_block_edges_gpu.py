@@ -1,7 +1,7 @@
 """The block-scaled E4M3 cache where it can go wrong: NaN in masked places, heads that
 share a tile, scales the caller wrote, pools past 32-bit offsets, memory around the
-buffers, streams of the caller's, two sequences on one page, and the bounds-checking
-build against the default build."""
+buffers, streams of the caller's, two sequences on one page, batches cut by their lengths,
+and the bounds-checking build against the default build."""
 import math
 
 import numpy as np
