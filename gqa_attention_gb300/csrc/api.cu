@@ -638,13 +638,14 @@ gqa_status run_kv_read(gqa::KvBlockParams* p, int start, int S_out, void* k_out,
 // the softmax, so that an SM without work is lost (fewer are bound by HBM, and ragged
 // batches within 10% either way), where that leaves at least two pieces a sequence and
 // pieces of 16 tiles on average.  64 rows, 8 sequences, 8 KV heads: 100 to 10K tokens 65.8 us in
-// even splits, 48.8 cut by the lengths; 100 to 33K 167 and 115; all of 10K 65.5 and 69.2,
-// since the cut takes the lengths' round trip before the first load.  One sequence, and few
-// pieces each (16 sequences: 104 and 104 us, all of 10K 104 and 120), are split evenly.
+// even splits, 48.5 cut by the lengths; 100 to 33K 167 and 115; all of 10K 65.5 and 70.6,
+// since the cut takes time before the first load.  32 rows: 38.8 and 29.6, all of 10K 38.6 and
+// 41.5.  One sequence, and few pieces each (64 rows, 16 sequences: 104 and 104 us, all of
+// 10K 104 and 120), are split evenly.
 int length_pieces(int B, long long groups, int rows, int S_max) {
   const long long sms = num_sms_current_device(), pieces = sms / groups;
   const long long tiles = ((long long)S_max + 127) / 128;
-  return rows > 16 && B > 1 && pieces >= 2LL * B && tiles * B * groups >= 16 * sms ? (int)pieces : 0;
+  return rows > 16 && B > 1 && B <= 96 && pieces >= 2LL * B && tiles * B * groups >= 16 * sms ? (int)pieces : 0;
 }
 
 gqa_status run_decode_fp8_block(const gqa::KvBlockParams& c, const void* q, int T_q, int H_q,

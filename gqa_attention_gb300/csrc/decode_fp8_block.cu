@@ -62,37 +62,33 @@ struct Piece {
 };
 // The batch is cut into pieces of as many tiles as are needed for at most `pieces` of them
 // (and n_split of a sequence; every sequence has one, also one of a bad length), and
-// this CTA takes piece blockIdx.x in the order of the sequences.  One warp; every
-// warp of the grid finds the same cut.
-__device__ __forceinline__ Piece find_piece(const DecodeParams& p, int pieces, int lane) {
-  auto tiles_of = [&](int s) {
-    const int L = p.seq_lens[s];
-    return L < p.T_q || L > p.S_max ? 0 : (L + kFbKeys - 1) / kFbKeys;
-  };
-  int total = 0, most = 1;
-  for (int s = lane; s < p.B; s += 32) {
-    const int t = tiles_of(s);
-    total += t;
-    most = max(most, t);
-  }
-  // (fewer than 2^24 tiles of one sequence, and at most 2^7 sequences)
+// this CTA takes piece `index` in the order of the sequences.  One warp, lane i with
+// the tiles of sequences i, 32 + i and 64 + i (0: a bad length); every warp of the
+// grid finds the same cut.
+constexpr int kMaxCut = 96;  // sequences
+__device__ __noinline__ Piece find_piece(int t0, int t1, int t2, int B, int n_split, int pieces,
+                                         int index, int lane) {
+  const int total = t0 + t1 + t2;  // (each below 2^24)
   const long long all = static_cast<long long>(__reduce_add_sync(0xffffffffu, total >> 12)) * 4096 +
                         __reduce_add_sync(0xffffffffu, total & 4095);
-  most = __reduce_max_sync(0xffffffffu, most);
-  int lo = static_cast<int>(max((all + pieces - 1) / pieces, (most + p.n_split - 1LL) / p.n_split));
-  lo = max(lo, 1);
+  const int most = max(1, __reduce_max_sync(0xffffffffu, max(max(t0, t1), t2)));
+  auto cuts = [&](int t, int k, int c) {  // pieces of sequence 32 k + lane
+    return 32 * k + lane < B ? max(1, (t + c - 1) / c) : 0;
+  };
+  int lo = max(1, static_cast<int>(max((all + pieces - 1) / pieces,
+                                       (most + n_split - 1LL) / n_split)));
   // sum of ceil(t / c) <= all / c + B
-  int hi = static_cast<int>(min((long long)most, max((long long)lo, all / (pieces - p.B) + 1)));
+  int hi = static_cast<int>(min((long long)most, max((long long)lo, all / (pieces - B) + 1)));
   while (lo < hi) {
     const int c = (lo + hi) / 2;
-    int need = 0;
-    for (int s = lane; s < p.B; s += 32) need += max(1, (tiles_of(s) + c - 1) / c);
+    const int need = cuts(t0, 0, c) + cuts(t1, 1, c) + cuts(t2, 2, c);
     if (static_cast<int>(__reduce_add_sync(0xffffffffu, need)) <= pieces) hi = c;
     else lo = c + 1;
   }
-  int left = blockIdx.x;
-  for (int s0 = 0; s0 < p.B; s0 += 32) {
-    const int mine = s0 + lane < p.B ? max(1, (tiles_of(s0 + lane) + hi - 1) / hi) : 0;
+  int left = index;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int mine = cuts(k == 0 ? t0 : k == 1 ? t1 : t2, k, hi);
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -103,7 +99,7 @@ __device__ __forceinline__ Piece find_piece(const DecodeParams& p, int pieces, i
     if (past != 0) {
       const int who = __ffs(past) - 1;
       const int count = __shfl_sync(0xffffffffu, mine, who);
-      return {s0 + who, left - (__shfl_sync(0xffffffffu, upto, who) - count), count, hi};
+      return {32 * k + who, left - (__shfl_sync(0xffffffffu, upto, who) - count), count, hi};
     }
     left -= __shfl_sync(0xffffffffu, upto, 31);
   }
@@ -116,7 +112,8 @@ __device__ __forceinline__ Piece find_piece(const DecodeParams& p, int pieces, i
 // take longer than its softmax: batch 16 of 4K to 60K tokens, two queries, 249 us with
 // one warp, 215 with two; 64 x 4K, d = 64, 28.4 and 26.9.  At 32 tokens the four boxes fit
 // (23.8 us, and 24.7 with the registers of two more warps), as they do beside 64
-// rows' softmax (32K, eight queries: 31.6 and 34.4).
+// rows' softmax (32K, eight queries: 31.6 and 34.4) and in batches cut by their lengths (32
+// rows, 8 x 100 to 10K: 31.9 and 32.4).
 enum class Load { kTile, kPages, kSmallPages };
 constexpr int kSmallPage = 16;
 
@@ -334,7 +331,7 @@ __device__ __forceinline__ ScaleTerms scale_terms(float ks, float vs) {
   return s;
 }
 
-template <typename Sh, Load LOAD>
+template <typename Sh, Load LOAD, bool CUT>
 __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
     gqa_decode_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 const __grid_constant__ CUtensorMap tm_v,
@@ -433,6 +430,34 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
     tmem_relinquish();
     tc_fence_before();
   }
+  // CUT, a batch cut by its lengths (a variant of its own, since what it keeps in registers
+  // costs the others 1 us in 30): the cut is worked out while the previous kernel finishes,
+  // from relaxed loads, and again after the dependency wait if a length has changed.
+  Piece piece{0, 0, 0, 0};
+  int cut_tiles[3] = {0, 0, 0};
+  auto take_piece = [&]() {
+    piece = find_piece(cut_tiles[0], cut_tiles[1], cut_tiles[2], p.B, p.n_split, pb.pieces,
+                       blockIdx.x, lane);
+    b = max(piece.b, 0);
+    split = piece.split;
+    chunk = piece.tiles * kFbKeys;
+    t0 = split * chunk;
+  };
+  auto tiles_of = [&](int L) {
+    return L < p.T_q || L > p.S_max ? 0 : (L + kFbKeys - 1) / kFbKeys;
+  };
+  if constexpr (CUT) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      int L = 0;
+      if (32 * k + lane < p.B)
+        asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];"
+                     : "=r"(L)
+                     : "l"(p.seq_lens + 32 * k + lane));
+      cut_tiles[k] = tiles_of(L);
+    }
+    take_piece();
+  }
   // While the previous kernel finishes, the producer warp prefetches the split's
   // first tiles into L2, one box per lane (see decode.cu: the extent comes from
   // relaxed loads that only aim the prefetch; a prefetch hands over no data).
@@ -465,25 +490,25 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
   const uint32_t tmem = tmem_base_sh;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  bool none = false;  // (a CTA past the batch's last piece)
-  if (R > 16 && pb.pieces > 0) {
-    const Piece mine = find_piece(p, pb.pieces, lane);
-    none = mine.b < 0;
-    b = max(mine.b, 0);
-    split = mine.split;
-    chunk = mine.tiles * kFbKeys;
-    t0 = split * chunk;
-    // the slots of the workspace that the sequence has no pieces for: the merge identity
-    if (!none && split == mine.count - 1) {
-      const int spare = p.n_split - mine.count;
-      for (int i = threadIdx.x; i < R * spare; i += Sh::threads(LOAD)) {
-        const int r = i / spare;
-        const size_t at = (size_t)out_row(live_row(r) ? r : 0) * p.n_split + mine.count + i % spare;
-        if (live_row(r) && in_bounds(at, 1, n_rows * p.n_split, p.err))
-          p.ws_ml[at] = make_float2(-INFINITY, 0.f);
-      }
+  if constexpr (CUT) {
+    bool changed = false;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int t = 32 * k + lane < p.B ? tiles_of(p.seq_lens[32 * k + lane]) : 0;
+      changed |= t != cut_tiles[k];
+      cut_tiles[k] = t;
     }
+    if (__any_sync(0xffffffffu, changed)) take_piece();
+    // the slots of the workspace that the sequence has no pieces for: the merge identity
+    if (piece.b >= 0 && split == piece.count - 1)
+      for (int r = warp; r < R; r += Sh::threads(LOAD) / 32)
+        for (int i = piece.count + lane; live_row(r) && i < p.n_split; i += 32) {
+          const size_t at = (size_t)out_row(r) * p.n_split + i;
+          if (in_bounds(at, 1, n_rows * p.n_split, p.err))
+            p.ws_ml[at] = make_float2(-INFINITY, 0.f);
+        }
   }
+  const bool none = piece.b < 0;  // a CTA past the batch's last piece
   // The softmax warps' rows of Q travel together with the length: row sw, sw +
   // kWarps, ..; lane takes columns 4 lane .. 4 lane + 3.
   const int sw = warp - 4;
@@ -1097,10 +1122,10 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
   }
 }
 
-template <typename Sh, Load LOAD>
+template <typename Sh, Load LOAD, bool CUT = false>
 cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
                       const CUtensorMap& tm_v, bool prefetch, cudaStream_t stream) {
-  auto kern = gqa_decode_fp8_block_kernel<Sh, LOAD>;
+  auto kern = gqa_decode_fp8_block_kernel<Sh, LOAD, CUT>;
   constexpr int smem = Sh::kBytes;
   static unsigned char done[64];
   int dev = 0;
@@ -1112,7 +1137,7 @@ cudaError_t launch_fb(const DecodeBlockParams& p_in, const CUtensorMap& tm_k,
     if (dev >= 0 && dev < 64) done[dev] = 1;
   }
   DecodeBlockParams p = p_in;
-  p.dec.prefetch_tiles = prefetch && p.pieces == 0 ? 3 : 0;
+  p.dec.prefetch_tiles = prefetch ? 3 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = p.pieces > 0 ? dim3(p.pieces, p.dec.H_kv / p.heads)
                              : dim3(p.dec.n_split, p.dec.H_kv / p.heads, p.dec.B);
@@ -1136,6 +1161,13 @@ cudaError_t launch_fb_r(const DecodeBlockParams& p, const CUtensorMap& tm_k,
   // the larger shapes hold one CTA per SM either way).
   const long long per_group = p.pieces > 0 ? p.pieces : (long long)p.dec.n_split * p.dec.B;
   const bool one_wave = per_group * (p.dec.H_kv / p.heads) <= sms;
+  if constexpr (Deep::R > 16) {
+    if (p.pieces > 0) {  // at most one CTA per SM
+      return p.dec.block_table == nullptr
+                 ? launch_fb<Deep, Load::kTile, true>(p, tm_k, tm_v, true, stream)
+                 : launch_fb<Deep, Load::kPages, true>(p, tm_k, tm_v, true, stream);
+    }
+  }
   if (p.dec.block_table == nullptr)
     return one_wave ? launch_fb<Deep, Load::kTile>(p, tm_k, tm_v, true, stream)
                     : launch_fb<Shallow, Load::kTile>(p, tm_k, tm_v, false, stream);
@@ -1154,7 +1186,8 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockParams& p, const CUtensorMa
                                     const CUtensorMap& tm_v, int sms, cudaStream_t stream) {
   const int rows = p.heads == 1 ? p.dec.T_q * p.dec.G : p.heads * p.head_rows;
   if (rows < 1 || rows > 64 || p.dec.chunk % kFbKeys != 0) return cudaErrorInvalidValue;
-  if (p.pieces > 0 && (rows <= 16 || p.pieces < 2 * p.dec.B)) return cudaErrorInvalidValue;
+  if (p.pieces > 0 && (rows <= 16 || p.pieces <= p.dec.B || p.dec.B > kMaxCut))
+    return cudaErrorInvalidValue;
   if (rows <= 8)
     return launch_fb_r<FbShape<8, 6, 2, 1>, FbShape<8, 3, 2, 1>>(p, tm_k, tm_v, sms, stream);
   if (rows <= 16)

@@ -527,7 +527,8 @@ gqa_status gqa_kv_read_paged_fp8_block(const void* k_pool, const void* v_pool,
  * be any finite fp32 numbers for keys; for values they must not be negative
  * (NaN outputs), and one below 2^-100 counts as zero.  The codes are multiplied
  * as they are, queries and weights as sums of two E4M3 terms (queries to 2^-21 of
- * their row's largest magnitude, weights as bf16 would hold them).  A partial's m
+ * their row's largest magnitude; weights times value scales to 2^-9 of themselves, as bf16
+ * would hold them, or to 2^-22 of the largest of their split).  A partial's m
  * is a reference near the split's largest x_j + ln v_scale_j, not max_j x_j; l
  * and O hold relative to it, so the merge is unchanged.  A query row with an
  * infinity or NaN gives NaN; NaN codes and scales reach the rows that see their

@@ -282,6 +282,14 @@ def test_splits_cut_by_the_lengths(T_q, G, page):
             check_decode(c, T_q, G, n_split, q=q.cpu(), what=f"{c.len}")
 
 
+def test_splits_cut_by_the_lengths_over_small_pages():
+    c = Cache(4, 20000, 4, 64, 16, 16, seed=72)
+    k, v = c.rows(3000)
+    c.append(k, v, [3000, 900, 5, 129])
+    for T_q, G in ((5, 4), (5, 10)):
+        check_decode(c, T_q, G, None)
+
+
 def test_splits_cut_by_the_lengths_follow_a_captured_step():
     """The cut is made on the device: a captured call replayed with other lengths."""
     B, H, d, S, T_q, G = 4, 4, 32, 20000, 5, 4  # 16 groups of heads, 157 tiles
