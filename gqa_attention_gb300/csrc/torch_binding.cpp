@@ -14,8 +14,9 @@
 #include <string>
 #include <vector>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -181,6 +182,23 @@ Stream stream_of(PyObject* o, c10::DeviceIndex dev) {
   return {static_cast<gqa_stream_t>(p), true};
 }
 
+// An output, from torch's allocator without its dispatcher (1.4 us a tensor, of a call of 5).
+at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, c10::DeviceIndex dev) {
+  return at::detail::empty_cuda(sizes, type, c10::Device(c10::kCUDA, dev), std::nullopt);
+}
+// Memory that a call's own kernels use, without a tensor around it: back in the
+// allocator at the end of the call, which hands it on in the order of its stream.
+struct Scratch {
+  void* ptr = nullptr;
+  void take(size_t bytes, const Stream& s) {
+    ptr = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(
+        bytes, reinterpret_cast<cudaStream_t>(s.raw));
+  }
+  ~Scratch() {
+    if (ptr) c10::cuda::CUDACachingAllocator::raw_delete(ptr);
+  }
+};
+
 PyObject* raise(const Refused& r) {
   PyObject* e = PyObject_CallFunction(g_error, "is", r.status, r.what.c_str());
   if (e) {
@@ -299,18 +317,21 @@ PyObject* decode_(PyObject* const* a) {
        "lse is dense float32, of q's shape without d, on the cache's device");
   const Stream s = stream_of(a[8], c.dev);
   const AllocateOn on(s, c.dev);
-  if (!out) out = at::empty(q.sizes(), q.options());
-  if (!lse) lse = at::empty(rows, q.options().dtype(at::kFloat));
+  if (!out) out = empty(q.sizes(), at::kBFloat16, c.dev);
+  if (!lse) lse = empty(rows, at::kFloat, c.dev);
+  Scratch scratch;
   const int n_split = a[11] == Py_None ? lib.default_splits(c.B, T_q, H_q, c.H, c.s_max())
                                        : as_int(a[11], call);
   if (n_split > 1) {
     const int64_t bytes = static_cast<int64_t>(
         lib.workspace_bytes(as_dim(int64_t(c.B) * T_q, call), H_q, c.d, n_split));
-    if (!ws) ws = at::empty({bytes}, q.options().dtype(at::kByte));
-    need(ws->is_cuda() && ws->get_device() == c.dev && ws->is_contiguous() &&
-             static_cast<int64_t>(ws->nbytes()) >= bytes,
+    need(!ws || (ws->is_cuda() && ws->get_device() == c.dev && ws->is_contiguous() &&
+                 static_cast<int64_t>(ws->nbytes()) >= bytes),
          call, "the workspace is too small, or not dense on the cache's device");
+    // (none for sizes that the call below refuses)
+    if (!ws && bytes > 0) scratch.take(static_cast<size_t>(bytes), s);
   }
+  void* const space = ws ? ws->data_ptr() : scratch.ptr;
   const float *ks = static_cast<const float*>(c.ks.data_ptr()),
               *vs = static_cast<const float*>(c.vs.data_ptr());
   const int32_t* lens = static_cast<const int32_t*>(c.lens.data_ptr());
@@ -319,9 +340,9 @@ PyObject* decode_(PyObject* const* a) {
   check(c.table ? lib.decode_paged(q.data_ptr(), c.k8.data_ptr(), c.v8.data_ptr(), ks, vs,
                                    ptr<int32_t>(c.table), lens, c.B, T_q, c.units, c.per,
                                    c.max_blocks, H_q, c.H, c.d, c.block, tau, n_split,
-                                   ptr<void>(ws), out->data_ptr(), l, s.raw)
+                                   space, out->data_ptr(), l, s.raw)
                 : lib.decode(q.data_ptr(), c.k8.data_ptr(), c.v8.data_ptr(), ks, vs, lens, c.B, T_q,
-                             c.per, H_q, c.H, c.d, c.block, tau, n_split, ptr<void>(ws),
+                             c.per, H_q, c.H, c.d, c.block, tau, n_split, space,
                              out->data_ptr(), l, s.raw),
         call);
   return pair(*out, *lse);
