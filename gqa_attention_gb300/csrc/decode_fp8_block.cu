@@ -326,7 +326,9 @@ __device__ __forceinline__ ScaleTerms scale_terms(float ks, float vs) {
   float lg;  // (to 2^-22; exact for powers of two)
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(vs));
   s.lv = live ? lg : (vs >= 0.f ? -100.f : NAN);
-  s.ivs = ex2_approx(-s.lv);  // 1 / vs, of the same logarithm
+  // 1 / vs, of the same logarithm. Where lv is NaN the weights carry it to the rows that see
+  // the block; those that do not have weights of zero, which a NaN here would make NaN.
+  s.ivs = vs >= 0.f ? ex2_approx(-s.lv) : 1.f;
   s.p_mask = vs >= 0.f && !live ? 0u : 0xffffffffu;
   return s;
 }

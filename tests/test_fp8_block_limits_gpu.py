@@ -1,0 +1,56 @@
+"""The block-scaled E4M3 cache at the limits of what its calls accept: scales that are NaN,
+negative or near the type's largest, heads that share a tile in batches of long capacity, and
+weights far below the largest."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_ref as ref
+import gqa_attention_gb300 as g
+from test_fp8_block_gpu import Cache, check_decode
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from gqa_attention_gb300 import build
+
+    build.build()
+    g.load()
+    yield
+    assert g.gqa_last_device_error() == g.GQA_OK
+
+
+# ------------------------------------------------------- scales behind the mask --
+@pytest.mark.parametrize("name,bad", [("v", math.nan), ("v", -1.0), ("v", -math.inf), ("k", math.nan)])
+@pytest.mark.parametrize("d,H,G,T_q,n_split", [(128, 2, 4, 2, 1), (128, 2, 8, 8, 3), (64, 1, 1, 64, 1),
+                                               (32, 4, 2, 5, 200), (128, 1, 16, 4, 2)])
+@pytest.mark.parametrize("ctx,page", [(17, 0), (129, 16), (163, 0), (401, 32)])
+def test_bad_scales_reach_the_rows_that_see_their_tokens(name, bad, d, H, G, T_q, n_split, ctx, page):
+    """A NaN scale, or a negative one of the values, on a block of one head that begins behind
+    the first query's last token: NaN for the queries that see the block, and no others."""
+    T_q = min(T_q, ctx)
+    c = Cache(2, ctx, H, d, 16, page, seed=d + T_q + ctx)
+    k, v = c.rows(ctx)
+    c.append(k, v, [ctx, ctx])
+    q = torch.randn(2, T_q, H * G, d, generator=c.gen).to(torch.bfloat16)
+    t = (ctx - 1) // 16 * 16  # of sequence 1, head H - 1
+    unit, at = (int(c.table[1, t // page]), t % page // 16) if page else (1, t // 16)
+    (c.vs if name == "v" else c.ks)[unit, at, H - 1] = bad
+    c.scale[name][1, t // 16, H - 1] = math.nan
+    hit = torch.zeros(2, T_q, H * G, dtype=torch.bool)
+    hit[1, max(0, t - (ctx - T_q)):, (H - 1) * G:] = True
+    out, lse = g.decode_fp8_block(q.to(DEV), *c.args(), c.lens(), 16, n_split=n_split,
+                                  block_table=c.table)
+    assert torch.equal(lse.isnan().cpu(), hit)
+    assert torch.equal(out.isnan().cpu(), hit[..., None].expand(-1, -1, -1, d))
+    o, l, to, tl = c.expect(q, 1 / math.sqrt(d))
+    ok = ~hit.numpy()
+    assert (np.abs(out.double().cpu().numpy() - o) <= to)[ok].all()
+    assert (np.abs(lse.double().cpu().numpy() - l) <= tl)[ok].all()
