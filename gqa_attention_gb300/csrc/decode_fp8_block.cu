@@ -328,7 +328,9 @@ __device__ __forceinline__ ScaleTerms scale_terms(float ks, float vs) {
   s.lv = live ? lg : (vs >= 0.f ? -100.f : NAN);
   // 1 / vs, of the same logarithm. Where lv is NaN the weights carry it to the rows that see
   // the block; those that do not have weights of zero, which a NaN here would make NaN.
-  s.ivs = vs >= 0.f ? ex2_approx(-s.lv) : 1.f;
+  // (Not ex2_approx, which flushes: the inverse of a scale above 2^126 is subnormal.)
+  s.ivs = 1.f;
+  if (vs >= 0.f) asm("ex2.approx.f32 %0, %1;" : "=f"(s.ivs) : "f"(-s.lv));
   s.p_mask = vs >= 0.f && !live ? 0u : 0xffffffffu;
   return s;
 }

@@ -54,3 +54,31 @@ def test_bad_scales_reach_the_rows_that_see_their_tokens(name, bad, d, H, G, T_q
     ok = ~hit.numpy()
     assert (np.abs(out.double().cpu().numpy() - o) <= to)[ok].all()
     assert (np.abs(lse.double().cpu().numpy() - l) <= tl)[ok].all()
+
+
+# ------------------------------------------------------------ the largest scales --
+@pytest.mark.parametrize("exps", [(127.0, 126.5, 120.0, 127.9), (127.5,) * 4])
+@pytest.mark.parametrize("T_q,G", [(1, 8), (2, 16)])
+def test_value_scales_up_to_the_largest(exps, T_q, G):
+    """Value scales up to 2^127.9 whose products with the codes, at most 1, are within bf16."""
+    c = Cache(1, 256, 1, 64, 64, 0, seed=T_q)
+    k, v = c.rows(256)
+    c.append(k, v, [256])
+    codes = torch.randint(0, 0x39, c.v8.shape, generator=c.gen, dtype=torch.uint8)
+    codes |= torch.randint(0, 2, c.v8.shape, generator=c.gen, dtype=torch.uint8) << 7
+    c.v8.copy_(codes)
+    c.val["v"] = ref.E4M3[codes.numpy()]
+    c.vs.copy_(torch.tensor([2.0 ** e for e in exps]).view(1, 4, 1))
+    c.scale["v"] = c.vs.double().cpu().numpy()
+    q = torch.randn(1, T_q, G, 64, generator=c.gen).to(torch.bfloat16)
+    o, l, to, tl = c.expect(q, 1 / 8)
+    # scores are held together with logarithms of up to 135, whose half step in fp32 is 2^-17:
+    # a key's own, the reference's and the sum's
+    more = 3 * 2.0 ** -17
+    mag = [ref.attention(q[0].double().numpy(), c.val["k"][0], c.scale["k"][0], np.abs(c.val["v"][0]),
+                         c.scale["v"][0], 256, 64, 1 / 8)[0]]
+    to = to + 2 * more * np.stack(mag)
+    for n_split in (1, 2):
+        out, lse = g.decode_fp8_block(q.to(DEV), *c.args(), c.lens(), 64, n_split=n_split)
+        assert (np.abs(lse.double().cpu().numpy() - l) <= tl + more).all()
+        assert (np.abs(out.double().cpu().numpy() - o) <= to).all()
