@@ -525,8 +525,10 @@ gqa_status gqa_kv_read_paged_fp8_block(const void* k_pool, const void* v_pool,
  * launch merges them into out and lse: no gqa_attn_decode_combine() follows.
  * 1 <= T_q <= 64, G = H_q / H_kv <= 16 and T_q * G <= 64 (GQA_ERR_UNSUPPORTED above); scale finite > 0.  Scales may
  * be any finite fp32 numbers for keys; for values they must not be negative
- * (NaN outputs), and one below 2^-100 counts as zero.  The codes are multiplied
- * as they are, queries and weights as sums of two E4M3 terms (queries to 2^-21 of
+ * (NaN outputs), and one below 2^-100 counts as zero.  Keep the value scales that a row
+ * sees within 2^100 of one another (zero as 2^-100): a key whose block's scale is 2^-s
+ * of another's is left out where its weight is below 2^(s - 126) of that key's.  The
+ * codes are multiplied as they are, queries and weights as sums of two E4M3 terms (queries to 2^-21 of
  * their row's largest magnitude; weights times value scales to 2^-9 of themselves, as bf16
  * would hold them, or to 2^-22 of the largest of their split).  A partial's m
  * is a reference near the split's largest x_j + ln v_scale_j, not max_j x_j; l

@@ -82,3 +82,34 @@ def test_value_scales_up_to_the_largest(exps, T_q, G):
         out, lse = g.decode_fp8_block(q.to(DEV), *c.args(), c.lens(), 64, n_split=n_split)
         assert (np.abs(lse.double().cpu().numpy() - l) <= tl + more).all()
         assert (np.abs(out.double().cpu().numpy() - o) <= to).all()
+
+
+@pytest.mark.parametrize("exps", [(-100.0, -6.0, -5.0), (-6.0, -math.inf, -math.inf, -7.0),
+                                  (20.0, -50.0), (-100.0, -100.0, -100.0, -100.0, 0.0)])
+@pytest.mark.parametrize("T_q,G", [(1, 8), (2, 8), (2, 16), (8, 8)])
+@pytest.mark.parametrize("block", [16, 64, 128])
+def test_value_scales_far_apart(exps, T_q, G, block):
+    """Blocks of no, or the smallest, values and others, next to one another, in the tiles of
+    another stream or in another split: all count alike in the sum of weights."""
+    S = 1100
+    c = Cache(1, S, 1, 64, block, 0, seed=T_q + block)
+    k, v = c.rows(S)
+    c.append(k, v, [S])
+    codes = torch.randint(0, 0x39, c.v8.shape, generator=c.gen, dtype=torch.uint8)
+    codes |= torch.randint(0, 2, c.v8.shape, generator=c.gen, dtype=torch.uint8) << 7
+    c.v8.copy_(codes)
+    c.val["v"] = ref.E4M3[codes.numpy()]
+    nb = c.vs.shape[1]
+    c.vs.copy_(torch.tensor([2.0 ** exps[i % len(exps)] for i in range(nb)]).view(1, nb, 1))
+    c.scale["v"] = c.vs.double().cpu().numpy()
+    q = torch.randn(1, T_q, G, 64, generator=c.gen).to(torch.bfloat16)
+    o, l, to, tl = c.expect(q, 1 / 8)
+    # logarithms of up to 115 in fp32: half a step of 2^-18 for a key's own, the reference's
+    # and the sum's; weights left out are below 2^(100 - 126) of the largest, 1100 of them
+    more = 3 * 2.0 ** -18 + 1100 * 2.0 ** -26
+    mag = ref.attention(q[0].double().numpy(), c.val["k"][0], c.scale["k"][0], np.abs(c.val["v"][0]),
+                        c.scale["v"][0], S, block, 1 / 8)[0]
+    for n_split in (1, 2, 3, 9):
+        out, lse = g.decode_fp8_block(q.to(DEV), *c.args(), c.lens(), block, n_split=n_split)
+        assert (np.abs(lse.double().cpu().numpy() - l) <= tl + more).all(), n_split
+        assert (np.abs(out.double().cpu().numpy() - o) <= to + 2 * more * mag).all(), n_split
