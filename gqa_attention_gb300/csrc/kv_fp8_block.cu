@@ -8,11 +8,9 @@
 // and never below 2^-100.  E4M3 is a floating-point format, so a power of two
 // costs no precision against a / 448 above its subnormals, and x / s and the
 // re-encoding of older codes are exact before their one rounding.
-#include <algorithm>
-
-
 #include "common.cuh"
 #include "internal.h"
+#include "kv_blocks.h"
 #include "tcgen05.cuh"
 
 namespace gqa {
@@ -88,8 +86,8 @@ __global__ void __launch_bounds__(AppendShape<D, BLK>::kThreads, AppendShape<D, 
     return;
   }
   const int first_new = L - n;
-  const int t0 = (first_new / BLK + slot) * BLK;  // the block's first token
-  if (n == 0 || t0 >= L) return;
+  const int t0 = append_block_start(L, n, slot, BLK);  // the block's first token
+  if (t0 < 0) return;
   // The new rows first: they do not depend on where the block lies.
   const __nv_bfloat16* const src = (is_v ? p.v_new : p.k_new) + (size_t)b * p.T * p.new_stride +
                                    (size_t)kv * D;
@@ -330,9 +328,7 @@ cudaError_t launch_pdl(K kern, dim3 grid, int threads, const KvBlockParams& p, c
 
 template <int D, int BLK>
 cudaError_t launch_append(const KvBlockParams& p, cudaStream_t stream) {
-  // T tokens touch at most this many blocks, wherever they start
-  const long long slots =
-      std::min(((long long)p.T + BLK - 2) / BLK, (long long)p.S_max / BLK) + 1;
+  const long long slots = append_slots(p.T, p.S_max, BLK);
   if (slots * 2 * p.H_kv > 0x7fffffffLL) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(slots * 2 * p.H_kv), 1, p.B);
   constexpr int threads = AppendShape<D, BLK>::kThreads;
