@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(AppendShape<D, BLK>::kThreads, AppendShape<D, 
   }
   const int e_new = scale_exp(amax);
   const float s_new = pow2f(e_new);
-  const float s = has_old && s_old >= s_new ? s_old : s_new;
+  // (by magnitude: a negative scale of the caller's, and a NaN one, is replaced)
+  const float s = has_old && fabsf(s_old) >= s_new ? fabsf(s_old) : s_new;
   const size_t code0 = ((row0 + r0) * p.H_kv + kv) * D + c * 8;  // of the first vector
   const size_t code_step = (size_t)Sh::kStep * p.H_kv * D;
   auto store = [&](int j, const uint32_t (&q)[4]) {
@@ -169,8 +170,9 @@ __global__ void __launch_bounds__(AppendShape<D, BLK>::kThreads, AppendShape<D, 
       *reinterpret_cast<uint2*>(cache + code) =
           make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
   };
-  if (has_old && s > s_old) {
-    // The older rows, under a scale that grew: their codes are rounded again.
+  if (has_old && s != s_old) {
+    // The older rows, under a scale that grew (or lost its sign, or was NaN and leaves NaN
+    // codes): their codes are rounded again.
     const float ratio = s_old / s;
 #pragma unroll
     for (int j = 0; j < Sh::kPer; ++j) {

@@ -468,10 +468,10 @@ gqa_status gqa_attn_decode_paged_multi(const void* q, const void* k_pool, const 
  * With a the largest finite |x| of the new tokens of a block and head, their scale
  * is the smallest power of two s >= 2^-100 with a / s <= 448.  A block whose first
  * token is new takes it; a block that holds older tokens takes the larger of it
- * and its present scale, and if that grows its older codes are rounded again:
- * e4m3(code * old / s).  New codes are e4m3(x / s), to nearest even; infinities
- * and NaN become the NaN code and do not enter the scale.  Nothing else is read or
- * written: rows at or past seq_lens[b], rows i >= n_new[b] and the blocks before
+ * and its present scale's magnitude, and if that is another number its older codes are
+ * rounded again: e4m3(code * old / s) (a NaN scale counts as the smaller: NaN codes).
+ * New codes are e4m3(x / s), to nearest even; infinities and NaN become
+ * the NaN code and do not enter the scale.  Nothing else is read or written: rows at or past seq_lens[b], rows i >= n_new[b] and the blocks before
  * the first new token are left alone, and a block's contents past seq_lens[b] may
  * be anything.  No atomics: the result does not depend on timing, and appending
  * the same tokens in one call or in several differs only where a scale grew later

@@ -113,3 +113,32 @@ def test_value_scales_far_apart(exps, T_q, G, block):
         out, lse = g.decode_fp8_block(q.to(DEV), *c.args(), c.lens(), block, n_split=n_split)
         assert (np.abs(lse.double().cpu().numpy() - l) <= tl + more).all(), n_split
         assert (np.abs(out.double().cpu().numpy() - o) <= to + 2 * more * mag).all(), n_split
+
+
+# ---------------------------------------------------- appending under odd scales --
+@pytest.mark.parametrize("old", [-5.0, -0.001, math.nan, 0.0, -0.0])
+def test_append_under_a_negative_or_nan_scale(old):
+    """A block keeps the larger of its present scale's magnitude and the new one, and its older
+    values: a negative scale moves its sign into the codes, a NaN one makes NaN codes."""
+    c = Cache(1, 64, 2, 64, 32, 0, seed=7)
+    k, v = c.rows(40)
+    c.append(k, v, [40])
+    c.ks[0, 1, 1] = old
+    held = float(c.ks[0, 1, 1])
+    before = c.gather()["k"][0][0, 32:40, 1].copy()
+    k, v = c.rows(12)
+    x = k[0, :, 1].double().numpy()
+    # (the reference holds what the call is to leave: the rest of the cache by its own rule)
+    c.append(k, v, [12])
+    fresh = ref.block_scale(np.abs(x).max())
+    s = max(abs(held), fresh) if held == held else fresh
+    c.scale["k"][0, 1, 1] = s
+    c.val["k"][0, 32:40, 1] = ref.round_e4m3(before * (held / s))
+    got = c.gather()["k"]
+    assert got[1][0, 1, 1] == s
+    assert np.array_equal(got[0][0, 32:40, 1], c.val["k"][0, 32:40, 1], equal_nan=True)
+    # x / s in fp32 (2^-24) may tip a tie: one step of the code at most
+    want = ref.round_e4m3(x / s)
+    assert (np.abs(got[0][0, 40:52, 1] - want) <= np.maximum(2.0 ** -3 * np.abs(want), 2.0 ** -9)).all()
+    c.val["k"][0, 40:52, 1] = got[0][0, 40:52, 1]
+    c.check()
