@@ -633,15 +633,16 @@ gqa_status run_kv_read(gqa::KvBlockParams* p, int start, int S_out, void* k_out,
   return cuda_status(gqa::launch_kv_read(*p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// Pieces of a batch that the kernel cuts by its lengths, for each of `groups` groups of
-// heads; 0: splits are even ones of S_max.  For more than 16 query rows, which are bound by
-// the softmax, so that an SM without work is lost (fewer are bound by HBM, and ragged
-// batches within 10% either way), where that leaves at least two pieces a sequence and
-// pieces of 16 tiles on average.  64 rows, 8 sequences, 8 KV heads: 100 to 10K tokens 65.8 us in
-// even splits, 48.5 cut by the lengths; 100 to 33K 167 and 115; all of 10K 65.5 and 70.6,
-// since the cut takes time before the first load.  32 rows: 38.8 and 29.6, all of 10K 38.6 and
-// 41.5.  One sequence, and few pieces each (64 rows, 16 sequences: 104 and 104 us, all of
-// 10K 104 and 120), are split evenly.
+// Pieces of a batch that the kernel cuts by its lengths, for each of `groups` groups of heads
+// that a CTA takes, with `rows` query rows together; 0: splits are even ones of S_max.  For
+// more than 16 rows, which are bound by the softmax, so that an SM without work is lost
+// (fewer are bound by HBM, and ragged batches within 10% either way), where that leaves at
+// least two pieces a sequence and pieces of 16 tiles on average.  64 rows, 8 sequences, 8 KV
+// heads: 100 to 10K tokens 65.8 us in even splits, 48.5 cut by the lengths; 100 to 33K 167
+// and 115; all of 10K 65.5 and 70.6, since the cut takes time before the first load.  32
+// rows: 38.8 and 29.6, all of 10K 38.6 and 41.5; 32 rows of four packed heads of d = 32 (32
+// sequences of 100 to 19K) 49.7 and 46.0, all of 16K 61.6 and 56.0.  One sequence, and few
+// pieces each (64 rows, 16 sequences: 104 and 104 us, all of 10K 104 and 120), are split evenly.
 int length_pieces(int B, long long groups, int rows, int S_max) {
   const long long sms = num_sms_current_device(), pieces = sms / groups;
   const long long tiles = ((long long)S_max + 127) / 128;

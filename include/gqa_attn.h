@@ -471,9 +471,9 @@ gqa_status gqa_attn_decode_paged_multi(const void* q, const void* k_pool, const 
  * and its present scale's magnitude, and if that is another number its older codes are
  * rounded again: e4m3(code * old / s) (a NaN scale counts as the smaller: NaN codes).
  * New codes are e4m3(x / s), to nearest even; infinities and NaN become
- * the NaN code and do not enter the scale.  Nothing else is read or written: rows at or past seq_lens[b], rows i >= n_new[b] and the blocks before
- * the first new token are left alone, and a block's contents past seq_lens[b] may
- * be anything.  No atomics: the result does not depend on timing, and appending
+ * the NaN code and do not enter the scale.  Nothing else is read or written: rows
+ * at or past seq_lens[b], rows i >= n_new[b] and the blocks before the first new
+ * token are left alone, and a block's contents past seq_lens[b] may be anything.  No atomics: the result does not depend on timing, and appending
  * the same tokens in one call or in several differs only where a scale grew later
  * (codes rounded twice below E4M3's normal range).  Two sequences must not share
  * a page that is written (shared prefixes end at a page boundary), and calls that
@@ -517,9 +517,11 @@ gqa_status gqa_kv_read_paged_fp8_block(const void* k_pool, const void* v_pool,
  * bf16 [B, T_q, H_q, d], lse fp32 [B, T_q, H_q]; 1 <= T_q <= seq_lens[b] <= S_max),
  * with splits of ceil(S_max / n_split) keys rounded up to 128; or, for batches with
  * more than 16 query rows per KV head (T_q * G) and n_split > 1 whose sequences have
- * two SMs each or more and work for them, at most n_split splits of a sequence, cut on the device
- * so that the batch's lengths fill the GPU (a sequence's splits, and so the rounding
- * of its outputs, then depend on the other lengths too).  With n_split > 1
+ * two SMs each or more and work for them, at most n_split splits of a sequence, cut on
+ * the device so that the batch's lengths fill the GPU (a sequence's splits, and so the
+ * rounding of its outputs, then depend on the other lengths too).  So may batches of
+ * d = 32 with fewer rows be cut, where H_kv is a multiple of 4 and the heads' splits are
+ * more than two for each SM: four heads then share a CTA, and their rows count together.  With n_split > 1
  * the partials go to `workspace` (gqa_attn_decode_workspace_bytes(B * T_q, H_q, d,
  * n_split) bytes, 256-byte aligned, in gqa_attn_decode's layout) and a second
  * launch merges them into out and lse: no gqa_attn_decode_combine() follows.

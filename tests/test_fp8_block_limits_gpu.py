@@ -142,3 +142,50 @@ def test_append_under_a_negative_or_nan_scale(old):
     assert (np.abs(got[0][0, 40:52, 1] - want) <= np.maximum(2.0 ** -3 * np.abs(want), 2.0 ** -9)).all()
     c.val["k"][0, 40:52, 1] = got[0][0, 40:52, 1]
     c.check()
+
+
+# ------------------------------------------------- packed heads of long capacity --
+@pytest.mark.parametrize("T_q,G,page", [(1, 8, 0), (1, 16, 0), (2, 5, 64), (1, 8, 128)])
+def test_heads_that_share_a_tile_in_batches_of_long_capacity(T_q, G, page):
+    """Four heads of d = 32 in a CTA, whose rows together are enough for splits that are cut by the
+    lengths: short sequences in a cache of long capacity, other lengths beside the same ones, bad
+    lengths among them."""
+    B, H, S = 24, 8, 19456
+    c = Cache(B, 700, H, 32, 64, page, seed=G)
+    k, v = c.rows(700)
+    lens = [700, T_q, 129] + [700 - 5 * i for i in range(B - 3)]
+    c.append(k, v, lens)
+    if page:  # a table of long capacity: what lies past the lengths is never read
+        table = torch.full((B, S // page), -1, dtype=torch.int32, device=DEV)
+        table[:, :c.table.shape[1]] = c.table
+        c.table = table
+    else:
+        wide = g.kv_cache_fp8_block(B, S, H, 32, 64, DEV)
+        for new, old in zip(wide, c.args()):
+            new[:, :old.shape[1]] = old
+        c.k8, c.v8, c.ks, c.vs = wide
+    assert g.gqa_attn_decode_fp8_block_default_splits(B, T_q, H * G, H, S) > 1
+    q = torch.randn(B, T_q, H * G, 32, generator=c.gen).to(torch.bfloat16)
+    check_decode(c, T_q, G, None, q=q)
+    check_decode(c, T_q, G, 30, q=q)
+    out, lse = check_decode(c, T_q, G, 7, q=q)
+    qd = q.to(DEV) if T_q > 1 else q[:, 0].contiguous().to(DEV)
+    others = c.lens()
+    others[3:] = torch.arange(B - 3, dtype=torch.int32, device=DEV) % 40 + T_q
+    out2, lse2 = g.decode_fp8_block(qd, *c.args(), others, 64, n_split=7,
+                                    block_table=c.table)
+    # the same sums in another cut: two results within the tolerances of check_decode
+    o, l, to, tl = c.expect(q, 1 / math.sqrt(32))
+
+    def same(out2, lse2):
+        assert (np.abs(out2[:3].double().cpu().numpy().reshape(o[:3].shape) - o[:3]) <= to[:3]).all()
+        assert (np.abs(lse2[:3].double().cpu().numpy().reshape(l[:3].shape) - l[:3]) <= tl[:3]).all()
+
+    same(out2, lse2)
+    others[5], others[6] = S + 1, T_q - 1
+    out2, lse2 = g.decode_fp8_block(qd, *c.args(), others, 64, n_split=7,
+                                    block_table=c.table)
+    assert g.gqa_last_device_error() == g.GQA_ERR_INVALID_ARG
+    assert bool(out2[5:7].isnan().all()) and bool(lse2[5:7].isnan().all())
+    same(out2, lse2)
+    assert bool(out2[7:].isfinite().all())
