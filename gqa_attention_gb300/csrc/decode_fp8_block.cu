@@ -145,7 +145,7 @@ struct FbShape {
   static constexpr int kPerSM =
       2 * (kBytes + 8192) <= 228 * 1024 && threads(Load::kPages) <= 384 && kCols <= 256 ? 2 : 1;
   static_assert(kUsed <= 512 && kRowsQ >= 1, "tensor memory; a row of Q for every warp");
-  static_assert(NT * R * 512 <= 2 * NS * (int)kFbTile, "the accumulators reuse the rings");
+  static_assert(NT * R * 512 <= NS * (int)kFbTile, "the accumulators reuse the K ring");
 };
 
 // Instruction descriptor of tcgen05.mma.kind::f8f6f4 with E4M3 operands and fp32
@@ -1163,8 +1163,7 @@ cudaError_t launch_fb_r(const DecodeBlockParams& p, const CUtensorMap& tm_k,
   // One CTA per SM at most: a deep ring, and the first tiles prefetched into L2 while
   // the previous kernel ends.  More CTAs than SMs: two shallow rings on each SM (8 rows;
   // the larger shapes hold one CTA per SM either way).
-  const long long per_group = p.pieces > 0 ? p.pieces : (long long)p.dec.n_split * p.dec.B;
-  const bool one_wave = per_group * (p.dec.H_kv / p.heads) <= sms;
+  const bool one_wave = (long long)p.dec.n_split * p.dec.B * (p.dec.H_kv / p.heads) <= sms;
   if constexpr (Deep::R > 16) {
     if (p.pieces > 0) {  // at most one CTA per SM
       return p.dec.block_table == nullptr
