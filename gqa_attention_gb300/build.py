@@ -6,12 +6,14 @@ the objects are linked into ``gqa_attention_gb300/libgqa_attn.so`` against the
 shared CUDA runtime (``libcudart.so.13``), so that a process that also uses
 PyTorch holds one runtime instance.  ``csrc/torch_binding.cpp``, the helpers for
 torch tensors of the block-scaled cache, is compiled against the installed
-PyTorch to ``_torch_binding.so`` at the same time.  Rebuilds only what changed.
+PyTorch to ``_torch_binding.so`` at the same time; the library itself needs neither
+PyTorch nor Python's headers.  Rebuilds only what changed.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -95,11 +97,13 @@ def build_torch_binding(force: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: str = LIB,
           build_dir: str = BUILD) -> str:
-    """Compile every csrc/*.cu for sm_103a and link libgqa_attn.so, and the torch binding beside
-    it; return the library's path.
+    """Compile every csrc/*.cu for sm_103a and link libgqa_attn.so; return its path.
 
     ``extra_flags``, ``lib_path`` and ``build_dir`` let a tuning run build a
     variant (e.g. ``-DGQA_DECODE_STAGES_D128=4``) beside the default library.
+    With the default library the torch binding is built too, where PyTorch is
+    installed.  If that fails the library stands all the same and the reason goes to
+    stderr: the helpers that need the binding build it again and raise.
     """
     BUILD_, LIB_ = build_dir, lib_path
     os.makedirs(BUILD_, exist_ok=True)
@@ -112,13 +116,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
                 os.path.getmtime(src), dep_t):
             jobs.append((src, obj))
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(build_torch_binding, force)
+        binding = None
+        if os.path.abspath(LIB_) == os.path.abspath(LIB) and importlib.util.find_spec("torch"):
+            binding = ex.submit(build_torch_binding, force)
         futs = {ex.submit(_compile, s, o, list(extra_flags)): s for s, o in jobs}
         for f in cf.as_completed(futs):
             msg = f.result()
             if verbose and msg:
                 print(f"[{os.path.basename(futs[f])}]\n{msg}", file=sys.stderr)
-        binding.result()
     objs = [os.path.join(BUILD_, os.path.basename(s)[:-3] + ".o") for s in srcs]
     if jobs or force or not os.path.exists(LIB_):
         lib64 = os.path.join(cuda_home(), "lib64")
@@ -129,6 +134,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}\n{r.stdout}")
         os.replace(tmp, LIB_)
+    if binding is not None and binding.exception() is not None:
+        print(f"torch binding not built: {binding.exception()}", file=sys.stderr)
     return LIB_
 
 
