@@ -542,9 +542,11 @@ def _torch_binding():
     if _ext is None:
         import torch  # noqa: F401  (its libraries first)
 
-        if not os.path.exists(os.path.join(PKG, "_torch_binding.so")):
-            from . import build as _build  # compile in-tree; raises if the compiler fails
-            _build.build_torch_binding()
+        # Compiled in-tree unless what is there was built for this Python, this PyTorch and
+        # these sources (another's would be called through the wrong layouts); raises if the
+        # compiler fails.
+        from . import build as _build
+        _build.build_torch_binding()
         from . import _torch_binding as ext
 
         ext.init(GQAError)

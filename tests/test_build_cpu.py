@@ -58,3 +58,44 @@ def test_module_builds_as_a_program():
     r = subprocess.run([sys.executable, "-m", "gqa_attention_gb300.build"], capture_output=True, text=True,
                        cwd=build.ROOT)
     assert r.returncode == 0 and r.stdout.strip().endswith("libgqa_attn.so"), r.stderr
+
+
+# ------------------------------------------------------------ a binding of another version --
+def test_helpers_ask_whether_the_binding_is_current(monkeypatch):
+    from gqa_attention_gb300 import _binding
+
+    build.build()
+    calls = []
+    real = build.build_torch_binding
+    monkeypatch.setattr(build, "build_torch_binding", lambda *a: (calls.append(a), real(*a))[1])
+    monkeypatch.setattr(_binding, "_ext", None)
+    _binding._torch_binding()
+    _binding._torch_binding()
+    assert len(calls) == 1
+
+
+@pytest.mark.parametrize("stamp", [None, "3.9 1.0", "current"])
+def test_binding_of_another_version_is_compiled_again(tmp_path, monkeypatch, stamp):
+    import torch
+
+    made = tmp_path / "_torch_binding.so"
+    made.write_text("old")
+    if stamp == "current":
+        stamp = f"{sys.version} {torch.__version__}"
+    if stamp is not None:
+        (tmp_path / "torch_binding.stamp").write_text(stamp)
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "TORCH_BINDING", str(made))
+
+    def compiler(cmd, **kw):
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("new")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    build.build_torch_binding()
+    current = stamp == f"{sys.version} {torch.__version__}"
+    assert made.read_text() == ("old" if current else "new")
+    made.write_text("again")
+    build.build_torch_binding()
+    assert made.read_text() == "again"
