@@ -33,6 +33,18 @@
 // costs one barrier that ORs that condition, and the row maxima are worked out
 // only when it holds.  The merge of the partials holds for any reference.
 //
+// Two E4M3 terms end at steps of 2^-14, which is 2^-22 of what the reference may be below the
+// largest y, and a first token that takes most of the weight (often with a value near
+// zero) would leave the rest of the row nothing but roundings: with 1% left to 32K
+// tokens of mean-zero values, O was off by 3.5% in 16 splits and by 24% in three.  So m
+// also falls: the stream's next tile after a rise of 2^12 or more (the first one among
+// them) is looked at, and if its largest y is 2^12 below m, m becomes that y, though not
+// less than 2^-24 of its highest, so that O and l keep clear of fp32's end (l also holds
+// 1 / vs: m stays where a value scale below 2^-60 has been seen).  Then only the tokens that
+// share a tile with such a first token have its rounding (2.1% either way; their values' own
+// rounding to E4M3 is as large).  Looking costs 0.15 us in a CTA of eight tiles and up to 2%
+// elsewhere; falls of 2^8, looked for at every update, took up to 9%.
+//
 // O^T stays in tensor memory and is rescaled there when m moves (thread = row d).
 //
 // What bounds it (device time with the merge, 8 KV heads of 128, 32K tokens): 8 query rows
@@ -53,6 +65,9 @@ constexpr uint32_t kFbTile = 128u * 128u;   // 128 rows of 128 bytes
 constexpr float kLoStep = 1.f / 32.f;       // weight of the low term
 constexpr float kPScaleLog2 = 7.f;          // P is held times 2^7
 constexpr float kPMaxLog2 = 8.f;            // and must not pass 2^8
+constexpr float kFall = 12.f;               // references fall where a tile lies 2^12 below, and
+constexpr float kFallMost = 24.f;           // by 2^24 from their highest at most (see below)
+constexpr float kFallScale = 8.6736174e-19f;  // 2^-60: not behind a smaller value scale
 constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100: smaller ones count as zero
 
 // A CTA's share of a batch whose splits follow the sequences' lengths: piece `split` of
@@ -367,6 +382,8 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
   constexpr int kScRounds = 8, kScRing = 32 * kScRounds;
   __shared__ ScaleTerms sc_sm[kScRing];
   __shared__ __align__(8) uint64_t sc_full[kScRounds];
+  __shared__ float fall_sm[kScRounds];  // how far a reference may fall, by round
+  __shared__ float most_sm[Sh::kWarps][RW];  // a row's highest reference before it fell
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -659,6 +676,7 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
     int pages = fetch(32 / nb), rows_l = PAGED ? row_of(0, fetch(0)) : 0, at = 0, slot = 0;
     uint32_t parity = 0;  // of the slot's present use
     int issued = 0;
+    float fall_most = kFallMost;  // (V's producer)
     for (int j = 0; j < n; ++j) {
       if (PAGED && at == 32) {  // a round has passed
         rows_l = row_of(j, pages);
@@ -686,6 +704,8 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
         // rounds, which the softmax is done with: V's slot of tile j - NS is empty.
         const int round = j >> round_log2;
         sc_sm[(round % kScRounds) * 32 + lane] = scale_terms(scales.x, scales.y);
+        if (__any_sync(0xffffffffu, scales.y < kFallScale)) fall_most = 0.f;
+        if (lane == 0) fall_sm[round % kScRounds] = fall_most;
         scales = sc_load(j + (1 << round_log2), sc_u);
         sc_u = sc_unit(j + (2 << round_log2));
         __syncwarp();
@@ -847,8 +867,11 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
 #pragma unroll
     for (int i = 0; i < RW; ++i) l[i] = 0.f;
     float m_mine = -INFINITY;  // reference of row r0 + lane (lanes below RW)
-    if (lane < RW) off_sm[sw][lane] = kPScaleLog2;  // (0 for a row without one)
-    bool unset = true;         // some row has no reference yet
+    if (lane < RW) {
+      off_sm[sw][lane] = kPScaleLog2;  // (0 for a row without one)
+      most_sm[sw][lane] = -INFINITY;
+    }
+    bool look = true;          // some row has no reference yet, or one that has just risen far
     const int lim_lo = min(t_end, L - p.T_q + 1);  // keys below it: visible from every row
     bool alive = true;
     const uint32_t tO = tmem + lane_base + Sh::kColO + 2 * R * st + 2 * r0;
@@ -904,10 +927,10 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
       tc_fence_before();
       __syncwarp();
       if (alive && lane == 0) mbar_arrive(smem_u32(&s_empty[j % NSB]));
-      const bool update = named_bar_any(1 + gi, 128, unset || top > kPMaxLog2);
+      const bool update = named_bar_any(1 + gi, 128, look || top > kPMaxLog2);
       if (update) {
         // The rows' maxima over the 128 keys become references where they are
-        // larger; lane i works out row r0 + i for its warp.
+        // larger, or far smaller; lane i works out row r0 + i for its warp.
         float mine = -INFINITY;
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
@@ -916,16 +939,25 @@ __global__ void __launch_bounds__(Sh::threads(LOAD), Sh::kPerSM)
         }
         if (lane < RW) red[st][r0 + lane][quarter] = mine - off_sm[sw][lane];
         named_bar_sync(1 + gi, 128);
+        bool rose = false;
         if (lane < RW) {
           const float4 mx = *reinterpret_cast<const float4*>(red[st][r0 + lane]);
-          const float m_new = fmax3(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w), m_mine);
+          float m_new = fmax3(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w), m_mine);
+          if (look) {
+            const float m_tile = fmaxf(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w));
+            const float most = fmaxf(most_sm[sw][lane], m_new);
+            most_sm[sw][lane] = most;
+            if (m_tile < m_mine - kFall && m_tile > -INFINITY)
+              m_new = fminf(m_new, fmaxf(m_tile, most - fall_sm[(j >> round_log2) % kScRounds]));
+          }
+          rose = m_new > m_mine + kFall;
           const float ref = m_new == -INFINITY ? 0.f : m_new;  // no (-inf) - (-inf)
           move_sm[sw][lane] = (m_mine == -INFINITY ? 0.f : m_mine) - ref;
           alpha_sm[sw][lane] = ex2_approx(m_mine - ref);
           off_sm[sw][lane] = kPScaleLog2 - ref;
           m_mine = m_new;
         }
-        unset = __any_sync(0xffffffffu, lane < RW && m_mine == -INFINITY);
+        look = __any_sync(0xffffffffu, lane < RW && (rose || m_mine == -INFINITY));
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < RW; i += 4) {

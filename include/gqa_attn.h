@@ -525,18 +525,22 @@ gqa_status gqa_kv_read_paged_fp8_block(const void* k_pool, const void* v_pool,
  * the partials go to `workspace` (gqa_attn_decode_workspace_bytes(B * T_q, H_q, d,
  * n_split) bytes, 256-byte aligned, in gqa_attn_decode's layout) and a second
  * launch merges them into out and lse: no gqa_attn_decode_combine() follows.
- * 1 <= T_q <= 64, G = H_q / H_kv <= 16 and T_q * G <= 64 (GQA_ERR_UNSUPPORTED above); scale finite > 0.  Scales may
- * be any finite fp32 numbers for keys; for values they must not be negative
- * (NaN outputs), and one below 2^-100 counts as zero.  Keep the value scales that a row
- * sees within 2^100 of one another (zero as 2^-100): a key whose block's scale is 2^-s
- * of another's is left out where its weight is below 2^(s - 126) of that key's.  The
- * codes are multiplied as they are, queries and weights as sums of two E4M3 terms (queries to 2^-21 of
- * their row's largest magnitude; weights times value scales to 2^-9 of themselves, as bf16
- * would hold them, or to 2^-22 of the largest of their split).  A partial's m
- * is a reference near the split's largest x_j + ln v_scale_j, not max_j x_j; l
- * and O hold relative to it, so the merge is unchanged.  A query row with an
- * infinity or NaN gives NaN; NaN codes and scales reach the rows that see their
- * tokens and no others.  Deterministic. */
+ * 1 <= T_q <= 64, G = H_q / H_kv <= 16 and T_q * G <= 64 (GQA_ERR_UNSUPPORTED above);
+ * scale finite > 0.  Key scales may be any finite fp32 numbers; value scales must not
+ * be negative (NaN outputs), and one below 2^-100 counts as zero.  Keep the value scales
+ * that a row sees within 2^100 of one another (zero as 2^-100): a key whose block's scale
+ * is 2^-s of another's is left out where its weight is below 2^(s - 126) of that key's.
+ * The codes are multiplied as they are, queries and weights as sums of two E4M3 terms:
+ * queries to 2^-21 of their row's largest magnitude; weights times value scales to 2^-9
+ * of themselves, as bf16 would hold them, or to 2^-22 of a reference.  That is the split's
+ * largest so far; where it rises by 2^12 or more (the first one does), it falls at the
+ * next tile of 128 tokens to that tile's largest, if that is 2^12 below, by up to 2^24 in
+ * all and not behind value scales below 2^-60.  So a first token that takes nearly all of
+ * a row's weight leaves only the tokens beside it in its tile without their low bits.
+ * A partial's m is that reference, in terms of x_j + ln v_scale_j, not max_j x_j; l and
+ * O hold relative to it, so the merge is unchanged.  A query row with an infinity or NaN
+ * gives NaN; NaN codes and scales reach the rows that see their tokens and no others.
+ * Deterministic. */
 gqa_status gqa_attn_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
                                      const float* k_scale, const float* v_scale,
                                      const int32_t* seq_lens, int B, int T_q, int S_max, int H_q,

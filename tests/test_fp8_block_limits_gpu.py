@@ -189,3 +189,92 @@ def test_heads_that_share_a_tile_in_batches_of_long_capacity(T_q, G, page):
     assert bool(out2[5:7].isnan().all()) and bool(lse2[5:7].isnan().all())
     same(out2, lse2)
     assert bool(out2[7:].isfinite().all())
+
+
+# ------------------------------------------------------ weights far below the largest --
+def _behind_a_sink(S, T_q, G, B, share, mean, at=0, seed=0):
+    """Codes, scales and queries such that token `at` has a value of zero and all but `share`
+    of every row's weight, the rest lying log-normally (0.7) over the other tokens, whose
+    values have the given mean."""
+    gen = torch.Generator().manual_seed(seed)
+    H, d = 1, 128
+    cache = g.kv_cache_fp8_block(B, S, H, d, 64, DEV)
+    k8, v8, ks, vs = cache
+    x = (0.7 * torch.randn(S, generator=gen)).double()
+    x[at] = -math.inf
+    x[at] = float(torch.logsumexp(x, 0)) + math.log((1 - share) / share)
+    # in two elements of the key, E4M3 each: x = a + b / 16
+    a = torch.from_numpy(ref.round_e4m3(x.numpy()))
+    b = torch.from_numpy(ref.round_e4m3(16 * (x - a).numpy()))
+    k = torch.zeros(S, d, dtype=torch.float64)
+    k[:, 0], k[:, 1] = a, b
+    v = torch.randn(S, d, generator=gen).double() + mean
+    v = torch.from_numpy(ref.round_e4m3(v.numpy()))
+    v[at] = 0
+    k8[:, :, 0] = k.float().to(torch.float8_e4m3fn).view(torch.uint8).to(DEV)
+    v8[:, :, 0] = v.float().to(torch.float8_e4m3fn).view(torch.uint8).to(DEV)
+    ks.fill_(1.0), vs.fill_(1.0)
+    q = torch.zeros(B, T_q, H * G, d, dtype=torch.bfloat16)
+    q[..., 0], q[..., 1] = 1.0, 1 / 16
+    p = torch.exp(a + b / 16)
+    z = p.cumsum(0)[-T_q:, None]  # of query t: the tokens up to its own
+    o = (p[:, None] * v).cumsum(0)[-T_q:] / z
+    mag = (p[:, None] * v.abs()).cumsum(0)[-T_q:] / z
+    tile = slice(at // 128 * 128, at // 128 * 128 + 128)
+    own = (p[tile, None] * v[tile].abs()).sum(0) / z
+    return cache, q.to(DEV), *(y.numpy() for y in (o, torch.log(z[:, 0]), mag, own))
+
+
+SINKS = [(32768, 1, 8, 1, None), (32768, 8, 8, 1, None), (8192, 8, 8, 1, 1), (32768, 8, 8, 3, 3),
+         (8192, 4, 4, 2, None), (4096, 2, 16, 1, 1), (1024, 1, 4, 1, 1)]
+
+
+@pytest.mark.parametrize("S,T_q,G,B,n_split", SINKS)
+@pytest.mark.parametrize("at", [0, 700])
+def test_a_tail_behind_a_sink_keeps_its_weight(S, T_q, G, B, n_split, at):
+    """A token with a value of zero and all but 2^-12 of the weight; values of mean 1. The tail's
+    weights are held to 2^-9 of themselves outside the sink's tile."""
+    cache, q, o, l, mag, own = _behind_a_sink(S, T_q, G, B, 2.0 ** -12, 1.0, at)
+    lens = torch.full((B,), S, dtype=torch.int32, device=DEV)
+    out, lse = g.decode_fp8_block(q, *cache, lens, 64, scale=1.0, n_split=n_split)
+    # O to 2^-8 (bf16), weights to 2^-9, or 2^-14 of their tile's largest, which is under 8 times
+    # the mean; the sink's tile may lose its own tail. Scores are below 32: 2^-18 in all.
+    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -9 + 2.0 ** -11 + 2.0 ** -17) * mag + own
+    do = np.abs(out.double().cpu().numpy() - o[None, :, None])
+    assert (do <= tol[None, :, None]).all(), float((do / tol[None, :, None]).max())
+    assert (np.abs(lse.double().cpu().numpy() - l[None, :, None]) <= 2.0 ** -16).all()
+
+
+@pytest.mark.parametrize("S,T_q,G,B,n_split", SINKS)
+@pytest.mark.parametrize("share", [0.03, 0.01])
+def test_a_tail_of_mean_zero_behind_a_sink(S, T_q, G, B, n_split, share):
+    """The same with 3% and 1% left and values of mean 0, whose sum is as small as the errors of
+    its terms add up to."""
+    cache, q, o, *_ = _behind_a_sink(S, T_q, G, B, share, 0.0)
+    lens = torch.full((B,), S, dtype=torch.int32, device=DEV)
+    out, _ = g.decode_fp8_block(q, *cache, lens, 64, scale=1.0, n_split=n_split)
+    err = np.linalg.norm(out.double().cpu().numpy() - o[None, :, None], axis=-1)
+    rel = err / np.linalg.norm(o, axis=-1)[None, :, None]
+    # The sink's tile: its weights are rounded in steps of 2^-14 where the sink's is 2^7, a
+    # deviation of 2^-14 / sqrt(12) each against weights of 2^7 share / (1 - share) / S on
+    # average, whose squares are e^0.49 of the average's; 128 of S tokens have it.
+    # Everything else: O to 2^-8, weights to less. Half as much again, for the scatter of a
+    # sum of 128 terms.
+    dev = 2.0 ** -14 / math.sqrt(12) * S * (1 - share) / (share * 2.0 ** 7)
+    dev *= math.sqrt(128 / S / math.exp(0.49))
+    assert rel.max() <= 1.5 * math.hypot(dev, 2.0 ** -8), (float(rel.max()), dev)
+
+
+@pytest.mark.parametrize("e", [-100, -61, -60, 0])
+@pytest.mark.parametrize("S,T_q,G,B,n_split", SINKS)
+def test_a_sink_over_value_scales_of_every_size(S, T_q, G, B, n_split, e):
+    """The sum of weights, which is held over the value scales, stays within fp32 whether or not
+    references fall."""
+    cache, q, o, l, mag, own = _behind_a_sink(S, T_q, G, B, 2.0 ** -20, 1.0)
+    cache[3].fill_(2.0 ** e)
+    lens = torch.full((B,), S, dtype=torch.int32, device=DEV)
+    out, lse = g.decode_fp8_block(q, *cache, lens, 64, scale=1.0, n_split=n_split)
+    # logarithms of up to 135: half a step of 2^-17 for a key's own, the reference's, the sum's
+    assert (np.abs(lse.double().cpu().numpy() - l[None, :, None]) <= 2.0 ** -16 + 3 * 2.0 ** -17).all()
+    assert bool(out.isfinite().all())
+    assert (np.abs(out.double().cpu().numpy()) <= 1.1 * mag[None, :, None] * 2.0 ** e).all()
