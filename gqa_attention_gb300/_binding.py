@@ -602,7 +602,12 @@ def decode_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=None, n
 def prefill_chunk_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=None, window=-1,
                             out=None, lse=None, block_table=None, stream=None):
     """A chunk of T_q queries ending each sequence (q [B, T_q, H_q, d], any T_q) over a
-    block-scaled E4M3 cache: the cache is read back as bf16 and prefill_chunk runs on it."""
+    block-scaled E4M3 cache: the cache is read back as bf16 and prefill_chunk runs on it.
+
+    Returns prefill_chunk's (out [B, T_q, H_q, d], lse [B, H_q, T_q]; decode_fp8_block's lse is
+    [B, T_q, H_q]).  The call allocates bf16 K and V of the cache's whole capacity for every
+    sequence, B * S_max (or max_blocks * page_size) * H_kv * d * 4 bytes in all: pass the block
+    table's columns that the lengths need, not a wider one."""
     import torch
 
     if q.dim() != 4 or q.dtype is not torch.bfloat16 or q.device != k8.device \
@@ -619,6 +624,12 @@ def prefill_chunk_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=
         if q.shape[0] != B or q.shape[3] != d:
             raise GQAError(GQA_ERR_INVALID_ARG, "prefill_chunk_fp8_block: q's B or d is not the "
                            "cache's")
+        for name, x, shape, dtype in (("out", out, q.shape, torch.bfloat16),
+                                      ("lse", lse, (B, q.shape[2], q.shape[1]), torch.float32)):
+            if x is not None and (x.shape != shape or x.dtype is not dtype or x.device != q.device
+                                  or not x.is_contiguous()):
+                raise GQAError(GQA_ERR_INVALID_ARG, f"prefill_chunk_fp8_block: {name} is dense "
+                               f"{dtype} {list(shape)} on the cache's device")
         k = torch.empty((B, per, H_kv, d), dtype=torch.bfloat16, device=q.device)
         v = torch.empty_like(k)
         kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, 0, k, v, block_table, stream)

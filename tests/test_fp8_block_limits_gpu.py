@@ -278,3 +278,21 @@ def test_a_sink_over_value_scales_of_every_size(S, T_q, G, B, n_split, e):
     assert (np.abs(lse.double().cpu().numpy() - l[None, :, None]) <= 2.0 ** -16 + 3 * 2.0 ** -17).all()
     assert bool(out.isfinite().all())
     assert (np.abs(out.double().cpu().numpy()) <= 1.1 * mag[None, :, None] * 2.0 ** e).all()
+
+
+# ----------------------------------------------------------------- refusals of a chunk --
+def test_chunk_refuses_outputs_of_another_shape():
+    c = Cache(2, 64, 2, 64, 16, 0, seed=3)
+    k, v = c.rows(40)
+    c.append(k, v, [40, 33])
+    q = torch.randn(2, 5, 8, 64, generator=c.gen).to(torch.bfloat16).to(DEV)
+    out = torch.empty(2, 5, 8, 64, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(2, 8, 5, device=DEV)
+    for bad in (dict(out=out[:1]), dict(out=out[:, :4]), dict(out=out.float()), dict(out=out.cpu()),
+                dict(out=out.transpose(1, 2)), dict(lse=lse[:, :, :4]), dict(lse=lse.half()),
+                dict(lse=torch.empty(2, 5, 8, device=DEV))):
+        with pytest.raises(g.GQAError):
+            g.prefill_chunk_fp8_block(q, *c.args(), c.lens(), 16, **bad)
+    want = g.prefill_chunk_fp8_block(q, *c.args(), c.lens(), 16)
+    got = g.prefill_chunk_fp8_block(q, *c.args(), c.lens(), 16, out=out, lse=lse)
+    assert got[0] is out and torch.equal(out, want[0]) and torch.equal(lse, want[1])
