@@ -638,11 +638,12 @@ gqa_status run_kv_read(gqa::KvBlockParams* p, int start, int S_out, void* k_out,
 // more than 16 rows, which are bound by the softmax, so that an SM without work is lost
 // (fewer are bound by HBM, and ragged batches within 10% either way), where that leaves at
 // least two pieces a sequence and pieces of 16 tiles on average.  64 rows, 8 sequences, 8 KV
-// heads: 100 to 10K tokens 65.8 us in even splits, 48.5 cut by the lengths; 100 to 33K 167
-// and 115; all of 10K 65.5 and 70.6, since the cut takes time before the first load.  32
-// rows: 38.8 and 29.6, all of 10K 38.6 and 41.5; 32 rows of four packed heads of d = 32 (32
-// sequences of 100 to 19K) 49.7 and 46.0, all of 16K 61.6 and 56.0.  One sequence, and few
-// pieces each (64 rows, 16 sequences: 104 and 104 us, all of 10K 104 and 120), are split evenly.
+// heads: 100 to 10K tokens 64.7 us in even splits, 47.9 cut by the lengths; 100 to 33K 165
+// and 112; all of 10K 65.8 and 69.1, since the cut takes time before the first load.  32
+// rows: 37.6 and 28.6, all of 10K 39.0 and 42.2; 32 rows of four packed heads of d = 32 (32
+// sequences of 100 to 19K) 50.5 and 46.5, all of 16K 62.6 and 56.9.  One sequence, and few
+// pieces each (64 rows, 16 sequences: 104 and 104 us, all of 10K 104 and 120), are split
+// evenly.
 int length_pieces(int B, long long groups, int rows, int S_max) {
   const long long sms = num_sms_current_device(), pieces = sms / groups;
   const long long tiles = ((long long)S_max + 127) / 128;

@@ -36,7 +36,7 @@
 // Two E4M3 terms end at steps of 2^-14, which is 2^-22 of what the reference may be below the
 // largest y, and a first token that takes most of the weight (often with a value near
 // zero) would leave the rest of the row nothing but roundings: with 1% left to 32K
-// tokens of mean-zero values, O was off by 3.5% in 16 splits and by 24% in three.  So m
+// tokens of mean-zero values, O was off by 3.5% in 128 splits and by 24% in three.  So m
 // also falls: the stream's next tile after a rise of 2^12 or more (the first one among
 // them) is looked at, and if its largest y is 2^12 below m, m becomes that y, though not
 // less than 2^-24 of its highest, so that O and l keep clear of fp32's end (l also holds
@@ -49,7 +49,7 @@
 //
 // What bounds it (device time with the merge, 8 KV heads of 128, 32K tokens): 8 query rows
 // 14.6 us for 67 MB, the tiles at HBM's rate after about 5 us of start and merge; 16
-// rows 16.3, 32 rows 20.3, 64 rows 30.8, the softmax of R weights a key in two terms.
+// rows 16.7, 32 rows 20.4, 64 rows 30.5, the softmax of R weights a key in two terms.
 // One CTA takes 0.35 us a tile with 8 rows, 1.8 us with 64.
 //
 // Roles: warps 0 and 3 TMA producers of K and V (and two more at the end, for small
