@@ -27,9 +27,9 @@
 // E4M3 codes.
 //
 // The value scale rides on the exponent: y_j = x_j log2 e + log2 vs_j, P = 2^(y - m + 7)
-// with m a running reference within 1 of the largest y so far, and l sums
+// with m a running reference within 1 of the largest y since it last fell, and l sums
 // P / vs_j in fp32.  So the range of P adapts to vs as well as to the scores.  m is
-// moved only when some y exceeds it by more than 1 (P stays below 2^8): a tile
+// raised only when some y exceeds it by more than 1 (P stays below 2^8): a tile
 // costs one barrier that ORs that condition, and the row maxima are worked out
 // only when it holds.  The merge of the partials holds for any reference.
 //
@@ -66,7 +66,7 @@ constexpr float kLoStep = 1.f / 32.f;       // weight of the low term
 constexpr float kPScaleLog2 = 7.f;          // P is held times 2^7
 constexpr float kPMaxLog2 = 8.f;            // and must not pass 2^8
 constexpr float kFall = 12.f;               // references fall where a tile lies 2^12 below, and
-constexpr float kFallMost = 24.f;           // by 2^24 from their highest at most (see below)
+constexpr float kFallMost = 24.f;           // by 2^24 from their highest at most (see above)
 constexpr float kFallScale = 8.6736174e-19f;  // 2^-60: not behind a smaller value scale
 constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100: smaller ones count as zero
 
