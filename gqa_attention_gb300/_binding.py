@@ -64,6 +64,21 @@ SIGNATURES = {
                                              _I, _I, _F, _I, _P, _P, _P, _P]),
     "gqa_attn_decode_fp8_block_default_splits": (_I, [_I, _I, _I, _I, _I]),
     "gqa_last_device_error": (_I, [_P]),
+    "gqa_kv_append": (_I, [_P, _P, _P, _I64, _I64, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                           _P, _P, _P, _P]),
+    "gqa_kv_append_paged": (_I, [_P, _P, _P, _I64, _I64, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I,
+                                 _I, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "gqa_kv_append_fp8": (_I, [_P, _P, _P, _I64, _I64, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I,
+                               _I, _P, _P, _P, _P, _P, _P]),
+    "gqa_kv_append_paged_fp8": (_I, [_P, _P, _P, _I64, _I64, _P, _I, _I, _P, _P, _P, _P, _I, _I,
+                                     _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "gqa_attn_decode_diff": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _I, _I, _I,
+                                  _I, _F, _P, _F, _F, _I, _P, _P, _P, _P]),
+    "gqa_attn_decode_paged_diff": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _I,
+                                        _I, _I, _I, _I, _I, _F, _P, _F, _F, _I, _P, _P, _P, _P]),
+    "gqa_attn_decode_diff_default_splits": (_I, [_I, _I, _I, _I, _I]),
+    "gqa_attn_prefill_diff": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _I, _I, _I,
+                                   _I, _F, _I, _P, _F, _F, _I, _P, _P, _P, _P]),
     "gqa_trace_clear": (_I, []),
     "gqa_trace_read": (_I, [_P, _SZ]),
     "gqa_trace_mma_rate": (_I, [_I, _I, _P]),
@@ -311,6 +326,79 @@ def gqa_attn_decode_fp8_block_default_splits(B, T_q, H_q, H_kv, S_max) -> int:
     return load().gqa_attn_decode_fp8_block_default_splits(B, T_q, H_q, H_kv, S_max)
 
 
+def gqa_kv_append(q, k_new, v_new, q_stride, kv_stride, freqs, rot, interleaved, n_new, positions,
+                  seq_lens, B, T, S_max, H_q, H_kv, d, k_cache, v_cache, q_out, stream=None) -> int:
+    return load().gqa_kv_append(
+        _ptr(q), _ptr(k_new), _ptr(v_new), q_stride, kv_stride, _ptr(freqs), rot, int(interleaved),
+        _ptr(n_new), _ptr(positions), _ptr(seq_lens), B, T, S_max, H_q, H_kv, d, _ptr(k_cache),
+        _ptr(v_cache), _ptr(q_out), _stream(stream))
+
+
+def gqa_kv_append_paged(q, k_new, v_new, q_stride, kv_stride, freqs, rot, interleaved, n_new,
+                        positions, block_table, seq_lens, B, T, num_pages, page_size, max_blocks,
+                        H_q, H_kv, d, k_pool, v_pool, q_out, stream=None) -> int:
+    return load().gqa_kv_append_paged(
+        _ptr(q), _ptr(k_new), _ptr(v_new), q_stride, kv_stride, _ptr(freqs), rot, int(interleaved),
+        _ptr(n_new), _ptr(positions), _ptr(block_table), _ptr(seq_lens), B, T, num_pages, page_size,
+        max_blocks, H_q, H_kv, d, _ptr(k_pool), _ptr(v_pool), _ptr(q_out), _stream(stream))
+
+
+def gqa_kv_append_fp8(q, k_new, v_new, q_stride, kv_stride, freqs, rot, interleaved, n_new,
+                      positions, seq_lens, B, T, S_max, H_q, H_kv, d, k_cache, v_cache, k_scale,
+                      v_scale, q_out, stream=None) -> int:
+    return load().gqa_kv_append_fp8(
+        _ptr(q), _ptr(k_new), _ptr(v_new), q_stride, kv_stride, _ptr(freqs), rot, int(interleaved),
+        _ptr(n_new), _ptr(positions), _ptr(seq_lens), B, T, S_max, H_q, H_kv, d, _ptr(k_cache),
+        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(q_out), _stream(stream))
+
+
+def gqa_kv_append_paged_fp8(q, k_new, v_new, q_stride, kv_stride, freqs, rot, interleaved, n_new,
+                            positions, block_table, seq_lens, B, T, num_pages, page_size,
+                            max_blocks, H_q, H_kv, d, k_pool, v_pool, k_scale, v_scale, q_out,
+                            stream=None) -> int:
+    return load().gqa_kv_append_paged_fp8(
+        _ptr(q), _ptr(k_new), _ptr(v_new), q_stride, kv_stride, _ptr(freqs), rot, int(interleaved),
+        _ptr(n_new), _ptr(positions), _ptr(block_table), _ptr(seq_lens), B, T, num_pages, page_size,
+        max_blocks, H_q, H_kv, d, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+        _ptr(q_out), _stream(stream))
+
+
+def gqa_attn_decode_diff(q, k_cache, v_cache, seq_lens, lam, lam_stride_b, lam_stride_t,
+                         lam_stride_h, B, T_q, S_max, H, H_kv, d, split_keys, scale, norm_weight,
+                         norm_eps, out_scale, n_split, workspace, out, lse, stream=None) -> int:
+    return load().gqa_attn_decode_diff(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seq_lens), _ptr(lam), lam_stride_b,
+        lam_stride_t, lam_stride_h, B, T_q, S_max, H, H_kv, d, int(split_keys), scale,
+        _ptr(norm_weight), norm_eps, out_scale, n_split, _ptr(workspace), _ptr(out), _ptr(lse),
+        _stream(stream))
+
+
+def gqa_attn_decode_paged_diff(q, k_pool, v_pool, block_table, seq_lens, lam, lam_stride_b,
+                               lam_stride_t, lam_stride_h, B, T_q, num_pages, page_size,
+                               max_blocks, H, H_kv, d, split_keys, scale, norm_weight, norm_eps,
+                               out_scale, n_split, workspace, out, lse, stream=None) -> int:
+    return load().gqa_attn_decode_paged_diff(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(seq_lens), _ptr(lam),
+        lam_stride_b, lam_stride_t, lam_stride_h, B, T_q, num_pages, page_size, max_blocks, H, H_kv,
+        d, int(split_keys), scale, _ptr(norm_weight), norm_eps, out_scale, n_split,
+        _ptr(workspace), _ptr(out), _ptr(lse), _stream(stream))
+
+
+def gqa_attn_decode_diff_default_splits(B, T_q, H, H_kv, S_max) -> int:
+    return load().gqa_attn_decode_diff_default_splits(B, T_q, H, H_kv, S_max)
+
+
+def gqa_attn_prefill_diff(q, k_cache, v_cache, seq_lens, lam, lam_stride_b, lam_stride_t,
+                          lam_stride_h, B, T_q, S_max, H, H_kv, d, split_keys, scale, window,
+                          norm_weight, norm_eps, out_scale, n_part, workspace, out, lse,
+                          stream=None) -> int:
+    return load().gqa_attn_prefill_diff(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seq_lens), _ptr(lam), lam_stride_b,
+        lam_stride_t, lam_stride_h, B, T_q, S_max, H, H_kv, d, int(split_keys), scale, int(window),
+        _ptr(norm_weight), norm_eps, out_scale, int(n_part), _ptr(workspace), _ptr(out), _ptr(lse),
+        _stream(stream))
+
+
 def gqa_trace_clear() -> int:
     return load().gqa_trace_clear()
 
@@ -534,9 +622,9 @@ _ext = None
 
 
 def _torch_binding():
-    """The C++ module that checks and passes on the tensors of the block-scaled cache's helpers
-    (the same checks in Python take longer than most of their kernels), and the handle of the
-    loaded library, which it calls."""
+    """The C++ module that checks and passes on the tensors of the newer helpers (the block-scaled
+    cache, kv_append, differential attention; the same checks in Python take longer than
+    most of their kernels), and the handle of the loaded library, which it calls."""
     global _ext
     lib = load()
     if _ext is None:
@@ -634,6 +722,53 @@ def prefill_chunk_fp8_block(q, k8, v8, k_scale, v_scale, seq_lens, block, scale=
         v = torch.empty_like(k)
         kv_read_fp8_block(k8, v8, k_scale, v_scale, seq_lens, block, 0, k, v, block_table, stream)
         return prefill_chunk(q, k, v, seq_lens, scale, window, out, lse, stream)
+
+
+def kv_append(k_new, v_new, k, v, seq_lens, freqs=None, interleaved=False, n_new=None,
+              positions=None, q=None, q_out=None, k_scale=None, v_scale=None, block_table=None,
+              stream=None):
+    """Append new tokens (bf16 [B, T, H_kv, d]; rows may be slices of wider ones) to a cache, the
+    keys turned by their positions on the way; return the step's queries, turned likewise.
+
+    The cache k, v is bf16, or uint8 (E4M3 codes) with k_scale, v_scale (one per token), as
+    decode, decode_paged and decode_fp8 take it; paged when block_table is given.  seq_lens are
+    the lengths after the call, n_new [B] the valid rows of each sequence (None: all T).
+    freqs fp32 [rot / 2]: radians per position of the pairs of the first rot channels (None:
+    nothing is turned), pairs being channels i and i + rot / 2, or 2i and 2i + 1 if
+    interleaved.  positions int32 [B, T] instead of the tokens' places in their sequences.
+    q bf16 [B, T, H_q, d]: turned into q_out (dense; q itself, if dense; new: rows past n_new
+    are zero).  Returns q_out, or None without q."""
+    ext, lib = _torch_binding()
+    return ext.append_turned(lib, k_new, v_new, k, v, seq_lens, freqs, interleaved, n_new,
+                             positions, q, q_out, k_scale, v_scale, block_table, stream)
+
+
+def decode_diff(q, k, v, seq_lens, lam, split_keys=False, norm_eps=None, norm_weight=None,
+                out_scale=1.0, scale=None, n_split=None, workspace=None, out=None, lse=None,
+                block_table=None, stream=None):
+    """Decode of differential attention, O = softmax(scale q1 K1') V - lam softmax(scale q2 K2') V,
+    over a bf16 cache (paged when block_table is given); returns (out, lse).
+
+    Shared keys: q [B, 2 H, d], or [B, T_q, 2 H, d] for the last T_q positions, q1 and q2
+    being heads 2h and 2h + 1.  split_keys: q [B, H, d] or [B, T_q, H, d], the maps being the
+    halves of a query and a key row.  lam: fp32, broadcast to [B, (T_q,) H].  norm_eps: O is
+    divided by the root of its mean square + norm_eps and multiplied by norm_weight (fp32 [d]).
+    out bf16 [B, (T_q,) H, d], lse fp32 [B, (T_q,) 2 H]; scale: 1 / sqrt(d), of the halves' d with
+    split_keys."""
+    ext, lib = _torch_binding()
+    return ext.decode_diff(lib, q, k, v, seq_lens, lam, split_keys, norm_eps, norm_weight,
+                           out_scale, scale, n_split, workspace, out, lse, block_table, stream)
+
+
+def prefill_diff(q, k, v, lam, seq_lens=None, split_keys=False, norm_eps=None, norm_weight=None,
+                 out_scale=1.0, window=-1, scale=None, n_part=None, workspace=None, out=None,
+                 lse=None, stream=None):
+    """Prefill of differential attention: T_q queries ending each sequence of k, v [B, S_max, H_kv,
+    d] (seq_lens None: sequences of S_max), optionally windowed; the arguments are decode_diff's
+    and prefill_chunk's.  Returns (out bf16 [B, T_q, H, d], lse fp32 [B, 2 H, T_q])."""
+    ext, lib = _torch_binding()
+    return ext.prefill_diff(lib, q, k, v, lam, seq_lens, split_keys, norm_eps, norm_weight,
+                            out_scale, window, scale, n_part, workspace, out, lse, stream)
 
 
 def prefill_causal(q, k, v, scale=None, out=None, lse=None, stream=None):

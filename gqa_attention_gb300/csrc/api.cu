@@ -9,8 +9,10 @@
 
 #include <cudaTypedefs.h>
 
+#include "diff.h"
 #include "gqa_attn.h"
 #include "internal.h"
+#include "kv_append.h"
 
 namespace {
 
@@ -106,6 +108,8 @@ bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 // tile (used above 16 rows).
 constexpr int kMaxMultiRows = 64;
 constexpr int kMaxMultiRowsTc = 128;
+// Token rows of a cache, at most, where a last tile may reach past them in 32 bits.
+constexpr long long kMaxCacheRows = 0x7fff0000LL;
 bool multi_uses_tc(int T_q, int G, int d) { return d == 128 && T_q * G > 16; }
 
 }  // namespace
@@ -445,6 +449,255 @@ gqa_status gqa_attn_decode_paged(const void* q, const void* k_pool, const void* 
   return gqa_attn_decode_paged_multi(q, k_pool, v_pool, block_table, seq_lens, B, 1, num_pages,
                                      page_size, max_blocks, H_q, H_kv, d, scale, n_split,
                                      workspace, out, lse, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The arguments of differential attention beside those of the two maps.
+gqa_status diff_params(const float* lam, int64_t lam_b, int64_t lam_t, int64_t lam_h, int H,
+                       int H_kv, int split_keys, const float* norm_weight, float norm_eps,
+                       float out_scale, gqa::DiffParams* p) {
+  if (!lam || !aligned(lam, 4) || lam_b < 0 || lam_t < 0 || lam_h < 0) return GQA_ERR_INVALID_ARG;
+  if (H < 1 || H > 32767 || H_kv < 1 || H % H_kv != 0) return GQA_ERR_INVALID_ARG;
+  if (split_keys != 0 && split_keys != 1) return GQA_ERR_INVALID_ARG;
+  if (!std::isfinite(norm_eps) || !std::isfinite(out_scale)) return GQA_ERR_INVALID_ARG;
+  if (norm_weight && (norm_eps < 0.f || !aligned(norm_weight, 4))) return GQA_ERR_INVALID_ARG;
+  *p = gqa::DiffParams{lam, lam_b, lam_t, lam_h, norm_weight, norm_eps, out_scale, split_keys};
+  return GQA_OK;
+}
+
+// The shape of a paged cache: S_max and the pools' token rows.
+gqa_status paged_shape(const int32_t* block_table, int num_pages, int page_size, int max_blocks,
+                       int* S_max, long long* rows) {
+  if (!block_table || !aligned(block_table, 4)) return GQA_ERR_INVALID_ARG;
+  if (num_pages < 1 || max_blocks < 1 || page_size < 1) return GQA_ERR_INVALID_ARG;
+  if (page_size < 16 || (page_size & (page_size - 1)) != 0) return GQA_ERR_UNSUPPORTED;
+  const long long s = (long long)max_blocks * page_size;
+  *rows = (long long)num_pages * page_size;
+  if (s > kMaxCacheRows) return GQA_ERR_INVALID_ARG;
+  *S_max = (int)s;
+  return GQA_OK;
+}
+
+gqa_status run_decode_diff(const void* q, const void* k, const void* v, const int32_t* block_table,
+                           const int32_t* seq_lens, const gqa::DiffParams& diff, int B, int T_q,
+                           int S_max, long long rows, int num_pages, int page_size, int max_blocks,
+                           int H, int H_kv, int d, float scale, int n_split, void* workspace,
+                           void* out, float* lse, gqa_stream_t stream) {
+  // (rows and tokens stay below 2^31 with the last tile's overhang)
+  if (rows < 1 || rows > kMaxCacheRows || S_max < 1 || S_max > kMaxCacheRows)
+    return GQA_ERR_INVALID_ARG;
+  if (T_q < 1 || T_q > 64 || T_q > S_max || n_split > 65535) return GQA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !aligned(lse, 8)) return GQA_ERR_INVALID_ARG;
+  if (head_dim_ok(d) && T_q * (2 * H / H_kv) > kMaxMultiRows) return GQA_ERR_UNSUPPORTED;
+  const int box = block_table && page_size < gqa::kDecodeTile ? page_size : gqa::kDecodeTile;
+  CUtensorMap tm_k, tm_v;
+  gqa::DecodeDiffParams p{};
+  gqa_status st = prepare_decode(q, k, v, seq_lens, B, S_max, rows, box, 2 * H, H_kv, d, scale,
+                                 n_split, workspace, out, lse, &tm_k, &tm_v, &p.dec);
+  if (st != GQA_OK) return st;
+  p.diff = diff;
+  p.dec.T_q = T_q;
+  p.dec.block_table = block_table;
+  p.dec.max_blocks = max_blocks;
+  p.dec.page_size = page_size;
+  p.dec.num_pages = num_pages;
+  // the partials are laid out for B * T_q rows of 2 H maps
+  if ((long long)B * T_q > 0x7fffffffLL / (2 * H)) return GQA_ERR_INVALID_ARG;
+  p.dec.ws_O = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                                    gqa::decode_ws_O_offset(B * T_q, 2 * H, n_split))
+                         : nullptr;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = cuda_status(gqa::launch_decode_diff(p, tm_k, tm_v, s));
+  if (st != GQA_OK || n_split == 1) return st;
+  gqa::DiffMergeParams m{};
+  m.diff = diff;
+  m.ws_ml = p.dec.ws_ml;
+  m.ws_O = p.dec.ws_O;
+  m.m_log2 = 1.4426950408889634f;
+  m.B = B;
+  m.T = T_q;
+  m.H_maps = 2 * H;
+  m.d = d;
+  m.n_part = n_split;
+  m.out = p.dec.out;
+  m.lse = lse;
+  m.lse_b = (long long)T_q * 2 * H;
+  m.lse_t = 2 * H;
+  m.lse_m = 1;
+  m.err = p.dec.err;
+  return cuda_status(gqa::launch_diff_merge(m, s));
+}
+
+// Checks what the appends share and launches; the cache's shape is in `p` already.
+gqa_status run_kv_append_rot(gqa::KvAppendParams* p, long long rows, const void* q,
+                             const void* k_new, const void* v_new, int64_t q_stride,
+                             int64_t kv_stride, const float* freqs, int rot, int interleaved,
+                             const int32_t* n_new, const int32_t* positions,
+                             const int32_t* seq_lens, int B, int T, int H_q, int H_kv, int d,
+                             void* k_cache, void* v_cache, void* q_out, gqa_stream_t stream) {
+  if (!k_new || !v_new || !seq_lens || !k_cache || !v_cache) return GQA_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return GQA_ERR_INVALID_ARG;
+  if (B < 1 || T < 1 || H_kv < 1 || H_kv > 65535 || (q && (H_q < 1 || H_q > 65535)))
+    return GQA_ERR_INVALID_ARG;
+  if (d != 16 && !head_dim_ok(d)) return GQA_ERR_UNSUPPORTED;
+  if (rows < 1 || rows > kMaxCacheRows || (long long)B * T > 0x7fffffffLL) return GQA_ERR_INVALID_ARG;
+  if (rot < 0 || rot > d || (rot > 0 && (!freqs || !aligned(freqs, 4)))) return GQA_ERR_INVALID_ARG;
+  if (rot % 16 != 0) return GQA_ERR_UNSUPPORTED;
+  if (interleaved != 0 && interleaved != 1) return GQA_ERR_INVALID_ARG;
+  if (kv_stride < (int64_t)H_kv * d || kv_stride % 8 != 0) return GQA_ERR_INVALID_ARG;
+  if (q && (q_stride < (int64_t)H_q * d || q_stride % 8 != 0)) return GQA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(seq_lens, 4) ||
+      !aligned(n_new, 4) || !aligned(positions, 4) || !aligned(p->k_scale, 4) ||
+      !aligned(p->v_scale, 4))
+    return GQA_ERR_INVALID_ARG;
+  unsigned* err = nullptr;
+  const gqa_status st = error_word(&err);
+  if (st != GQA_OK) return st;
+  p->q = static_cast<const __nv_bfloat16*>(q);
+  p->k = static_cast<const __nv_bfloat16*>(k_new);
+  p->v = static_cast<const __nv_bfloat16*>(v_new);
+  p->q_stride = q_stride;
+  p->kv_stride = kv_stride;
+  p->freqs = freqs;
+  p->rot = rot;
+  p->interleaved = interleaved;
+  p->n_new = n_new;
+  p->seq_lens = seq_lens;
+  p->positions = positions;
+  p->B = B;
+  p->T = T;
+  p->H_q = q ? H_q : 0;
+  p->H_kv = H_kv;
+  p->d = d;
+  p->k_cache = k_cache;
+  p->v_cache = v_cache;
+  p->q_out = static_cast<__nv_bfloat16*>(q_out);
+  p->err = err;
+  return cuda_status(gqa::launch_kv_append_rot(*p, num_sms_current_device(),
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+gqa_status gqa_kv_append(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                         int64_t kv_stride, const float* freqs, int rot, int interleaved,
+                         const int32_t* n_new, const int32_t* positions, const int32_t* seq_lens,
+                         int B, int T, int S_max, int H_q, int H_kv, int d, void* k_cache,
+                         void* v_cache, void* q_out, gqa_stream_t stream) {
+  gqa::KvAppendParams p{};
+  p.S_max = S_max;
+  return run_kv_append_rot(&p, S_max < 1 ? 0 : (long long)B * S_max, q, k_new, v_new, q_stride,
+                           kv_stride, freqs, rot, interleaved, n_new, positions, seq_lens, B, T,
+                           H_q, H_kv, d, k_cache, v_cache, q_out, stream);
+}
+
+gqa_status gqa_kv_append_paged(const void* q, const void* k_new, const void* v_new,
+                               int64_t q_stride, int64_t kv_stride, const float* freqs, int rot,
+                               int interleaved, const int32_t* n_new, const int32_t* positions,
+                               const int32_t* block_table, const int32_t* seq_lens, int B, int T,
+                               int num_pages, int page_size, int max_blocks, int H_q, int H_kv,
+                               int d, void* k_pool, void* v_pool, void* q_out,
+                               gqa_stream_t stream) {
+  gqa::KvAppendParams p{};
+  long long rows = 0;
+  const gqa_status st = paged_shape(block_table, num_pages, page_size, max_blocks, &p.S_max, &rows);
+  if (st != GQA_OK) return st;
+  p.block_table = block_table;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.max_blocks = max_blocks;
+  return run_kv_append_rot(&p, rows, q, k_new, v_new, q_stride, kv_stride, freqs, rot, interleaved,
+                           n_new, positions, seq_lens, B, T, H_q, H_kv, d, k_pool, v_pool, q_out,
+                           stream);
+}
+
+gqa_status gqa_kv_append_fp8(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                             int64_t kv_stride, const float* freqs, int rot, int interleaved,
+                             const int32_t* n_new, const int32_t* positions,
+                             const int32_t* seq_lens, int B, int T, int S_max, int H_q, int H_kv,
+                             int d, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                             void* q_out, gqa_stream_t stream) {
+  if (!k_scale || !v_scale) return GQA_ERR_INVALID_ARG;
+  gqa::KvAppendParams p{};
+  p.S_max = S_max;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  return run_kv_append_rot(&p, S_max < 1 ? 0 : (long long)B * S_max, q, k_new, v_new, q_stride,
+                           kv_stride, freqs, rot, interleaved, n_new, positions, seq_lens, B, T,
+                           H_q, H_kv, d, k_cache, v_cache, q_out, stream);
+}
+
+gqa_status gqa_kv_append_paged_fp8(const void* q, const void* k_new, const void* v_new,
+                                   int64_t q_stride, int64_t kv_stride, const float* freqs,
+                                   int rot, int interleaved, const int32_t* n_new,
+                                   const int32_t* positions, const int32_t* block_table,
+                                   const int32_t* seq_lens, int B, int T, int num_pages,
+                                   int page_size, int max_blocks, int H_q, int H_kv, int d,
+                                   void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                   void* q_out, gqa_stream_t stream) {
+  if (!k_scale || !v_scale) return GQA_ERR_INVALID_ARG;
+  gqa::KvAppendParams p{};
+  long long rows = 0;
+  const gqa_status st = paged_shape(block_table, num_pages, page_size, max_blocks, &p.S_max, &rows);
+  if (st != GQA_OK) return st;
+  p.block_table = block_table;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.max_blocks = max_blocks;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  return run_kv_append_rot(&p, rows, q, k_new, v_new, q_stride, kv_stride, freqs, rot, interleaved,
+                           n_new, positions, seq_lens, B, T, H_q, H_kv, d, k_pool, v_pool, q_out,
+                           stream);
+}
+
+int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_max) {
+  if (B < 1 || T_q < 1 || H < 1 || H_kv < 1 || H % H_kv != 0) return 1;
+  return gqa_attn_decode_default_splits(B, H_kv, S_max, -1);
+}
+
+gqa_status gqa_attn_decode_diff(const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* seq_lens, const float* lam, int64_t lam_stride_b,
+                                int64_t lam_stride_t, int64_t lam_stride_h, int B, int T_q,
+                                int S_max, int H, int H_kv, int d, int split_keys, float scale,
+                                const float* norm_weight, float norm_eps, float out_scale,
+                                int n_split, void* workspace, void* out, float* lse,
+                                gqa_stream_t stream) {
+  gqa::DiffParams diff;
+  const gqa_status st = diff_params(lam, lam_stride_b, lam_stride_t, lam_stride_h, H, H_kv,
+                                    split_keys, norm_weight, norm_eps, out_scale, &diff);
+  if (st != GQA_OK) return st;
+  return run_decode_diff(q, k_cache, v_cache, nullptr, seq_lens, diff, B, T_q, S_max,
+                         (long long)B * S_max, 0, 0, 0, H, H_kv, d, scale, n_split, workspace, out,
+                         lse, stream);
+}
+
+gqa_status gqa_attn_decode_paged_diff(const void* q, const void* k_pool, const void* v_pool,
+                                      const int32_t* block_table, const int32_t* seq_lens,
+                                      const float* lam, int64_t lam_stride_b, int64_t lam_stride_t,
+                                      int64_t lam_stride_h, int B, int T_q, int num_pages,
+                                      int page_size, int max_blocks, int H, int H_kv, int d,
+                                      int split_keys, float scale, const float* norm_weight,
+                                      float norm_eps, float out_scale, int n_split,
+                                      void* workspace, void* out, float* lse,
+                                      gqa_stream_t stream) {
+  gqa::DiffParams diff;
+  gqa_status st = diff_params(lam, lam_stride_b, lam_stride_t, lam_stride_h, H, H_kv, split_keys,
+                              norm_weight, norm_eps, out_scale, &diff);
+  if (st != GQA_OK) return st;
+  int S_max = 0;
+  long long rows = 0;
+  st = paged_shape(block_table, num_pages, page_size, max_blocks, &S_max, &rows);
+  if (st != GQA_OK) return st;
+  return run_decode_diff(q, k_pool, v_pool, block_table, seq_lens, diff, B, T_q, S_max, rows,
+                         num_pages, page_size, max_blocks, H, H_kv, d, scale, n_split, workspace,
+                         out, lse, stream);
 }
 
 }  // extern "C"
@@ -904,11 +1157,12 @@ gqa_status gqa_attn_decode_combine(const void* workspace, int B, int H_q, int d,
 namespace {
 
 // Shared checks and launch of the causal prefill kernel: S query rows per
-// sequence against S_kv key rows (chunk: the queries end each sequence).
+// sequence against S_kv key rows (chunk: the queries end each sequence).  With `diff`, H_q
+// counts the maps of differential attention, two per head.
 gqa_status run_prefill(bool chunk, const void* q, const void* k, const void* v,
                        const int32_t* seq_lens, int B, int S, int S_kv, int H_q, int H_kv, int d,
                        float scale, int window, int n_part, void* workspace, void* out, float* lse,
-                       gqa_stream_t stream) {
+                       gqa_stream_t stream, const gqa::DiffParams* diff = nullptr) {
   if (!q || !k || !v || !out || !lse) return GQA_ERR_INVALID_ARG;
   if (n_part < 1 || n_part > 8 || (n_part > 1 && (!chunk || !workspace))) return GQA_ERR_INVALID_ARG;
   if (workspace && !aligned(workspace, 256)) return GQA_ERR_INVALID_ARG;
@@ -930,8 +1184,9 @@ gqa_status run_prefill(bool chunk, const void* q, const void* k, const void* v,
   // wide (two boxes per 128-wide row), 128-byte swizzle; K and V likewise.  For
   // d = 32 the 64-element box is wider than the tensor: TMA fills elements
   // 32..63 with zeros, the padding the kernel's 64-wide tiles expect.
-  const uint64_t dq[4] = {(uint64_t)d, (uint64_t)H_q, (uint64_t)S, (uint64_t)B};
-  const uint64_t sq[3] = {(uint64_t)d * 2, (uint64_t)H_q * d * 2, (uint64_t)S * H_q * d * 2};
+  const uint64_t rows_q = diff && diff->split_keys ? H_q / 2 : H_q;
+  const uint64_t dq[4] = {(uint64_t)d, rows_q, (uint64_t)S, (uint64_t)B};
+  const uint64_t sq[3] = {(uint64_t)d * 2, rows_q * d * 2, (uint64_t)S * rows_q * d * 2};
   const uint64_t dk[4] = {(uint64_t)d, (uint64_t)H_kv, (uint64_t)S_kv, (uint64_t)B};
   const uint64_t sk[3] = {(uint64_t)d * 2, (uint64_t)H_kv * d * 2, (uint64_t)S_kv * H_kv * d * 2};
   const uint32_t box[4] = {64u, 1u, 128u, 1u};
@@ -962,6 +1217,28 @@ gqa_status run_prefill(bool chunk, const void* q, const void* k, const void* v,
                       : nullptr;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int sms = num_sms_current_device();
+  if (diff) {
+    const gqa::PrefillDiffParams pd{p, *diff};
+    st = cuda_status(gqa::launch_prefill_diff(pd, chunk, tm_q, tm_k, tm_v, sms, s));
+    if (st != GQA_OK || n_part == 1) return st;
+    gqa::DiffMergeParams m{};
+    m.diff = *diff;
+    m.ws_ml = p.ws_ml;
+    m.ws_O = p.ws_O;
+    m.m_log2 = 1.f;
+    m.B = B;
+    m.T = S;
+    m.H_maps = H_q;
+    m.d = d;
+    m.n_part = n_part;
+    m.out = p.out;
+    m.lse = lse;
+    m.lse_b = (long long)H_q * S;
+    m.lse_t = 1;
+    m.lse_m = S;
+    m.err = err;
+    return cuda_status(gqa::launch_diff_merge(m, s));
+  }
   if (!chunk) return cuda_status(gqa::launch_prefill_causal(p, tm_q, tm_k, tm_v, sms, s));
   st = cuda_status(gqa::launch_prefill_chunk(p, tm_q, tm_k, tm_v, sms, s));
   if (st != GQA_OK || n_part == 1) return st;
@@ -1019,6 +1296,22 @@ gqa_status gqa_attn_prefill_chunk_split(const void* q, const void* k_cache, cons
                                         gqa_stream_t stream) {
   return run_prefill(true, q, k_cache, v_cache, seq_lens, B, T_q, S_max, H_q, H_kv, d, scale,
                      window, n_part, workspace, out, lse, stream);
+}
+
+gqa_status gqa_attn_prefill_diff(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* seq_lens, const float* lam, int64_t lam_stride_b,
+                                 int64_t lam_stride_t, int64_t lam_stride_h, int B, int T_q,
+                                 int S_max, int H, int H_kv, int d, int split_keys, float scale,
+                                 int window, const float* norm_weight, float norm_eps,
+                                 float out_scale, int n_part, void* workspace, void* out,
+                                 float* lse, gqa_stream_t stream) {
+  gqa::DiffParams diff;
+  const gqa_status st = diff_params(lam, lam_stride_b, lam_stride_t, lam_stride_h, H, H_kv,
+                                    split_keys, norm_weight, norm_eps, out_scale, &diff);
+  if (st != GQA_OK) return st;
+  const bool chunk = seq_lens || T_q != S_max || window >= 0 || n_part > 1;
+  return run_prefill(chunk, q, k_cache, v_cache, seq_lens, B, T_q, S_max, 2 * H, H_kv, d, scale,
+                     window < S_max ? window : -1, n_part, workspace, out, lse, stream, &diff);
 }
 
 gqa_status gqa_last_device_error(gqa_stream_t stream) {

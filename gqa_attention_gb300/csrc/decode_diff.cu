@@ -1,0 +1,656 @@
+// decode_diff.cu -- split-KV decode of differential attention, and the merge of its
+// partials (also those of a split chunk prefill).
+//
+// A head h has two maps over the keys of its KV head:
+//   O_u = softmax(tau q_u K_u^T) V  (u = 1, 2),   O = O_1 - lam O_2,
+// then optionally O / sqrt(mean(O^2) + eps) * w, times a constant.  Both maps read the same
+// V rows, and their keys are the same K rows (shared keys: q_1, q_2 are two query
+// heads) or the two halves of them (split keys: q_1, q_2 are the halves of one query
+// head).  So both sit in the M rows of the grouped-query decode: with shared keys as
+// two rows, with split keys as the rows (q_1, 0) and (0, q_2), whose products with whole
+// key rows are the two halves' products.  K and V are read once for all maps of a
+// KV head, and a row's softmax is the streaming (m, l, O) update of the other decodes.
+// The difference needs both maps' final sums, so it is taken where they are known: in the
+// epilogue with one split, in the merge with several.
+//
+// One CTA per (split, 32 query rows, KV head, sequence): a producer warp fills a ring of
+// 64-token K/V stages by TMA, and each group of four warps takes 16 query rows (one
+// m16n8k16 tile), a warp a 16-token slice of every stage.  Rows are ordered (query, map),
+// the maps of a head side by side, so a head's rows never part.
+//
+// Bound by HBM up to 16 rows.
+#include <type_traits>
+
+#include "decode_common.cuh"
+#include "diff.h"
+
+namespace gqa {
+namespace {
+
+constexpr int kTile = kDecodeTile;
+constexpr int kGroupWarps = 4;  // warps of a row group: 16 tokens of a stage each
+
+// The epilogue's last step on one head's row: each of `LANES` neighbouring lanes holds
+// 4 columns of O_1 and O_2 (divided by their sums); all of them call it together.
+template <int LANES>
+__device__ __forceinline__ float4 diff_row(const DiffParams& p, float4 a, float4 b, float lam, int c4) {
+  float4 y = make_float4(a.x - lam * b.x, a.y - lam * b.y, a.z - lam * b.z, a.w - lam * b.w);
+  float f = p.out_scale;
+  if (p.norm_eps >= 0.f) {
+    float ss = (y.x * y.x + y.y * y.y) + (y.z * y.z + y.w * y.w);
+#pragma unroll
+    for (int o = 1; o < LANES; o *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    f *= rsqrtf(ss * (1.f / (4 * LANES)) + p.norm_eps);
+    if (p.norm_weight) {
+      const float* w = p.norm_weight + 4 * c4;
+      y = make_float4(y.x * w[0], y.y * w[1], y.z * w[2], y.w * w[3]);
+    }
+  }
+  return make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+}
+
+template <int D, int NRG>
+constexpr int merge_bytes() {
+  return NRG * kGroupWarps * 16 * (D * 4 + 8);
+}
+
+// NRG: row groups of 16 of a CTA.  ROWS16 = false: one group of at most 8 rows.
+template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED>
+__global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 : 1)
+    gqa_decode_diff_kernel(const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v, const DecodeDiffParams pp) {
+  static_assert(ROWS16 || NRG == 1, "fewer than nine rows are one group");
+  using Lay = DecodeLayout<D>;
+  constexpr int kCW = kGroupWarps * NRG;  // consumer warps
+  constexpr int kStageBytes = Lay::kStageBytes;
+  static_assert(merge_bytes<D, NRG>() <= NSTAGE * kStageBytes, "the partials reuse the ring");
+  const DecodeParams& p = pp.dec;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE];
+  __shared__ int abort_flag, bad_page;
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t smem_base = smem_u32(smem);
+  volatile int* const abort_v = &abort_flag;
+  volatile int* const bad_v = &bad_page;
+
+  // (the row groups of one split are neighbours in launch order, so that their reads of
+  // the same K/V tiles meet in L2)
+  const int split = blockIdx.x / p.n_rg;
+  const int row0 = (blockIdx.x % p.n_rg) * (16 * NRG);  // first query row of this CTA
+  const int kv = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.G, h0 = kv * G;
+  const int R = min(16 * NRG, p.T_q * G - row0);  // live rows (even)
+  // Row x of the KV head is map h0 + x % G of query x / G; x / G without a division: (x +
+  // 1/2) / G lies at least 1/32 from the nearest integer, far above the float error.
+  const float inv_g = 1.f / static_cast<float>(G);
+  auto query_of = [&](int x) { return static_cast<int>((static_cast<float>(x) + 0.5f) * inv_g); };
+  auto out_row = [&](int r) -> size_t {  // row of lse and the workspace
+    const int x = row0 + r, tq = query_of(x);
+    return ((size_t)b * p.T_q + tq) * p.H_q + h0 + (x - tq * G);
+  };
+  const size_t n_rows = (size_t)p.B * p.T_q * p.H_q;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NSTAGE; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), kCW);
+    }
+    abort_flag = 0;
+    bad_page = 0;
+    fence_barrier_init();
+  }
+  // While the previous kernel finishes, the producer warp prefetches the split's first
+  // tiles into L2, one (tile, page segment) per lane.  The lengths and pages come
+  // from relaxed loads that may see values from before the previous kernel's writes;
+  // they only aim the prefetch, which hands no data to the kernel.
+  const int box = PAGED ? min(p.page_size, kTile) : kTile;  // rows per box
+  const int subs = kTile / box;
+  if (p.prefetch_tiles > 0 && warp == kCW && row0 == 0) {
+    int L_hint;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(L_hint) : "l"(p.seq_lens + b));
+    const int i = lane / subs, sub = lane % subs;
+    const int tk = split * p.chunk + i * kTile + sub * box;
+    if (i < p.prefetch_tiles && tk < min(min(p.S_max, L_hint), split * p.chunk + p.chunk)) {
+      int row = b * p.S_max + tk;
+      bool ok = true;
+      if constexpr (PAGED) {
+        int pg;
+        asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];"
+                     : "=r"(pg)
+                     : "l"(p.block_table + (size_t)b * p.max_blocks + tk / p.page_size));
+        ok = pg >= 0 && pg < p.num_pages;
+        row = pg * p.page_size + tk % p.page_size;
+      }
+      if (ok) {
+#pragma unroll
+        for (int blk = 0; blk < Lay::kBlocks; ++blk) {
+          tma_prefetch_l2_3d(&tm_k, blk * Lay::kBox, kv, row);
+          tma_prefetch_l2_3d(&tm_v, blk * Lay::kBox, kv, row);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int L = p.seq_lens[b];
+
+  // A bad length: NaN outputs (with several splits a NaN partial).  An empty split: the
+  // merge identity (-inf, 0), its O is not written.
+  const bool bad_len = L < p.T_q || L > p.S_max || L < 1;
+  const long long t_first = static_cast<long long>(split) * p.chunk;
+  if (bad_len || t_first >= L) {
+    if (bad_len && threadIdx.x == 0 && split == 0 && kv == 0 && row0 == 0)
+      atomicOr(p.err, kErrBadSeqLen);
+    const float2 ml = bad_len ? make_float2(NAN, NAN) : make_float2(-INFINITY, 0.f);
+    for (int r = threadIdx.x; r < R; r += blockDim.x) {
+      const size_t row = out_row(r);
+      if (p.n_split > 1) {
+        if (in_bounds(row * p.n_split + split, 1, n_rows * p.n_split, p.err))
+          p.ws_ml[row * p.n_split + split] = ml;
+      } else {
+        if (in_bounds(row, 1, n_rows, p.err)) p.lse[row] = NAN;
+      }
+    }
+    if (p.n_split == 1)
+      for (int e = threadIdx.x; e < R / 2 * D; e += blockDim.x) {
+        const size_t row = out_row(2 * (e / D)) / 2;
+        if (in_bounds(row * D + e % D, 1, n_rows / 2 * D, p.err))
+          p.out[row * D + e % D] = __float2bfloat16(NAN);
+      }
+    return;
+  }
+  const int t0 = static_cast<int>(t_first);
+  const int t_end = min(p.chunk, L - t0) + t0;
+  const int n_tiles = (t_end - t0 + kTile - 1) / kTile;
+
+  // ------------------------------------------------------------ producer ----
+  if (warp == kCW) {
+    if (lane == 0) {
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+    }
+    // Lane 0 takes the slot and arms its barrier; box `sub` of a tile is issued by lane
+    // `sub` (one box for a contiguous cache).  A page's index is read one tile ahead, so
+    // that the read is in flight while the producer waits for a slot.
+    const uint64_t pol = p.n_rg == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+    auto page_of = [&](int i) -> int {
+      const int tok = t0 + i * kTile + lane * box;
+      if (!PAGED || lane >= subs || tok >= t_end) return -1;
+      return p.block_table[(size_t)b * p.max_blocks + tok / p.page_size];
+    };
+    int page = page_of(0);
+    int issued = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int st = i % NSTAGE;
+      const int next = page_of(i + 1);
+      bool go = true;
+      if (lane == 0 && i >= NSTAGE) {
+        const uint32_t eb = smem_u32(&empty_bar[st]), par = ((i / NSTAGE) - 1) & 1;
+        if (!mbar_try_wait(eb, par) && (*abort_v || !mbar_wait(eb, par, p.wait_ns, p.err))) {
+          *abort_v = 1;
+          go = false;
+        }
+      }
+      const int tok = t0 + i * kTile + lane * box;
+      int row;
+      if constexpr (PAGED) {
+        // A box wholly past the split's end reads rows past the pool, which arrive as zeros.
+        const bool has = lane < subs && tok < t_end;
+        const bool bad = has && (page < 0 || page >= p.num_pages);
+        row = !has ? p.num_pages * p.page_size
+                   : (bad ? 0 : page) * p.page_size + tok % p.page_size;
+        // (recorded before lane 0's arrive releases it to the consumers)
+        if (__any_sync(0xffffffffu, bad) && lane == 0) {
+          if (!*bad_v) atomicOr(p.err, kErrBadPage);
+          *bad_v = 1;
+        }
+      } else {
+        row = b * p.S_max + tok;
+      }
+      if (lane == 0 && go) mbar_arrive_expect_tx(smem_u32(&full_bar[st]), kStageBytes);
+      if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      const uint32_t fb = smem_u32(&full_bar[st]);
+      if (lane < subs) {
+        const uint32_t dst = smem_base + st * kStageBytes + lane * box * Lay::kSpan;
+#pragma unroll
+        for (int blk = 0; blk < Lay::kBlocks; ++blk) {
+          tma_load_3d(dst + blk * Lay::kBlockBytes, &tm_k, fb, blk * Lay::kBox, kv, row, pol);
+          tma_load_3d(dst + Lay::kTileBytes + blk * Lay::kBlockBytes, &tm_v, fb, blk * Lay::kBox, kv,
+                      row, pol);
+        }
+      }
+      page = next;
+      issued = i + 1;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      // The next kernel may be scheduled now; it waits for this grid before it reads.
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      // No copy may still target this CTA's shared memory when it exits.
+      for (int i = max(0, issued - NSTAGE); i < issued; ++i)
+        mbar_wait(smem_u32(&full_bar[i % NSTAGE]), (i / NSTAGE) & 1, p.wait_ns, p.err);
+    }
+    __syncwarp();
+    return;
+  }
+
+  // ------------------------------------------------------------ consumers ---
+  const int g = lane >> 2, t = lane & 3;
+  const int ws = warp % kGroupWarps, grp = warp / kGroupWarps;
+  const int rb = row0 + 16 * grp;  // first row of this warp's group
+  // Q as the A operand; rows past T_q * G are zero, and with split keys the half of a row
+  // that is its head's other map (rows g and g + 8 have one parity, G being even).
+  uint32_t qa[D / 16][4];
+  {
+    const uint32_t* q32 = reinterpret_cast<const uint32_t*>(p.q);
+    auto word = [&](int x, int kk, int c) -> uint32_t {
+      if (x >= p.T_q * G) return 0u;
+      const int tq = query_of(x);
+      size_t row = ((size_t)b * p.T_q + tq) * p.H_q + h0 + (x - tq * G);
+      if (pp.diff.split_keys) {
+        if ((kk >= D / 32 ? 1 : 0) != (x & 1)) return 0u;
+        row >>= 1;
+      }
+      return q32[row * (D / 2) + c];
+    };
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      qa[kk][0] = word(rb + g, kk, kk * 8 + t);
+      qa[kk][1] = ROWS16 ? word(rb + g + 8, kk, kk * 8 + t) : 0u;
+      qa[kk][2] = word(rb + g, kk, kk * 8 + t + 4);
+      qa[kk][3] = ROWS16 ? word(rb + g + 8, kk, kk * 8 + t + 4) : 0u;
+    }
+  }
+  float o[D / 8][4];
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;
+  // ldmatrix lane roles.  K (non-transposed): matrix mi = lane / 8 covers tokens
+  // (mi / 2) * 8.. and d-chunk (mi % 2); V (transposed): tokens (mi % 2) * 8.., chunk mi / 2.
+  const int k_row = ws * 16 + ((lane >> 4) << 3) + (lane & 7), k_chk = (lane >> 3) & 1;
+  const int v_row = ws * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), v_chk = lane >> 4;
+  // Query t sees keys below L - T_q + 1 + t.
+  const int lim0 = min(t_end, L - p.T_q + 1 + query_of(rb + g));
+  const int lim1 = min(t_end, L - p.T_q + 1 + query_of(rb + g + 8));
+  const int lim_lo = min(t_end, L - p.T_q + 1 + query_of(rb));
+
+  for (int i = 0; i < n_tiles; ++i) {
+    const int st = i % NSTAGE;
+    const uint32_t fb = smem_u32(&full_bar[st]), par = (i / NSTAGE) & 1;
+    bool ok = mbar_try_wait(fb, par);
+    if (!ok) ok = *abort_v == 0 && mbar_wait(fb, par, p.wait_ns, p.err);
+    if (!__all_sync(0xffffffffu, ok)) {  // (the warp stays converged for ldmatrix and mma)
+      *abort_v = 1;
+      break;
+    }
+    const uint32_t kbase = smem_base + st * kStageBytes, vbase = kbase + Lay::kTileBytes;
+    const int tok0 = t0 + i * kTile + ws * 16;  // first token of this warp's slice
+    float sacc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t b00, b01, b10, b11;
+      ldsm_x4(kbase + Lay::offset(k_row, kk * 2 + k_chk), b00, b01, b10, b11);
+      mma_bf16_16816(sacc[0], qa[kk], b00, b01);
+      mma_bf16_16816(sacc[1], qa[kk], b10, b11);
+    }
+    const bool partial = tok0 + 16 > lim_lo;
+    float x0[4], x1[4];  // rows g and g + 8, tokens tok0 + 8 nt + 2 t + c
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int tk = tok0 + nt * 8 + 2 * t + c;
+        x0[nt * 2 + c] = !partial || tk < lim0 ? sacc[nt][c] * p.scale_log2 : -INFINITY;
+        x1[nt * 2 + c] = !partial || tk < lim1 ? sacc[nt][2 + c] * p.scale_log2 : -INFINITY;
+      }
+    float p0[4], p1[4] = {0.f, 0.f, 0.f, 0.f};
+    const float a0 = online_update(x0, m0, l0, p0);
+    float a1 = 1.f;
+    if (ROWS16) a1 = online_update(x1, m1, l1, p1);
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      o[n][0] *= a0;
+      o[n][1] *= a0;
+      if (ROWS16) {
+        o[n][2] *= a1;
+        o[n][3] *= a1;
+      }
+    }
+    const uint32_t pa[4] = {pack_bf16x2(p0[0], p0[1]), pack_bf16x2(p1[0], p1[1]),
+                            pack_bf16x2(p0[2], p0[3]), pack_bf16x2(p1[2], p1[3])};
+    // O += P V with V's elements under the masks; of the accumulators, rows g and g + 8
+    // are kept as they were unless `in0`, `in1`.
+    auto pv = [&](uint32_t vm0, uint32_t vm1, auto some, bool in0, bool in1) {
+#pragma unroll
+      for (int jj = 0; jj < D / 16; ++jj) {
+        uint32_t v[4];
+        ldsm_x4_trans(vbase + Lay::offset(v_row, jj * 2 + v_chk), v[0], v[1], v[2], v[3]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float(&acc)[4] = o[2 * jj + u];
+          if constexpr (decltype(some)::value) {
+            float x[4] = {acc[0], acc[1], acc[2], acc[3]};
+            mma_bf16_16816(x, pa, v[2 * u] & vm0, v[2 * u + 1] & vm1);
+            acc[0] = in0 ? x[0] : acc[0];
+            acc[1] = in0 ? x[1] : acc[1];
+            acc[2] = in1 ? x[2] : acc[2];
+            acc[3] = in1 ? x[3] : acc[3];
+          } else {
+            mma_bf16_16816(acc, pa, v[2 * u] & vm0, v[2 * u + 1] & vm1);
+          }
+        }
+      }
+    };
+    if (!partial) {
+      pv(0xffffffffu, 0xffffffffu, std::false_type{}, true, true);
+    } else {
+      // Rows of V that a query does not see may hold anything, and 0 * NaN is NaN: those
+      // at or past a limit are zero in the product.
+      const int ta = tok0 + 2 * t, tc = ta + 8;
+      auto mask = [](int tk, int lim) {
+        return (tk < lim ? 0x0000ffffu : 0u) | (tk + 1 < lim ? 0xffff0000u : 0u);
+      };
+      bool odd = false;  // an infinity or NaN that only some of several queries see?
+      if (p.T_q > 1) {
+#pragma unroll
+        for (int jj = 0; jj < D / 16; ++jj) {
+          uint32_t v[4];
+          ldsm_x4_trans(vbase + Lay::offset(v_row, jj * 2 + v_chk), v[0], v[1], v[2], v[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x = v[e] & mask(e & 1 ? tc : ta, t_end);
+            odd |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+          }
+        }
+        odd = __any_sync(0xffffffffu, odd);
+      }
+      if (!odd) {
+        pv(mask(ta, t_end), mask(tc, t_end), std::false_type{}, true, true);
+      } else {  // one query's rows at a time, with that query's limit
+        const int q_end = query_of(min(rb + 16, p.T_q * G) - 1);
+        const int q0 = query_of(rb + g), q1 = query_of(rb + g + 8);
+#pragma unroll 1
+        for (int tq = query_of(rb); tq <= q_end; ++tq) {
+          const int lim = min(t_end, L - p.T_q + 1 + tq);
+          pv(mask(ta, lim), mask(tc, lim), std::true_type{}, q0 == tq, q1 == tq);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&empty_bar[st]));
+  }
+  l0 = quad_sum(l0);
+  if (ROWS16) l1 = quad_sum(l1);
+
+  // ------------------------------------------- merge the four warp partials --
+  named_bar_sync(1, kCW * 32);
+  const bool failed = *abort_v != 0 || (PAGED && *bad_v != 0);
+  float* mO = reinterpret_cast<float*>(smem);                                  // [kCW][16][D]
+  float2* mML = reinterpret_cast<float2*>(smem + kCW * 16 * D * 4);            // [kCW][16]
+  if (!failed) {
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      const int col = n * 8 + 2 * t;
+      *reinterpret_cast<float2*>(&mO[(warp * 16 + g) * D + col]) = make_float2(o[n][0], o[n][1]);
+      if (ROWS16)
+        *reinterpret_cast<float2*>(&mO[(warp * 16 + g + 8) * D + col]) =
+            make_float2(o[n][2], o[n][3]);
+    }
+    if (t == 0) {
+      mML[warp * 16 + g] = make_float2(m0, l0);
+      if (ROWS16) mML[warp * 16 + g + 8] = make_float2(m1, l1);
+    }
+  }
+  named_bar_sync(1, kCW * 32);
+
+  constexpr int V4 = D / 4;                        // lanes of a row, 4 columns each
+  constexpr int kRows = ROWS16 ? 16 * NRG : 8;     // rows in shared memory
+  auto merged = [&](int r, int c4, float& M, float& Ls) -> float4 {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    M = -INFINITY;
+    Ls = 0.f;
+    if (failed) {
+      M = Ls = NAN;
+      return make_float4(NAN, NAN, NAN, NAN);
+    }
+    const int at = (r / 16) * (kGroupWarps * 16) + r % 16;
+#pragma unroll
+    for (int w = 0; w < kGroupWarps; ++w) M = fmaxf(M, mML[at + w * 16].x);
+    const float ref = (M == -INFINITY) ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < kGroupWarps; ++w) {
+      const float2 ml = mML[at + w * 16];
+      const float a = ex2_approx(ml.x - ref);
+      Ls += a * ml.y;
+      const float4 ow = *reinterpret_cast<const float4*>(&mO[(at + w * 16) * D + c4 * 4]);
+      acc.x += a * ow.x;
+      acc.y += a * ow.y;
+      acc.z += a * ow.z;
+      acc.w += a * ow.w;
+    }
+    return acc;
+  };
+  if (p.n_split > 1) {
+    for (int e = threadIdx.x; e < kRows * V4; e += kCW * 32) {
+      const int r = e / V4, c4 = e % V4;
+      if (r >= R) break;
+      float M, Ls;
+      const float4 acc = merged(r, c4, M, Ls);
+      const size_t idx = out_row(r) * p.n_split + split;
+      if (in_bounds(idx * D + c4 * 4, 4, n_rows * p.n_split * D, p.err))
+        *reinterpret_cast<float4*>(&p.ws_O[idx * D + c4 * 4]) = acc;
+      if (c4 == 0 && in_bounds(idx, 1, n_rows * p.n_split, p.err))
+        p.ws_ml[idx] = make_float2(M * kLn2, Ls);
+    }
+    return;
+  }
+  // One split: both rows of a head, divided by their sums, and the difference.  A warp
+  // holds whole rows (V4 divides 32), and whole warps take part or not.
+  for (int e = threadIdx.x; e < kRows / 2 * V4; e += kCW * 32) {
+    const int r = 2 * (e / V4), c4 = e % V4;
+    float Ma, La, Mb, Lb;
+    float4 a = merged(r, c4, Ma, La), c = merged(r + 1, c4, Mb, Lb);
+    const float ia = 1.f / La, ic = 1.f / Lb;
+    // (each map rounded before the difference, so that equal maps leave exactly nothing at
+    // lam = 1)
+    a = make_float4(__fmul_rn(a.x, ia), __fmul_rn(a.y, ia), __fmul_rn(a.z, ia), __fmul_rn(a.w, ia));
+    c = make_float4(__fmul_rn(c.x, ic), __fmul_rn(c.y, ic), __fmul_rn(c.z, ic), __fmul_rn(c.w, ic));
+    const bool live = r < R;
+    const int x = row0 + r, tq = query_of(x), h = (h0 + (x - tq * G)) >> 1;
+    const float lam = live ? pp.diff.lam[(long long)b * pp.diff.lam_b + tq * pp.diff.lam_t +
+                                         h * pp.diff.lam_h]
+                           : 0.f;
+    const float4 y = diff_row<V4>(pp.diff, a, c, lam, c4);
+    if (!live) continue;
+    const size_t row = out_row(r);
+    const size_t orow = row / 2;
+    if (in_bounds(orow * D + c4 * 4, 4, n_rows / 2 * D, p.err))
+      *reinterpret_cast<uint2*>(&p.out[orow * D + c4 * 4]) =
+          make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    if (c4 == 0 && in_bounds(row, 2, n_rows, p.err))
+      *reinterpret_cast<float2*>(&p.lse[row]) =
+          make_float2((Ma + log2f(La)) * kLn2, (Mb + log2f(Lb)) * kLn2);
+  }
+}
+
+// ---------------------------------------------------------------- merge ----
+// One CTA per head row: 2 D threads, the first D for the first map's columns, the others for
+// the second's.  Each folds the parts of its column itself (the (m, l) pairs are read by
+// all of them, L1 hits), kMergeChunk parts to a round of loads; the second map's
+// columns then cross through shared memory.
+constexpr int kMergeChunk = 16;
+
+template <int D>
+__global__ void __launch_bounds__(2 * D) gqa_diff_merge_kernel(const DiffMergeParams p) {
+  __shared__ float s_o[D], s_ss[D / 32];
+  __shared__ float s_ml;
+  const int col = threadIdx.x % D, u = threadIdx.x / D;
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int H = p.H_maps / 2;
+  const size_t bt = blockIdx.x / static_cast<unsigned>(H);  // b * T + t
+  const int h = blockIdx.x % static_cast<unsigned>(H);
+  const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt % p.T);
+  const size_t row = bt * p.H_maps + 2 * h + u;
+  const float2* ml = p.ws_ml + row * p.n_part;
+  const float* O = p.ws_O + row * p.n_part * D + col;
+  float M = -INFINITY, L = 0.f, acc = 0.f;
+  bool bad = false;
+  for (int s0 = 0; s0 < p.n_part; s0 += kMergeChunk) {
+    float2 mlv[kMergeChunk];
+    float ov[kMergeChunk];
+#pragma unroll
+    for (int s = 0; s < kMergeChunk; ++s) {
+      const bool in = s0 + s < p.n_part;
+      mlv[s] = in ? ml[s0 + s] : make_float2(-INFINITY, 0.f);
+      ov[s] = in ? O[(size_t)(s0 + s) * D] : 0.f;
+      mlv[s].x *= p.m_log2;
+    }
+    float cm = M;
+#pragma unroll
+    for (int s = 0; s < kMergeChunk; ++s) {
+      bad |= isnan(mlv[s].x) || isnan(mlv[s].y);
+      cm = fmaxf(cm, mlv[s].x);
+    }
+    const float ref = (cm == -INFINITY) ? 0.f : cm;
+    const float a = ex2_approx(M - ref);
+    L *= a;
+    acc *= a;
+#pragma unroll
+    for (int s = 0; s < kMergeChunk; ++s) {
+      // an empty part (m = -inf) has weight 0 and its O (never written) is not used
+      const bool live = mlv[s].x != -INFINITY;
+      const float w = live ? ex2_approx(mlv[s].x - ref) : 0.f;
+      L += w * mlv[s].y;
+      acc += live ? w * ov[s] : 0.f;
+    }
+    M = cm;
+  }
+  const bool poisoned = bad || !(L > 0.f);
+  const size_t n_rows = (size_t)p.B * p.T * p.H_maps;
+  float o = poisoned ? NAN : acc / L;
+  if (col == 0 && in_bounds(b * p.lse_b + t * p.lse_t + (2 * h + u) * p.lse_m, 1, n_rows, p.err))
+    p.lse[b * p.lse_b + t * p.lse_t + (2 * h + u) * p.lse_m] =
+        poisoned ? NAN : (M + log2f(L)) * kLn2;
+  if (u == 1) s_o[col] = o;
+  __syncthreads();
+  float f = p.diff.out_scale;
+  if (u == 0) {
+    o -= p.diff.lam[(long long)b * p.diff.lam_b + t * p.diff.lam_t + h * p.diff.lam_h] * s_o[col];
+    if (p.diff.norm_eps >= 0.f) {
+      float ss = o * o;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+      if ((col & 31) == 0) s_ss[col / 32] = ss;
+    }
+  }
+  if (p.diff.norm_eps >= 0.f) {
+    __syncthreads();
+    float ss = 0.f;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) ss += s_ss[w];
+    f *= rsqrtf(ss * (1.f / D) + p.diff.norm_eps);
+    if (p.diff.norm_weight) o *= p.diff.norm_weight[col];
+  }
+  const size_t orow = bt * H + h;
+  if (u == 0 && in_bounds(orow * D + col, 1, n_rows / 2 * D, p.err))
+    p.out[orow * D + col] = __float2bfloat16(o * f);
+}
+
+template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED>
+cudaError_t launch(const DecodeDiffParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                   cudaStream_t stream) {
+  constexpr int smem = NSTAGE * DecodeLayout<D>::kStageBytes + 1024;
+  constexpr int threads = (kGroupWarps * NRG + 1) * 32;
+  auto kern = gqa_decode_diff_kernel<D, NRG, ROWS16, NSTAGE, PAGED>;
+  static unsigned char done[64];
+  static int resident[64];
+  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), smem, done);
+  if (e != cudaSuccess) return e;
+  int fit = 0;
+  e = resident_ctas(reinterpret_cast<const void*>(kern), threads, smem, resident, &fit);
+  if (e != cudaSuccess) return e;
+  DecodeDiffParams p = p_in;
+  // The L2 prefetch pays only when every CTA is resident while the previous kernel drains.
+  const long long ctas = (long long)p.dec.n_split * p.dec.n_rg * p.dec.H_kv * p.dec.B;
+  constexpr int kBytes = 98304 / DecodeLayout<D>::kStageBytes;
+  p.dec.prefetch_tiles = ctas <= fit ? (kBytes < 6 ? kBytes : 6) : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.dec.n_split * p.dec.n_rg, p.dec.H_kv, p.dec.B);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tm_k, tm_v, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D, bool PAGED>
+cudaError_t launch_rows(const DecodeDiffParams& p_in, const CUtensorMap& tm_k,
+                        const CUtensorMap& tm_v, cudaStream_t stream) {
+  DecodeDiffParams p = p_in;
+  const int rows = p.dec.T_q * p.dec.G;
+  p.dec.n_rg = rows <= 16 ? 1 : (rows + 31) / 32;
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  // A grid of at most one CTA per SM takes a deeper ring in the room of a second CTA.
+  const bool one = (long long)p.dec.n_split * p.dec.n_rg * p.dec.H_kv * p.dec.B <= sms;
+  constexpr int kShallow = D == 128 ? 3 : 6, kDeep = 6;
+  if (rows > 16) return launch<D, 2, true, kDeep, PAGED>(p, tm_k, tm_v, stream);
+  if (rows > 8)
+    return one ? launch<D, 1, true, kDeep, PAGED>(p, tm_k, tm_v, stream)
+               : launch<D, 1, true, kShallow, PAGED>(p, tm_k, tm_v, stream);
+  return one ? launch<D, 1, false, kDeep, PAGED>(p, tm_k, tm_v, stream)
+             : launch<D, 1, false, kShallow, PAGED>(p, tm_k, tm_v, stream);
+}
+
+template <int D>
+cudaError_t launch_merge(const DiffMergeParams& p, cudaStream_t stream) {
+  const long long ctas = (long long)p.B * p.T * (p.H_maps / 2);
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(2 * D);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gqa_diff_merge_kernel<D>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode_diff(const DecodeDiffParams& p, const CUtensorMap& tm_k,
+                               const CUtensorMap& tm_v, cudaStream_t stream) {
+  const bool paged = p.dec.block_table != nullptr;
+  switch (p.dec.d) {
+    case 32: return paged ? launch_rows<32, true>(p, tm_k, tm_v, stream)
+                          : launch_rows<32, false>(p, tm_k, tm_v, stream);
+    case 64: return paged ? launch_rows<64, true>(p, tm_k, tm_v, stream)
+                          : launch_rows<64, false>(p, tm_k, tm_v, stream);
+    case 128: return paged ? launch_rows<128, true>(p, tm_k, tm_v, stream)
+                           : launch_rows<128, false>(p, tm_k, tm_v, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_diff_merge(const DiffMergeParams& p, cudaStream_t stream) {
+  switch (p.d) {
+    case 32: return launch_merge<32>(p, stream);
+    case 64: return launch_merge<64>(p, stream);
+    case 128: return launch_merge<128>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace gqa

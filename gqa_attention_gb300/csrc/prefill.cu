@@ -43,8 +43,19 @@
 // (base 2); p = 2^(x - m_ref) then stays <= 2^8, and because l and O always
 // share the same reference m_ref, the final O / l is unchanged (p.3 §5 holds
 // for any reference value, not only the running maximum).
+//
+// Differential attention (DIFF): the two heads of an item are the two maps of one
+// output head, O = O_1 / l_1 - lam O_2 / l_2 with an optional norm over the head.  Loads,
+// products and softmaxes are those of a head pair; only the epilogue differs: each
+// warpgroup takes half of the columns of both maps from tensor memory (for the norm's
+// sum all of them), and the two threads of a row, one in each warpgroup, tell each
+// other 1 / l through shared memory.  DIFF = 1: two query heads over
+// the same keys.  DIFF = 2 (split keys): the maps are the halves of one query row and of
+// the key rows, so S_X takes the k-steps of its half only.
 #include <climits>
+#include <type_traits>
 
+#include "diff.h"
 #include "gqa_attn.h"
 #include "tcgen05.cuh"
 
@@ -135,9 +146,11 @@ struct Geom {
   int j0, n, q_off;
   bool bad;
 };
-constexpr int kLensSm = 256;  // sequence lengths kept in shared memory
+// Sequence lengths kept in shared memory (fewer with the differential kernels' exchange, so
+// that both fit beside the ring).
+constexpr int lens_kept(int diff) { return diff ? 64 : 256; }
 
-template <bool GENERAL>
+template <bool GENERAL, int DIFF>
 __device__ __forceinline__ Geom item_geom(const PrefillParams& p, const Item& it,
                                           const int* lens_sm) {
   Geom g;
@@ -148,7 +161,7 @@ __device__ __forceinline__ Geom item_geom(const PrefillParams& p, const Item& it
     g.bad = false;
     return g;
   }
-  int L = !p.seq_lens ? p.S_kv : it.b < kLensSm ? lens_sm[it.b] : p.seq_lens[it.b];
+  int L = !p.seq_lens ? p.S_kv : it.b < lens_kept(DIFF) ? lens_sm[it.b] : p.seq_lens[it.b];
   g.bad = L < p.S || L > p.S_kv;
   if (g.bad) L = p.S;
   g.q_off = L - p.S;
@@ -166,11 +179,56 @@ __device__ __forceinline__ Geom item_geom(const PrefillParams& p, const Item& it
   return g;
 }
 
-template <bool GENERAL, int DP>
+// The 32 columns x[] of this lane's row, stored as bf16: at(row, column) is where a row of
+// the warp's 32 has 8 columns from `column` on, or null for a row that is not stored.  Lane
+// r's four 16-byte units u[k] (columns 8k .. 8k+7) go through a 4 x 4 transpose across each quad of
+// lanes, which leaves lane 4q + t with unit t of the quad's rows 4q .. 4q+3, so that every
+// store instruction writes 64 contiguous bytes of each of 8 rows.
+template <typename At>
+__device__ __forceinline__ void store_rows32(const float (&x)[32], int lane, At&& at) {
+  uint32_t u[4][4];
+#pragma unroll
+  for (int k4 = 0; k4 < 4; ++k4)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) u[k4][w] = pack_bf16x2(x[8 * k4 + 2 * w], x[8 * k4 + 2 * w + 1]);
+  const int t = lane & 3;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {  // swap the off-diagonal 2 x 2 blocks (lanes t, t ^ 2)
+    const uint32_t s0 = (t & 2) ? u[0][w] : u[2][w];
+    const uint32_t s1 = (t & 2) ? u[1][w] : u[3][w];
+    const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 2);
+    const uint32_t r1 = __shfl_xor_sync(0xffffffffu, s1, 2);
+    if (t & 2) { u[0][w] = r0; u[1][w] = r1; } else { u[2][w] = r0; u[3][w] = r1; }
+  }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {  // transpose each 2 x 2 block (lanes t, t ^ 1)
+    const uint32_t s0 = (t & 1) ? u[0][w] : u[1][w];
+    const uint32_t s1 = (t & 1) ? u[2][w] : u[3][w];
+    const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 1);
+    const uint32_t r1 = __shfl_xor_sync(0xffffffffu, s1, 1);
+    if (t & 1) { u[0][w] = r0; u[2][w] = r1; } else { u[1][w] = r0; u[3][w] = r1; }
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {  // u[v]: unit t of the quad's row v
+    __nv_bfloat16* dst = at((lane & ~3) + v, 8 * t);
+    if (dst) *reinterpret_cast<uint4*>(dst) = make_uint4(u[v][0], u[v][1], u[v][2], u[v][3]);
+  }
+}
+
+__host__ __device__ __forceinline__ const PrefillParams& base_params(const PrefillParams& p) { return p; }
+__host__ __device__ __forceinline__ const PrefillParams& base_params(const PrefillDiffParams& p) {
+  return p.pre;
+}
+template <int DIFF>
+using PrefillParamsOf = std::conditional_t<DIFF != 0, PrefillDiffParams, PrefillParams>;
+
+template <bool GENERAL, int DP, int DIFF>
 __global__ void __launch_bounds__(kPThreads, 1)
     gqa_prefill_causal_kernel(const __grid_constant__ CUtensorMap tm_q,
                               const __grid_constant__ CUtensorMap tm_k,
-                              const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
+                              const __grid_constant__ CUtensorMap tm_v,
+                              const PrefillParamsOf<DIFF> pp) {
+  const PrefillParams& p = base_params(pp);
   using Lay = PrefillLayout<DP>;
   constexpr int kSlots = Lay::kSlots;
   constexpr uint32_t kTileB = Lay::kTileB, kHalfB = Lay::kHalfB;
@@ -182,7 +240,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   // every role derives each item's key range from seq_lens[b]: read it once
-  __shared__ int lens_sm[GENERAL ? kLensSm : 1];
+  __shared__ int lens_sm[GENERAL ? lens_kept(DIFF) : 1];
+  // differential: 1 / l, which the two threads of a row tell each other, and per quarter of
+  // rows the barrier that says it is there
+  __shared__ float row_inv[DIFF ? 2 : 1][DIFF ? 128 : 1];
+  __shared__ __align__(8) uint64_t inv_ready[2][DIFF ? 4 : 1];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -208,13 +270,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(smem_u32(&s_full[x]), 1);
       mbar_init(smem_u32(&p_ready[x]), 4);
       mbar_init(smem_u32(&o_full[x]), 1);
-      mbar_init(smem_u32(&o_empty[x]), 4);
+      mbar_init(smem_u32(&o_empty[x]), DIFF ? 8 : 4);
+      if (DIFF)
+        for (int quarter = 0; quarter < 4; ++quarter)
+          mbar_init(smem_u32(&inv_ready[x][quarter]), 1);
     }
     abort_flag = 0;
     fence_barrier_init();
   }
   if (GENERAL && p.seq_lens)
-    for (int i = threadIdx.x; i < min(p.B, kLensSm); i += kPThreads) lens_sm[i] = p.seq_lens[i];
+    for (int i = threadIdx.x; i < min(p.B, lens_kept(DIFF)); i += kPThreads) lens_sm[i] = p.seq_lens[i];
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_base_sh), 512);
     tmem_relinquish();
@@ -257,14 +322,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (!item_of(k, n_items, per_qt, n_qt, n_pairs, p.H_kv, p.n_part, it)) continue;
           const bool pair = 2 * it.hp + 1 < p.G;
           const int hA = it.kv * p.G + 2 * it.hp;
-          const Geom gm = item_geom<GENERAL>(p, it, lens_sm);
+          const Geom gm = item_geom<GENERAL, DIFF>(p, it, lens_sm);
           if (GENERAL && gm.n == 0) continue;  // an empty part: nothing to load
           if (q_iter > 0 && !wait(&q_empty, (q_iter - 1) & 1)) break;
           const uint32_t qb = smem_u32(&q_full);
-          mbar_arrive_expect_tx(qb, pair ? 2 * kTileB : kTileB);
+          mbar_arrive_expect_tx(qb, pair && DIFF != 2 ? 2 * kTileB : kTileB);
           for (int dh = 0; dh < Lay::kHalves; ++dh) {
-            tma_load_4d(sb + kOffQ + dh * kHalfB, &tm_q, qb, dh * 64, hA, it.qt * 128, it.b);
-            if (pair)
+            // (split keys: both maps' queries are one row of head hA / 2)
+            tma_load_4d(sb + kOffQ + dh * kHalfB, &tm_q, qb, dh * 64, DIFF == 2 ? hA / 2 : hA,
+                        it.qt * 128, it.b);
+            if (pair && DIFF != 2)
               tma_load_4d(sb + kOffQ + kTileB + dh * kHalfB, &tm_q, qb, dh * 64, hA + 1,
                           it.qt * 128, it.b);
           }
@@ -298,6 +365,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
         constexpr uint32_t idS = instr_desc_bf16_f32(128, 128, false);
         constexpr uint32_t idPV = instr_desc_bf16_f32(128, DP, true);
         auto issue_s = [&](int x, uint32_t slot) {  // S_x = Q_x K^T, K = DP in steps of 16
+          if constexpr (DIFF == 2) {  // the d / 32 steps of half x of the rows
+            const uint32_t qa = sb + kOffQ, kb = sb + kOffRing + slot * kTileB;
+            const int steps = DP == 128 ? 4 : p.d / 32;
+  #pragma unroll
+            for (int ki = 0; ki < DP / 32; ++ki) {
+              if (ki >= steps) break;
+              const int kk = x * steps + ki;
+              const uint32_t off = (kk >> 2) * kHalfB + (kk & 3) * 32;
+              tc_mma_ss(tmem + 128 * x, smem_desc_sw128(qa + off, 16, 1024),
+                        smem_desc_sw128(kb + off, 16, 1024), idS, ki > 0);
+            }
+            return;
+          }
           const uint32_t qa = sb + kOffQ + x * kTileB, kb = sb + kOffRing + slot * kTileB;
   #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
@@ -321,7 +401,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (!item_of(k, n_items, per_qt, n_qt, n_pairs, p.H_kv, p.n_part, it)) continue;
           const bool pair = 2 * it.hp + 1 < p.G;
           const int nx = pair ? 2 : 1;
-          const int n = item_geom<GENERAL>(p, it, lens_sm).n;
+          const int n = item_geom<GENERAL, DIFF>(p, it, lens_sm).n;
           if (GENERAL && n == 0) continue;  // an empty part: no work
           if (!wait_all(&q_full, q_iter & 1)) break;
           ++q_iter;
@@ -408,6 +488,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int n_oc = p.d / 32;  // 32-column chunks of O that are stored
     const float c2 = p.scale_log2;
     uint32_t s_ph = 0, of_ph = 0;
+    uint32_t xc_ph = 0;  // differential: phase of the exchange between the warpgroups
     uint32_t ring_base = 0;  // ring position of this item's K_0 (chunk mode bookkeeping)
     bool alive = true;
     for (int k = 0; alive && k < n_rounds; ++k) {
@@ -416,7 +497,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const bool pair = 2 * it.hp + 1 < p.G;
       if (x == 1 && !pair) continue;
       const int h = it.kv * p.G + 2 * it.hp + x;
-      const Geom gm = item_geom<GENERAL>(p, it, lens_sm);
+      const Geom gm = item_geom<GENERAL, DIFF>(p, it, lens_sm);
       const int n = gm.n;
       const int q_row = it.qt * 128 + r;
       const size_t ws_row = (static_cast<size_t>(it.b) * p.S + q_row) * p.H_q + h;
@@ -580,8 +661,69 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (GENERAL && gm.bad && x == 0 && warp == 4 && lane == 0) atomicOr(p.err, kErrBadSeqLen);
       const bool split = GENERAL && p.n_part > 1;
       const int D = p.d;  // row width of out and of the O partials
+      if constexpr (DIFF != 0) {
+        if (!split) {
+          // This thread's columns: chunks of 32 from n_oc / 2 * x on (d = 32 has one chunk,
+          // the first warpgroup's).
+          const DiffParams& df = pp.diff;
+          row_inv[x][r] = inv;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&inv_ready[x][quarter]));
+          if (!wait_all(&inv_ready[1 - x][quarter], xc_ph) || !wait_all(&o_full[1 - x], of_ph ^ 1)) break;
+          tc_fence_after();
+          const int head = h >> 1;
+          const float lam =
+              store ? df.lam[it.b * df.lam_b + q_row * df.lam_t + head * df.lam_h] : 0.f;
+          const float i0 = row_inv[0][r], i1 = row_inv[1][r];
+          auto chunk = [&](int c, float (&y)[32]) {
+            uint32_t o[32], o2[32];
+            tmem_ld32(tmem + lane_base + 256 + 32 * c, o);
+            tmem_ld32(tmem + lane_base + 256 + DP + 32 * c, o2);
+            tmem_wait_ld();
+            reg_fence32(o);
+            reg_fence32(o2);
+            // (each map rounded first: equal maps leave exactly nothing at lam = 1)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              y[i] = fmaf(-lam, __fmul_rn(__uint_as_float(o2[i]), i1),
+                          __fmul_rn(__uint_as_float(o[i]), i0));
+          };
+          float f = df.out_scale;
+          if (df.norm_eps >= 0.f) {  // both threads of a row sum all of its squares
+            float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-      for (int c = 0; c < n_oc; ++c) {
+            for (int c = 0; c < n_oc; ++c) {
+              float y[32];
+              chunk(c, y);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s4[i & 3] += y[i] * y[i];
+            }
+            f *= rsqrtf(((s4[0] + s4[1]) + (s4[2] + s4[3])) / static_cast<float>(D) + df.norm_eps);
+          }
+          const int c_end = D == 32 ? 1 - x : n_oc / 2 * (x + 1);
+#pragma unroll 1
+          for (int c = n_oc / 2 * x; c < c_end; ++c) {
+            float y[32];
+            chunk(c, y);
+            if (df.norm_weight) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] *= f * __ldg(df.norm_weight + 32 * c + i);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] *= f;
+            }
+            store_rows32(y, lane, [&](int rr, int col) -> __nv_bfloat16* {
+              const int qrow = it.qt * 128 + quarter * 32 + rr;
+              const size_t at =
+                  ((static_cast<size_t>(it.b) * p.S + qrow) * (p.H_q / 2) + head) * D + 32 * c + col;
+              return qrow < p.S && in_bounds(at, 8, n_rows / 2 * D, p.err) ? p.out + at : nullptr;
+            });
+          }
+          xc_ph ^= 1;
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < (DIFF && !split ? 0 : n_oc); ++c) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * c, o);
         tmem_wait_ld();
@@ -597,42 +739,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
             st_global_v8(d + 8 * v, o[8 * v], o[8 * v + 1], o[8 * v + 2], o[8 * v + 3], o[8 * v + 4],
                          o[8 * v + 5], o[8 * v + 6], o[8 * v + 7]);
         } else if (!split) {
-          // Row r's 32 columns as four 16-byte units u[k] (columns 8k .. 8k+7).
-          // A 4 x 4 transpose of units across each quad of lanes leaves lane
-          // 4q + t with unit t of the quad's rows 4q .. 4q+3, so that every
-          // store instruction writes 64 contiguous bytes of each of 8 rows.
-          uint32_t u[4][4];
+          float y[32];
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4)
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-              u[k4][w] = pack_bf16x2(__uint_as_float(o[8 * k4 + 2 * w]) * inv,
-                                     __uint_as_float(o[8 * k4 + 2 * w + 1]) * inv);
-          const int t = lane & 3;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {  // swap the off-diagonal 2 x 2 blocks (lanes t, t ^ 2)
-            const uint32_t s0 = (t & 2) ? u[0][w] : u[2][w];
-            const uint32_t s1 = (t & 2) ? u[1][w] : u[3][w];
-            const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 2);
-            const uint32_t r1 = __shfl_xor_sync(0xffffffffu, s1, 2);
-            if (t & 2) { u[0][w] = r0; u[1][w] = r1; } else { u[2][w] = r0; u[3][w] = r1; }
-          }
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {  // transpose each 2 x 2 block (lanes t, t ^ 1)
-            const uint32_t s0 = (t & 1) ? u[0][w] : u[1][w];
-            const uint32_t s1 = (t & 1) ? u[2][w] : u[3][w];
-            const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 1);
-            const uint32_t r1 = __shfl_xor_sync(0xffffffffu, s1, 1);
-            if (t & 1) { u[0][w] = r0; u[2][w] = r1; } else { u[1][w] = r0; u[3][w] = r1; }
-          }
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {  // u[v]: unit t of the quad's row v
-            const int qrow = it.qt * 128 + quarter * 32 + (lane & ~3) + v;
-            const size_t orow = (static_cast<size_t>(it.b) * p.S + qrow) * p.H_q + h;
-            if (qrow < p.S && in_bounds(orow * D + 32 * c + 8 * t, 8, n_rows * D, p.err))
-              *reinterpret_cast<uint4*>(p.out + orow * D + 32 * c + 8 * t) =
-                  make_uint4(u[v][0], u[v][1], u[v][2], u[v][3]);
-          }
+          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * inv;
+          store_rows32(y, lane, [&](int rr, int col) -> __nv_bfloat16* {
+            const int qrow = it.qt * 128 + quarter * 32 + rr;
+            const size_t at = ((static_cast<size_t>(it.b) * p.S + qrow) * p.H_q + h) * D + 32 * c + col;
+            return qrow < p.S && in_bounds(at, 8, n_rows * D, p.err) ? p.out + at : nullptr;
+          });
         }
       }
       const size_t lse_at = (static_cast<size_t>(it.b) * p.H_q + h) * p.S + q_row;
@@ -643,7 +757,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         p.lse[lse_at] = (GENERAL && gm.bad) ? NAN : (m_ref + log2f(l)) * kLn2;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&o_empty[x]));
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&o_empty[x]));
+        // (differential: both warpgroups read both maps, or with parts their own only)
+        if (DIFF) mbar_arrive(smem_u32(&o_empty[split ? x : 1 - x]));
+      }
       if (GENERAL) ring_base += 2 * n;
     }
   }
@@ -656,16 +774,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 }
 
-template <bool GENERAL, int DP>
-cudaError_t launch_prefill_dp(const PrefillParams& p, const CUtensorMap& tm_q,
+template <bool GENERAL, int DP, int DIFF>
+cudaError_t launch_prefill_dp(const PrefillParamsOf<DIFF>& pp, const CUtensorMap& tm_q,
                               const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
                               cudaStream_t stream) {
   static unsigned char attr_done[64];
   constexpr uint32_t smem = PrefillLayout<DP>::kSmem;
+  const PrefillParams& p = base_params(pp);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto kern = gqa_prefill_causal_kernel<GENERAL, DP>;
+  auto kern = gqa_prefill_causal_kernel<GENERAL, DP, DIFF>;
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -674,18 +793,19 @@ cudaError_t launch_prefill_dp(const PrefillParams& p, const CUtensorMap& tm_q,
   const long long n_items =
       (long long)((p.S + 127) / 128) * p.B * p.H_kv * ((p.G + 1) / 2) * (GENERAL ? p.n_part : 1);
   const int grid = (int)(n_items < num_sms ? n_items : num_sms);
-  kern<<<grid, kPThreads, smem, stream>>>(tm_q, tm_k, tm_v, p);
+  kern<<<grid, kPThreads, smem, stream>>>(tm_q, tm_k, tm_v, pp);
   return cudaGetLastError();
 }
 
 // d = 128 on 128-wide tiles; d = 64 and d = 32 on 64-wide tiles (d = 32 zero-padded by TMA).
-template <bool GENERAL>
-cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                           const CUtensorMap& tm_v, int num_sms, cudaStream_t stream) {
-  switch (p.d) {
-    case 128: return launch_prefill_dp<GENERAL, 128>(p, tm_q, tm_k, tm_v, num_sms, stream);
+template <bool GENERAL, int DIFF = 0>
+cudaError_t launch_prefill(const PrefillParamsOf<DIFF>& p, const CUtensorMap& tm_q,
+                           const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
+                           cudaStream_t stream) {
+  switch (base_params(p).d) {
+    case 128: return launch_prefill_dp<GENERAL, 128, DIFF>(p, tm_q, tm_k, tm_v, num_sms, stream);
     case 64:
-    case 32: return launch_prefill_dp<GENERAL, 64>(p, tm_q, tm_k, tm_v, num_sms, stream);
+    case 32: return launch_prefill_dp<GENERAL, 64, DIFF>(p, tm_q, tm_k, tm_v, num_sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -762,6 +882,16 @@ cudaError_t launch_prefill_chunk(const PrefillParams& p, const CUtensorMap& tm_q
                                  const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
                                  cudaStream_t stream) {
   return launch_prefill<true>(p, tm_q, tm_k, tm_v, num_sms, stream);
+}
+
+cudaError_t launch_prefill_diff(const PrefillDiffParams& p, bool general, const CUtensorMap& tm_q,
+                                const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
+                                cudaStream_t stream) {
+  if (p.diff.split_keys)
+    return general ? launch_prefill<true, 2>(p, tm_q, tm_k, tm_v, num_sms, stream)
+                   : launch_prefill<false, 2>(p, tm_q, tm_k, tm_v, num_sms, stream);
+  return general ? launch_prefill<true, 1>(p, tm_q, tm_k, tm_v, num_sms, stream)
+                 : launch_prefill<false, 1>(p, tm_q, tm_k, tm_v, num_sms, stream);
 }
 
 }  // namespace gqa

@@ -49,6 +49,10 @@
  *   gqa_attn_prefill_chunk for the next chunk of a prompt (each also paged).  At 32K
  *   one token takes 14.6-14.9 us; eight take 31, and 25.5 over a bf16 cache by
  *   gqa_attn_decode_multi: with many query rows the 8-bit cache saves memory, not time.
+ * - New tokens into the bf16 or the per-token E4M3 caches, keys and queries turned by
+ *   their positions: gqa_kv_append and its _paged and _fp8 forms.
+ * - Differential attention (the difference of two softmax maps per head):
+ *   gqa_attn_decode_diff / _paged_diff, gqa_attn_prefill_diff.
  * - A few new tokens per sequence (speculative verification, T_q <= 64):
  *   gqa_attn_decode_multi / gqa_attn_decode_paged_multi (+ combine with B * T_q
  *   rows); above 16 query rows per KV head at d = 128 they run on the tensor
@@ -565,6 +569,143 @@ gqa_status gqa_attn_decode_paged_fp8_block(const void* q, const void* k_pool, co
  * rows, a capacity of 128K: 113 us by default, 47 us in one split).  Returns >= 1 (1
  * for invalid input). */
 int gqa_attn_decode_fp8_block_default_splits(int B, int T_q, int H_q, int H_kv, int S_max);
+
+/* ------------------------------------------------------------------------
+ * Appending to the bf16 and the per-token E4M3 caches, keys and queries turned
+ * ------------------------------------------------------------------------
+ * Writes the last tokens of each sequence into a cache of gqa_attn_decode(),
+ * _paged, _fp8 or _paged_fp8, and turns the keys, and the same tokens' queries, by
+ * their positions on the way (rotary position embedding).  A pair (x, y) of
+ * channels with frequency f at position p becomes
+ *   (x cos(p f) - y sin(p f),  x sin(p f) + y cos(p f)),
+ * computed in fp32 and rounded once, to bf16 or E4M3.  The angle is the product of
+ * the integer p and the fp32 number f, modulo a turn, to 2^-21 of a radian (for
+ * |p f| below 2^28).
+ *   q             device bf16, token (b, i) of [B, T] at q + (b * T + i) * q_stride
+ *                 elements, H_q * d dense elements; or NULL, with q_out NULL (H_q is
+ *                 not looked at then)
+ *   k_new, v_new  device bf16, likewise at (b * T + i) * kv_stride, H_kv * d elements.
+ *                 The strides are multiples of 8 and at least a token's elements: dense
+ *                 [B, T, H, d], or slices of the rows of a fused projection.
+ *   freqs         device fp32 [rot / 2], finite: radians per position of each pair
+ *                 (NULL with rot = 0, where nothing is turned)
+ *   rot           channels of a head that are turned, 0 .. rot - 1; a multiple of 16 up to
+ *                 d (GQA_ERR_UNSUPPORTED for other multiples).  The rest is copied.
+ *   interleaved   0: pair i is channels i and i + rot / 2; 1: channels 2i and 2i + 1
+ *   n_new         device int32 [B] with 0 <= n_new[b] <= T, or NULL (every one T)
+ *   positions     device int32 [B, T], the tokens' positions p (any sign); or NULL: a
+ *                 token's place in its sequence
+ *   seq_lens      device int32 [B], lengths AFTER the call: rows i < n_new[b] become
+ *                 tokens seq_lens[b] - n_new[b] + i.  n_new[b] <= seq_lens[b] <= S_max.
+ *   q_out         device bf16 [B, T, H_q, d]: turned queries of the rows i < n_new[b]; the
+ *                 others are left as they were.  May be q itself if q is dense.
+ *   d             16, 32, 64 or 128 (16: the halves of heads of 32, see below)
+ * Caches and pages are those of the decode calls, up to 2^31 - 2^16 token rows.  The
+ * _fp8 calls write E4M3 codes and one scale per token for all KV heads, K and V apart:
+ * the smallest power of two s >= 2^-100 with a / s <= 448, a the largest finite |x|
+ * of the token's (turned) values; codes are e4m3(x / s) to nearest even, infinities and
+ * NaN become the NaN code.
+ * Nothing else is read or written, in particular no row past n_new[b].  A bad length
+ * or count (checked on the device) leaves that sequence's cache untouched and makes its
+ * rows of q_out NaN; an entry of the block table outside the pool leaves its tokens
+ * unwritten (their queries are turned); both are reported through the error word
+ * (GQA_ERR_INVALID_ARG).  Two tokens must not share a cache row.  Deterministic.
+ * For split keys (differential attention below) a head is two heads of d / 2 here:
+ * pass 2 * H_q, 2 * H_kv and d / 2. */
+gqa_status gqa_kv_append(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                         int64_t kv_stride, const float* freqs, int rot, int interleaved,
+                         const int32_t* n_new, const int32_t* positions, const int32_t* seq_lens,
+                         int B, int T, int S_max, int H_q, int H_kv, int d, void* k_cache,
+                         void* v_cache, void* q_out, gqa_stream_t stream);
+gqa_status gqa_kv_append_paged(const void* q, const void* k_new, const void* v_new,
+                               int64_t q_stride, int64_t kv_stride, const float* freqs, int rot,
+                               int interleaved, const int32_t* n_new, const int32_t* positions,
+                               const int32_t* block_table, const int32_t* seq_lens, int B, int T,
+                               int num_pages, int page_size, int max_blocks, int H_q, int H_kv,
+                               int d, void* k_pool, void* v_pool, void* q_out,
+                               gqa_stream_t stream);
+gqa_status gqa_kv_append_fp8(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                             int64_t kv_stride, const float* freqs, int rot, int interleaved,
+                             const int32_t* n_new, const int32_t* positions,
+                             const int32_t* seq_lens, int B, int T, int S_max, int H_q, int H_kv,
+                             int d, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                             void* q_out, gqa_stream_t stream);
+gqa_status gqa_kv_append_paged_fp8(const void* q, const void* k_new, const void* v_new,
+                                   int64_t q_stride, int64_t kv_stride, const float* freqs,
+                                   int rot, int interleaved, const int32_t* n_new,
+                                   const int32_t* positions, const int32_t* block_table,
+                                   const int32_t* seq_lens, int B, int T, int num_pages,
+                                   int page_size, int max_blocks, int H_q, int H_kv, int d,
+                                   void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                   void* q_out, gqa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Differential attention
+ * ------------------------------------------------------------------------
+ * Head h has two maps over the keys of KV head floor(h / (H / H_kv)):
+ *   O_u = softmax(tau q_u K_u^T) V,  u = 1, 2,      O = O_1 - lam O_2,
+ * and with norm_eps >= 0  O <- O / sqrt(mean_c(O_c^2) + norm_eps) * norm_weight;
+ * the output is O times out_scale.  The difference, the norm and the constants are in fp32,
+ * with one rounding to bf16.  Two forms:
+ *   split_keys = 0  q_1, q_2 are query heads 2h and 2h + 1, K_1 = K_2 = K:
+ *                   q bf16 [B, T_q, 2 H, d]
+ *   split_keys = 1  q_1, q_2 and K_1, K_2 are the first and the second half of a query
+ *                   and a key row, V is whole: q bf16 [B, T_q, H, d]
+ * scale is tau (usually 1 / sqrt(d), and 1 / sqrt(d / 2) for split keys).
+ *   lam          device fp32, lam of (b, t, h) at b * lam_stride_b + t * lam_stride_t +
+ *                h * lam_stride_h elements (strides >= 0; 0 shares a value)
+ *   norm_weight  device fp32 [d], or NULL (ones); needs norm_eps >= 0
+ *   norm_eps     finite; negative: no norm.  O's squares are summed in fp32: keep |O| below
+ *                2^60, and norm_eps above 0 where all of O may be 0.
+ *   out          device bf16 [B, T_q, H, d]
+ * The cache has no more than 2^31 - 2^16 token rows.  The maps' query rows are rows of
+ * the grouped-query kernels: K and V are read once for both.
+ *
+ * Decode of the last T_q positions of each sequence: query t of sequence b is at
+ * L - T_q + t, L = seq_lens[b], and sees keys 0 .. L - T_q + t.  Cache, pages,
+ * lengths, splits (gqa_attn_decode_split_chunk) and workspace are those of
+ * gqa_attn_decode() / gqa_attn_decode_paged() for B * T_q sequences of 2 H query heads
+ * (gqa_attn_decode_workspace_bytes(B * T_q, 2 * H, d, n_split) bytes, 256-byte aligned);
+ * a second launch merges several splits, no gqa_attn_decode_combine() follows.
+ * lse: device fp32 [B, T_q, 2 H], of map u of head h at 2h + u - 1, 8-byte aligned.
+ * 1 <= T_q <= 64, 2 H / H_kv <= 16 and T_q * 2 H / H_kv <= 64 (GQA_ERR_UNSUPPORTED
+ * above), n_split <= 65535.  A row of V that a query does not see never reaches it, whatever
+ * it holds; with split keys, infinities and NaN of a key row count for both maps.
+ * Deterministic. */
+gqa_status gqa_attn_decode_diff(const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* seq_lens, const float* lam, int64_t lam_stride_b,
+                                int64_t lam_stride_t, int64_t lam_stride_h, int B, int T_q,
+                                int S_max, int H, int H_kv, int d, int split_keys, float scale,
+                                const float* norm_weight, float norm_eps, float out_scale,
+                                int n_split, void* workspace, void* out, float* lse,
+                                gqa_stream_t stream);
+gqa_status gqa_attn_decode_paged_diff(const void* q, const void* k_pool, const void* v_pool,
+                                      const int32_t* block_table, const int32_t* seq_lens,
+                                      const float* lam, int64_t lam_stride_b, int64_t lam_stride_t,
+                                      int64_t lam_stride_h, int B, int T_q, int num_pages,
+                                      int page_size, int max_blocks, int H, int H_kv, int d,
+                                      int split_keys, float scale, const float* norm_weight,
+                                      float norm_eps, float out_scale, int n_split,
+                                      void* workspace, void* out, float* lse,
+                                      gqa_stream_t stream);
+
+/* Split count for gqa_attn_decode_diff on the current device.  Returns >= 1 (1 for invalid
+ * input). */
+int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_max);
+
+/* Prefill: q's T_q queries end each sequence, rows, lengths, window, parts and errors
+ * being those of gqa_attn_prefill_chunk_split() for 2 H query heads (seq_lens NULL, T_q ==
+ * S_max and window < 0: a causal prompt; n_part = 1: workspace unused; workspace of
+ * gqa_attn_prefill_chunk_workspace_bytes(B, T_q, 2 * H, d, n_part) bytes).  lse: device
+ * fp32 [B, 2 H, T_q].  B * T_q * 2 H is below 2^31.  As in the other prefill calls, an
+ * infinity or NaN in V reaches every query row of the 128-row tile that sees its token. */
+gqa_status gqa_attn_prefill_diff(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* seq_lens, const float* lam, int64_t lam_stride_b,
+                                 int64_t lam_stride_t, int64_t lam_stride_h, int B, int T_q,
+                                 int S_max, int H, int H_kv, int d, int split_keys, float scale,
+                                 int window, const float* norm_weight, float norm_eps,
+                                 float out_scale, int n_part, void* workspace, void* out,
+                                 float* lse, gqa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Decode with the merge inside thread-block clusters
