@@ -76,7 +76,7 @@ SIGNATURES = {
                                   _I, _F, _P, _F, _F, _I, _P, _P, _P, _P]),
     "gqa_attn_decode_paged_diff": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _I,
                                         _I, _I, _I, _I, _I, _F, _P, _F, _F, _I, _P, _P, _P, _P]),
-    "gqa_attn_decode_diff_default_splits": (_I, [_I, _I, _I, _I, _I]),
+    "gqa_attn_decode_diff_default_splits": (_I, [_I, _I, _I, _I, _I, _I]),
     "gqa_attn_prefill_diff": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _I, _I, _I,
                                    _I, _F, _I, _P, _F, _F, _I, _P, _P, _P, _P]),
     "gqa_trace_clear": (_I, []),
@@ -384,8 +384,8 @@ def gqa_attn_decode_paged_diff(q, k_pool, v_pool, block_table, seq_lens, lam, la
         _ptr(workspace), _ptr(out), _ptr(lse), _stream(stream))
 
 
-def gqa_attn_decode_diff_default_splits(B, T_q, H, H_kv, S_max) -> int:
-    return load().gqa_attn_decode_diff_default_splits(B, T_q, H, H_kv, S_max)
+def gqa_attn_decode_diff_default_splits(B, T_q, H, H_kv, S_max, d) -> int:
+    return load().gqa_attn_decode_diff_default_splits(B, T_q, H, H_kv, S_max, d)
 
 
 def gqa_attn_prefill_diff(q, k_cache, v_cache, seq_lens, lam, lam_stride_b, lam_stride_t,

@@ -481,6 +481,8 @@ gqa_status paged_shape(const int32_t* block_table, int num_pages, int page_size,
   return GQA_OK;
 }
 
+int length_pieces(int B, long long groups, int rows, int S_max);
+
 gqa_status run_decode_diff(const void* q, const void* k, const void* v, const int32_t* block_table,
                            const int32_t* seq_lens, const gqa::DiffParams& diff, int B, int T_q,
                            int S_max, long long rows, int num_pages, int page_size, int max_blocks,
@@ -492,11 +494,14 @@ gqa_status run_decode_diff(const void* q, const void* k, const void* v, const in
   if (T_q < 1 || T_q > 64 || T_q > S_max || n_split > 65535) return GQA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !aligned(lse, 8)) return GQA_ERR_INVALID_ARG;
   if (head_dim_ok(d) && T_q * (2 * H / H_kv) > kMaxMultiRows) return GQA_ERR_UNSUPPORTED;
-  const int box = block_table && page_size < gqa::kDecodeTile ? page_size : gqa::kDecodeTile;
+  // More than 16 rows of d = 128: one tensor-core tile of 128 keys.
+  const bool tc = multi_uses_tc(T_q, 2 * H / H_kv, d);
+  const int tile = tc ? 128 : gqa::kDecodeTile;
   CUtensorMap tm_k, tm_v;
   gqa::DecodeDiffParams p{};
-  gqa_status st = prepare_decode(q, k, v, seq_lens, B, S_max, rows, box, 2 * H, H_kv, d, scale,
-                                 n_split, workspace, out, lse, &tm_k, &tm_v, &p.dec);
+  gqa_status st = prepare_decode(q, k, v, seq_lens, B, S_max, rows,
+                                 block_table && page_size < tile ? page_size : tile, 2 * H, H_kv, d,
+                                 scale, n_split, workspace, out, lse, &tm_k, &tm_v, &p.dec);
   if (st != GQA_OK) return st;
   p.diff = diff;
   p.dec.T_q = T_q;
@@ -510,7 +515,29 @@ gqa_status run_decode_diff(const void* q, const void* k, const void* v, const in
                                                     gqa::decode_ws_O_offset(B * T_q, 2 * H, n_split))
                          : nullptr;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  st = cuda_status(gqa::launch_decode_diff(p, tm_k, tm_v, s));
+  if (tc) {
+    const uint64_t G = 2 * H / H_kv, BT = (uint64_t)B * T_q;
+    CUtensorMap tm_q;
+    if (diff.split_keys) {
+      const uint64_t dims[4] = {64, 2, (uint64_t)H, BT}, strides[3] = {128, 256, (uint64_t)H * 256};
+      const uint32_t box[4] = {64u, 2u, (uint32_t)G / 2, (uint32_t)T_q};
+      st = encode_bf16(&tm_q, q, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    } else {
+      const uint64_t dims[3] = {128, 2 * (uint64_t)H, BT}, strides[2] = {256, 2 * (uint64_t)H * 256};
+      const uint32_t box[3] = {64u, (uint32_t)G, (uint32_t)T_q};
+      st = encode_bf16(&tm_q, q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    if (st != GQA_OK) return st;
+    const long long per = ((long long)S_max + n_split - 1) / n_split;
+    p.dec.n_rg = 1;
+    p.dec.chunk = (int)((per + 127) / 128 * 128);
+    p.pieces = n_split == 1 ? 0 : length_pieces(B, H_kv, T_q * (int)G, S_max);
+    if ((long long)n_split * p.dec.chunk > 0x7fffffffLL) return GQA_ERR_INVALID_ARG;
+    st = cuda_status(gqa::launch_decode_diff_tc(p, tm_q, tm_k, tm_v, s));
+  } else {
+    if ((long long)n_split * p.dec.chunk > 0x7fffffffLL) return GQA_ERR_INVALID_ARG;
+    st = cuda_status(gqa::launch_decode_diff(p, tm_k, tm_v, s));
+  }
   if (st != GQA_OK || n_split == 1) return st;
   gqa::DiffMergeParams m{};
   m.diff = diff;
@@ -657,8 +684,19 @@ gqa_status gqa_kv_append_paged_fp8(const void* q, const void* k_new, const void*
                            stream);
 }
 
-int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_max) {
+int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_max, int d) {
   if (B < 1 || T_q < 1 || H < 1 || H_kv < 1 || H % H_kv != 0) return 1;
+  const int rows = (int)std::min<long long>((long long)T_q * (2LL * H / H_kv), 1 << 20);
+  if (multi_uses_tc(T_q, (int)std::min(2LL * H / H_kv, 1LL << 20), d)) {
+    // Cut by the lengths: room for twice as many pieces of a sequence as they have on average.
+    const int pieces = length_pieces(B, H_kv, rows, S_max);
+    if (pieces > 0) return 2 * ((pieces + B - 1) / B);
+    // One CTA on an SM: no more than fill them once (4 sequences of 8K, 8 KV heads, 32 rows:
+    // 45 us in five splits, 29 in four), and at least two tiles each.
+    const long long fill = num_sms_current_device() / ((long long)B * H_kv);
+    const long long tiles = ((long long)S_max + 127) / 128;
+    return (int)std::max(1LL, std::min(fill, (tiles + 1) / 2));
+  }
   return gqa_attn_decode_default_splits(B, H_kv, S_max, -1);
 }
 

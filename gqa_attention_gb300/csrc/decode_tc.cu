@@ -40,6 +40,18 @@
 // block table (p.17 §2-§4, p.18 §5); each 128-key tile arrives as boxes of
 // min(page_size, 128) rows, one page each.  A page index outside the pool is
 // reported and replaced by page 0, and the CTA's outputs become NaN.
+//
+// Differential attention (DIFF; decode_diff.cu says what it is): the rows are the maps of
+// the heads, two neighbours each.  With several splits only the merge differs; with one
+// the two lanes of a head exchange halves of their columns in the epilogue.  DIFF = 2, split
+// keys: both half-tiles of Q get all half rows from TMA, and the softmax warps then zero
+// the rows that are the other map's.  Batches of several sequences are cut by their
+// lengths (decode_cut.cuh), and a row of V among the last T_q tokens that holds an
+// infinity or NaN reaches the queries that see it and no others.
+#include <type_traits>
+
+#include "decode_cut.cuh"
+#include "diff.h"
 #include "tcgen05.cuh"
 
 namespace gqa {
@@ -61,11 +73,23 @@ constexpr uint32_t kTcSmem = kOffV + kTcSlots * kTileB + 1024;
 constexpr uint32_t kColO = 256;                 // O after S_0, S_1
 constexpr float kRescaleLog2 = 8.f;
 
-template <bool PAGED>
+__host__ __device__ __forceinline__ const DecodeParams& base_params(const DecodeParams& p) {
+  return p;
+}
+__host__ __device__ __forceinline__ const DecodeParams& base_params(const DecodeDiffParams& p) {
+  return p.dec;
+}
+template <int DIFF>
+using TcParamsOf = std::conditional_t<DIFF != 0, DecodeDiffParams, DecodeParams>;
+
+// CUT = true: the batch is cut by its lengths.  A variant of its own, so that the others'
+// splits stay plainly the block's index.
+template <bool PAGED, int DIFF, bool CUT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     gqa_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
+                         const __grid_constant__ CUtensorMap tm_v, const TcParamsOf<DIFF> pp) {
+  const DecodeParams& p = base_params(pp);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t q_full, drain;
   __shared__ __align__(8) uint64_t k_full[kTcSlots], k_empty[kTcSlots], v_full[kTcSlots],
@@ -74,12 +98,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ int bad_page;
+  // differential: Q's zeros are in place; per column of V, the first of the last T_q tokens
+  // that holds an infinity or NaN there
+  __shared__ __align__(8) uint64_t q_ready;
+  __shared__ int odd_from[DIFF ? 128 : 1], odd_seen;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x, kv = blockIdx.y, b = blockIdx.z;
+  int split = blockIdx.x, b = CUT ? 0 : blockIdx.z, chunk = p.chunk;
+  const int kv = blockIdx.y;
   const int G = p.G, rows = p.T_q * G;  // rows <= 128 (checked on the host)
   auto out_row = [&](int r) -> size_t {
     return ((size_t)b * p.T_q + r / G) * p.H_q + kv * G + r % G;
@@ -88,8 +117,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // NaN outputs of a row (one split), or its partial (m, l) alone (O is not read)
   auto write_nan_or_ml = [&](size_t row, float2 ml) {
     if (p.n_split == 1) {
-      if (in_bounds(row * 128, 128, n_rows * 128, p.err))
-        for (int c = 0; c < 128; ++c) p.out[row * 128 + c] = __float2bfloat16(NAN);
+      if (DIFF && (row & 1)) {
+        // (the head's output row is its first map's to write)
+      } else if (const size_t at = (DIFF ? row / 2 : row) * 128;
+                 in_bounds(at, 128, (DIFF ? n_rows / 2 : n_rows) * 128, p.err)) {
+        for (int c = 0; c < 128; ++c) p.out[at + c] = __float2bfloat16(NAN);
+      }
       if (in_bounds(row, 1, n_rows, p.err)) p.lse[row] = NAN;
     } else if (in_bounds(row * p.n_split + split, 1, n_rows * p.n_split, p.err)) {
       p.ws_ml[row * p.n_split + split] = ml;
@@ -112,10 +145,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(smem_u32(&p_ready[x]), 4);
     }
     mbar_init(smem_u32(&pv_done), 1);
+    if (DIFF) {
+      mbar_init(smem_u32(&q_ready), 4);
+      odd_seen = 0;
+    }
     abort_flag = 0;
     bad_page = 0;
     fence_barrier_init();
   }
+  if (DIFF && threadIdx.x < 128) odd_from[threadIdx.x] = 0x7fffffff;
   // Q rows past T_q * G are zero (their S, P and O rows are never stored, but
   // stay finite); the TMA box fills rows 0 .. rows - 1 only.
   for (int i = threadIdx.x; i < (128 - rows) * 16; i += kTcThreads) {
@@ -127,6 +165,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tmem_alloc(smem_u32(&tmem_base_sh), 512);
     tmem_relinquish();
     tc_fence_before();
+  }
+  // A batch cut by its lengths: the cut is worked out while the previous kernel
+  // finishes, from relaxed loads, and again after the dependency wait if a length has
+  // changed.
+  Piece piece{0, 0, 0, 0};
+  int cut_tiles[3] = {0, 0, 0};
+  auto tiles_of = [&](int L) {
+    return L < p.T_q || L > p.S_max ? 0 : (L + kTcKeys - 1) / kTcKeys;
+  };
+  auto take_piece = [&]() {
+    if constexpr (CUT) {
+      piece = find_piece(cut_tiles[0], cut_tiles[1], cut_tiles[2], p.B, p.n_split, pp.pieces,
+                         blockIdx.x, lane);
+      // (the same in every lane; a reduction's result is known to be)
+      piece.b = __reduce_max_sync(0xffffffffu, piece.b);
+      piece.split = __reduce_max_sync(0xffffffffu, piece.split);
+      piece.count = __reduce_max_sync(0xffffffffu, piece.count);
+      piece.tiles = __reduce_max_sync(0xffffffffu, piece.tiles);
+      b = max(piece.b, 0);
+      split = piece.split;
+      chunk = piece.tiles * kTcKeys;
+    }
+  };
+  if constexpr (CUT) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      int L = 0;
+      if (32 * k + lane < p.B)
+        asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];"
+                     : "=r"(L)
+                     : "l"(p.seq_lens + 32 * k + lane));
+      cut_tiles[k] = tiles_of(L);
+    }
+    take_piece();
   }
   // While the previous kernel finishes, the producer warp prefetches this
   // split's first K/V tiles into L2, one tile (paged: one page segment of a
@@ -142,8 +214,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int i = lane / nb, sub = lane % nb;
     int L_hint;
     asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(L_hint) : "l"(p.seq_lens + b));
-    const int tk = split * p.chunk + i * kTcKeys + sub * h;
-    if (i < p.prefetch_tiles && tk < min(min(p.S_max, L_hint), split * p.chunk + p.chunk)) {
+    const int tk = split * chunk + i * kTcKeys + sub * h;
+    if (i < p.prefetch_tiles && tk < min(min(p.S_max, L_hint), split * chunk + chunk)) {
       int row = b * p.S_max + tk;
       bool ok = true;
       if constexpr (PAGED) {
@@ -165,10 +237,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Launched as a programmatic dependent of the previous kernel in the
   // stream: nothing is read or written before that kernel has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (CUT) {
+    bool changed = false;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int t = 32 * k + lane < p.B ? tiles_of(p.seq_lens[32 * k + lane]) : 0;
+      changed |= t != cut_tiles[k];
+      cut_tiles[k] = t;
+    }
+    if (__any_sync(0xffffffffu, changed)) take_piece();
+    // the slots of the workspace that the sequence has no pieces for: the merge identity
+    if (piece.b >= 0 && split == piece.count - 1)
+      for (int r = warp; r < rows; r += kTcThreads / 32)
+        for (int i = piece.count + lane; i < p.n_split; i += 32) {
+          const size_t at = out_row(r) * p.n_split + i;
+          if (in_bounds(at, 1, n_rows * p.n_split, p.err))
+            p.ws_ml[at] = make_float2(-INFINITY, 0.f);
+        }
+  }
+  const bool none = CUT && piece.b < 0;  // a CTA past the batch's last piece
   const int L = p.seq_lens[b];
   const bool bad = L < p.T_q || L > p.S_max;  // (L >= T_q >= 1 otherwise)
-  const int t0 = split * p.chunk;
-  const int t_end = bad ? 0 : min(t0 + p.chunk, L);
+  const int t0 = split * chunk;
+  const int t_end = bad || none ? 0 : min(t0 + chunk, L);
   const int n = t_end > t0 ? (t_end - t0 + kTcKeys - 1) / kTcKeys : 0;
   __syncthreads();
   tc_fence_after();
@@ -177,7 +268,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // A bad length: NaN outputs and the error bit.  An empty split: the merge
     // identity (-inf, 0); its O is not written.  (One split is never empty.)
     if (bad && threadIdx.x == 0 && split == 0 && kv == 0) atomicOr(p.err, kErrBadSeqLen);
-    for (int r = threadIdx.x; r < rows; r += kTcThreads)
+    for (int r = threadIdx.x; r < rows && !none; r += kTcThreads)
       write_nan_or_ml(out_row(r), bad ? make_float2(NAN, NAN) : make_float2(-INFINITY, 0.f));
     tc_fence_before();
     __syncthreads();
@@ -216,8 +307,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tma_prefetch_map(&tm_k);
       tma_prefetch_map(&tm_v);
       mbar_arrive_expect_tx(qb, static_cast<uint32_t>(rows) * 256u);
-      for (int dh = 0; dh < 2; ++dh)
-        tma_load_3d(sb + kOffQ + dh * kHalfB, &tm_q, qb, dh * 64, kv * G, b * p.T_q);
+      for (int dh = 0; dh < 2; ++dh) {
+        if constexpr (DIFF == 2)  // all half rows, in the order of the maps, to both half-tiles
+          tma_load_4d(sb + kOffQ + dh * kHalfB, &tm_q, qb, 0, 0, kv * (G / 2), b * p.T_q);
+        else
+          tma_load_3d(sb + kOffQ + dh * kHalfB, &tm_q, qb, dh * 64, kv * G, b * p.T_q);
+      }
     }
     // K_0, then K_{j+1} and V_j: the order in which the tensor core reads
     // them.  A tile's slot is refilled once the MMA that read it completed.
@@ -332,7 +427,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc_commit(smem_u32(&v_empty[j % kTcSlots]));
       return true;
     };
-    bool ok = wait_all(&q_full, 0);
+    bool ok = wait_all(DIFF == 2 ? &q_ready : &q_full, 0);
+    if (DIFF == 2) tc_fence_after();
     // Tensor-pipe order S_0, S_1, P_0 V_0, S_2, P_1 V_1, ...: S_{j+1} runs while
     // the softmax works on S_j.  S_j overwrites P_{j-2}, whose P V was issued
     // before it (the MMAs of one thread execute in issue order).
@@ -368,7 +464,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int lim_lo = min(t_end, L - p.T_q + 1);
     float m_ref = -INFINITY, l = 0.f;
     bool alive = true;
-    for (int j = 0; j < n; ++j) {
+    if constexpr (DIFF == 2) {  // row r is map r & 1: zero in the other half's columns
+      alive = wait_all(&q_full, 0);
+      if (alive) {
+        const uint32_t at = sb + kOffQ + ((r & 1) ? 0u : kHalfB) + r * 128;
+#pragma unroll
+        for (int c16 = 0; c16 < 8; ++c16) st_shared_v4(at + c16 * 16, 0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&q_ready));
+      }
+    }
+    for (int j = 0; alive && j < n; ++j) {
       const int x = j & 1;
       const uint32_t tS = tmem + lane_base + 128 * x;
       if (!wait_all(&s_full[x], (j >> 1) & 1)) {
@@ -465,7 +572,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // padding of a sequence, or the next sequence's rows), and 0 * NaN would
       // reach O through P V, so row r of this V tile is zeroed if it lies past
       // the end, once the tile has landed (it is refilled only after P_j V_j).
-      if (tb + kTcKeys > t_end) {
+      // (Differential: nor may what the last T_q tokens hold reach the queries before
+      // them.  Elements that are not finite become zeros, and the epilogue gives NaN in
+      // their columns to the rows that see them.)
+      if (tb + kTcKeys > (DIFF ? lim_lo : t_end)) {
         if (!wait_all(&v_full[j % kTcSlots], (j / kTcSlots) & 1)) {
           alive = false;
           break;
@@ -477,6 +587,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int c16 = 0; c16 < 8; ++c16)
               st_shared_v4(vrow + hh * kHalfB + c16 * 16, 0u, 0u, 0u, 0u);
+        }
+        if constexpr (DIFF != 0) {
+          // (16-byte pieces of those rows, shared out among the threads: a row's thread
+          // looking through its row alone took 4 us)
+          const int first = max(lim_lo - tb, 0), pieces = (min(t_end - tb, kTcKeys) - first) * 16;
+          for (int e = threadIdx.x - 64; e < pieces; e += 128) {
+            const int row = first + (e >> 4), u = e & 15;
+            const uint32_t at = sb + kOffV + (j % kTcSlots) * kTileB + (u >> 3) * kHalfB + row * 128 +
+                                (u & 7) * 16;
+            uint4 w = ld_shared_v4(at);
+            auto odd = [](uint32_t x) {
+              return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+            };
+            if (odd(w.x) || odd(w.y) || odd(w.z) || odd(w.w)) {
+              // piece u of its half is logical piece (u ^ row) % 8 (128-byte swizzle)
+              const int col0 = (u >> 3) * 64 + ((u ^ row) & 7) * 8;
+              uint32_t* const wp = &w.x;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t ex = i & 1 ? 0x7f800000u : 0x7f80u;
+                if ((wp[i / 2] & ex) != ex) continue;
+                wp[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+                atomicMin(&odd_from[col0 + i], tb + row);
+              }
+              st_shared_v4(at, w.x, w.y, w.z, w.w);
+              odd_seen = 1;
+            }
+          }
         }
         fence_proxy_async_smem();
       }
@@ -490,6 +628,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // Paged: a bad page index (recorded before the producer's arrive on the
     // last V tile, which this wait acquires) makes the outputs NaN.
     bool page_ok = true;
+    // (every warp comes here; what the others found in V is in place behind this)
+    if constexpr (DIFF != 0) named_bar_sync(1, 128);
     if (PAGED && alive) {
       if (wait_all(&v_full[(n - 1) % kTcSlots], ((n - 1) / kTcSlots) & 1))
         page_ok = *reinterpret_cast<volatile int*>(&bad_page) == 0;
@@ -502,12 +642,85 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const size_t row = store ? out_row(r) : 0;
       const bool one = p.n_split == 1;
       const float inv = 1.f / l;
+      if constexpr (DIFF != 0) {
+        if (odd_seen) {  // NaN where this row sees what was not finite in V
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (odd_from[32 * c + i] < lim) o[i] = __float_as_uint(NAN);
+            tmem_st32(tO + 32 * c, o);
+          }
+          tmem_wait_st();
+        }
+      }
+      auto load_o = [&](int c, uint32_t (&o)[32]) {  // 32 columns of this row's O
         tmem_ld32(tO + 32 * c, o);
         tmem_wait_ld();
         reg_fence32(o);
+      };
+      if constexpr (DIFF != 0) {
+        if (one) {
+          // Lanes 2h and 2h + 1 hold the maps of a head: of each chunk the even lane takes
+          // columns 0 .. 15 of both, the odd one the others.
+          const DiffParams& df = pp.diff;
+          const bool second = lane & 1;
+          const float inv_a = __shfl_sync(0xffffffffu, inv, lane & ~1);
+          const float inv_b = __shfl_sync(0xffffffffu, inv, lane | 1);
+          const int tq = r / G, head = (kv * G + r % G) >> 1;
+          const float lam = store ? df.lam[b * df.lam_b + tq * df.lam_t + head * df.lam_h] : 0.f;
+          auto difference = [&](int c, float (&y)[16]) {
+            uint32_t o[32];
+            load_o(c, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? o[i] : o[16 + i], 1);
+              const float a = __uint_as_float(second ? got : o[i]);
+              const float z = __uint_as_float(second ? o[16 + i] : got);
+              y[i] = fmaf(-lam, __fmul_rn(z, inv_b), __fmul_rn(a, inv_a));
+            }
+          };
+          float f = df.out_scale;
+          if (df.norm_eps >= 0.f) {
+            float ss = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float y[16];
+              difference(c, y);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) ss += y[i] * y[i];
+            }
+            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            f *= rsqrtf(ss * (1.f / 128.f) + df.norm_eps);
+          }
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float y[16];
+            difference(c, y);
+            const int col = 32 * c + (second ? 16 : 0);
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float w0 = df.norm_weight ? df.norm_weight[col + 2 * i] : 1.f;
+              const float w1 = df.norm_weight ? df.norm_weight[col + 2 * i + 1] : 1.f;
+              w[i] = pack_bf16x2(y[2 * i] * w0 * f, y[2 * i + 1] * w1 * f);
+            }
+            const size_t at = row / 2 * 128 + col;
+            if (store && in_bounds(at, 16, n_rows / 2 * 128, p.err)) {
+              *reinterpret_cast<uint4*>(p.out + at) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(p.out + at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < (DIFF && one ? 0 : 4); ++c) {
+        uint32_t o[32];
+        load_o(c, o);
         if (!store) continue;
         const size_t at = (one ? row : row * p.n_split + split) * 128 + 32 * c;
         if (!in_bounds(at, 32, n_rows * (one ? 1 : p.n_split) * 128, p.err)) continue;
@@ -553,22 +766,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_decode_tc(const DecodeParams& p_in, const CUtensorMap& tm_q,
-                             const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                             cudaStream_t stream) {
-  if (p_in.d != 128 || p_in.T_q * p_in.G > 128 || p_in.chunk % kTcKeys != 0)
-    return cudaErrorInvalidValue;
+namespace {
+
+template <bool PAGED, int DIFF, bool CUT = false>
+cudaError_t launch_tc(const TcParamsOf<DIFF>& p_in, int pieces, const CUtensorMap& tm_q,
+                      const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
+  auto kern = gqa_decode_tc_kernel<PAGED, DIFF, CUT>;
   static unsigned char attr_done[64];
   static int sm_count[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    e = cudaFuncSetAttribute(gqa_decode_tc_kernel<false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(gqa_decode_tc_kernel<true>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e != cudaSuccess) return e;
     int sms = 0;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -578,18 +788,19 @@ cudaError_t launch_decode_tc(const DecodeParams& p_in, const CUtensorMap& tm_q,
       attr_done[dev] = 1;
     }
   }
-  DecodeParams p = p_in;
+  TcParamsOf<DIFF> pp = p_in;
+  DecodeParams& p = const_cast<DecodeParams&>(base_params(pp));
   // One CTA per SM: the L2 prefetch pays only when every CTA is resident
   // while the previous kernel drains, and for a paged cache only with pages
   // of at least 64 tokens (T_q = 8, Llama3-70B 32K: 28.9 -> 26.5 us at page
   // 128, but 32.8 -> 34.3 us at page 16, whose 24 small boxes per CTA cost
   // more than they hide).
-  const long long ctas = (long long)p.n_split * p.H_kv * p.B;
+  const long long ctas = pieces > 0 ? (long long)pieces * p.H_kv : (long long)p.n_split * p.H_kv * p.B;
   const int sms = (dev >= 0 && dev < 64) ? sm_count[dev] : 0;
-  const bool small_pages = p.block_table && p.page_size < 64;
+  const bool small_pages = PAGED && p.page_size < 64;
   p.prefetch_tiles = (ctas <= sms && !small_pages) ? GQA_TC_PREFETCH_TILES : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.n_split, p.H_kv, p.B);
+  cfg.gridDim = pieces > 0 ? dim3(pieces, p.H_kv) : dim3(p.n_split, p.H_kv, p.B);
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = kTcSmem;
   cfg.stream = stream;
@@ -598,10 +809,41 @@ cudaError_t launch_decode_tc(const DecodeParams& p_in, const CUtensorMap& tm_q,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = p.block_table ? cudaLaunchKernelEx(&cfg, gqa_decode_tc_kernel<true>, tm_q, tm_k, tm_v, p)
-                    : cudaLaunchKernelEx(&cfg, gqa_decode_tc_kernel<false>, tm_q, tm_k, tm_v, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, pp);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+bool tc_shape_ok(const DecodeParams& p) {
+  return p.d == 128 && p.T_q * p.G <= 128 && p.chunk % kTcKeys == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_tc(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                             const CUtensorMap& tm_v, cudaStream_t stream) {
+  if (!tc_shape_ok(p)) return cudaErrorInvalidValue;
+  return p.block_table ? launch_tc<true, 0>(p, 0, tm_q, tm_k, tm_v, stream)
+                       : launch_tc<false, 0>(p, 0, tm_q, tm_k, tm_v, stream);
+}
+
+cudaError_t launch_decode_diff_tc(const DecodeDiffParams& p, const CUtensorMap& tm_q,
+                                  const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                  cudaStream_t stream) {
+  if (!tc_shape_ok(p.dec)) return cudaErrorInvalidValue;
+  if (p.pieces > 0 && (p.dec.n_split < 2 || p.pieces <= p.dec.B || p.dec.B > kMaxCut))
+    return cudaErrorInvalidValue;
+  auto go = [&](auto paged, auto form, auto cut) {
+    return launch_tc<decltype(paged)::value, decltype(form)::value, decltype(cut)::value>(
+        p, p.pieces, tm_q, tm_k, tm_v, stream);
+  };
+  auto with_form = [&](auto paged, auto form) {
+    return p.pieces > 0 ? go(paged, form, std::true_type{}) : go(paged, form, std::false_type{});
+  };
+  auto with_page = [&](auto paged) {
+    return p.diff.split_keys ? with_form(paged, std::integral_constant<int, 2>{})
+                             : with_form(paged, std::integral_constant<int, 1>{});
+  };
+  return p.dec.block_table ? with_page(std::true_type{}) : with_page(std::false_type{});
 }
 
 }  // namespace gqa

@@ -23,6 +23,9 @@ struct DiffParams {
 struct DecodeDiffParams {
   DecodeParams dec;
   DiffParams diff;
+  // > 0: the batch is cut by its lengths into at most as many pieces, at most n_split of a
+  // sequence, and grid x is the piece; 0: split x of sequence z has dec.chunk keys.
+  int pieces;
 };
 
 // The merge of a head's partials, two maps of n_part parts each, and the epilogue.
@@ -50,6 +53,12 @@ cudaError_t launch_decode_diff(const DecodeDiffParams& p, const CUtensorMap& tm_
 cudaError_t launch_prefill_diff(const PrefillDiffParams& p, bool general, const CUtensorMap& tm_q,
                                 const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
                                 cudaStream_t stream);
+// d = 128, up to 128 rows of maps per KV head in one tensor-core tile (decode_tc.cu), 128-key
+// boxes and chunks.  tm_q: q as [B * T_q][2 H][d], box {64, G, T_q}; with split keys as
+// [B * T_q][H][2][64], box {64, 2, G / 2, T_q}.
+cudaError_t launch_decode_diff_tc(const DecodeDiffParams& p, const CUtensorMap& tm_q,
+                                  const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                  cudaStream_t stream);
 cudaError_t launch_diff_merge(const DiffMergeParams& p, cudaStream_t stream);
 
 }  // namespace gqa

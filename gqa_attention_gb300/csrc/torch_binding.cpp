@@ -586,7 +586,7 @@ PyObject* decode_diff_(PyObject* const* a) {
   if (!out) out = empty(o_shape, at::kBFloat16, c.dev);
   if (!lse) lse = empty(l_shape, at::kFloat, c.dev);
   Scratch scratch;
-  const int n_split = a[11] == Py_None ? lib.diff_splits(c.B, f.T, f.H, c.H, c.s_max())
+  const int n_split = a[11] == Py_None ? lib.diff_splits(c.B, f.T, f.H, c.H, c.s_max(), c.d)
                                        : as_int(a[11], call);
   if (n_split > 1) {
     const int64_t bytes = static_cast<int64_t>(lib.workspace_bytes(

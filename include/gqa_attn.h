@@ -669,7 +669,11 @@ gqa_status gqa_kv_append_paged_fp8(const void* q, const void* k_new, const void*
  * a second launch merges several splits, no gqa_attn_decode_combine() follows.
  * lse: device fp32 [B, T_q, 2 H], of map u of head h at 2h + u - 1, 8-byte aligned.
  * 1 <= T_q <= 64, 2 H / H_kv <= 16 and T_q * 2 H / H_kv <= 64 (GQA_ERR_UNSUPPORTED
- * above), n_split <= 65535.  A row of V that a query does not see never reaches it, whatever
+ * above), n_split <= 65535 and n_split splits' keys below 2^31.  With d = 128 and more than 16
+ * rows (T_q * 2 H / H_kv) all rows form one tensor-core tile, splits are of 128-key
+ * multiples, and batches of several sequences that fill the GPU are cut on the device by
+ * their lengths, into at most n_split splits of a sequence (a sequence's splits, and so
+ * the rounding of its outputs, then depend on the other lengths too).  A row of V that a query does not see never reaches it, whatever
  * it holds; with split keys, infinities and NaN of a key row count for both maps.
  * Deterministic. */
 gqa_status gqa_attn_decode_diff(const void* q, const void* k_cache, const void* v_cache,
@@ -691,7 +695,7 @@ gqa_status gqa_attn_decode_paged_diff(const void* q, const void* k_pool, const v
 
 /* Split count for gqa_attn_decode_diff on the current device.  Returns >= 1 (1 for invalid
  * input). */
-int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_max);
+int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_max, int d);
 
 /* Prefill: q's T_q queries end each sequence, rows, lengths, window, parts and errors
  * being those of gqa_attn_prefill_chunk_split() for 2 H query heads (seq_lens NULL, T_q ==

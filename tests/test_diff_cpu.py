@@ -140,11 +140,11 @@ def test_prefill_refusals():
 def test_default_splits():
     for B, T, H, Hk, S in [(1, 1, 32, 8, 32768), (8, 1, 32, 8, 65536), (1, 1, 4, 2, 1024),
                            (4, 4, 32, 8, 16384), (64, 1, 8, 4, 4001)]:
-        n = g.gqa_attn_decode_diff_default_splits(B, T, H, Hk, S)
+        n = g.gqa_attn_decode_diff_default_splits(B, T, H, Hk, S, 128)
         assert -(-S // 8192) <= n <= max(1, -(-S // 128))
-    assert g.gqa_attn_decode_diff_default_splits(1, 1, 9, 8, 4096) == 1
-    assert g.gqa_attn_decode_diff_default_splits(0, 1, 8, 8, 4096) == 1
-    assert g.gqa_attn_decode_diff_default_splits(1, 0, 8, 8, 4096) == 1
+    assert g.gqa_attn_decode_diff_default_splits(1, 1, 9, 8, 4096, 128) == 1
+    assert g.gqa_attn_decode_diff_default_splits(0, 1, 8, 8, 4096, 128) == 1
+    assert g.gqa_attn_decode_diff_default_splits(1, 0, 8, 8, 4096, 128) == 1
 
 
 def test_helpers_refuse_cpu_tensors():

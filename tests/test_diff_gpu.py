@@ -113,6 +113,39 @@ def test_decode(d, split, page, T, H, Hk, norm):
         c.compare(out, lse, want, n_split)
 
 
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("page,T,H,Hk", [(0, 2, 16, 2), (64, 4, 8, 1), (16, 5, 4, 1), (0, 3, 8, 1)])
+def test_decode_of_a_batch_cut_by_its_lengths(split, page, T, H, Hk):
+    # (enough tiles of one or two KV heads that the cut is taken: 16 to an SM)
+    S = 90000 if Hk == 2 else 180000
+    lens = [9000, T, 2000, 300, 129]
+    c = Case(lens, T, H, Hk, 128, split, page, norm=page != 64, S=None, lam="head")
+    want = c.expect()
+    if page:  # a table much wider than the sequences
+        wide = torch.zeros(c.B, S // page, dtype=torch.int32, device=DEV)
+        wide[:, :c.table.shape[1]] = c.table
+        c.table = wide
+        for n in (None, 2, 7, 64):
+            c.compare(*c.decode(n_split=n), want, n)
+        a, b = c.decode(), c.decode()
+        assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+        lens = c.dev_lens()
+        lens[2] = T - 1
+        out, lse = g.decode_diff(c.q.to(DEV), c.k, c.v, lens, c.lam.to(DEV), block_table=c.table, **c.form)
+        torch.cuda.synchronize()
+        assert g.gqa_last_device_error() == g.GQA_ERR_INVALID_ARG
+        assert out[2].isnan().all() and lse[2].isnan().all()
+        ok = [0, 1, 3, 4]
+        assert (np.abs(out.double().cpu().numpy() - want[0])[ok] <= want[2][ok]).all()
+    else:
+        k, v = (torch.full((c.B, S, Hk, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+                for _ in "kv")
+        k[:, :c.S], v[:, :c.S] = c.k, c.v
+        c.k, c.v = k, v
+        for n in (None, 3, 16):
+            c.compare(*c.decode(n_split=n), want, n)
+
+
 @pytest.mark.parametrize("L", [1, 2, 15, 16, 17, 63, 64, 65, 127, 129, 1000, 5003])
 def test_decode_lengths(L):
     for page, n in ((0, 1), (16, None), (64, 7), (0, 40)):
@@ -171,8 +204,9 @@ def test_decode_is_deterministic():
 
 def test_values_that_a_query_does_not_see_do_not_reach_it():
     for bad in (float("nan"), float("inf")):
-        for d, T, n_split in ((64, 6, 1), (128, 6, 2), (32, 4, 1)):
-            c = Case([70 + T, 64 + T // 2], T, 4, 2, d, seed=d)
+        for d, T, n_split, H in ((64, 6, 1, 4), (128, 4, 2, 4), (32, 4, 1, 4), (128, 6, 1, 4),
+                                 (128, 12, 2, 4), (128, 9, 1, 6)):
+            c = Case([70 + T, 123 + T // 2], T, H, 2, d, split=T == 9, seed=d + T)
             want = c.expect()
             first = c.decode(n_split=n_split)
             c.compare(*first, want)
