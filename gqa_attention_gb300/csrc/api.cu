@@ -697,7 +697,19 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
     const long long tiles = ((long long)S_max + 127) / 128;
     return (int)std::max(1LL, std::min(fill, (tiles + 1) / 2));
   }
-  return gqa_attn_decode_default_splits(B, H_kv, S_max, -1);
+  // Up to 1024 tokens one launch, which is a cluster of CTAs where the grid leaves room, and up
+  // to 2048 if it leaves room for eight CTAs (8 KV heads of 128, 2K tokens: 6.6 us, 5.6 in 16
+  // splits, but a second launch takes the host 2.5 us).
+  const long long sms = num_sms_current_device();
+  const long long groups = (long long)B * H_kv * (rows <= 16 ? 1 : (rows + 31) / 32);
+  if (S_max <= 1024 || (S_max <= 2048 && rows <= 32 && groups * 8 <= sms)) return 1;
+  // One sequence: a CTA to an SM.  Several: two (one and a half of more than 16 rows, which
+  // have an SM to themselves), since sequences are seldom equally long and two fill
+  // it better: 2 x 4K-30K tokens, 8 KV heads of 128, 35 us in 9 splits, 28 in 18 (all of
+  // 30K 39 and 39); 8 x 8K, 4 of 64, 21.7 in four, 13.9 in eight.  Splits of 128 to 8192 tokens.
+  long long n = B == 1 ? sms / groups : (rows <= 16 ? 4 : 3) * sms / (2 * groups);
+  n = std::min(n, ((long long)S_max + 127) / 128);
+  return (int)std::max({1LL, n, ((long long)S_max + 8191) / 8192});
 }
 
 gqa_status gqa_attn_decode_diff(const void* q, const void* k_cache, const void* v_cache,

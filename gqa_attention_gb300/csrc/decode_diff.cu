@@ -13,8 +13,9 @@
 // The difference needs both maps' final sums, so it is taken where they are known: in the
 // epilogue with one split, in the merge with several.
 //
-// One CTA per (split, 32 query rows, KV head, sequence): a producer warp fills a ring of
-// 64-token K/V stages by TMA, and each group of four warps takes 16 query rows (one
+// One CTA per (split, 32 query rows, KV head, sequence): two producer warps, one for K and one
+// for V, fill a ring of 64-token stages by TMA (a warp takes about 150 cycles to issue a
+// box, and a stage of 16-token pages has 8 to 16 of them), and each group of four warps takes 16 query rows (one
 // m16n8k16 tile), a warp a 16-token slice of every stage.  Rows are ordered (query, map),
 // the maps of a head side by side, so a head's rows never part.
 //
@@ -28,6 +29,8 @@ namespace gqa {
 namespace {
 
 constexpr int kTile = kDecodeTile;
+constexpr int kProducers = 2;   // warps: K, V
+constexpr int kMaxCluster = 8;  // CTAs of a cluster (the portable size)
 constexpr int kGroupWarps = 4;  // warps of a row group: 16 tokens of a stage each
 
 // The epilogue's last step on one head's row: each of `LANES` neighbouring lanes holds
@@ -49,21 +52,37 @@ __device__ __forceinline__ float4 diff_row(const DiffParams& p, float4 a, float4
   return make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
 }
 
+// Stages of a CTA that has an SM to itself, and of one that shares it.  (d = 64 and 32: 96 and
+// 48 KB, two and three CTAs of one row group on an SM.  Registers for a third and a
+// fourth slowed every CTA down: the tiny decode 3.4 -> 4.2 us, 8 x 8K of 64 in eight splits
+// 13.9 -> 15.5.)
+template <int D>
+struct Ring {
+  static constexpr int kDeep = 6;
+  static constexpr int kShallow = D == 128 ? 3 : 6;
+};
+
 template <int D, int NRG>
 constexpr int merge_bytes() {
   return NRG * kGroupWarps * 16 * (D * 4 + 8);
 }
 
 // NRG: row groups of 16 of a CTA.  ROWS16 = false: one group of at most 8 rows.
-template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED>
-__global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 : 1)
+// CLUSTER: p.n_split CTAs (8 at most) of one KV head and sequence are a thread-block cluster that
+// merges its partials itself: each leaves its (m, l, O) in its shared memory, and CTA `rank`
+// finishes heads rank, rank + n_split, .. from all of them, through distributed shared
+// memory.  One launch, no workspace.
+template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED, bool CLUSTER>
+__global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
+                                  NSTAGE == Ring<D>::kDeep ? 1 : 2)
     gqa_decode_diff_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const DecodeDiffParams pp) {
   static_assert(ROWS16 || NRG == 1, "fewer than nine rows are one group");
   using Lay = DecodeLayout<D>;
   constexpr int kCW = kGroupWarps * NRG;  // consumer warps
   constexpr int kStageBytes = Lay::kStageBytes;
-  static_assert(merge_bytes<D, NRG>() <= NSTAGE * kStageBytes, "the partials reuse the ring");
+  static_assert(merge_bytes<D, NRG>() + (CLUSTER ? 16 * NRG * (D * 4 + 8) : 0) <= NSTAGE * kStageBytes,
+                "the partials reuse the ring");
   const DecodeParams& p = pp.dec;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE];
@@ -94,20 +113,22 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
   const size_t n_rows = (size_t)p.B * p.T_q * p.H_q;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NSTAGE; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&full_bar[s]), kProducers);
       mbar_init(smem_u32(&empty_bar[s]), kCW);
     }
     abort_flag = 0;
     bad_page = 0;
     fence_barrier_init();
   }
-  // While the previous kernel finishes, the producer warp prefetches the split's first
+  // While the previous kernel finishes, the producer warps prefetch the split's first
   // tiles into L2, one (tile, page segment) per lane.  The lengths and pages come
   // from relaxed loads that may see values from before the previous kernel's writes;
   // they only aim the prefetch, which hands no data to the kernel.
   const int box = PAGED ? min(p.page_size, kTile) : kTile;  // rows per box
   const int subs = kTile / box;
-  if (p.prefetch_tiles > 0 && warp == kCW && row0 == 0) {
+  const bool is_v = warp == kCW + 1;  // the second producer
+  const CUtensorMap* const tm = is_v ? &tm_v : &tm_k;
+  if (p.prefetch_tiles > 0 && warp >= kCW && row0 == 0) {
     int L_hint;
     asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(L_hint) : "l"(p.seq_lens + b));
     const int i = lane / subs, sub = lane % subs;
@@ -125,10 +146,8 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
       }
       if (ok) {
 #pragma unroll
-        for (int blk = 0; blk < Lay::kBlocks; ++blk) {
-          tma_prefetch_l2_3d(&tm_k, blk * Lay::kBox, kv, row);
-          tma_prefetch_l2_3d(&tm_v, blk * Lay::kBox, kv, row);
-        }
+        for (int blk = 0; blk < Lay::kBlocks; ++blk)
+          tma_prefetch_l2_3d(tm, blk * Lay::kBox, kv, row);
       }
     }
   }
@@ -140,20 +159,21 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
   // merge identity (-inf, 0), its O is not written.
   const bool bad_len = L < p.T_q || L > p.S_max || L < 1;
   const long long t_first = static_cast<long long>(split) * p.chunk;
-  if (bad_len || t_first >= L) {
+  // (A cluster's CTAs all see the same length; its empty splits take part in the merge.)
+  if (bad_len || (!CLUSTER && t_first >= L)) {
     if (bad_len && threadIdx.x == 0 && split == 0 && kv == 0 && row0 == 0)
       atomicOr(p.err, kErrBadSeqLen);
     const float2 ml = bad_len ? make_float2(NAN, NAN) : make_float2(-INFINITY, 0.f);
     for (int r = threadIdx.x; r < R; r += blockDim.x) {
       const size_t row = out_row(r);
-      if (p.n_split > 1) {
+      if (!CLUSTER && p.n_split > 1) {
         if (in_bounds(row * p.n_split + split, 1, n_rows * p.n_split, p.err))
           p.ws_ml[row * p.n_split + split] = ml;
-      } else {
+      } else if (split == 0) {
         if (in_bounds(row, 1, n_rows, p.err)) p.lse[row] = NAN;
       }
     }
-    if (p.n_split == 1)
+    if (split == 0 && (CLUSTER || p.n_split == 1))
       for (int e = threadIdx.x; e < R / 2 * D; e += blockDim.x) {
         const size_t row = out_row(2 * (e / D)) / 2;
         if (in_bounds(row * D + e % D, 1, n_rows / 2 * D, p.err))
@@ -161,16 +181,13 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
       }
     return;
   }
-  const int t0 = static_cast<int>(t_first);
+  const int t0 = static_cast<int>(min(t_first, static_cast<long long>(L)));
   const int t_end = min(p.chunk, L - t0) + t0;
   const int n_tiles = (t_end - t0 + kTile - 1) / kTile;
 
   // ------------------------------------------------------------ producer ----
-  if (warp == kCW) {
-    if (lane == 0) {
-      tma_prefetch_map(&tm_k);
-      tma_prefetch_map(&tm_v);
-    }
+  if (warp >= kCW) {
+    if (lane == 0) tma_prefetch_map(tm);
     // Lane 0 takes the slot and arms its barrier; box `sub` of a tile is issued by lane
     // `sub` (one box for a contiguous cache).  A page's index is read one tile ahead, so
     // that the read is in flight while the producer waits for a slot.
@@ -182,6 +199,7 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
     };
     int page = page_of(0);
     int issued = 0;
+    bool told = false;  // of a page outside the pool
     for (int i = 0; i < n_tiles; ++i) {
       const int st = i % NSTAGE;
       const int next = page_of(i + 1);
@@ -203,23 +221,22 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
                    : (bad ? 0 : page) * p.page_size + tok % p.page_size;
         // (recorded before lane 0's arrive releases it to the consumers)
         if (__any_sync(0xffffffffu, bad) && lane == 0) {
-          if (!*bad_v) atomicOr(p.err, kErrBadPage);
+          if (!is_v && !told) atomicOr(p.err, kErrBadPage);
+          told = true;
           *bad_v = 1;
         }
       } else {
         row = b * p.S_max + tok;
       }
-      if (lane == 0 && go) mbar_arrive_expect_tx(smem_u32(&full_bar[st]), kStageBytes);
+      if (lane == 0 && go) mbar_arrive_expect_tx(smem_u32(&full_bar[st]), Lay::kTileBytes);
       if (!__shfl_sync(0xffffffffu, go, 0)) break;
       const uint32_t fb = smem_u32(&full_bar[st]);
       if (lane < subs) {
-        const uint32_t dst = smem_base + st * kStageBytes + lane * box * Lay::kSpan;
+        const uint32_t dst = smem_base + st * kStageBytes + (is_v ? Lay::kTileBytes : 0) +
+                             lane * box * Lay::kSpan;
 #pragma unroll
-        for (int blk = 0; blk < Lay::kBlocks; ++blk) {
-          tma_load_3d(dst + blk * Lay::kBlockBytes, &tm_k, fb, blk * Lay::kBox, kv, row, pol);
-          tma_load_3d(dst + Lay::kTileBytes + blk * Lay::kBlockBytes, &tm_v, fb, blk * Lay::kBox, kv,
-                      row, pol);
-        }
+        for (int blk = 0; blk < Lay::kBlocks; ++blk)
+          tma_load_3d(dst + blk * Lay::kBlockBytes, tm, fb, blk * Lay::kBox, kv, row, pol);
       }
       page = next;
       issued = i + 1;
@@ -228,11 +245,16 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
     if (lane == 0) {
       // The next kernel may be scheduled now; it waits for this grid before it reads.
       asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-      // No copy may still target this CTA's shared memory when it exits.
+      // No copy may still target this CTA's shared memory when it exits.  (After an abort the
+      // other producer may not have armed the last stages; the waits are bounded.)
       for (int i = max(0, issued - NSTAGE); i < issued; ++i)
         mbar_wait(smem_u32(&full_bar[i % NSTAGE]), (i / NSTAGE) & 1, p.wait_ns, p.err);
     }
     __syncwarp();
+    if constexpr (CLUSTER) {  // the consumers' two cluster barriers
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
 
@@ -432,7 +454,7 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
     }
     return acc;
   };
-  if (p.n_split > 1) {
+  if (!CLUSTER && p.n_split > 1) {
     for (int e = threadIdx.x; e < kRows * V4; e += kCW * 32) {
       const int r = e / V4, c4 = e % V4;
       if (r >= R) break;
@@ -446,12 +468,9 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
     }
     return;
   }
-  // One split: both rows of a head, divided by their sums, and the difference.  A warp
-  // holds whole rows (V4 divides 32), and whole warps take part or not.
-  for (int e = threadIdx.x; e < kRows / 2 * V4; e += kCW * 32) {
-    const int r = 2 * (e / V4), c4 = e % V4;
-    float Ma, La, Mb, Lb;
-    float4 a = merged(r, c4, Ma, La), c = merged(r + 1, c4, Mb, Lb);
+  // Columns 4 c4 .. of rows r and r + 1, the maps of a head: divided by their sums, and
+  // the difference.  A warp holds whole rows (V4 divides 32) and calls this converged.
+  auto finish = [&](int r, int c4, float4 a, float Ma, float La, float4 c, float Mb, float Lb) {
     const float ia = 1.f / La, ic = 1.f / Lb;
     // (each map rounded before the difference, so that equal maps leave exactly nothing at
     // lam = 1)
@@ -463,7 +482,7 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
                                          h * pp.diff.lam_h]
                            : 0.f;
     const float4 y = diff_row<V4>(pp.diff, a, c, lam, c4);
-    if (!live) continue;
+    if (!live) return;
     const size_t row = out_row(r);
     const size_t orow = row / 2;
     if (in_bounds(orow * D + c4 * 4, 4, n_rows / 2 * D, p.err))
@@ -472,99 +491,171 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + 1) * 32, NSTAGE <= 3 ? 2 
     if (c4 == 0 && in_bounds(row, 2, n_rows, p.err))
       *reinterpret_cast<float2*>(&p.lse[row]) =
           make_float2((Ma + log2f(La)) * kLn2, (Mb + log2f(Lb)) * kLn2);
+  };
+  if constexpr (!CLUSTER) {  // one split; whole warps take part or not
+    for (int e = threadIdx.x; e < kRows / 2 * V4; e += kCW * 32) {
+      const int r = 2 * (e / V4), c4 = e % V4;
+      float Ma, La, Mb, Lb;
+      const float4 a = merged(r, c4, Ma, La), c = merged(r + 1, c4, Mb, Lb);
+      finish(r, c4, a, Ma, La, c, Mb, Lb);
+    }
+  } else {
+    float* cO = reinterpret_cast<float*>(smem + merge_bytes<D, NRG>());  // [kRows][D]
+    float2* cML = reinterpret_cast<float2*>(cO + kRows * D);             // [kRows]
+#pragma unroll
+    for (int it = 0; it < (kRows * V4 + kCW * 32 - 1) / (kCW * 32); ++it) {
+      const int e = threadIdx.x + it * kCW * 32, r = e / V4, c4 = e % V4;
+      if (r >= kRows) break;
+      float M, Ls;
+      const float4 acc = merged(r, c4, M, Ls);
+      *reinterpret_cast<float4*>(&cO[r * D + c4 * 4]) = acc;
+      if (c4 == 0) cML[r] = make_float2(M, Ls);
+    }
+    __syncwarp();
+    cluster_sync();  // every partial of the cluster is in place
+    const int C = p.n_split;
+    const uint32_t sO = smem_u32(cO), sML = smem_u32(cML);
+    // One row folded over the cluster; an empty split has weight 0 (and O = 0).
+    auto folded = [&](int r, int c4, float& M, float& Ls) -> float4 {
+      float2 ml[kMaxCluster];
+      float4 ov[kMaxCluster];
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        ml[q] = make_float2(-INFINITY, 0.f);
+        ov[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q < C) {
+          ml[q] = ld_dsmem_f32x2(mapa_shared(sML + r * 8, q));
+          ov[q] = ld_dsmem_f32x4(mapa_shared(sO + (r * D + c4 * 4) * 4, q));
+        }
+      }
+      M = -INFINITY;
+      bool bad = false;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        bad |= isnan(ml[q].x) || isnan(ml[q].y);
+        M = fmaxf(M, ml[q].x);
+      }
+      const float ref = (M == -INFINITY) ? 0.f : M;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      Ls = 0.f;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        // (no key of such a split is seen: 0 * NaN must not come of its O)
+        if (ml[q].x == -INFINITY) continue;
+        const float w = ex2_approx(ml[q].x - ref);
+        Ls += w * ml[q].y;
+        acc.x += w * ov[q].x;
+        acc.y += w * ov[q].y;
+        acc.z += w * ov[q].z;
+        acc.w += w * ov[q].w;
+      }
+      if (bad) M = Ls = NAN;
+      return acc;
+    };
+    constexpr int kAtOnce = kCW * 32 / V4;  // heads that the CTA takes at a time
+    const int rank = static_cast<int>(cluster_ctarank());
+    for (int i = threadIdx.x / V4; 2 * (rank + C * (i - (i % (32 / V4)))) < kRows; i += kAtOnce) {
+      // (a warp's lanes stay together: heads past the last are folded from the last's rows)
+      const int r = 2 * (rank + C * i), c4 = threadIdx.x % V4, rr = min(r, kRows - 2);
+      float Ma, La, Mb, Lb;
+      const float4 a = folded(rr, c4, Ma, La), c = folded(rr + 1, c4, Mb, Lb);
+      finish(r, c4, a, Ma, La, c, Mb, Lb);
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another may still read its partial
   }
 }
 
 // ---------------------------------------------------------------- merge ----
 // One CTA per head row: 2 D threads, the first D for the first map's columns, the others for
-// the second's.  Each folds the parts of its column itself (the (m, l) pairs are read by
-// all of them, L1 hits), kMergeChunk parts to a round of loads; the second map's
-// columns then cross through shared memory.
-constexpr int kMergeChunk = 16;
-
-template <int D>
-__global__ void __launch_bounds__(2 * D) gqa_diff_merge_kernel(const DiffMergeParams p) {
+// the second's.  A thread folds the parts of its column, CHUNK to a round of loads; lane i
+// of its warp works out the weight of part i of the round and hands it round.  The
+// second map's columns then cross through shared memory.  A chain of latencies (the
+// partials, the exchange, the store), with lam and the weight loaded beside the
+// partials.  Registers are kept few: the CTAs are to be resident beside those of the
+// decode, waiting (8K tokens, 19 splits, every thread holding all (m, l) pairs in 128
+// registers: 9.4 us a step).
+template <int D, int CHUNK>
+__global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) gqa_diff_merge_kernel(const DiffMergeParams p) {
+  static_assert(CHUNK <= 32, "a lane for each part of a round");
   __shared__ float s_o[D], s_ss[D / 32];
-  __shared__ float s_ml;
-  const int col = threadIdx.x % D, u = threadIdx.x / D;
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int col = threadIdx.x % D, u = threadIdx.x / D, lane = threadIdx.x & 31;
   const int H = p.H_maps / 2;
-  const size_t bt = blockIdx.x / static_cast<unsigned>(H);  // b * T + t
-  const int h = blockIdx.x % static_cast<unsigned>(H);
-  const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt % p.T);
-  const size_t row = bt * p.H_maps + 2 * h + u;
+  const unsigned bt = blockIdx.x / static_cast<unsigned>(H);  // b * T + t
+  const int h = blockIdx.x - bt * H;
+  const int b = bt / static_cast<unsigned>(p.T), t = bt - b * p.T;
+  const size_t row = static_cast<size_t>(bt) * p.H_maps + 2 * h + u;
   const float2* ml = p.ws_ml + row * p.n_part;
   const float* O = p.ws_O + row * p.n_part * D + col;
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float M = -INFINITY, L = 0.f, acc = 0.f;
   bool bad = false;
-  for (int s0 = 0; s0 < p.n_part; s0 += kMergeChunk) {
-    float2 mlv[kMergeChunk];
-    float ov[kMergeChunk];
+  const float lam = p.diff.lam[b * p.diff.lam_b + t * p.diff.lam_t + h * p.diff.lam_h];
+  const float weight = p.diff.norm_weight ? p.diff.norm_weight[col] : 1.f;
+  for (int s0 = 0; s0 < p.n_part; s0 += CHUNK) {
+    const bool mine = lane < CHUNK && s0 + lane < p.n_part;
+    float2 part = mine ? ml[s0 + lane] : make_float2(-INFINITY, 0.f);
+    float ov[CHUNK];
 #pragma unroll
-    for (int s = 0; s < kMergeChunk; ++s) {
-      const bool in = s0 + s < p.n_part;
-      mlv[s] = in ? ml[s0 + s] : make_float2(-INFINITY, 0.f);
-      ov[s] = in ? O[(size_t)(s0 + s) * D] : 0.f;
-      mlv[s].x *= p.m_log2;
-    }
-    float cm = M;
+    for (int s = 0; s < CHUNK; ++s) ov[s] = s0 + s < p.n_part ? O[(size_t)(s0 + s) * D] : 0.f;
+    part.x *= p.m_log2;
+    bad |= __any_sync(0xffffffffu, isnan(part.x) || isnan(part.y));
+    float cm = part.x;
 #pragma unroll
-    for (int s = 0; s < kMergeChunk; ++s) {
-      bad |= isnan(mlv[s].x) || isnan(mlv[s].y);
-      cm = fmaxf(cm, mlv[s].x);
-    }
+    for (int k = 16; k > 0; k >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, k));
+    cm = fmaxf(cm, M);
     const float ref = (cm == -INFINITY) ? 0.f : cm;
     const float a = ex2_approx(M - ref);
-    L *= a;
+    // an empty part (m = -inf) has weight 0 and its O (never written) is not used
+    const bool live = part.x != -INFINITY;
+    const float w = live ? ex2_approx(part.x - ref) : 0.f;
+    const unsigned alive = __ballot_sync(0xffffffffu, live);
+    float lsum = live ? w * part.y : 0.f;
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, k);
+    L = L * a + lsum;
     acc *= a;
 #pragma unroll
-    for (int s = 0; s < kMergeChunk; ++s) {
-      // an empty part (m = -inf) has weight 0 and its O (never written) is not used
-      const bool live = mlv[s].x != -INFINITY;
-      const float w = live ? ex2_approx(mlv[s].x - ref) : 0.f;
-      L += w * mlv[s].y;
-      acc += live ? w * ov[s] : 0.f;
+    for (int s = 0; s < CHUNK; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      acc += (alive >> s & 1) ? ws * ov[s] : 0.f;
     }
     M = cm;
   }
   const bool poisoned = bad || !(L > 0.f);
   const size_t n_rows = (size_t)p.B * p.T * p.H_maps;
   float o = poisoned ? NAN : acc / L;
-  if (col == 0 && in_bounds(b * p.lse_b + t * p.lse_t + (2 * h + u) * p.lse_m, 1, n_rows, p.err))
-    p.lse[b * p.lse_b + t * p.lse_t + (2 * h + u) * p.lse_m] =
-        poisoned ? NAN : (M + log2f(L)) * kLn2;
   if (u == 1) s_o[col] = o;
+  const long long lse_at = b * p.lse_b + t * p.lse_t + (2 * h + u) * p.lse_m;
+  if (col == 0 && in_bounds(lse_at, 1, n_rows, p.err))
+    p.lse[lse_at] = poisoned ? NAN : (M + log2f(L)) * kLn2;
   __syncthreads();
   float f = p.diff.out_scale;
-  if (u == 0) {
-    o -= p.diff.lam[(long long)b * p.diff.lam_b + t * p.diff.lam_t + h * p.diff.lam_h] * s_o[col];
-    if (p.diff.norm_eps >= 0.f) {
+  if (u == 0) o = fmaf(-lam, s_o[col], o);
+  if (p.diff.norm_eps >= 0.f) {
+    if (u == 0) {
       float ss = o * o;
 #pragma unroll
       for (int k = 16; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
       if ((col & 31) == 0) s_ss[col / 32] = ss;
     }
-  }
-  if (p.diff.norm_eps >= 0.f) {
     __syncthreads();
     float ss = 0.f;
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) ss += s_ss[w];
     f *= rsqrtf(ss * (1.f / D) + p.diff.norm_eps);
-    if (p.diff.norm_weight) o *= p.diff.norm_weight[col];
   }
-  const size_t orow = bt * H + h;
-  if (u == 0 && in_bounds(orow * D + col, 1, n_rows / 2 * D, p.err))
-    p.out[orow * D + col] = __float2bfloat16(o * f);
+  const size_t at = (static_cast<size_t>(bt) * H + h) * D + col;
+  if (u == 0 && in_bounds(at, 1, n_rows / 2 * D, p.err)) p.out[at] = __float2bfloat16(o * weight * f);
 }
 
-template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED>
+template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED, bool CLUSTER = false>
 cudaError_t launch(const DecodeDiffParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                    cudaStream_t stream) {
   constexpr int smem = NSTAGE * DecodeLayout<D>::kStageBytes + 1024;
-  constexpr int threads = (kGroupWarps * NRG + 1) * 32;
-  auto kern = gqa_decode_diff_kernel<D, NRG, ROWS16, NSTAGE, PAGED>;
+  constexpr int threads = (kGroupWarps * NRG + kProducers) * 32;
+  auto kern = gqa_decode_diff_kernel<D, NRG, ROWS16, NSTAGE, PAGED, CLUSTER>;
   static unsigned char done[64];
   static int resident[64];
   cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), smem, done);
@@ -582,11 +673,15 @@ cudaError_t launch(const DecodeDiffParams& p_in, const CUtensorMap& tm_k, const 
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.dec.n_split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = CLUSTER ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, tm_k, tm_v, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -600,10 +695,30 @@ cudaError_t launch_rows(const DecodeDiffParams& p_in, const CUtensorMap& tm_k,
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
+  constexpr int kShallow = Ring<D>::kShallow, kDeep = Ring<D>::kDeep;
+  // One split of a grid that leaves SMs idle: a cluster for each KV head and sequence (8
+  // maps on 2 KV heads of 32, 1024 tokens: 3.4 us, one CTA each 6.4; 32 KV heads' worth of
+  // 64 maps of 128, 1024 tokens: 6.8 and 9.6), but for short caches (128 tokens, d = 128: 4.4
+  // and 3.5 us; 256 tokens, d = 32: 3.2 and 3.0).
+  const long long groups = (long long)p.dec.n_rg * p.dec.H_kv * p.dec.B;
+  if (p.dec.n_split == 1 && p.dec.n_rg == 1 && p.dec.S_max > 256) {
+    int c = kMaxCluster;
+    while (c > 1 && (c * groups > sms || (c - 1) * 64 >= p.dec.S_max)) c /= 2;
+    if (c > 1) {
+      p.dec.n_split = c;
+      const int per = (p.dec.S_max + c - 1) / c;
+      p.dec.chunk = (per + kTile - 1) / kTile * kTile;
+      if constexpr (D < 128)  // (d = 128 takes the tensor-core tile, decode_tc.cu)
+        if (rows > 16) return launch<D, 2, true, kDeep, PAGED, true>(p, tm_k, tm_v, stream);
+      if (rows > 8) return launch<D, 1, true, kShallow, PAGED, true>(p, tm_k, tm_v, stream);
+      return launch<D, 1, false, kShallow, PAGED, true>(p, tm_k, tm_v, stream);
+    }
+  }
   // A grid of at most one CTA per SM takes a deeper ring in the room of a second CTA.
-  const bool one = (long long)p.dec.n_split * p.dec.n_rg * p.dec.H_kv * p.dec.B <= sms;
-  constexpr int kShallow = D == 128 ? 3 : 6, kDeep = 6;
-  if (rows > 16) return launch<D, 2, true, kDeep, PAGED>(p, tm_k, tm_v, stream);
+  const bool one = p.dec.n_split * groups <= sms;
+  if constexpr (D < 128)
+    if (rows > 16) return launch<D, 2, true, kDeep, PAGED>(p, tm_k, tm_v, stream);
+  if (rows > 16) return cudaErrorInvalidValue;
   if (rows > 8)
     return one ? launch<D, 1, true, kDeep, PAGED>(p, tm_k, tm_v, stream)
                : launch<D, 1, true, kShallow, PAGED>(p, tm_k, tm_v, stream);
@@ -611,12 +726,10 @@ cudaError_t launch_rows(const DecodeDiffParams& p_in, const CUtensorMap& tm_k,
              : launch<D, 1, false, kShallow, PAGED>(p, tm_k, tm_v, stream);
 }
 
-template <int D>
+template <int D, int CHUNK>
 cudaError_t launch_merge(const DiffMergeParams& p, cudaStream_t stream) {
-  const long long ctas = (long long)p.B * p.T * (p.H_maps / 2);
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.B * p.T * (p.H_maps / 2)));
   cfg.blockDim = dim3(2 * D);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -624,8 +737,14 @@ cudaError_t launch_merge(const DiffMergeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, gqa_diff_merge_kernel<D>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gqa_diff_merge_kernel<D, CHUNK>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_merge_d(const DiffMergeParams& p, cudaStream_t stream) {
+  if ((long long)p.B * p.T * (p.H_maps / 2) > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return p.n_part <= 8 ? launch_merge<D, 8>(p, stream) : launch_merge<D, 32>(p, stream);
 }
 
 }  // namespace
@@ -646,9 +765,9 @@ cudaError_t launch_decode_diff(const DecodeDiffParams& p, const CUtensorMap& tm_
 
 cudaError_t launch_diff_merge(const DiffMergeParams& p, cudaStream_t stream) {
   switch (p.d) {
-    case 32: return launch_merge<32>(p, stream);
-    case 64: return launch_merge<64>(p, stream);
-    case 128: return launch_merge<128>(p, stream);
+    case 32: return launch_merge_d<32>(p, stream);
+    case 64: return launch_merge_d<64>(p, stream);
+    case 128: return launch_merge_d<128>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }
