@@ -483,6 +483,21 @@ gqa_status paged_shape(const int32_t* block_table, int num_pages, int page_size,
 
 int length_pieces(int B, long long groups, int rows, int S_max);
 
+// Pieces for every KV head that a batch of differential decode on mma.sync is cut into by its
+// lengths, or 0: even splits.  One piece for each CTA that the GPU holds (two to an SM, one
+// of more than 16 rows).  Where a piece has 32 tiles of 64 keys (8 sequences of 1K to 64K, 8 KV
+// heads of 128: 174 us, 238 in 8 even splits, 177 in 12), or, of more than 16 rows, 4 (8 x
+// 20K, 3 heads of 64, 30 rows: all equally long 38.7 us, even 48.8; 3K to 20K 28.8 and
+// 28.0); with less the cut takes what it saves (4 x 8K, 4 heads of 128: 14.6 and 12.9).
+// Fewer than four pieces a sequence fill the GPU badly (24 x 20K, 5 heads of 32: 102 and 69).
+int diff_pieces(int B, int H_kv, int rows, int S_max) {
+  const long long groups = (long long)H_kv * (rows <= 16 ? 1 : (rows + 31) / 32);
+  const long long slots = (rows <= 16 ? 2LL : 1LL) * num_sms_current_device();
+  const long long pieces = slots / groups, tiles = ((long long)S_max + 63) / 64;
+  const long long least = rows <= 16 ? 32 : 4;
+  return B > 1 && B <= 96 && pieces >= 4LL * B && tiles * B * groups >= least * slots ? (int)pieces : 0;
+}
+
 gqa_status run_decode_diff(const void* q, const void* k, const void* v, const int32_t* block_table,
                            const int32_t* seq_lens, const gqa::DiffParams& diff, int B, int T_q,
                            int S_max, long long rows, int num_pages, int page_size, int max_blocks,
@@ -536,6 +551,7 @@ gqa_status run_decode_diff(const void* q, const void* k, const void* v, const in
     st = cuda_status(gqa::launch_decode_diff_tc(p, tm_q, tm_k, tm_v, s));
   } else {
     if ((long long)n_split * p.dec.chunk > 0x7fffffffLL) return GQA_ERR_INVALID_ARG;
+    p.pieces = n_split == 1 ? 0 : diff_pieces(B, H_kv, T_q * (2 * H / H_kv), S_max);
     st = cuda_status(gqa::launch_decode_diff(p, tm_k, tm_v, s));
   }
   if (st != GQA_OK || n_split == 1) return st;
@@ -702,6 +718,8 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
   // splits, but a second launch takes the host 2.5 us).
   const long long sms = num_sms_current_device();
   const long long groups = (long long)B * H_kv * (rows <= 16 ? 1 : (rows + 31) / 32);
+  const int pieces = diff_pieces(B, H_kv, rows, S_max);
+  if (pieces > 0 && S_max > 1024) return 2 * ((pieces + B - 1) / B);
   if (S_max <= 1024 || (S_max <= 2048 && rows <= 32 && groups * 8 <= sms)) return 1;
   // One sequence: a CTA to an SM.  Several: two (one and a half of more than 16 rows, which
   // have an SM to themselves), since sequences are seldom equally long and two fill

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "decode_common.cuh"
+#include "decode_cut.cuh"
 #include "diff.h"
 
 namespace gqa {
@@ -72,12 +73,14 @@ constexpr int merge_bytes() {
 // merges its partials itself: each leaves its (m, l, O) in its shared memory, and CTA `rank`
 // finishes heads rank, rank + n_split, .. from all of them, through distributed shared
 // memory.  One launch, no workspace.
-template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED, bool CLUSTER>
+// CUT: the batch is cut by its lengths (decode_cut.cuh) and grid x is the piece.
+template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED, bool CLUSTER, bool CUT>
 __global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
                                   NSTAGE == Ring<D>::kDeep ? 1 : 2)
     gqa_decode_diff_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const DecodeDiffParams pp) {
   static_assert(ROWS16 || NRG == 1, "fewer than nine rows are one group");
+  static_assert(!(CLUSTER && CUT), "a cluster's splits are even");
   using Lay = DecodeLayout<D>;
   constexpr int kCW = kGroupWarps * NRG;  // consumer warps
   constexpr int kStageBytes = Lay::kStageBytes;
@@ -96,9 +99,9 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
 
   // (the row groups of one split are neighbours in launch order, so that their reads of
   // the same K/V tiles meet in L2)
-  const int split = blockIdx.x / p.n_rg;
   const int row0 = (blockIdx.x % p.n_rg) * (16 * NRG);  // first query row of this CTA
-  const int kv = blockIdx.y, b = blockIdx.z;
+  const int kv = blockIdx.y;
+  int split = blockIdx.x / p.n_rg, b = CUT ? 0 : blockIdx.z, chunk = p.chunk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.G, h0 = kv * G;
   const int R = min(16 * NRG, p.T_q * G - row0);  // live rows (even)
@@ -120,6 +123,33 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
     bad_page = 0;
     fence_barrier_init();
   }
+  // A batch cut by its lengths: the cut is worked out while the previous kernel
+  // finishes, from relaxed loads, and again after the dependency wait if a length has
+  // changed.
+  Piece piece{0, 0, 0, 0};
+  int cut_tiles[3] = {0, 0, 0};
+  auto tiles_of = [&](int L) {
+    return L < p.T_q || L > p.S_max ? 0 : (L + kTile - 1) / kTile;
+  };
+  auto take_piece = [&]() {
+    piece = find_piece(cut_tiles[0], cut_tiles[1], cut_tiles[2], p.B, p.n_split, pp.pieces,
+                       blockIdx.x / p.n_rg, lane);
+    b = max(piece.b, 0);
+    split = piece.split;
+    chunk = piece.tiles * kTile;
+  };
+  if constexpr (CUT) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      int L = 0;
+      if (32 * k + lane < p.B)
+        asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];"
+                     : "=r"(L)
+                     : "l"(p.seq_lens + 32 * k + lane));
+      cut_tiles[k] = tiles_of(L);
+    }
+    take_piece();
+  }
   // While the previous kernel finishes, the producer warps prefetch the split's first
   // tiles into L2, one (tile, page segment) per lane.  The lengths and pages come
   // from relaxed loads that may see values from before the previous kernel's writes;
@@ -132,8 +162,8 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
     int L_hint;
     asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(L_hint) : "l"(p.seq_lens + b));
     const int i = lane / subs, sub = lane % subs;
-    const int tk = split * p.chunk + i * kTile + sub * box;
-    if (i < p.prefetch_tiles && tk < min(min(p.S_max, L_hint), split * p.chunk + p.chunk)) {
+    const int tk = split * chunk + i * kTile + sub * box;
+    if (i < p.prefetch_tiles && tk < min(min(p.S_max, L_hint), split * chunk + chunk)) {
       int row = b * p.S_max + tk;
       bool ok = true;
       if constexpr (PAGED) {
@@ -153,12 +183,31 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
   }
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (CUT) {
+    bool changed = false;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int t = 32 * k + lane < p.B ? tiles_of(p.seq_lens[32 * k + lane]) : 0;
+      changed |= t != cut_tiles[k];
+      cut_tiles[k] = t;
+    }
+    if (__any_sync(0xffffffffu, changed)) take_piece();
+    if (piece.b < 0) return;  // a CTA past the batch's last piece
+    // the slots of the workspace that the sequence has no pieces for: the merge identity
+    if (split == piece.count - 1)
+      for (int r = warp; r < R; r += kCW + kProducers)
+        for (int i = piece.count + lane; i < p.n_split; i += 32) {
+          const size_t at = out_row(r) * p.n_split + i;
+          if (in_bounds(at, 1, n_rows * p.n_split, p.err))
+            p.ws_ml[at] = make_float2(-INFINITY, 0.f);
+        }
+  }
   const int L = p.seq_lens[b];
 
   // A bad length: NaN outputs (with several splits a NaN partial).  An empty split: the
   // merge identity (-inf, 0), its O is not written.
   const bool bad_len = L < p.T_q || L > p.S_max || L < 1;
-  const long long t_first = static_cast<long long>(split) * p.chunk;
+  const long long t_first = static_cast<long long>(split) * chunk;
   // (A cluster's CTAs all see the same length; its empty splits take part in the merge.)
   if (bad_len || (!CLUSTER && t_first >= L)) {
     if (bad_len && threadIdx.x == 0 && split == 0 && kv == 0 && row0 == 0)
@@ -182,7 +231,7 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
     return;
   }
   const int t0 = static_cast<int>(min(t_first, static_cast<long long>(L)));
-  const int t_end = min(p.chunk, L - t0) + t0;
+  const int t_end = min(chunk, L - t0) + t0;
   const int n_tiles = (t_end - t0 + kTile - 1) / kTile;
 
   // ------------------------------------------------------------ producer ----
@@ -650,12 +699,12 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) gqa_diff_merge_kernel(c
   if (u == 0 && in_bounds(at, 1, n_rows / 2 * D, p.err)) p.out[at] = __float2bfloat16(o * weight * f);
 }
 
-template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED, bool CLUSTER = false>
+template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED, bool CLUSTER = false, bool CUT = false>
 cudaError_t launch(const DecodeDiffParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                    cudaStream_t stream) {
   constexpr int smem = NSTAGE * DecodeLayout<D>::kStageBytes + 1024;
   constexpr int threads = (kGroupWarps * NRG + kProducers) * 32;
-  auto kern = gqa_decode_diff_kernel<D, NRG, ROWS16, NSTAGE, PAGED, CLUSTER>;
+  auto kern = gqa_decode_diff_kernel<D, NRG, ROWS16, NSTAGE, PAGED, CLUSTER, CUT>;
   static unsigned char done[64];
   static int resident[64];
   cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), smem, done);
@@ -665,11 +714,13 @@ cudaError_t launch(const DecodeDiffParams& p_in, const CUtensorMap& tm_k, const 
   if (e != cudaSuccess) return e;
   DecodeDiffParams p = p_in;
   // The L2 prefetch pays only when every CTA is resident while the previous kernel drains.
-  const long long ctas = (long long)p.dec.n_split * p.dec.n_rg * p.dec.H_kv * p.dec.B;
+  const long long ctas = (CUT ? (long long)p.pieces : (long long)p.dec.n_split * p.dec.B) *
+                         p.dec.n_rg * p.dec.H_kv;
   constexpr int kBytes = 98304 / DecodeLayout<D>::kStageBytes;
   p.dec.prefetch_tiles = ctas <= fit ? (kBytes < 6 ? kBytes : 6) : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.dec.n_split * p.dec.n_rg, p.dec.H_kv, p.dec.B);
+  cfg.gridDim = CUT ? dim3(p.pieces * p.dec.n_rg, p.dec.H_kv)
+                    : dim3(p.dec.n_split * p.dec.n_rg, p.dec.H_kv, p.dec.B);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -713,6 +764,14 @@ cudaError_t launch_rows(const DecodeDiffParams& p_in, const CUtensorMap& tm_k,
       if (rows > 8) return launch<D, 1, true, kShallow, PAGED, true>(p, tm_k, tm_v, stream);
       return launch<D, 1, false, kShallow, PAGED, true>(p, tm_k, tm_v, stream);
     }
+  }
+  if (p.pieces > 0) {
+    if (p.dec.n_split < 2 || p.pieces <= p.dec.B || p.dec.B > kMaxCut) return cudaErrorInvalidValue;
+    if constexpr (D < 128)
+      if (rows > 16) return launch<D, 2, true, kDeep, PAGED, false, true>(p, tm_k, tm_v, stream);
+    if (rows > 16) return cudaErrorInvalidValue;
+    return rows > 8 ? launch<D, 1, true, kShallow, PAGED, false, true>(p, tm_k, tm_v, stream)
+                    : launch<D, 1, false, kShallow, PAGED, false, true>(p, tm_k, tm_v, stream);
   }
   // A grid of at most one CTA per SM takes a deeper ring in the room of a second CTA.
   const bool one = p.dec.n_split * groups <= sms;

@@ -146,6 +146,32 @@ def test_decode_of_a_batch_cut_by_its_lengths(split, page, T, H, Hk):
             c.compare(*c.decode(n_split=n), want, n)
 
 
+@pytest.mark.parametrize("d,T,H,Hk,page", [(128, 1, 8, 1, 64), (64, 3, 6, 1, 16), (32, 1, 2, 1, 128),
+                                           (64, 16, 2, 1, 32)])
+def test_smaller_rows_of_a_batch_cut_by_its_lengths(d, T, H, Hk, page):
+    # a table much wider than the sequences: enough tiles of one KV head that the cut is taken
+    lens = [9000, T, 64, 129]
+    c = Case(lens, T, H, Hk, d, d == 64, page, norm=True, lam="head")
+    want = c.expect()
+    wide = torch.zeros(c.B, 200000 // page, dtype=torch.int32, device=DEV)
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    for n in (None, 2, 7, 64):
+        c.compare(*c.decode(n_split=n), want, n)
+    a, b = c.decode(), c.decode()
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+    for wrong in (0, 200001):
+        bad = c.dev_lens()
+        bad[1] = wrong
+        q, lam = c.q.to(DEV), c.lam.to(DEV)
+        out, lse = g.decode_diff(q, c.k, c.v, bad, lam, block_table=c.table, **c.form)
+        torch.cuda.synchronize()
+        assert g.gqa_last_device_error() == g.GQA_ERR_INVALID_ARG
+        assert out[1].isnan().all() and lse[1].isnan().all()
+        ok = [0, 2, 3]
+        assert (np.abs(out.double().cpu().numpy() - want[0])[ok] <= want[2][ok]).all()
+
+
 @pytest.mark.parametrize("L", [1, 2, 15, 16, 17, 63, 64, 65, 127, 129, 1000, 5003])
 def test_decode_lengths(L):
     for page, n in ((0, 1), (16, None), (64, 7), (0, 40)):
