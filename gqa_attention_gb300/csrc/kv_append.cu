@@ -13,6 +13,9 @@
 // cosines of every pair go to shared memory once and serve all heads.  A thread then
 // takes 16 channels of a row at a time, the two 16-byte pieces that hold 8 pairs, so the
 // turned values leave in the pieces that they came in.
+#include <algorithm>
+#include <cstdlib>
+
 #include "common.cuh"
 #include "kv_append.h"
 
@@ -22,7 +25,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 16;  // tokens of a CTA, at most
 constexpr int kUnroll = 4;   // rows whose pieces a thread loads at once
-constexpr int kHold = 4;     // E4M3: slots a lane keeps between the maximum and the rounding
 
 // 2^64 f / 2 pi modulo 2^64.
 __device__ __forceinline__ uint64_t turns_of(float f) {
@@ -31,11 +33,8 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
   return __double2ull_rn(t * 18446744073709551616.0);
 }
 
-// Two fp32 values to two E4M3 codes (lo in the low byte), to nearest even; what is not
-// finite becomes NaN (the conversion alone would clamp an infinity to 448).
+// Two fp32 values to two E4M3 codes (lo in the low byte), to nearest even; NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  lo = isfinite(lo) ? lo : NAN;
-  hi = isfinite(hi) ? hi : NAN;
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
@@ -117,18 +116,24 @@ constexpr long long kSkip = -1;    // a token past the new ones of its sequence
 constexpr long long kBad = -2;     // of a sequence with a bad length: its query rows become NaN
 constexpr long long kNoPage = -3;  // of a bad page: its query rows are turned all the same
 
-// FP8 = false: rows (queries, keys, values) of all tokens are one list.  FP8 = true: the
-// list holds the queries alone, and each warp takes the keys or the values of a token
-// whole, for the maximum over its heads.
-template <int D, bool FP8>
+// HOLD = 0 (bf16): rows (queries, keys, values) of all tokens are one list.  HOLD > 0 (E4M3):
+// the list holds the queries alone, and the CTAs of the last grid row take the keys
+// and values: `team` warps take those of a token whole, for the maximum over its heads,
+// HOLD slots of a lane staying in registers between the maximum and the rounding.
+// EARLY: the CTA's list is one round, whose rows are loaded before the angles are worked
+// out.  (With several rounds that is slower: 32K tokens of 80 heads of 128 232 us, 201 if
+// each round is loaded when its turn comes.)
+template <int D, int HOLD, bool EARLY>
 __global__ void __launch_bounds__(kThreads) gqa_kv_append_rot_kernel(const KvAppendParams p,
-                                                                     int tok_per) {
+                                                                     int tok_per, int team) {
+  constexpr bool FP8 = HOLD > 0;
   constexpr int kSlots = D / 16;
   constexpr int kRowStep = kThreads / kSlots;  // rows that the CTA takes at a time
   __shared__ float4 cs_sm[kMaxTok][4][kSlots];
   __shared__ uint64_t turns_sm[D / 2];
   __shared__ long long dst_sm[kMaxTok];  // row of the cache, kSkip or kBad
   __shared__ int pos_sm[kMaxTok];
+  __shared__ uint32_t max_sm[FP8 ? 3 : 1][kThreads / 32];  // E4M3: a warp's share of a maximum
   const int tid = threadIdx.x;
   const long long tok0 = static_cast<long long>(blockIdx.x) * tok_per;
   const int n_tok = static_cast<int>(min(static_cast<long long>(tok_per),
@@ -136,6 +141,63 @@ __global__ void __launch_bounds__(kThreads) gqa_kv_append_rot_kernel(const KvApp
   const bool inter = p.interleaved != 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const bool kv_role = FP8 && blockIdx.y == gridDim.y - 1;
+  const size_t hq = static_cast<size_t>(p.H_q) * D, hkv = static_cast<size_t>(p.H_kv) * D;
+  const int q_rows = p.q ? p.H_q : 0;
+  const int rows = q_rows + (FP8 ? 0 : 2 * p.H_kv);
+  const Slot sl = slot_of(tid % kSlots, p.rot, inter);
+  // The list's (token, row) pairs, from this thread's first on.
+  const int step = kRowStep * (FP8 ? gridDim.y - 1 : gridDim.y);
+  int k = 0, r = tid / kSlots + kRowStep * blockIdx.y;
+  uint4 a[kUnroll], c[kUnroll];
+  int kk[kUnroll], rr[kUnroll];
+  auto load_round = [&]() {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      while (r >= rows && k < n_tok) {
+        r -= rows;
+        ++k;
+      }
+      kk[u] = k;
+      rr[u] = r;
+      if (k < n_tok && dst_sm[k] != kSkip) {
+        const long long g = tok0 + k;
+        const __nv_bfloat16* src =
+            r < q_rows ? p.q + g * p.q_stride + r * D
+            : r < q_rows + p.H_kv ? p.k + g * p.kv_stride + (r - q_rows) * D
+                                  : p.v + g * p.kv_stride + (r - q_rows - p.H_kv) * D;
+        a[u] = *reinterpret_cast<const uint4*>(src + sl.off0);
+        c[u] = *reinterpret_cast<const uint4*>(src + sl.off1);
+      } else if (k < n_tok) {
+        kk[u] = kMaxTok;  // not a row to write
+      }
+      r += step;
+    }
+  };
+  // A token's keys or values (unit 2 k or 2 k + 1) of a team: this lane's slots are `at0`,
+  // at0 + stride, ..
+  constexpr int kKeep = FP8 ? HOLD : 1;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int n_slots = p.H_kv * kSlots;
+  const int stride = 32 * team, at0 = tid % stride;
+  const int n_teams = kThreads / 32 / team, my_team = warp / team;
+  const Slot ls = slot_of(lane % kSlots, p.rot, inter);
+  uint4 na[kKeep], nc[kKeep];
+  auto unit_rows = [&](int unit) {
+    return ((unit & 1) ? p.v : p.k) + (tok0 + (unit >> 1)) * p.kv_stride;
+  };
+  auto load_unit = [&](int unit) {
+    if (unit >= 2 * n_tok || dst_sm[unit >> 1] < 0) return;
+#pragma unroll
+    for (int h = 0; h < kKeep; ++h) {
+      const int s = at0 + stride * h;
+      if (s >= n_slots) continue;
+      const __nv_bfloat16* src = unit_rows(unit) + (s / kSlots) * D;
+      na[h] = *reinterpret_cast<const uint4*>(src + ls.off0);
+      nc[h] = *reinterpret_cast<const uint4*>(src + ls.off1);
+    }
+  };
 
   // Where the tokens go.
   if (tid < n_tok) {
@@ -167,54 +229,34 @@ __global__ void __launch_bounds__(kThreads) gqa_kv_append_rot_kernel(const KvApp
   }
   if (tid >= 64 && tid - 64 < p.rot / 2) turns_sm[tid - 64] = turns_of(p.freqs[tid - 64]);
   __syncthreads();
+  // (the first rows travel while the angles are worked out)
+  if (kv_role) {
+    load_unit(my_team);
+  } else if constexpr (EARLY) {
+    load_round();
+  }
   for (int e = tid; e < n_tok * (p.rot / 2); e += kThreads) {
-    const int k = e / (p.rot / 2), i = e - k * (p.rot / 2);
-    const uint64_t a = static_cast<uint64_t>(static_cast<long long>(pos_sm[k])) * turns_sm[i];
+    const int t = e / (p.rot / 2), i = e - t * (p.rot / 2);
+    const uint64_t angle = static_cast<uint64_t>(static_cast<long long>(pos_sm[t])) * turns_sm[i];
     float sn, cn;
-    sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * (1.f / 2147483648.f), &sn, &cn);
-    float2* at = reinterpret_cast<float2*>(&cs_sm[k][(i % 8) / 2][i / 8]) + (i & 1);
+    sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * (1.f / 2147483648.f), &sn, &cn);
+    float2* at = reinterpret_cast<float2*>(&cs_sm[t][(i % 8) / 2][i / 8]) + (i & 1);
     *at = make_float2(cn, sn);
   }
   __syncthreads();
 
-  const size_t hq = static_cast<size_t>(p.H_q) * D, hkv = static_cast<size_t>(p.H_kv) * D;
   const size_t n_cache = (p.block_table ? static_cast<size_t>(p.num_pages) * p.page_size
                                         : static_cast<size_t>(p.B) * p.S_max) * hkv;
   const size_t n_q = static_cast<size_t>(p.B) * p.T * hq;
-  const int rows = (p.q ? p.H_q : 0) + (FP8 ? 0 : 2 * p.H_kv);
-  const int q_rows = p.q ? p.H_q : 0;
-  const Slot sl = slot_of(tid % kSlots, p.rot, inter);
-  {
-    // (token, row) pairs, kRowStep * gridDim.y apart
-    const int step = kRowStep * gridDim.y;
-    int k = 0, r = tid / kSlots + kRowStep * blockIdx.y;
-    while (rows > 0) {
-      uint4 a[kUnroll], c[kUnroll];
-      int kk[kUnroll], rr[kUnroll];
-      bool any = false;
+  if (!kv_role) {
+    for (;;) {
+      if constexpr (!EARLY) {
+        load_round();
+        bool any = false;
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        while (r >= rows && k < n_tok) {
-          r -= rows;
-          ++k;
-        }
-        kk[u] = k;
-        rr[u] = r;
-        if (k < n_tok && dst_sm[k] != kSkip) {
-          const long long g = tok0 + k;
-          const __nv_bfloat16* src =
-              r < q_rows ? p.q + g * p.q_stride + r * D
-              : r < q_rows + p.H_kv ? p.k + g * p.kv_stride + (r - q_rows) * D
-                                    : p.v + g * p.kv_stride + (r - q_rows - p.H_kv) * D;
-          a[u] = *reinterpret_cast<const uint4*>(src + sl.off0);
-          c[u] = *reinterpret_cast<const uint4*>(src + sl.off1);
-        } else {
-          kk[u] = n_tok;
-        }
-        any |= k < n_tok;
-        r += step;
+        for (int u = 0; u < kUnroll; ++u) any |= kk[u] != n_tok;
+        if (!any) break;
       }
-      if (!any) break;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (kk[u] >= n_tok) continue;
@@ -248,105 +290,147 @@ __global__ void __launch_bounds__(kThreads) gqa_kv_append_rot_kernel(const KvApp
         if (in_bounds(at + sl.off1, 8, extent, p.err))
           *reinterpret_cast<uint4*>(out + at + sl.off1) = c[u];
       }
+      if constexpr (EARLY) break;
     }
   }
 
   if constexpr (FP8) {
-    const int warp = tid >> 5, lane = tid & 31;
-    const int n_slots = p.H_kv * kSlots;  // of a token's keys or values
-    const Slot ls = slot_of(lane % kSlots, p.rot, inter);
-    for (int unit = warp + 8 * blockIdx.y; unit < 2 * n_tok; unit += 8 * gridDim.y) {
-      const int k = unit >> 1;
+    // The largest of a team's values, given as bits (positive floats compare as those).  One
+    // barrier: the buffers are taken in turn.
+    int buffer = 0;
+    auto team_max = [&](uint32_t v) -> uint32_t {
+      v = __reduce_max_sync(0xffffffffu, v);
+      if (team == 1) return v;
+      if (lane == 0) max_sm[buffer][warp] = v;
+      named_bar_sync(1 + my_team, stride);
+      const uint32_t got = lane < team ? max_sm[buffer][my_team * team + lane] : 0u;
+      buffer = buffer == 2 ? 0 : buffer + 1;
+      return __reduce_max_sync(0xffffffffu, got);
+    };
+    for (int unit = my_team; kv_role && unit < 2 * n_tok; unit += n_teams) {
+      uint4 va[kKeep], vc[kKeep];
+#pragma unroll
+      for (int h = 0; h < kKeep; ++h) {
+        va[h] = na[h];
+        vc[h] = nc[h];
+      }
+      load_unit(unit + n_teams);  // (the next one's rows travel meanwhile)
+      const int t = unit >> 1;
       const bool is_v = unit & 1;
-      const long long dst = dst_sm[k];
+      const long long dst = dst_sm[t];
       if (dst < 0) continue;
-      const __nv_bfloat16* src = (is_v ? p.v : p.k) + (tok0 + k) * p.kv_stride;
+      const __nv_bfloat16* src = unit_rows(unit);
       float4 cs[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cs[j] = cs_sm[k][j][lane % kSlots];
+      for (int j = 0; j < 4; ++j) cs[j] = cs_sm[t][j][lane % kSlots];
       const bool turned = ls.turned && !is_v;
-      auto values = [&](const uint4& a, const uint4& c, float (&x)[8], float (&y)[8]) {
+      auto values = [&](const uint4& u, const uint4& w, float (&x)[8], float (&y)[8]) {
         if (turned) {
-          turn(a, c, cs, inter, x, y);
+          turn(u, w, cs, inter, x, y);
         } else {
-          widen(a, x);
-          widen(c, y);
+          widen(u, x);
+          widen(w, y);
         }
       };
-      uint4 a[kHold], c[kHold];
-#pragma unroll
-      for (int h = 0; h < kHold; ++h) {
-        const int s = lane + 32 * h;
-        if (s < n_slots) {
-          a[h] = *reinterpret_cast<const uint4*>(src + (s / kSlots) * D + ls.off0);
-          c[h] = *reinterpret_cast<const uint4*>(src + (s / kSlots) * D + ls.off1);
-        }
-      }
+      auto values_of = [&](int s, float (&x)[8], float (&y)[8]) {
+        const __nv_bfloat16* row = src + (s / kSlots) * D;
+        values(*reinterpret_cast<const uint4*>(row + ls.off0),
+               *reinterpret_cast<const uint4*>(row + ls.off1), x, y);
+      };
+      float x[kKeep][8], y[kKeep][8];
       float amax = 0.f;
-      auto widest = [&](const uint4& va, const uint4& vc) {
-        float x[8], y[8];
-        values(va, vc, x, y);
+      auto widest = [&](const float (&v)[8]) {  // (fmaxf passes over NaN)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (isfinite(x[j])) amax = fmaxf(amax, fabsf(x[j]));
-          if (isfinite(y[j])) amax = fmaxf(amax, fabsf(y[j]));
-        }
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
       };
 #pragma unroll
-      for (int h = 0; h < kHold; ++h)
-        if (lane + 32 * h < n_slots) widest(a[h], c[h]);
-      for (int s = lane + 32 * kHold; s < n_slots; s += 32)
-        widest(*reinterpret_cast<const uint4*>(src + (s / kSlots) * D + ls.off0),
-               *reinterpret_cast<const uint4*>(src + (s / kSlots) * D + ls.off1));
+      for (int h = 0; h < kKeep; ++h) {
+        if (at0 + stride * h >= n_slots) continue;
+        values(va[h], vc[h], x[h], y[h]);
+        widest(x[h]);
+        widest(y[h]);
+      }
+      for (int s = at0 + stride * kKeep; s < n_slots; s += stride) {
+        float u[8], w[8];
+        values_of(s, u, w);
+        widest(u);
+        widest(w);
+      }
+      amax = __uint_as_float(team_max(__float_as_uint(amax)));
+      const bool infinite = amax > 3.4028235e38f;  // rare: the maximum again, of what is finite
+      if (infinite) {
+        amax = 0.f;
+        auto widest_finite = [&](const float (&v)[8]) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          for (int j = 0; j < 8; ++j)
+            if (isfinite(v[j])) amax = fmaxf(amax, fabsf(v[j]));
+        };
+#pragma unroll
+        for (int h = 0; h < kKeep; ++h) {
+          if (at0 + stride * h >= n_slots) continue;
+          widest_finite(x[h]);
+          widest_finite(y[h]);
+        }
+        for (int s = at0 + stride * kKeep; s < n_slots; s += stride) {
+          float u[8], w[8];
+          values_of(s, u, w);
+          widest_finite(u);
+          widest_finite(w);
+        }
+        amax = __uint_as_float(team_max(__float_as_uint(amax)));
+      }
       const int e = scale_exp(amax);
       const float inv = pow2f(-e);
       uint8_t* codes = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache);
-      auto put = [&](int s, const uint4& va, const uint4& vc) {
-        float x[8], y[8];
-        values(va, vc, x, y);
-        uint32_t w[4];
+      auto coded = [&](float (&v)[8]) -> uint2 {
+        if (infinite) {  // (the conversion alone would clamp an infinity to 448)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          w[j] = e4m3x2(x[4 * j] * inv, x[4 * j + 1] * inv) |
-                 e4m3x2(x[4 * j + 2] * inv, x[4 * j + 3] * inv) << 16;
-          w[2 + j] = e4m3x2(y[4 * j] * inv, y[4 * j + 1] * inv) |
-                     e4m3x2(y[4 * j + 2] * inv, y[4 * j + 3] * inv) << 16;
+          for (int j = 0; j < 8; ++j) v[j] = isfinite(v[j]) ? v[j] : NAN;
         }
+        return make_uint2(e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16,
+                          e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16);
+      };
+      auto put = [&](int s, float (&u)[8], float (&w)[8]) {
         const size_t at = static_cast<size_t>(dst) * hkv + static_cast<size_t>(s / kSlots) * D;
         if (in_bounds(at + ls.off0, 8, n_cache, p.err))
-          *reinterpret_cast<uint2*>(codes + at + ls.off0) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(codes + at + ls.off0) = coded(u);
         if (in_bounds(at + ls.off1, 8, n_cache, p.err))
-          *reinterpret_cast<uint2*>(codes + at + ls.off1) = make_uint2(w[2], w[3]);
+          *reinterpret_cast<uint2*>(codes + at + ls.off1) = coded(w);
       };
 #pragma unroll
-      for (int h = 0; h < kHold; ++h)
-        if (lane + 32 * h < n_slots) put(lane + 32 * h, a[h], c[h]);
-      for (int s = lane + 32 * kHold; s < n_slots; s += 32)
-        put(s, *reinterpret_cast<const uint4*>(src + (s / kSlots) * D + ls.off0),
-            *reinterpret_cast<const uint4*>(src + (s / kSlots) * D + ls.off1));
-      if (lane == 0 && in_bounds(dst, 1, n_cache / hkv, p.err))
+      for (int h = 0; h < kKeep; ++h)
+        if (at0 + stride * h < n_slots) put(at0 + stride * h, x[h], y[h]);
+      for (int s = at0 + stride * kKeep; s < n_slots; s += stride) {
+        float u[8], w[8];
+        values_of(s, u, w);
+        put(s, u, w);
+      }
+      if (at0 == 0 && in_bounds(dst, 1, n_cache / hkv, p.err))
         (is_v ? p.v_scale : p.k_scale)[dst] = pow2f(e);
     }
   }
 }
 
-template <int D, bool FP8>
-cudaError_t launch(const KvAppendParams& p, int sms, cudaStream_t stream) {
-  // Tokens to a CTA: enough CTAs for eight on every SM, then as many tokens as share the
-  // set-up.  Few tokens: their rows are divided among CTAs.
+template <int D, int HOLD>
+cudaError_t launch(const KvAppendParams& p, int sms, int team, cudaStream_t stream) {
+  constexpr bool FP8 = HOLD > 0;
+  // Tokens to a CTA: enough CTAs for four on every SM, then as many tokens as share the
+  // set-up, but of few rows (half of a round to a token or less) no more than one round
+  // takes.  Few tokens: their rows are divided among CTAs.
   const long long tokens = (long long)p.B * p.T;
-  long long tok_per = tokens / (16LL * sms);
-  tok_per = tok_per < 1 ? 1 : tok_per > kMaxTok ? kMaxTok : tok_per;
+  const int rows = (p.q ? p.H_q : 0) + (FP8 ? 0 : 2 * p.H_kv);
+  const int pieces = rows * (D / 16);  // of a token in the list
+  static const long long per_sm = getenv("GQA_TOK") ? atoi(getenv("GQA_TOK")) : 4;
+  long long tok_per = tokens / (per_sm * sms);
+  if (!FP8 && pieces <= kUnroll * kThreads / 2) tok_per = std::min(tok_per, (long long)kUnroll * kThreads / pieces);
+  tok_per = std::max(1LL, std::min(tok_per, (long long)kMaxTok));
   const long long x = (tokens + tok_per - 1) / tok_per;
   if (x > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const int rows = (p.q ? p.H_q : 0) + (FP8 ? 0 : 2 * p.H_kv);
-  const int passes = (rows * (D / 16) + kThreads - 1) / kThreads;
-  long long y = 2LL * sms / x;
-  y = y < 1 ? 1 : y > passes ? (passes < 1 ? 1 : passes) : y;
+  const int passes = (pieces + kThreads - 1) / kThreads;
+  const long long y = std::min((long long)passes, std::max(1LL, 2LL * sms / x));  // (0: no list)
+  const bool early = tok_per * pieces <= kUnroll * kThreads * y;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
+  cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(y + (FP8 ? 1 : 0)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -354,20 +438,30 @@ cudaError_t launch(const KvAppendParams& p, int sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, gqa_kv_append_rot_kernel<D, FP8>, p, static_cast<int>(tok_per));
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, early ? gqa_kv_append_rot_kernel<D, HOLD, true> : gqa_kv_append_rot_kernel<D, HOLD, false>,
+      p, static_cast<int>(tok_per), team);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const KvAppendParams& p, int sms, cudaStream_t stream) {
+  if (!p.k_scale) return launch<D, 0>(p, sms, 1, stream);
+  const int slots = p.H_kv * (D / 16);
+  if (slots <= 32) return launch<D, 1>(p, sms, 1, stream);
+  int team = 1;  // warps whose lanes hold two slots each
+  while (team < kThreads / 32 && slots > 64 * team) team *= 2;
+  return launch<D, 2>(p, sms, team, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append_rot(const KvAppendParams& p, int sms, cudaStream_t stream) {
-  const bool fp8 = p.k_scale != nullptr;
   switch (p.d) {
-    case 16: return fp8 ? launch<16, true>(p, sms, stream) : launch<16, false>(p, sms, stream);
-    case 32: return fp8 ? launch<32, true>(p, sms, stream) : launch<32, false>(p, sms, stream);
-    case 64: return fp8 ? launch<64, true>(p, sms, stream) : launch<64, false>(p, sms, stream);
-    case 128: return fp8 ? launch<128, true>(p, sms, stream) : launch<128, false>(p, sms, stream);
+    case 16: return launch_d<16>(p, sms, stream);
+    case 32: return launch_d<32>(p, sms, stream);
+    case 64: return launch_d<64>(p, sms, stream);
+    case 128: return launch_d<128>(p, sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }
