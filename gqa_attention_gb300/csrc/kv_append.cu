@@ -14,10 +14,9 @@
 // takes 16 channels of a row at a time, the two 16-byte pieces that hold 8 pairs, so the
 // turned values leave in the pieces that they came in.
 #include <algorithm>
-#include <cstdlib>
 
-#include "common.cuh"
 #include "kv_append.h"
+#include "tcgen05.cuh"
 
 namespace gqa {
 namespace {
@@ -69,7 +68,8 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Turns the 8 pairs of a slot: a, b the two pieces, cs the pairs' (cos, sin, cos, sin).
+// Turns the 8 pairs of a slot: a, b the two pieces, cs[j] the cosines and the sines of pairs
+// 2j and 2j + 1.
 __device__ __forceinline__ void turn(const uint4& a, const uint4& b, const float4 (&cs)[4],
                                      bool interleaved, float (&x)[8], float (&y)[8]) {
   const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
@@ -77,16 +77,17 @@ __device__ __forceinline__ void turn(const uint4& a, const uint4& b, const float
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 u = unpack_bf16(aw[j]), v = unpack_bf16(bw[j]);
-      x[2 * j] = u.x * cs[j].x - v.x * cs[j].y;
-      y[2 * j] = u.x * cs[j].y + v.x * cs[j].x;
-      x[2 * j + 1] = u.y * cs[j].z - v.y * cs[j].w;
-      y[2 * j + 1] = u.y * cs[j].w + v.y * cs[j].z;
+      float t0, t1;
+      fmul2(t0, t1, v.x, v.y, cs[j].z, cs[j].w);
+      ffma2(x[2 * j], x[2 * j + 1], u.x, u.y, cs[j].x, cs[j].y, -t0, -t1);
+      fmul2(t0, t1, v.x, v.y, cs[j].x, cs[j].y);
+      ffma2(y[2 * j], y[2 * j + 1], u.x, u.y, cs[j].z, cs[j].w, t0, t1);
     }
   } else {  // pair j: channels 2j and 2j + 1 of the 16; x, y are the pieces again
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float2 u = unpack_bf16(j < 4 ? aw[j] : bw[j - 4]);
-      const float c = j & 1 ? cs[j / 2].z : cs[j / 2].x, s = j & 1 ? cs[j / 2].w : cs[j / 2].y;
+      const float c = j & 1 ? cs[j / 2].y : cs[j / 2].x, s = j & 1 ? cs[j / 2].w : cs[j / 2].z;
       const float p = u.x * c - u.y * s, q = u.x * s + u.y * c;
       if (j < 4) {
         x[2 * j] = p;
@@ -124,8 +125,8 @@ constexpr long long kNoPage = -3;  // of a bad page: its query rows are turned a
 // out.  (With several rounds that is slower: 32K tokens of 80 heads of 128 232 us, 201 if
 // each round is loaded when its turn comes.)
 template <int D, int HOLD, bool EARLY>
-__global__ void __launch_bounds__(kThreads) gqa_kv_append_rot_kernel(const KvAppendParams p,
-                                                                     int tok_per, int team) {
+__global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ? 4 : 3)
+    gqa_kv_append_rot_kernel(const KvAppendParams p, int tok_per, int team) {
   constexpr bool FP8 = HOLD > 0;
   constexpr int kSlots = D / 16;
   constexpr int kRowStep = kThreads / kSlots;  // rows that the CTA takes at a time
@@ -240,8 +241,9 @@ __global__ void __launch_bounds__(kThreads) gqa_kv_append_rot_kernel(const KvApp
     const uint64_t angle = static_cast<uint64_t>(static_cast<long long>(pos_sm[t])) * turns_sm[i];
     float sn, cn;
     sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * (1.f / 2147483648.f), &sn, &cn);
-    float2* at = reinterpret_cast<float2*>(&cs_sm[t][(i % 8) / 2][i / 8]) + (i & 1);
-    *at = make_float2(cn, sn);
+    float* at = reinterpret_cast<float*>(&cs_sm[t][(i % 8) / 2][i / 8]) + (i & 1);
+    at[0] = cn;
+    at[2] = sn;
   }
   __syncthreads();
 
@@ -340,8 +342,10 @@ __global__ void __launch_bounds__(kThreads) gqa_kv_append_rot_kernel(const KvApp
       float x[kKeep][8], y[kKeep][8];
       float amax = 0.f;
       auto widest = [&](const float (&v)[8]) {  // (fmaxf passes over NaN)
+        float m[3];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+        for (int j = 0; j < 3; ++j) m[j] = fmaxf(fabsf(v[2 * j]), fabsf(v[2 * j + 1]));
+        amax = fmax3(amax, fmax3(m[0], m[1], m[2]), fmaxf(fabsf(v[6]), fabsf(v[7])));
       };
 #pragma unroll
       for (int h = 0; h < kKeep; ++h) {
@@ -387,11 +391,18 @@ __global__ void __launch_bounds__(kThreads) gqa_kv_append_rot_kernel(const KvApp
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = isfinite(v[j]) ? v[j] : NAN;
         }
-        return make_uint2(e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16,
-                          e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo, hi;
+          fmul2(lo, hi, v[2 * j], v[2 * j + 1], inv, inv);
+          w[j] = e4m3x2(lo, hi);
+        }
+        return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
       };
+      const size_t row = static_cast<size_t>(dst) * hkv;
       auto put = [&](int s, float (&u)[8], float (&w)[8]) {
-        const size_t at = static_cast<size_t>(dst) * hkv + static_cast<size_t>(s / kSlots) * D;
+        const size_t at = row + (s / kSlots) * D;
         if (in_bounds(at + ls.off0, 8, n_cache, p.err))
           *reinterpret_cast<uint2*>(codes + at + ls.off0) = coded(u);
         if (in_bounds(at + ls.off1, 8, n_cache, p.err))
@@ -420,8 +431,7 @@ cudaError_t launch(const KvAppendParams& p, int sms, int team, cudaStream_t stre
   const long long tokens = (long long)p.B * p.T;
   const int rows = (p.q ? p.H_q : 0) + (FP8 ? 0 : 2 * p.H_kv);
   const int pieces = rows * (D / 16);  // of a token in the list
-  static const long long per_sm = getenv("GQA_TOK") ? atoi(getenv("GQA_TOK")) : 4;
-  long long tok_per = tokens / (per_sm * sms);
+  long long tok_per = tokens / (4LL * sms);
   if (!FP8 && pieces <= kUnroll * kThreads / 2) tok_per = std::min(tok_per, (long long)kUnroll * kThreads / pieces);
   tok_per = std::max(1LL, std::min(tok_per, (long long)kMaxTok));
   const long long x = (tokens + tok_per - 1) / tok_per;
@@ -448,10 +458,13 @@ template <int D>
 cudaError_t launch_d(const KvAppendParams& p, int sms, cudaStream_t stream) {
   if (!p.k_scale) return launch<D, 0>(p, sms, 1, stream);
   const int slots = p.H_kv * (D / 16);
-  if (slots <= 32) return launch<D, 1>(p, sms, 1, stream);
-  int team = 1;  // warps whose lanes hold two slots each
-  while (team < kThreads / 32 && slots > 64 * team) team *= 2;
-  return launch<D, 2>(p, sms, team, stream);
+  // A lane of a team holds one slot, or two where that makes one warp of it and there are
+  // tokens to fill the GPU (32K tokens of 8 heads of 128: 47 us with two slots, 54 with
+  // two warps, which meet at a barrier for each maximum; 128 tokens: 4.8 and 3.2).
+  const bool two = slots > 32 && (long long)p.B * p.T > 4LL * sms;
+  int team = 1;
+  while (team < kThreads / 32 && slots > (two ? 64 : 32) * team) team *= 2;
+  return two ? launch<D, 2>(p, sms, team, stream) : launch<D, 1>(p, sms, team, stream);
 }
 
 }  // namespace
