@@ -79,6 +79,7 @@ SIGNATURES = {
     "gqa_attn_decode_diff_default_splits": (_I, [_I, _I, _I, _I, _I, _I]),
     "gqa_attn_prefill_diff": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _I, _I, _I,
                                    _I, _F, _I, _P, _F, _F, _I, _P, _P, _P, _P]),
+    "gqa_attn_prefill_diff_default_parts": (_I, [_I, _I, _I, _I, _I, _I]),
     "gqa_trace_clear": (_I, []),
     "gqa_trace_read": (_I, [_P, _SZ]),
     "gqa_trace_mma_rate": (_I, [_I, _I, _P]),
@@ -397,6 +398,10 @@ def gqa_attn_prefill_diff(q, k_cache, v_cache, seq_lens, lam, lam_stride_b, lam_
         lam_stride_t, lam_stride_h, B, T_q, S_max, H, H_kv, d, int(split_keys), scale, int(window),
         _ptr(norm_weight), norm_eps, out_scale, int(n_part), _ptr(workspace), _ptr(out), _ptr(lse),
         _stream(stream))
+
+
+def gqa_attn_prefill_diff_default_parts(B, T_q, S_max, H, H_kv, window) -> int:
+    return load().gqa_attn_prefill_diff_default_parts(B, T_q, S_max, H, H_kv, int(window))
 
 
 def gqa_trace_clear() -> int:

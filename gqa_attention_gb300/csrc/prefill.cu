@@ -47,9 +47,9 @@
 // Differential attention (DIFF): the two heads of an item are the two maps of one
 // output head, O = O_1 / l_1 - lam O_2 / l_2 with an optional norm over the head.  Loads,
 // products and softmaxes are those of a head pair; only the epilogue differs: each
-// warpgroup takes half of the columns of both maps from tensor memory (for the norm's
-// sum all of them), and the two threads of a row, one in each warpgroup, tell each
-// other 1 / l through shared memory.  DIFF = 1: two query heads over
+// warpgroup takes half of the columns of both maps from tensor memory, and the two
+// threads of a row, one in each warpgroup, tell each other 1 / l through shared memory.  (All columns by the second warpgroup, while the first
+// goes on: 8 prompts of 512, 64 maps of 128, 65 us, 56 shared out.)  DIFF = 1: two query heads over
 // the same keys.  DIFF = 2 (split keys): the maps are the halves of one query row and of
 // the key rows, so S_X takes the k-steps of its half only.
 #include <climits>
@@ -241,10 +241,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __shared__ int abort_flag;
   // every role derives each item's key range from seq_lens[b]: read it once
   __shared__ int lens_sm[GENERAL ? lens_kept(DIFF) : 1];
-  // differential: 1 / l, which the two threads of a row tell each other, and per quarter of
-  // rows the barrier that says it is there
+  // differential: 1 / l, which the two threads of a row tell each other, per quarter of rows
+  // the barrier that says it is there,
   __shared__ float row_inv[DIFF ? 2 : 1][DIFF ? 128 : 1];
   __shared__ __align__(8) uint64_t inv_ready[2][DIFF ? 4 : 1];
+  __shared__ __align__(16) float weight_sm[DIFF ? DP : 1];  // and the norm's weight
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -277,6 +278,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     abort_flag = 0;
     fence_barrier_init();
+  }
+  if constexpr (DIFF != 0) {
+    if (pp.diff.norm_weight)
+      for (int i = threadIdx.x; i < p.d; i += kPThreads) weight_sm[i] = pp.diff.norm_weight[i];
   }
   if (GENERAL && p.seq_lens)
     for (int i = threadIdx.x; i < min(p.B, lens_kept(DIFF)); i += kPThreads) lens_sm[i] = p.seq_lens[i];
@@ -508,6 +513,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         continue;
       }
       float m_ref = -INFINITY, l = 0.f;
+      float lam = 0.f;  // differential: this row's weight of the second map, for the epilogue
+      if constexpr (DIFF != 0) {
+        if (q_row < p.S && p.n_part <= 1)
+          lam = pp.diff.lam[it.b * pp.diff.lam_b + q_row * pp.diff.lam_t + (h >> 1) * pp.diff.lam_h];
+      }
       for (int j = 0; j < n; ++j) {
         if (!wait_all(&s_full[x], s_ph)) {
           alive = false;
@@ -653,69 +663,103 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (!alive) break;
 
       // Epilogue: O / l in bf16 and LSE = (m_ref + log2 l) * ln 2.
-      if (!wait_all(&o_full[x], of_ph)) break;
+      const bool split = GENERAL && p.n_part > 1;
+      if ((DIFF == 0 || split) && !wait_all(&o_full[x], of_ph)) break;
       of_ph ^= 1;
       tc_fence_after();
       const float inv = (GENERAL && gm.bad) ? NAN : 1.f / l;
       const bool store = q_row < p.S;
       if (GENERAL && gm.bad && x == 0 && warp == 4 && lane == 0) atomicOr(p.err, kErrBadSeqLen);
-      const bool split = GENERAL && p.n_part > 1;
       const int D = p.d;  // row width of out and of the O partials
       if constexpr (DIFF != 0) {
         if (!split) {
-          // This thread's columns: chunks of 32 from n_oc / 2 * x on (d = 32 has one chunk,
-          // the first warpgroup's).
+          // This thread's columns: chunks of 32 from kOwn * x on (d = 32 has one chunk, the
+          // first warpgroup's).  The first map's O is ready half a tile before the second's
+          // and waits in registers.
           const DiffParams& df = pp.diff;
           row_inv[x][r] = inv;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&inv_ready[x][quarter]));
-          if (!wait_all(&inv_ready[1 - x][quarter], xc_ph) || !wait_all(&o_full[1 - x], of_ph ^ 1)) break;
+          constexpr int kOwn = DP / 64;
+          const int c0 = D == 32 ? 0 : kOwn * x, n_own = D == 32 ? 1 - x : kOwn;
+          float y[kOwn][32];
+          if (!wait_all(&o_full[0], of_ph ^ 1)) break;
           tc_fence_after();
-          const int head = h >> 1;
-          const float lam =
-              store ? df.lam[it.b * df.lam_b + q_row * df.lam_t + head * df.lam_h] : 0.f;
-          const float i0 = row_inv[0][r], i1 = row_inv[1][r];
-          auto chunk = [&](int c, float (&y)[32]) {
-            uint32_t o[32], o2[32];
-            tmem_ld32(tmem + lane_base + 256 + 32 * c, o);
-            tmem_ld32(tmem + lane_base + 256 + DP + 32 * c, o2);
+#pragma unroll
+          for (int c = 0; c < kOwn; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_base + 256 + 32 * (c0 + c), o);
             tmem_wait_ld();
             reg_fence32(o);
-            reg_fence32(o2);
-            // (each map rounded first: equal maps leave exactly nothing at lam = 1)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              y[i] = fmaf(-lam, __fmul_rn(__uint_as_float(o2[i]), i1),
-                          __fmul_rn(__uint_as_float(o[i]), i0));
+            for (int i = 0; i < 32; ++i) y[c][i] = __uint_as_float(o[i]);
+          }
+          if (!wait_all(&inv_ready[1 - x][quarter], xc_ph) || !wait_all(&o_full[1], of_ph ^ 1)) break;
+          tc_fence_after();
+          const float i0 = row_inv[0][r], i1 = row_inv[1][r];
+          // (each map rounded before the difference: equal maps leave exactly nothing at
+          // lam = 1)
+          auto difference = [&](float a, uint32_t b) {
+            return fmaf(-lam, __fmul_rn(__uint_as_float(b), i1), __fmul_rn(a, i0));
           };
-          float f = df.out_scale;
-          if (df.norm_eps >= 0.f) {  // both threads of a row sum all of its squares
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int c = 0; c < n_oc; ++c) {
-              float y[32];
-              chunk(c, y);
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s4[i & 3] += y[i] * y[i];
+          for (int c = 0; c < kOwn; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_base + 256 + DP + 32 * (c0 + c), o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              y[c][i] = difference(y[c][i], o[i]);
+              s4[i & 3] = fmaf(y[c][i], y[c][i], s4[i & 3]);
+            }
+          }
+          float f = df.out_scale;
+          if (df.norm_eps >= 0.f) {
+            // The other columns' squares are worked out here too (exchanging the sums through
+            // two more barriers took as long).  (d = 32: the second warpgroup has no columns.)
+            if (D != 32) {
+#pragma unroll 1
+              for (int c = 0; c < kOwn; ++c) {
+                const uint32_t at = tmem + lane_base + 256 + 32 * (kOwn * (1 - x) + c);
+                uint32_t o[32], o2[32];
+                tmem_ld32(at, o);
+                tmem_ld32(at + DP, o2);
+                tmem_wait_ld();
+                reg_fence32(o);
+                reg_fence32(o2);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float v = difference(__uint_as_float(o[i]), o2[i]);
+                  s4[i & 3] = fmaf(v, v, s4[i & 3]);
+                }
+              }
             }
             f *= rsqrtf(((s4[0] + s4[1]) + (s4[2] + s4[3])) / static_cast<float>(D) + df.norm_eps);
           }
-          const int c_end = D == 32 ? 1 - x : n_oc / 2 * (x + 1);
-#pragma unroll 1
-          for (int c = n_oc / 2 * x; c < c_end; ++c) {
-            float y[32];
-            chunk(c, y);
+          const int head = h >> 1;
+#pragma unroll
+          for (int c = 0; c < kOwn; ++c) {
+            if (c >= n_own) break;
+            const int col0 = 32 * (c0 + c);
             if (df.norm_weight) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) y[i] *= f * __ldg(df.norm_weight + 32 * c + i);
+              for (int i = 0; i < 32; i += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(&weight_sm[col0 + i]);
+                y[c][i] *= f * w.x;
+                y[c][i + 1] *= f * w.y;
+                y[c][i + 2] *= f * w.z;
+                y[c][i + 3] *= f * w.w;
+              }
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) y[i] *= f;
+              for (int i = 0; i < 32; ++i) y[c][i] *= f;
             }
-            store_rows32(y, lane, [&](int rr, int col) -> __nv_bfloat16* {
+            store_rows32(y[c], lane, [&](int rr, int col) -> __nv_bfloat16* {
               const int qrow = it.qt * 128 + quarter * 32 + rr;
               const size_t at =
-                  ((static_cast<size_t>(it.b) * p.S + qrow) * (p.H_q / 2) + head) * D + 32 * c + col;
+                  ((static_cast<size_t>(it.b) * p.S + qrow) * (p.H_q / 2) + head) * D + col0 + col;
               return qrow < p.S && in_bounds(at, 8, n_rows / 2 * D, p.err) ? p.out + at : nullptr;
             });
           }

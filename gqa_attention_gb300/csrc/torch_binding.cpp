@@ -45,7 +45,7 @@ struct Library {
   decltype(&gqa_attn_decode_paged_diff) decode_diff_paged;
   decltype(&gqa_attn_decode_diff_default_splits) diff_splits;
   decltype(&gqa_attn_prefill_diff) prefill_diff;
-  decltype(&gqa_attn_prefill_chunk_default_parts) chunk_parts;
+  decltype(&gqa_attn_prefill_diff_default_parts) diff_parts;
   decltype(&gqa_attn_prefill_chunk_workspace_bytes) chunk_workspace_bytes;
 };
 
@@ -86,7 +86,7 @@ const Library& library(PyObject* arg) {
   symbol(handle, "gqa_attn_decode_paged_diff", &l.decode_diff_paged);
   symbol(handle, "gqa_attn_decode_diff_default_splits", &l.diff_splits);
   symbol(handle, "gqa_attn_prefill_diff", &l.prefill_diff);
-  symbol(handle, "gqa_attn_prefill_chunk_default_parts", &l.chunk_parts);
+  symbol(handle, "gqa_attn_prefill_diff_default_parts", &l.diff_parts);
   symbol(handle, "gqa_attn_prefill_chunk_workspace_bytes", &l.chunk_workspace_bytes);
   known.reserve(64);  // (references stay valid)
   if (known.size() == known.capacity()) throw Refused{GQA_ERR_UNSUPPORTED, "too many libraries"};
@@ -644,7 +644,7 @@ PyObject* prefill_diff_(PyObject* const* a) {
   if (!out) out = empty(at::IntArrayRef(o_shape, 4), at::kBFloat16, dev);
   if (!lse) lse = empty(at::IntArrayRef(l_shape, 3), at::kFloat, dev);
   const int maps = as_dim(2 * int64_t(f.H), call);
-  const int n_part = a[12] == Py_None ? lib.chunk_parts(B, f.T, S, maps, Hk) : as_int(a[12], call);
+  const int n_part = a[12] == Py_None ? lib.diff_parts(B, f.T, S, f.H, Hk, window) : as_int(a[12], call);
   Scratch scratch;
   if (n_part > 1) {
     const int64_t bytes = static_cast<int64_t>(lib.chunk_workspace_bytes(B, f.T, maps, d, n_part));

@@ -147,6 +147,15 @@ def test_default_splits():
     assert g.gqa_attn_decode_diff_default_splits(1, 0, 8, 8, 4096, 128) == 1
 
 
+def test_default_parts():
+    # (no GPU here: the SM count falls back to a default)
+    assert g.gqa_attn_prefill_diff_default_parts(3, 333, 2903, 8, 2, 1000) == 1
+    assert 1 <= g.gqa_attn_prefill_diff_default_parts(1, 128, 32768, 8, 2, -1) <= 4
+    for bad in ((0, 128, 32768, 8, 2, -1), (1, 0, 32768, 8, 2, -1), (1, 128, 0, 8, 2, -1),
+                (1, 128, 32768, 7, 2, -1), (1, 128, 32768, 8, 0, -1), (1, 128, 32768, 1 << 30, 2, -1)):
+        assert g.gqa_attn_prefill_diff_default_parts(*bad) == 1
+
+
 def test_helpers_refuse_cpu_tensors():
     k = torch.zeros(1, 8, 2, 64, dtype=torch.bfloat16)
     lens, lam = torch.ones(1, dtype=torch.int32), torch.ones(1)
