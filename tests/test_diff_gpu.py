@@ -301,6 +301,18 @@ def test_a_long_split_of_small_pages():
     c.compare(*c.decode(n_split=1), c.expect())
 
 
+def test_pages_that_sequences_share_and_repeat():
+    c = Case([64, 64], 1, 4, 2, 64, page=16)
+    table = c.table.clone()
+    table[1, :2] = table[0, :2]  # a shared prefix
+    table[0, 3] = table[0, 2]    # the same page twice in a sequence
+    seq = [[torch.cat([x[:48], x[32:48]]) for x in c.seq[0]],
+           [torch.cat([x[:32], y[32:]]) for x, y in zip(c.seq[0], c.seq[1])]]
+    c.seq, c.table = seq, table
+    for n in (1, 2):
+        c.compare(*c.decode(n_split=n), c.expect(), n)
+
+
 def test_cache_rows_past_2_31_elements():
     if torch.cuda.mem_get_info()[0] < 20 << 30:
         pytest.skip("needs 20 GB")
@@ -467,23 +479,40 @@ def test_a_sequence_from_its_prompt_on(split, page):
         check(q, out, lse, lens, step, False)
 
 
-def test_captured_step_replays_over_new_lengths():
-    c = Case([100, 40], 1, 8, 2, 64, norm=True, lam="layer", S=128)
-    q, lam, lens = c.q[:, 0].contiguous().to(DEV), c.lam.to(DEV), c.dev_lens()
+@pytest.mark.parametrize("d,T,S,n_split", [(64, 1, 128, 2), (64, 1, 900, None), (128, 4, 600, None),
+                                           (32, 1, 5000, None), (128, 1, 200, 1)])
+def test_captured_step_replays_over_new_lengths(d, T, S, n_split):
+    c = Case([100, S - 20], T, 8, 2, d, norm=True, lam="layer", S=S)
+    q, lam, lens = c.q.to(DEV), c.lam.to(DEV), c.dev_lens()
+    if T == 1:
+        q = q[:, 0].contiguous()
     args = (q, c.k, c.v, lens, lam)
-    want = [x.clone() for x in g.decode_diff(*args, n_split=2, **c.form)]
+    want = [x.clone() for x in g.decode_diff(*args, n_split=n_split, **c.form)]
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        got = g.decode_diff(*args, n_split=2, **c.form)
+        got = g.decode_diff(*args, n_split=n_split, **c.form)
     for _ in range(2):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     lens -= 7
     graph.replay()
-    fresh = g.decode_diff(*args, n_split=2, **c.form)
+    fresh = g.decode_diff(*args, n_split=n_split, **c.form)
     torch.cuda.synchronize()
     assert torch.equal(got[0], fresh[0]) and torch.equal(got[1], fresh[1])
+
+
+def test_captured_prefill_in_parts():
+    c = Case([700, 300], 100, 4, 2, 64, norm=True, lam="layer", S=800)
+    q, lam, lens = c.q.to(DEV), c.lam.to(DEV), c.dev_lens()
+    graph = torch.cuda.CUDAGraph()
+    run = lambda: g.prefill_diff(q, c.k, c.v, lam, lens, n_part=3, **c.form)  # noqa: E731
+    want = [x.clone() for x in run()]
+    with torch.cuda.graph(graph):
+        got = run()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_two_streams_at_once():

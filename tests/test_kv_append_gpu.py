@@ -318,3 +318,55 @@ def test_what_the_helper_refuses():
         g.kv_append(k.transpose(0, 1).contiguous().transpose(0, 1), v, s.kc, s.vc, lens)
     with pytest.raises(g.GQAError):
         g.kv_append(k, v, s.kc, s.vc, lens[:1])
+
+
+# ------------------------------------------------- with the attention over it --
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [0, 16])
+def test_appended_tokens_are_what_decode_attends_to(page, fp8):
+    """Prompts of a padded batch, then single tokens, through the append and the library's decode:
+    the output against attention in 64 bits over what the cache then holds, and what it holds
+    against the turned rows."""
+    B, S, Hq, Hk, d = 3, 96, 8, 2, 64
+    s = Step(B, 40, Hq, Hk, d, d, page=page, fp8=fp8, counts=[40, 7, 23], lens=[40, 7, 23], S=S)
+    s.run()
+    s.check()
+    for step in range(3):
+        rows = [torch.randn(B, 1, h, d, generator=s.gen).to(torch.bfloat16) for h in (Hq, Hk, Hk)]
+        s.lens = [n + 1 for n in s.lens]
+        lens = torch.tensor(s.lens, dtype=torch.int32, device=DEV)
+        q, k, v = (x.to(DEV) for x in rows)
+        a = {**s.args(), "n_new": None}
+        q = g.kv_append(k, v, s.kc, s.vc, lens, q=q, **a)[:, 0].contiguous()
+        if fp8:
+            out, lse = g.decode_fp8(q, s.kc, s.vc, s.ks, s.vs, lens, block_table=a["block_table"])
+        elif page:
+            out, lse = g.decode_paged(q, s.kc, s.vc, a["block_table"], lens)
+        else:
+            out, lse = g.decode(q, s.kc, s.vc, lens)
+        torch.cuda.synchronize()
+        assert g.gqa_last_device_error() == g.GQA_OK
+        for b, L in enumerate(s.lens):
+            at = [s.place(b, t) for t in range(L)]
+            unit, row = torch.tensor([x[0] for x in at]), torch.tensor([x[1] for x in at])
+
+            def held(c, sc):
+                c = c.cpu()[unit, row]
+                if not fp8:
+                    return c.double().numpy()
+                return E4M3[c.numpy()] * sc.cpu().double()[unit, row].numpy()[:, None, None]
+
+            kk, vv = held(s.kc, s.ks), held(s.vc, s.vs)
+            # the new key, turned by its place
+            y, tol = ref.turn(rows[1][b].double().numpy(), [L - 1], s.freqs.double().numpy(), False)
+            near = ref.bf16_tol(y[0], tol[0])
+            if fp8:
+                near = 2.0 ** -4 * np.abs(y[0]) + s.ks.cpu()[at[-1]].item() * 2.0 ** -10 + 2 * tol[0]
+            assert (np.abs(kk[-1] - y[0]) <= near).all()
+            for h in range(Hq):
+                x = kk[:, h // (Hq // Hk)] @ q[b, h].double().cpu().numpy() / np.sqrt(d)
+                z = np.log(np.exp(x - x.max()).sum()) + x.max()
+                o = np.exp(x - z) @ vv[:, h // (Hq // Hk)]
+                # the parity bar of the decodes
+                assert abs(lse[b, h].item() - z) <= 1e-3
+                assert np.abs(out[b, h].double().cpu().numpy() - o).max() <= 2e-2
