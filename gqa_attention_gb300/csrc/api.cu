@@ -1367,12 +1367,16 @@ gqa_status gqa_attn_prefill_chunk_split(const void* q, const void* k_cache, cons
 }
 
 int gqa_attn_prefill_diff_default_parts(int B, int T_q, int S_max, int H, int H_kv, int window) {
-  if (H < 1 || H > 32767 || H_kv < 1 || H % H_kv != 0 || S_max < 1 || T_q < 1) return 1;
-  // Parts pay for long items only, and within a window no item is long (333 queries of three
-  // sequences of 1.3K to 2.9K, 1000 keys back: 32 us in parts, 24 without).
+  if (B < 1 || T_q < 1 || S_max < T_q || H < 1 || H > 32767 || H_kv < 1 || H % H_kv != 0) return 1;
+  // Parts are for a short chunk over long keys, whose few work items leave SMs idle: as many
+  // as fill them, of eight key tiles or more.  (A part writes and a merge reads fp32
+  // partials.  512 queries at 4K, 16 maps of 128: 57 us in one, 28 in four, 33 in eight; 1024
+  // queries at 8K, 32 maps: 108 in one, 127 in two; 333 queries of three sequences of 1.3K to
+  // 2.9K, 1000 keys back: 24 in one, 32 in three.)
   const long long keys = window < 0 ? S_max : std::min<long long>(S_max, (long long)window + 128);
-  if (keys / 128 < 16) return 1;
-  return gqa_attn_prefill_chunk_default_parts(B, T_q, S_max, 2 * H, H_kv);
+  const long long tiles = keys / 128, items = ((long long)T_q + 127) / 128 * B * H;
+  if (T_q == S_max || tiles < 16) return 1;
+  return (int)std::max(1LL, std::min({8LL, num_sms_current_device() / items, tiles / 8}));
 }
 
 gqa_status gqa_attn_prefill_diff(const void* q, const void* k_cache, const void* v_cache,
@@ -1386,9 +1390,12 @@ gqa_status gqa_attn_prefill_diff(const void* q, const void* k_cache, const void*
   const gqa_status st = diff_params(lam, lam_stride_b, lam_stride_t, lam_stride_h, H, H_kv,
                                     split_keys, norm_weight, norm_eps, out_scale, &diff);
   if (st != GQA_OK) return st;
-  const bool chunk = seq_lens || T_q != S_max || window >= 0 || n_part > 1;
+  // Whole prompts, also given with lengths (all of them S_max, or bad), take the causal kernel
+  // (8K tokens, 64 maps of 128: 693 us, 752 as a chunk).
+  const int back = window < S_max ? window : -1;
+  const bool chunk = T_q != S_max || back >= 0 || n_part > 1;
   return run_prefill(chunk, q, k_cache, v_cache, seq_lens, B, T_q, S_max, 2 * H, H_kv, d, scale,
-                     window < S_max ? window : -1, n_part, workspace, out, lse, stream, &diff);
+                     back, n_part, workspace, out, lse, stream, &diff);
 }
 
 gqa_status gqa_last_device_error(gqa_stream_t stream) {

@@ -699,6 +699,103 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) gqa_diff_merge_kernel(c
   if (u == 0 && in_bounds(at, 1, n_rows / 2 * D, p.err)) p.out[at] = __float2bfloat16(o * weight * f);
 }
 
+// The same merge for many rows (a chunk prefill's): one warp per head row, a lane with
+// D / 32 columns of both maps, no exchange through shared memory.
+constexpr int kRowWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kRowWarps * 32) gqa_diff_merge_rows_kernel(const DiffMergeParams p) {
+  constexpr int VEC = D / 32;
+  using Vec = std::conditional_t<VEC == 4, float4, std::conditional_t<VEC == 2, float2, float>>;
+  const int lane = threadIdx.x & 31;
+  const unsigned H = p.H_maps / 2;
+  const size_t item = static_cast<size_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (item >= static_cast<size_t>(p.B) * p.T * H) return;
+  const unsigned bt = static_cast<unsigned>(item / H);
+  const int h = static_cast<int>(item - static_cast<size_t>(bt) * H);
+  const int b = bt / static_cast<unsigned>(p.T), t = bt - b * p.T;
+  const float lam = p.diff.lam[b * p.diff.lam_b + t * p.diff.lam_t + h * p.diff.lam_h];
+  const size_t row = static_cast<size_t>(bt) * p.H_maps + 2 * h;
+  const size_t n_rows = (size_t)p.B * p.T * p.H_maps;
+  float o[2][VEC];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float2* ml = p.ws_ml + (row + u) * p.n_part;
+    const Vec* O = reinterpret_cast<const Vec*>(p.ws_O + (row + u) * p.n_part * D) + lane;
+    float M = -INFINITY, L = 0.f;
+    bool bad = false;
+    float acc[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
+    for (int s0 = 0; s0 < p.n_part; s0 += 8) {
+      const bool mine = lane < 8 && s0 + lane < p.n_part;
+      float2 part = mine ? ml[s0 + lane] : make_float2(-INFINITY, 0.f);
+      Vec ov[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) ov[s] = s0 + s < p.n_part ? O[(size_t)(s0 + s) * 32] : Vec{};
+      part.x *= p.m_log2;
+      bad |= __any_sync(0xffffffffu, isnan(part.x) || isnan(part.y));
+      float cm = part.x;
+#pragma unroll
+      for (int k = 4; k > 0; k >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, k));
+      cm = fmaxf(__shfl_sync(0xffffffffu, cm, 0), M);
+      const float ref = (cm == -INFINITY) ? 0.f : cm;
+      const float a = ex2_approx(M - ref);
+      // an empty part (m = -inf) has weight 0 and its O (never written) is not used
+      const bool live = part.x != -INFINITY;
+      const float w = live ? ex2_approx(part.x - ref) : 0.f;
+      const unsigned alive = __ballot_sync(0xffffffffu, live);
+      const float wl = live ? w * part.y : 0.f;
+      L *= a;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) acc[v] *= a;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        L += __shfl_sync(0xffffffffu, wl, s);
+        if (!(alive >> s & 1)) continue;
+        const float* x = reinterpret_cast<const float*>(&ov[s]);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) acc[v] = fmaf(ws, x[v], acc[v]);
+      }
+      M = cm;
+    }
+    const bool poisoned = bad || !(L > 0.f);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) o[u][v] = poisoned ? NAN : acc[v] / L;
+    const long long at = b * p.lse_b + t * p.lse_t + (2 * h + u) * p.lse_m;
+    if (lane == 0 && in_bounds(at, 1, n_rows, p.err))
+      p.lse[at] = poisoned ? NAN : (M + log2f(L)) * kLn2;
+  }
+  float y[VEC], f = p.diff.out_scale, ss = 0.f;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    y[v] = fmaf(-lam, o[1][v], o[0][v]);
+    ss += y[v] * y[v];
+  }
+  if (p.diff.norm_eps >= 0.f) {
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+    f *= rsqrtf(ss * (1.f / D) + p.diff.norm_eps);
+  }
+  const int col = lane * VEC;
+  const size_t at = item * D + col;
+  if (!in_bounds(at, VEC, n_rows / 2 * D, p.err)) return;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const float w = p.diff.norm_weight ? p.diff.norm_weight[col + v] : 1.f;
+    y[v] *= w * f;
+  }
+  if constexpr (VEC == 4)
+    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  else if constexpr (VEC == 2)
+    *reinterpret_cast<uint32_t*>(p.out + at) = pack_bf16x2(y[0], y[1]);
+  else
+    p.out[at] = __float2bfloat16(y[0]);
+}
+
 template <int D, int NRG, bool ROWS16, int NSTAGE, bool PAGED, bool CLUSTER = false, bool CUT = false>
 cudaError_t launch(const DecodeDiffParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                    cudaStream_t stream) {
@@ -785,25 +882,35 @@ cudaError_t launch_rows(const DecodeDiffParams& p_in, const CUtensorMap& tm_k,
              : launch<D, 1, false, kShallow, PAGED>(p, tm_k, tm_v, stream);
 }
 
-template <int D, int CHUNK>
-cudaError_t launch_merge(const DiffMergeParams& p, cudaStream_t stream) {
+cudaError_t launch_merge(void (*kern)(const DiffMergeParams), long long ctas, int threads,
+                         const DiffMergeParams& p, cudaStream_t stream) {
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.B * p.T * (p.H_maps / 2)));
-  cfg.blockDim = dim3(2 * D);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, gqa_diff_merge_kernel<D, CHUNK>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_merge_d(const DiffMergeParams& p, cudaStream_t stream) {
-  if ((long long)p.B * p.T * (p.H_maps / 2) > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return p.n_part <= 8 ? launch_merge<D, 8>(p, stream) : launch_merge<D, 32>(p, stream);
+  const long long rows = (long long)p.B * p.T * (p.H_maps / 2);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  // A CTA per row finishes soonest while all of them are on the GPU at once; a warp per row
+  // has less to do for each.
+  if (rows > 8LL * sms)
+    return launch_merge(gqa_diff_merge_rows_kernel<D>, (rows + kRowWarps - 1) / kRowWarps,
+                        kRowWarps * 32, p, stream);
+  return p.n_part <= 8 ? launch_merge(gqa_diff_merge_kernel<D, 8>, rows, 2 * D, p, stream)
+                       : launch_merge(gqa_diff_merge_kernel<D, 32>, rows, 2 * D, p, stream);
 }
 
 }  // namespace

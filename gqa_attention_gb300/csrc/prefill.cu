@@ -513,6 +513,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         continue;
       }
       float m_ref = -INFINITY, l = 0.f;
+      // (a whole prompt given with lengths runs without them, each of them being S or bad)
+      const bool bad_len =
+          GENERAL ? gm.bad : DIFF != 0 && p.seq_lens && p.seq_lens[it.b] != p.S;
       float lam = 0.f;  // differential: this row's weight of the second map, for the epilogue
       if constexpr (DIFF != 0) {
         if (q_row < p.S && p.n_part <= 1)
@@ -667,9 +670,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if ((DIFF == 0 || split) && !wait_all(&o_full[x], of_ph)) break;
       of_ph ^= 1;
       tc_fence_after();
-      const float inv = (GENERAL && gm.bad) ? NAN : 1.f / l;
+      const float inv = bad_len ? NAN : 1.f / l;
       const bool store = q_row < p.S;
-      if (GENERAL && gm.bad && x == 0 && warp == 4 && lane == 0) atomicOr(p.err, kErrBadSeqLen);
+      if (bad_len && x == 0 && warp == 4 && lane == 0) atomicOr(p.err, kErrBadSeqLen);
       const int D = p.d;  // row width of out and of the O partials
       if constexpr (DIFF != 0) {
         if (!split) {
@@ -796,9 +799,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const size_t lse_at = (static_cast<size_t>(it.b) * p.H_q + h) * p.S + q_row;
       if (split && store && in_bounds(ws_row * p.n_part + it.part, 1, n_rows * p.n_part, p.err))
         p.ws_ml[ws_row * p.n_part + it.part] =
-            gm.bad ? make_float2(NAN, NAN) : make_float2(m_ref, l);
+            bad_len ? make_float2(NAN, NAN) : make_float2(m_ref, l);
       else if (!split && store && in_bounds(lse_at, 1, n_rows, p.err))
-        p.lse[lse_at] = (GENERAL && gm.bad) ? NAN : (m_ref + log2f(l)) * kLn2;
+        p.lse[lse_at] = bad_len ? NAN : (m_ref + log2f(l)) * kLn2;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {

@@ -712,7 +712,7 @@ gqa_status gqa_attn_prefill_diff(const void* q, const void* k_cache, const void*
                                  float out_scale, int n_part, void* workspace, void* out,
                                  float* lse, gqa_stream_t stream);
 
-/* A part count for gqa_attn_prefill_diff on the current device (1: no parts; at most 4).
+/* A part count for gqa_attn_prefill_diff on the current device (1: no parts; at most 8).
  * Returns 1 for invalid input. */
 int gqa_attn_prefill_diff_default_parts(int B, int T_q, int S_max, int H, int H_kv, int window);
 

@@ -150,7 +150,8 @@ def test_default_splits():
 def test_default_parts():
     # (no GPU here: the SM count falls back to a default)
     assert g.gqa_attn_prefill_diff_default_parts(3, 333, 2903, 8, 2, 1000) == 1
-    assert 1 <= g.gqa_attn_prefill_diff_default_parts(1, 128, 32768, 8, 2, -1) <= 4
+    assert g.gqa_attn_prefill_diff_default_parts(1, 128, 32768, 8, 2, -1) == 8
+    assert g.gqa_attn_prefill_diff_default_parts(1, 4096, 4096, 8, 2, -1) == 1
     for bad in ((0, 128, 32768, 8, 2, -1), (1, 0, 32768, 8, 2, -1), (1, 128, 0, 8, 2, -1),
                 (1, 128, 32768, 7, 2, -1), (1, 128, 32768, 8, 0, -1), (1, 128, 32768, 1 << 30, 2, -1)):
         assert g.gqa_attn_prefill_diff_default_parts(*bad) == 1
