@@ -708,8 +708,10 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
     const int pieces = length_pieces(B, H_kv, rows, S_max);
     if (pieces > 0) return 2 * ((pieces + B - 1) / B);
     // One CTA on an SM: no more than fill them once (4 sequences of 8K, 8 KV heads, 32 rows:
-    // 45 us in five splits, 29 in four), and at least two tiles each.
-    const long long fill = num_sms_current_device() / ((long long)B * H_kv);
+    // 45 us in five splits, 26 in four), from 16 on a multiple of eight (32 rows, 8 KV heads,
+    // in 16 splits / 19: 8K tokens 10.9 / 11.8 us, 32K 23.7 / 24.1), and at least two tiles each.
+    long long fill = num_sms_current_device() / ((long long)B * H_kv);
+    if (fill >= 16) fill -= fill % 8;
     const long long tiles = ((long long)S_max + 127) / 128;
     return (int)std::max(1LL, std::min(fill, (tiles + 1) / 2));
   }
@@ -721,11 +723,14 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
   const int pieces = diff_pieces(B, H_kv, rows, S_max);
   if (pieces > 0 && S_max > 1024) return 2 * ((pieces + B - 1) / B);
   if (S_max <= 1024 || (S_max <= 2048 && rows <= 32 && groups * 8 <= sms)) return 1;
-  // One sequence: a CTA to an SM.  Several: two (one and a half of more than 16 rows, which
+  // One sequence: a CTA to an SM, or somewhat fewer, a multiple of eight (8 KV heads of 128 in 16
+  // splits / 19: 4K tokens 6.2 us / 6.8, 8K 8.3 / 9.4, 32K 22.5-23.1 / 23.1-23.4; 4 of 64 in 32 / 38:
+  // 4K 4.3 / 5.4, 32K 9.4 / 10.3, 64K 16.0 / 15.9).  Several: two (one and a half of more than 16 rows, which
   // have an SM to themselves), since sequences are seldom equally long and two fill
   // it better: 2 x 4K-30K tokens, 8 KV heads of 128, 35 us in 9 splits, 28 in 18 (all of
   // 30K 39 and 39); 8 x 8K, 4 of 64, 21.7 in four, 13.9 in eight.  Splits of 128 to 8192 tokens.
   long long n = B == 1 ? sms / groups : (rows <= 16 ? 4 : 3) * sms / (2 * groups);
+  if (B == 1 && n >= 16) n -= n % 8;
   n = std::min(n, ((long long)S_max + 127) / 128);
   return (int)std::max({1LL, n, ((long long)S_max + 8191) / 8192});
 }

@@ -909,8 +909,10 @@ cudaError_t launch_merge_d(const DiffMergeParams& p, cudaStream_t stream) {
   if (rows > 8LL * sms)
     return launch_merge(gqa_diff_merge_rows_kernel<D>, (rows + kRowWarps - 1) / kRowWarps,
                         kRowWarps * 32, p, stream);
-  return p.n_part <= 8 ? launch_merge(gqa_diff_merge_kernel<D, 8>, rows, 2 * D, p, stream)
-                       : launch_merge(gqa_diff_merge_kernel<D, 32>, rows, 2 * D, p, stream);
+  return launch_merge(p.n_part <= 8    ? gqa_diff_merge_kernel<D, 8>
+                      : p.n_part <= 16 ? gqa_diff_merge_kernel<D, 16>
+                                       : gqa_diff_merge_kernel<D, 32>,
+                      rows, 2 * D, p, stream);
 }
 
 }  // namespace
