@@ -24,6 +24,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 16;  // tokens of a CTA, at most
 constexpr int kUnroll = 4;   // rows whose pieces a thread loads at once
+constexpr int kRing = 2;     // E4M3: tiles that a thread has copies in flight or waiting for
+
+__device__ __forceinline__ void copy_async_16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
 
 // 2^64 f / 2 pi modulo 2^64.
 __device__ __forceinline__ uint64_t turns_of(float f) {
@@ -119,14 +127,17 @@ constexpr long long kNoPage = -3;  // of a bad page: its query rows are turned a
 
 // HOLD = 0 (bf16): rows (queries, keys, values) of all tokens are one list.  HOLD > 0 (E4M3):
 // the list holds the queries alone, and the CTAs of the last grid row take the keys
-// and values: `team` warps take those of a token whole, for the maximum over its heads,
-// HOLD slots of a lane staying in registers between the maximum and the rounding.
+// and values.  A token's keys, or its values, are a unit that `width` lanes take whole, for
+// the maximum over its heads: a part of a warp, a warp, or several warps, which meet at a
+// barrier.  HOLD slots of a lane stay in registers between the maximum and the rounding.  A
+// lane copies its own pieces of the next units to shared memory meanwhile, where they
+// cost no registers and no barrier.
 // EARLY: the CTA's list is one round, whose rows are loaded before the angles are worked
 // out.  (With several rounds that is slower: 32K tokens of 80 heads of 128 232 us, 201 if
 // each round is loaded when its turn comes.)
 template <int D, int HOLD, bool EARLY>
 __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ? 4 : 3)
-    gqa_kv_append_rot_kernel(const KvAppendParams p, int tok_per, int team) {
+    gqa_kv_append_rot_kernel(const KvAppendParams p, int tok_per, int width) {
   constexpr bool FP8 = HOLD > 0;
   constexpr int kSlots = D / 16;
   constexpr int kRowStep = kThreads / kSlots;  // rows that the CTA takes at a time
@@ -135,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
   __shared__ long long dst_sm[kMaxTok];  // row of the cache, kSkip or kBad
   __shared__ int pos_sm[kMaxTok];
   __shared__ uint32_t max_sm[FP8 ? 3 : 1][kThreads / 32];  // E4M3: a warp's share of a maximum
+  __shared__ uint4 ring_sm[FP8 ? kRing : 1][FP8 ? 2 * HOLD : 1][FP8 ? kThreads : 1];
   const int tid = threadIdx.x;
   const long long tok0 = static_cast<long long>(blockIdx.x) * tok_per;
   const int n_tok = static_cast<int>(min(static_cast<long long>(tok_per),
@@ -147,9 +159,10 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
   const size_t hq = static_cast<size_t>(p.H_q) * D, hkv = static_cast<size_t>(p.H_kv) * D;
   const int q_rows = p.q ? p.H_q : 0;
   const int rows = q_rows + (FP8 ? 0 : 2 * p.H_kv);
+  const bool list_role = !FP8 || (rows && (!kv_role || gridDim.y == 1));
   const Slot sl = slot_of(tid % kSlots, p.rot, inter);
   // The list's (token, row) pairs, from this thread's first on.
-  const int step = kRowStep * (FP8 ? gridDim.y - 1 : gridDim.y);
+  const int step = kRowStep * (FP8 && gridDim.y > 1 ? gridDim.y - 1 : gridDim.y);
   int k = 0, r = tid / kSlots + kRowStep * blockIdx.y;
   uint4 a[kUnroll], c[kUnroll];
   int kk[kUnroll], rr[kUnroll];
@@ -176,28 +189,35 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
       r += step;
     }
   };
-  // A token's keys or values (unit 2 k or 2 k + 1) of a team: this lane's slots are `at0`,
-  // at0 + stride, ..
+  // Tile i of the units: the keys (i even) or values of the `many` tokens from (i / 2) many on,
+  // a token to each `width` lanes.  This lane's slots are `at0`, at0 + width, ..
   constexpr int kKeep = FP8 ? HOLD : 1;
   const int warp = tid >> 5, lane = tid & 31;
   const int n_slots = p.H_kv * kSlots;
-  const int stride = 32 * team, at0 = tid % stride;
-  const int n_teams = kThreads / 32 / team, my_team = warp / team;
-  const Slot ls = slot_of(lane % kSlots, p.rot, inter);
-  uint4 na[kKeep], nc[kKeep];
-  auto unit_rows = [&](int unit) {
-    return ((unit & 1) ? p.v : p.k) + (tok0 + (unit >> 1)) * p.kv_stride;
+  const int many = width < 32 ? 32 / width : 1, mine = width < 32 ? lane / width : 0;
+  const int at0 = tid % width;
+  const int n_teams = width < 32 ? kThreads / 32 : kThreads / width;
+  const int my_team = width < 32 ? warp : tid / width;
+  const int n_tiles = 2 * ((n_tok + many - 1) / many);
+  const Slot ls = slot_of(at0 % kSlots, p.rot, inter);
+  auto token_of = [&](int tile) { return (tile >> 1) * many + mine; };
+  auto unit_rows = [&](int tile) {
+    return ((tile & 1) ? p.v : p.k) + (tok0 + token_of(tile)) * p.kv_stride;
   };
-  auto load_unit = [&](int unit) {
-    if (unit >= 2 * n_tok || dst_sm[unit >> 1] < 0) return;
+  auto copy_tile = [&](int tile, int stage) {
+    const int t = token_of(tile);
+    if (tile < n_tiles && t < n_tok && dst_sm[t] >= 0) {
+      const __nv_bfloat16* src = unit_rows(tile);
 #pragma unroll
-    for (int h = 0; h < kKeep; ++h) {
-      const int s = at0 + stride * h;
-      if (s >= n_slots) continue;
-      const __nv_bfloat16* src = unit_rows(unit) + (s / kSlots) * D;
-      na[h] = *reinterpret_cast<const uint4*>(src + ls.off0);
-      nc[h] = *reinterpret_cast<const uint4*>(src + ls.off1);
+      for (int h = 0; h < kKeep; ++h) {
+        const int s = at0 + width * h;
+        if (s >= n_slots) continue;
+        const __nv_bfloat16* row = src + (s / kSlots) * D;
+        copy_async_16(&ring_sm[stage][2 * h][tid], row + ls.off0);
+        copy_async_16(&ring_sm[stage][2 * h + 1][tid], row + ls.off1);
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   // Where the tokens go.
@@ -232,12 +252,15 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
   __syncthreads();
   // (the first rows travel while the angles are worked out)
   if (kv_role) {
-    load_unit(my_team);
-  } else if constexpr (EARLY) {
-    load_round();
+    if constexpr (FP8) {
+#pragma unroll
+      for (int i = 0; i < kRing; ++i) copy_tile(my_team + i * n_teams, i);
+    }
   }
-  for (int e = tid; e < n_tok * (p.rot / 2); e += kThreads) {
-    const int t = e / (p.rot / 2), i = e - t * (p.rot / 2);
+  if constexpr (EARLY) {
+    if (list_role) load_round();
+  }
+  for (int t = tid / (D / 2), i = tid % (D / 2); t < n_tok && i < p.rot / 2; t += kThreads / (D / 2)) {
     const uint64_t angle = static_cast<uint64_t>(static_cast<long long>(pos_sm[t])) * turns_sm[i];
     float sn, cn;
     sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * (1.f / 2147483648.f), &sn, &cn);
@@ -250,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
   const size_t n_cache = (p.block_table ? static_cast<size_t>(p.num_pages) * p.page_size
                                         : static_cast<size_t>(p.B) * p.S_max) * hkv;
   const size_t n_q = static_cast<size_t>(p.B) * p.T * hq;
-  if (!kv_role) {
+  if (list_role) {
     for (;;) {
       if constexpr (!EARLY) {
         load_round();
@@ -297,34 +320,40 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
   }
 
   if constexpr (FP8) {
-    // The largest of a team's values, given as bits (positive floats compare as those).  One
-    // barrier: the buffers are taken in turn.
+    // The largest of a unit's values, given as bits (positive floats compare as those).  Of
+    // several warps at one barrier: the buffers are taken in turn.
     int buffer = 0;
-    auto team_max = [&](uint32_t v) -> uint32_t {
+    auto unit_max = [&](uint32_t v) -> uint32_t {
+      if (width < 32) {
+        for (int m = width / 2; m; m /= 2) v = max(v, __shfl_xor_sync(0xffffffffu, v, m));
+        return v;
+      }
       v = __reduce_max_sync(0xffffffffu, v);
-      if (team == 1) return v;
+      if (width == 32) return v;
       if (lane == 0) max_sm[buffer][warp] = v;
-      named_bar_sync(1 + my_team, stride);
-      const uint32_t got = lane < team ? max_sm[buffer][my_team * team + lane] : 0u;
+      named_bar_sync(1 + my_team, width);
+      const uint32_t got = lane < width / 32 ? max_sm[buffer][my_team * (width / 32) + lane] : 0u;
       buffer = buffer == 2 ? 0 : buffer + 1;
       return __reduce_max_sync(0xffffffffu, got);
     };
-    for (int unit = my_team; kv_role && unit < 2 * n_tok; unit += n_teams) {
+    int stage = 0;
+    for (int tile = my_team; kv_role && tile < n_tiles; tile += n_teams) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
       uint4 va[kKeep], vc[kKeep];
 #pragma unroll
       for (int h = 0; h < kKeep; ++h) {
-        va[h] = na[h];
-        vc[h] = nc[h];
+        va[h] = ring_sm[stage][2 * h][tid];
+        vc[h] = ring_sm[stage][2 * h + 1][tid];
       }
-      load_unit(unit + n_teams);  // (the next one's rows travel meanwhile)
-      const int t = unit >> 1;
-      const bool is_v = unit & 1;
-      const long long dst = dst_sm[t];
-      if (dst < 0) continue;
-      const __nv_bfloat16* src = unit_rows(unit);
+      const int t = min(token_of(tile), n_tok - 1);
+      const bool is_v = tile & 1;
+      const long long dst = token_of(tile) < n_tok ? dst_sm[t] : kSkip;
+      const bool live = dst >= 0;
+      const int own = live ? n_slots : 0;  // slots of this lane's unit
+      const __nv_bfloat16* src = unit_rows(tile);
       float4 cs[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cs[j] = cs_sm[t][j][lane % kSlots];
+      for (int j = 0; j < 4; ++j) cs[j] = cs_sm[t][j][at0 % kSlots];
       const bool turned = ls.turned && !is_v;
       auto values = [&](const uint4& u, const uint4& w, float (&x)[8], float (&y)[8]) {
         if (turned) {
@@ -349,48 +378,50 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
       };
 #pragma unroll
       for (int h = 0; h < kKeep; ++h) {
-        if (at0 + stride * h >= n_slots) continue;
+        if (at0 + width * h >= own) continue;
         values(va[h], vc[h], x[h], y[h]);
         widest(x[h]);
         widest(y[h]);
       }
-      for (int s = at0 + stride * kKeep; s < n_slots; s += stride) {
+      for (int s = at0 + width * kKeep; s < own; s += width) {
         float u[8], w[8];
         values_of(s, u, w);
         widest(u);
         widest(w);
       }
-      amax = __uint_as_float(team_max(__float_as_uint(amax)));
-      const bool infinite = amax > 3.4028235e38f;  // rare: the maximum again, of what is finite
-      if (infinite) {
-        amax = 0.f;
-        auto widest_finite = [&](const float (&v)[8]) {
+      // (the pieces have been read: their places take the tile after the next)
+      copy_tile(tile + kRing * n_teams, stage);
+      stage = stage == kRing - 1 ? 0 : stage + 1;
+      amax = __uint_as_float(unit_max(__float_as_uint(amax)));
+              auto widest_finite = [&](float (&v)[8]) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (isfinite(v[j])) amax = fmaxf(amax, fabsf(v[j]));
-        };
+                for (int j = 0; j < 8; ++j) {
+                  v[j] = isfinite(v[j]) ? v[j] : NAN;  // (an infinity would be clamped to 448)
+                  amax = fmaxf(amax, fabsf(v[j]));
+                }
+              };
+      // Rare: the maximum again, of what is finite.  (Lanes of one warp go together.)
+      const bool infinite = amax > 3.4028235e38f;
+      if (__any_sync(0xffffffffu, infinite)) {
+        amax = 0.f;
 #pragma unroll
         for (int h = 0; h < kKeep; ++h) {
-          if (at0 + stride * h >= n_slots) continue;
+          if (at0 + width * h >= own) continue;
           widest_finite(x[h]);
           widest_finite(y[h]);
         }
-        for (int s = at0 + stride * kKeep; s < n_slots; s += stride) {
+        for (int s = at0 + width * kKeep; s < own; s += width) {
           float u[8], w[8];
           values_of(s, u, w);
           widest_finite(u);
           widest_finite(w);
         }
-        amax = __uint_as_float(team_max(__float_as_uint(amax)));
+        amax = __uint_as_float(unit_max(__float_as_uint(amax)));
       }
       const int e = scale_exp(amax);
       const float inv = pow2f(-e);
       uint8_t* codes = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache);
       auto coded = [&](float (&v)[8]) -> uint2 {
-        if (infinite) {  // (the conversion alone would clamp an infinity to 448)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = isfinite(v[j]) ? v[j] : NAN;
-        }
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -410,37 +441,47 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
       };
 #pragma unroll
       for (int h = 0; h < kKeep; ++h)
-        if (at0 + stride * h < n_slots) put(at0 + stride * h, x[h], y[h]);
-      for (int s = at0 + stride * kKeep; s < n_slots; s += stride) {
+        if (at0 + width * h < own) put(at0 + width * h, x[h], y[h]);
+      for (int s = at0 + width * kKeep; s < own; s += width) {
         float u[8], w[8];
         values_of(s, u, w);
+        if (infinite) {
+          widest_finite(u);
+          widest_finite(w);
+        }
         put(s, u, w);
       }
-      if (at0 == 0 && in_bounds(dst, 1, n_cache / hkv, p.err))
+      if (live && at0 == 0 && in_bounds(dst, 1, n_cache / hkv, p.err))
         (is_v ? p.v_scale : p.k_scale)[dst] = pow2f(e);
     }
   }
 }
 
 template <int D, int HOLD>
-cudaError_t launch(const KvAppendParams& p, int sms, int team, cudaStream_t stream) {
+cudaError_t launch(const KvAppendParams& p, int sms, int width, cudaStream_t stream) {
   constexpr bool FP8 = HOLD > 0;
   // Tokens to a CTA: enough CTAs for four on every SM, then as many tokens as share the
   // set-up, but of few rows (half of a round to a token or less) no more than one round
-  // takes.  Few tokens: their rows are divided among CTAs.
+  // takes.  Few tokens: their rows are divided among CTAs.  E4M3: one wave of the two or
+  // three CTAs that an SM holds; the same CTA turns the queries and then takes the keys and
+  // values, whose copies travel meanwhile, and only where CTAs are few do those go to CTAs of
+  // their own (32 / 8 heads of 128: 1000 tokens 5.1 us, 13.3 with four CTAs to an SM and the
+  // keys and values always apart; 32K 120 and 130, 95% of the copy rate with 64 query heads).
   const long long tokens = (long long)p.B * p.T;
   const int rows = (p.q ? p.H_q : 0) + (FP8 ? 0 : 2 * p.H_kv);
   const int pieces = rows * (D / 16);  // of a token in the list
-  long long tok_per = tokens / (4LL * sms);
+  const long long ctas = (HOLD == 0 ? 4 : HOLD == 1 ? 3 : 2) * (long long)sms;
+  long long tok_per = FP8 ? (tokens + ctas - 1) / ctas : tokens / ctas;
   if (!FP8 && pieces <= kUnroll * kThreads / 2) tok_per = std::min(tok_per, (long long)kUnroll * kThreads / pieces);
   tok_per = std::max(1LL, std::min(tok_per, (long long)kMaxTok));
   const long long x = (tokens + tok_per - 1) / tok_per;
   if (x > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int passes = (pieces + kThreads - 1) / kThreads;
   const long long y = std::min((long long)passes, std::max(1LL, 2LL * sms / x));  // (0: no list)
+  const bool apart = FP8 && (y != 1 || x <= sms);
   const bool early = tok_per * pieces <= kUnroll * kThreads * y;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(y + (FP8 ? 1 : 0)));
+  cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(y + (apart ? 1 : 0)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -450,21 +491,22 @@ cudaError_t launch(const KvAppendParams& p, int sms, int team, cudaStream_t stre
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(
       &cfg, early ? gqa_kv_append_rot_kernel<D, HOLD, true> : gqa_kv_append_rot_kernel<D, HOLD, false>,
-      p, static_cast<int>(tok_per), team);
+      p, static_cast<int>(tok_per), width);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const KvAppendParams& p, int sms, cudaStream_t stream) {
-  if (!p.k_scale) return launch<D, 0>(p, sms, 1, stream);
+  if (!p.k_scale) return launch<D, 0>(p, sms, 32, stream);
   const int slots = p.H_kv * (D / 16);
-  // A lane of a team holds one slot, or two where that makes one warp of it and there are
-  // tokens to fill the GPU (32K tokens of 8 heads of 128: 47 us with two slots, 54 with
-  // two warps, which meet at a barrier for each maximum; 128 tokens: 4.8 and 3.2).
+  // A lane holds one slot, or two where that makes one warp of more (32K tokens, K and V
+  // alone: 8 heads of 128 41.7 us, 51.6 with two warps to a unit, which meet at a barrier for
+  // each maximum; 8 heads of 64, which one warp holds either way, 28.9 and 27.4) and
+  // there are tokens to fill the GPU.
   const bool two = slots > 32 && (long long)p.B * p.T > 4LL * sms;
-  int team = 1;
-  while (team < kThreads / 32 && slots > (two ? 64 : 32) * team) team *= 2;
-  return two ? launch<D, 2>(p, sms, team, stream) : launch<D, 1>(p, sms, team, stream);
+  int width = D / 16;
+  while (width < kThreads && slots > (two ? 2 : 1) * width) width *= 2;
+  return two ? launch<D, 2>(p, sms, width, stream) : launch<D, 1>(p, sms, width, stream);
 }
 
 }  // namespace

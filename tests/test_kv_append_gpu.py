@@ -150,6 +150,39 @@ def test_sizes(B, T, Hq, Hk, d, fp8):
     s.check()
 
 
+@pytest.mark.parametrize("Hq,Hk,d,T", [
+    (4, 1, 128, 1203),   # four tokens to a warp
+    (3, 3, 16, 1203), (2, 5, 32, 1203), (4, 2, 128, 331),
+    (5, 5, 128, 1203),   # two slots to a lane
+    (1, 37, 128, 651),   # several warps to a token, two slots to a lane
+    (1, 70, 128, 651),   # more than they hold at once
+])
+def test_many_e4m3_tokens_and_one_that_is_not_finite(Hq, Hk, d, T):
+    s = Step(1, T, Hq, Hk, d, d, fp8=True, counts=[T - 2], lens=[T + 1], page=16, seed=Hk)
+    s.run()
+    s.check()
+    was = [x.clone() for x in (s.kc, s.vc, s.ks, s.vs)]
+    hit = torch.zeros(T - 2, Hk, d, dtype=torch.bool)
+    at = [0, 1, 6, 17, 600, T - 3] if T > 603 else [0, 1, 6, 17, T - 3]
+    for n, i in enumerate(at):
+        s.dev_rows[2][0, i, i % Hk, i % d] = [float("inf"), float("nan"), -float("inf")][n % 3]
+        hit[i, i % Hk, i % d] = True
+    s.run()
+    where = [s.place(0, s.lens[0] - (T - 2) + i) for i in range(T - 2)]
+    unit, row = (torch.tensor(x, device=DEV) for x in zip(*where))
+    assert torch.equal(s.kc, was[0])
+    assert torch.equal(s.ks.view(torch.int32), was[2].view(torch.int32))
+    got = torch.from_numpy(E4M3[s.vc[unit, row].cpu().numpy()])
+    assert torch.equal(~torch.isfinite(got), hit)
+    clean = torch.ones(T - 2, dtype=torch.bool, device=DEV)
+    clean[at] = False
+    assert torch.equal(s.vc[unit, row][clean], was[1][unit, row][clean])
+    assert torch.equal(s.vs[unit, row][clean], was[3][unit, row][clean])
+    for i in at:  # its scale is that of what is finite
+        rest = s.v[0, i].double().abs()[~hit[i]].max().item()
+        assert s.vs[where[i]].item() == ref.block_scale(rest)
+
+
 def test_far_and_negative_positions():
     pos = torch.tensor([[0, 131071, 131072, 1 << 20, (1 << 24) + 1, (1 << 28) - 1, -1, -70000]],
                        dtype=torch.int32)
