@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
   };
 
   // Where the tokens go.
+  bool wanted = false;
   if (tid < n_tok) {
     const long long g = tok0 + tid;
     const int b = static_cast<int>(g / p.T), i = static_cast<int>(g - static_cast<long long>(b) * p.T);
@@ -247,9 +248,10 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
     }
     dst_sm[tid] = dst;
     pos_sm[tid] = pos;
+    wanted = dst != kSkip;
   }
   if (tid >= 64 && tid - 64 < p.rot / 2) turns_sm[tid - 64] = turns_of(p.freqs[tid - 64]);
-  __syncthreads();
+  if (!__syncthreads_or(wanted)) return;  // (all of them padding)
   // (the first rows travel while the angles are worked out)
   if (kv_role) {
     if constexpr (FP8) {
@@ -261,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
     if (list_role) load_round();
   }
   for (int t = tid / (D / 2), i = tid % (D / 2); t < n_tok && i < p.rot / 2; t += kThreads / (D / 2)) {
+    if (dst_sm[t] == kSkip) continue;
     const uint64_t angle = static_cast<uint64_t>(static_cast<long long>(pos_sm[t])) * turns_sm[i];
     float sn, cn;
     sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * (1.f / 2147483648.f), &sn, &cn);
