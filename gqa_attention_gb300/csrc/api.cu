@@ -1373,15 +1373,18 @@ gqa_status gqa_attn_prefill_chunk_split(const void* q, const void* k_cache, cons
 
 int gqa_attn_prefill_diff_default_parts(int B, int T_q, int S_max, int H, int H_kv, int window) {
   if (B < 1 || T_q < 1 || S_max < T_q || H < 1 || H > 32767 || H_kv < 1 || H % H_kv != 0) return 1;
-  // Parts are for a short chunk over long keys, whose few work items leave SMs idle: as many
-  // as fill them, of eight key tiles or more.  (A part writes and a merge reads fp32
-  // partials.  512 queries at 4K, 16 maps of 128: 57 us in one, 28 in four, 33 in eight; 1024
-  // queries at 8K, 32 maps: 108 in one, 127 in two; 333 queries of three sequences of 1.3K to
-  // 2.9K, 1000 keys back: 24 in one, 32 in three.)
+  // Parts are for few queries over long keys, whose few work items leave SMs idle: as many as
+  // fill them, of two key tiles or more, since a tile takes an item 1.4 us and the partials
+  // and their merge 3 to 5.  100 queries of 32 maps of 128: 1K keys 19.2 / 15.1 us in one /
+  // four parts (8 maps 19.2 / 12.5), 2K 32.8 / 18 in seven, 4K 56 / 18.9 in eight; 768
+  // keys 16.1 / 14.8 in three, but 512 13.0 / 14.4 in two.  Two parts do not pay for short keys (1099
+  // queries at 1.6K, 16 maps of 64: 25.5 and 25.9; 1024 at 2K, of 128, 32.0 and 30.3; a
+  // prompt of 4K, 4 maps, 53 and 43), nor do more than fill the SMs (512 queries at 2K, 16
+  // maps: 31.6 in one, 21.6 in four, 28.8 in six).
   const long long keys = window < 0 ? S_max : std::min<long long>(S_max, (long long)window + 128);
   const long long tiles = keys / 128, items = ((long long)T_q + 127) / 128 * B * H;
-  if (T_q == S_max || tiles < 16) return 1;
-  return (int)std::max(1LL, std::min({8LL, num_sms_current_device() / items, tiles / 8}));
+  const long long n = std::min({8LL, num_sms_current_device() / items, tiles / 2});
+  return n < 2 || tiles < (n == 2 ? 16 : 6) ? 1 : (int)n;
 }
 
 gqa_status gqa_attn_prefill_diff(const void* q, const void* k_cache, const void* v_cache,
