@@ -725,9 +725,9 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
   if (S_max <= 1024 || (S_max <= 2048 && rows <= 32 && groups * 8 <= sms)) return 1;
   // One sequence: a CTA to an SM, or somewhat fewer, a multiple of eight (8 KV heads of 128 in 16
   // splits / 19: 4K tokens 6.2 us / 6.8, 8K 8.3 / 9.4, 32K 22.5-23.1 / 23.1-23.4; 4 of 64 in 32 / 38:
-  // 4K 4.3 / 5.4, 32K 9.4 / 10.3, 64K 16.0 / 15.9).  Several: two (one and a half of more than 16 rows, which
-  // have an SM to themselves), since sequences are seldom equally long and two fill
-  // it better: 2 x 4K-30K tokens, 8 KV heads of 128, 35 us in 9 splits, 28 in 18 (all of
+  // 4K 4.3 / 5.4, 32K 9.4 / 10.3, 64K 16.0 / 15.9).  Several: two (one and a half of more than
+  // 16 rows, which have an SM to themselves), since sequences are seldom equally long and
+  // two fill it better: 2 x 4K-30K tokens, 8 KV heads of 128, 35 us in 9 splits, 28 in 18 (all of
   // 30K 39 and 39); 8 x 8K, 4 of 64, 21.7 in four, 13.9 in eight.  Splits of 128 to 8192 tokens.
   long long n = B == 1 ? sms / groups : (rows <= 16 ? 4 : 3) * sms / (2 * groups);
   if (B == 1 && n >= 16) n -= n % 8;

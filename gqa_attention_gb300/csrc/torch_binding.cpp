@@ -1,8 +1,9 @@
 // torch_binding.cpp -- the helpers for torch tensors of the block-scaled cache, of the
-// rotated append and of differential attention: checks of types, shapes and devices, outputs and workspaces from torch's allocator, and
-// the calls of the C ABI (include/gqa_attn.h).  Argument marshalling only, like the
-// ctypes binding; in C++ because these calls launch kernels of 2 to 20 us, and the
-// same checks and allocations took 10 to 20 us in Python.
+// rotated append and of differential attention: checks of types, shapes and devices,
+// outputs and workspaces from torch's allocator, and the calls of the C ABI
+// (include/gqa_attn.h).  Argument marshalling only, like the ctypes binding; in C++
+// because these calls launch kernels of 2 to 20 us, and the same checks and allocations
+// took 10 to 20 us in Python.
 //
 // The module does not link the library: every function takes the handle of the
 // loaded libgqa_attn.so and looks its entry points up once per handle.
