@@ -23,7 +23,7 @@
 // TB/s; one of 32K 22.4 us, 6.0 TB/s, of which about 4.5 are the start and the merge's
 // launch.  Short sequences are a chain of latencies: 1024 tokens of 2 KV heads of 32,
 // 3.5 us.  From 17 rows on, without the tensor-core tile of decode_tc.cu, by mma.sync and the
-// softmax (20 sequences of 2.5K, 6 KV heads of 64, 64 rows: 38 us, floor 10.5).
+// softmax (20 sequences of 2.5K, 6 KV heads of 64, 64 rows: 36 us, floor 10.5).
 #include <type_traits>
 
 #include "decode_common.cuh"
@@ -60,11 +60,17 @@ __device__ __forceinline__ float4 diff_row(const DiffParams& p, float4 a, float4
 // Stages of a CTA that has an SM to itself, and of one that shares it.  (d = 64 and 32: 96 and
 // 48 KB, two and three CTAs of one row group on an SM.  Registers for a third and a
 // fourth slowed every CTA down: the tiny decode 3.4 -> 4.2 us, 8 x 8K of 64 in eight splits
-// 13.9 -> 15.5.)
+// 13.9 -> 15.5.  Two row groups: 96 registers for a second CTA slow each down, too (5 sequences
+// of up to 5K, 30 rows, d = 64: 10.5 -> 12.7 us), but pay where there are more KV heads and
+// sequences than SMs (60 x 1K, 5 KV heads, 64 rows: 52 -> 37; 40 x 2.5K, 5 of 32, 24 rows
+// 27.0 -> 20.7; 10 x 2.5K, 6 of 64, 64 rows 21 and 29), and for clusters of eight
+// that would otherwise want nearly every SM, of which the GPU's parts hold few whole ones
+// (4 x 900, 4 KV heads, 24 rows: 11.0 -> 7.7).)
 template <int D>
 struct Ring {
   static constexpr int kDeep = 6;
   static constexpr int kShallow = D == 128 ? 3 : 6;
+  static constexpr int kPair = 5;  // two row groups, in 96 registers for two CTAs on an SM
 };
 
 template <int D, int NRG>
@@ -847,7 +853,7 @@ cudaError_t launch_rows(const DecodeDiffParams& p_in, const CUtensorMap& tm_k,
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  constexpr int kShallow = Ring<D>::kShallow, kDeep = Ring<D>::kDeep;
+  constexpr int kShallow = Ring<D>::kShallow, kDeep = Ring<D>::kDeep, kPair = Ring<D>::kPair;
   // One split of a grid that leaves SMs idle: a cluster for each KV head and sequence (8
   // maps on 2 KV heads of 32, 1024 tokens: 3.4 us, one CTA each 6.4; 32 KV heads' worth of
   // 64 maps of 128, 1024 tokens: 6.8 and 9.6), but for short caches (128 tokens, d = 128: 4.4
@@ -861,7 +867,10 @@ cudaError_t launch_rows(const DecodeDiffParams& p_in, const CUtensorMap& tm_k,
       const int per = (p.dec.S_max + c - 1) / c;
       p.dec.chunk = (per + kTile - 1) / kTile * kTile;
       if constexpr (D < 128)  // (d = 128 takes the tensor-core tile, decode_tc.cu)
-        if (rows > 16) return launch<D, 2, true, kDeep, PAGED, true>(p, tm_k, tm_v, stream);
+        if (rows > 16)
+          return c == kMaxCluster && 2 * c * groups > sms
+                     ? launch<D, 2, true, kPair, PAGED, true>(p, tm_k, tm_v, stream)
+                     : launch<D, 2, true, kDeep, PAGED, true>(p, tm_k, tm_v, stream);
       if (rows > 8) return launch<D, 1, true, kShallow, PAGED, true>(p, tm_k, tm_v, stream);
       return launch<D, 1, false, kShallow, PAGED, true>(p, tm_k, tm_v, stream);
     }
@@ -877,7 +886,9 @@ cudaError_t launch_rows(const DecodeDiffParams& p_in, const CUtensorMap& tm_k,
   // A grid of at most one CTA per SM takes a deeper ring in the room of a second CTA.
   const bool one = p.dec.n_split * groups <= sms;
   if constexpr (D < 128)
-    if (rows > 16) return launch<D, 2, true, kDeep, PAGED>(p, tm_k, tm_v, stream);
+    if (rows > 16)
+      return groups > sms ? launch<D, 2, true, kPair, PAGED>(p, tm_k, tm_v, stream)
+                          : launch<D, 2, true, kDeep, PAGED>(p, tm_k, tm_v, stream);
   if (rows > 16) return cudaErrorInvalidValue;
   if (rows > 8)
     return one ? launch<D, 1, true, kDeep, PAGED>(p, tm_k, tm_v, stream)
