@@ -724,12 +724,20 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
   if (pieces > 0 && S_max > 1024) return 2 * ((pieces + B - 1) / B);
   if (S_max <= 1024 || (S_max <= 2048 && rows <= 32 && groups * 8 <= sms)) return 1;
   // One sequence: a CTA to an SM, or somewhat fewer, a multiple of eight (8 KV heads of 128 in 16
-  // splits / 19: 4K tokens 6.2 us / 6.8, 8K 8.3 / 9.4, 32K 22.5-23.1 / 23.1-23.4; 4 of 64 in 32 / 38:
-  // 4K 4.3 / 5.4, 32K 9.4 / 10.3, 64K 16.0 / 15.9).  Several: two (one and a half of more than
-  // 16 rows, which have an SM to themselves), since sequences are seldom equally long and
-  // two fill it better: 2 x 4K-30K tokens, 8 KV heads of 128, 35 us in 9 splits, 28 in 18 (all of
-  // 30K 39 and 39); 8 x 8K, 4 of 64, 21.7 in four, 13.9 in eight.  Splits of 128 to 8192 tokens.
-  long long n = B == 1 ? sms / groups : (rows <= 16 ? 4 : 3) * sms / (2 * groups);
+  // splits / 19: 4K tokens 6.2 us / 6.8, 8K 8.3 / 9.4, 32K 22.5-23.1 / 23.1-23.4; 4 of 64 in
+  // 32 / 38: 4K 4.3 / 5.4, 32K 9.4 / 10.3, 64K 16.0 / 15.9).  Small heads do not fill HBM with
+  // a CTA to an SM: two, unless that takes more than 32 splits, which the merge folds in two
+  // rounds (8 heads in 16 / 32: of 64, 8K 6.6 / 5.9, 64K 28.9 / 22.2; of 32, 64K 24.1 /
+  // 16.9).  Several: two (one and a half of more than 16 rows of 64, which have an
+  // SM to themselves; three of up to 16 of d = 32), since sequences are seldom equally long
+  // and two fill it better: 2 x 4K-30K tokens, 8 KV heads of 128, 35 us in 9 splits, 28 in 18 (all of 30K 39
+  // and 39); 8 x 8K, 4 of 64, 21.7 in four, 13.9 in eight; 32 x 0.5K-2.5K, 5 of 32, 14.4 in
+  // one, 12.5 in two; 26 x 5K-9K, one of 32, 42 rows, 28.6 in two, 19.2 in five.  Splits of 128 to 8192 tokens.
+  long long n = sms / groups;
+  if (B > 1)
+    n = (rows > 16 ? (d == 32 ? 4 : 3) : d == 32 && S_max >= 1536 ? 6 : 4) * sms / (2 * groups);
+  else if (rows <= 16 && d < 128)
+    n = std::max(n, std::min(32LL, 2 * sms / groups));
   if (B == 1 && n >= 16) n -= n % 8;
   n = std::min(n, ((long long)S_max + 127) / 128);
   return (int)std::max({1LL, n, ((long long)S_max + 8191) / 8192});

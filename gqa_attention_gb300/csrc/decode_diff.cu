@@ -63,9 +63,10 @@ __device__ __forceinline__ float4 diff_row(const DiffParams& p, float4 a, float4
 // 13.9 -> 15.5.  Two row groups: 96 registers for a second CTA slow each down, too (5 sequences
 // of up to 5K, 30 rows, d = 64: 10.5 -> 12.7 us), but pay where there are more KV heads and
 // sequences than SMs (60 x 1K, 5 KV heads, 64 rows: 52 -> 37; 40 x 2.5K, 5 of 32, 24 rows
-// 27.0 -> 20.7; 10 x 2.5K, 6 of 64, 64 rows 21 and 29), and for clusters of eight
-// that would otherwise want nearly every SM, of which the GPU's parts hold few whole ones
-// (4 x 900, 4 KV heads, 24 rows: 11.0 -> 7.7).)
+// 27.0 -> 20.7; 10 x 2.5K, 6 of 64, 64 rows 21 and 29), for d = 32, which loses little,
+// where splits do (26 x 5K-9K, one KV head, 42 rows, in five: 25.8 -> 19.2), and for
+// clusters of eight that would otherwise want nearly every SM, of which the GPU's parts
+// hold few whole ones (4 x 900, 4 KV heads, 24 rows: 11.0 -> 7.7).)
 template <int D>
 struct Ring {
   static constexpr int kDeep = 6;
@@ -887,8 +888,9 @@ cudaError_t launch_rows(const DecodeDiffParams& p_in, const CUtensorMap& tm_k,
   const bool one = p.dec.n_split * groups <= sms;
   if constexpr (D < 128)
     if (rows > 16)
-      return groups > sms ? launch<D, 2, true, kPair, PAGED>(p, tm_k, tm_v, stream)
-                          : launch<D, 2, true, kDeep, PAGED>(p, tm_k, tm_v, stream);
+      return (D == 32 ? p.dec.n_split : 1) * groups > sms
+                 ? launch<D, 2, true, kPair, PAGED>(p, tm_k, tm_v, stream)
+                 : launch<D, 2, true, kDeep, PAGED>(p, tm_k, tm_v, stream);
   if (rows > 16) return cudaErrorInvalidValue;
   if (rows > 8)
     return one ? launch<D, 1, true, kDeep, PAGED>(p, tm_k, tm_v, stream)

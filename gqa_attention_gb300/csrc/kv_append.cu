@@ -470,7 +470,7 @@ cudaError_t launch(const KvAppendParams& p, int sms, int width, cudaStream_t str
   constexpr bool FP8 = HOLD > 0;
   // Tokens to a CTA: enough CTAs for four on every SM, then as many tokens as share the
   // set-up, but of few rows (half of a round to a token or less) no more than one round
-  // takes.  Few tokens: their rows are divided among CTAs.  E4M3: one wave of the two or
+  // takes.  Few tokens: their rows are divided among CTAs.  E4M3: whole waves of the two or
   // three CTAs that an SM holds; the same CTA turns the queries and then takes the keys and
   // values, whose copies travel meanwhile, and only where CTAs are few do those go to CTAs of
   // their own (32 / 8 heads of 128: 1000 tokens 5.1 us, 13.3 with four CTAs to an SM and the
@@ -479,7 +479,8 @@ cudaError_t launch(const KvAppendParams& p, int sms, int width, cudaStream_t str
   const int rows = (p.q ? p.H_q : 0) + (FP8 ? 0 : 2 * p.H_kv);
   const int pieces = rows * (D / 16);  // of a token in the list
   const long long ctas = (HOLD == 0 ? 4 : HOLD == 1 ? 3 : 2) * (long long)sms;
-  long long tok_per = FP8 ? (tokens + ctas - 1) / ctas : tokens / ctas;
+  const long long slots = ctas * ((tokens + ctas * kMaxTok - 1) / (ctas * kMaxTok));  // of whole waves
+  long long tok_per = FP8 ? (tokens + slots - 1) / slots : tokens / ctas;
   if (!FP8 && pieces <= kUnroll * kThreads / 2)
     tok_per = std::min(tok_per, (long long)kUnroll * kThreads / pieces);
   tok_per = std::max(1LL, std::min(tok_per, (long long)kMaxTok));
