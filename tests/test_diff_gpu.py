@@ -113,6 +113,40 @@ def test_decode(d, split, page, T, H, Hk, norm):
         c.compare(out, lse, want, n_split)
 
 
+@pytest.mark.parametrize("d,split", [(32, False), (64, True), (64, False)])
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("T", [3, 8])
+def test_decode_of_more_heads_and_sequences_than_sms(d, split, page, T):
+    lens = [700, T] + [T + 37 * i % 211 for i in range(38)]
+    c = Case(lens, T, 20, 5, d, split, page, norm=T == 3, lam="token", seed=d + T)
+    want = c.expect()
+    for n_split in (1, 2, 5, None):
+        c.compare(*c.decode(n_split=n_split), want, n_split)
+
+
+@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("page", [0, 16])
+def test_decode_of_clusters_on_nearly_every_sm(d, page):
+    c = Case([900, 3, 500, 65], 3, 16, 4, d, False, page, norm=True, lam="token", seed=d)
+    want = c.expect()
+    a, b = c.decode(n_split=1), c.decode(n_split=1)
+    c.compare(*a, want)
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("d,split,S,window", [(64, False, 1030, -1), (128, True, 900, -1),
+                                              (32, False, 1500, 900)])
+def test_prompts_of_few_heads_in_the_default_parts(d, split, S, window):
+    c = Case([S], S, 2, 1, d, split, norm=True, lam="token", seed=S)
+    assert g.gqa_attn_prefill_diff_default_parts(1, S, S, 2, 1, window) > 1
+    want = c.expect(window)
+    o, l, tol, tol_l = want
+    want = (o, l.transpose(0, 2, 1), tol, tol_l.transpose(0, 2, 1))
+    c.compare(*c.prefill(window=window), want)
+    if window < 0:
+        c.compare(*c.prefill(seq_lens=None), want)
+
+
 @pytest.mark.parametrize("split", [False, True])
 @pytest.mark.parametrize("page,T,H,Hk", [(0, 2, 16, 2), (64, 4, 8, 1), (16, 5, 4, 1), (0, 3, 8, 1)])
 def test_decode_of_a_batch_cut_by_its_lengths(split, page, T, H, Hk):
