@@ -95,8 +95,8 @@ def _recorded_traffic(profile_name, files):
         return None
 
 
-DECODE_SOURCES = ["decode.cu", "common.cuh", "internal.h"]
-PREFILL_SOURCES = ["prefill.cu", "tcgen05.cuh", "common.cuh", "internal.h"]
+DECODE_SOURCES = ["decode.cu", "decode_common.cuh", "common.cuh", "internal.h"]
+PREFILL_SOURCES = ["prefill.cu", "diff.h", "tcgen05.cuh", "common.cuh", "internal.h"]
 
 
 def cpu_model():
