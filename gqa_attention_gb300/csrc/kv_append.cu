@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
         a[u] = *reinterpret_cast<const uint4*>(src + sl.off0);
         c[u] = *reinterpret_cast<const uint4*>(src + sl.off1);
       } else if (k < n_tok) {
-        kk[u] = kMaxTok;  // not a row to write
+        kk[u] = kMaxTok + 1;  // not a row to write, nor (n_tok) the list's end
       }
       r += step;
     }

@@ -183,6 +183,16 @@ def test_many_e4m3_tokens_and_one_that_is_not_finite(Hq, Hk, d, T):
         assert s.vs[where[i]].item() == ref.block_scale(rest)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hq,Hk,d", [(64, 8, 128), (120, 6, 64), (6, 2, 64)])
+def test_padding_in_front_of_a_sequence_in_a_large_batch(Hq, Hk, d, fp8):
+    # (enough tokens that a CTA takes several: padding, then the next sequence's first)
+    s = Step(8, 1300, Hq, Hk, d, d, fp8=fp8, counts=[3, 40, 0, 17, 1300, 1, 1299, 20], S=1400,
+             lens=[5, 40, 9, 1000, 1300, 1, 1299, 33])
+    s.run()
+    s.check()
+
+
 def test_far_and_negative_positions():
     pos = torch.tensor([[0, 131071, 131072, 1 << 20, (1 << 24) + 1, (1 << 28) - 1, -1, -70000]],
                        dtype=torch.int32)
