@@ -683,6 +683,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
           // first warpgroup's).  The first map's O is ready half a tile before the second's
           // and waits in registers.
           const DiffParams& df = pp.diff;
+          // (The other warpgroup has read what the last item left there once it has handed
+          // back O.  With two tiles or more this item's own P V has waited for that.)
+          if (!wait_all(&o_empty[x], xc_ph ^ 1)) break;
           row_inv[x][r] = inv;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&inv_ready[x][quarter]));

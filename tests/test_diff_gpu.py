@@ -134,6 +134,18 @@ def test_decode_of_clusters_on_nearly_every_sm(d, page):
     assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("d,split", [(32, False), (64, True), (128, False)])
+def test_many_prompts_of_one_tile(d, split):
+    # (a CTA takes one item of one tile after another: ten rounds)
+    c = Case([100 - b % 7 for b in range(48)], 40, 32, 8, d, split, norm=True, lam="token", seed=d)
+    a = c.prefill()
+    o, l, tol, tol_l = c.expect()
+    c.compare(*a, (o, l.transpose(0, 2, 1), tol, tol_l.transpose(0, 2, 1)))
+    for _ in range(20):
+        b = c.prefill()
+        assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("d,split,S,window", [(64, False, 1030, -1), (128, True, 900, -1),
                                               (32, False, 1500, 900)])
 def test_prompts_of_few_heads_in_the_default_parts(d, split, S, window):
