@@ -719,7 +719,8 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
   // to 2048 if it leaves room for eight CTAs (8 KV heads of 128, 2K tokens: 6.6 us, 5.6 in 16
   // splits, but a second launch takes the host 2.5 us).
   const long long sms = num_sms_current_device();
-  const long long groups = (long long)B * H_kv * (rows <= 16 ? 1 : (rows + 31) / 32);
+  const long long groups =
+      std::min((long long)B * H_kv, 1LL << 40) * (rows <= 16 ? 1 : (rows + 31) / 32);
   const int pieces = diff_pieces(B, H_kv, rows, S_max);
   if (pieces > 0 && S_max > 1024) return 2 * ((pieces + B - 1) / B);
   if (S_max <= 1024 || (S_max <= 2048 && rows <= 32 && groups * 8 <= sms)) return 1;
@@ -1390,7 +1391,8 @@ int gqa_attn_prefill_diff_default_parts(int B, int T_q, int S_max, int H, int H_
   // prompt of 4K, 4 maps, 53 and 43), nor do more than fill the SMs (512 queries at 2K, 16
   // maps: 31.6 in one, 21.6 in four, 28.8 in six).
   const long long keys = window < 0 ? S_max : std::min<long long>(S_max, (long long)window + 128);
-  const long long tiles = keys / 128, items = ((long long)T_q + 127) / 128 * B * H;
+  const long long tiles = keys / 128;
+  const long long items = std::min(((long long)T_q + 127) / 128 * B, 1LL << 40) * H;
   const long long n = std::min({8LL, num_sms_current_device() / items, tiles / 2});
   return n < 2 || tiles < (n == 2 ? 16 : 6) ? 1 : (int)n;
 }

@@ -157,6 +157,20 @@ def test_default_parts():
         assert g.gqa_attn_prefill_diff_default_parts(*bad) == 1
 
 
+def test_defaults_of_the_largest_arguments():
+    M = 2 ** 31 - 1
+    for T in (1, 8, M):
+        for S in (1, 1 << 20, M):
+            for d in (32, 64, 128):
+                for B, H, Hk in ((M, M, M), (1, M, M), (M, 1, 1), (1, M, 1), (1 << 30, 1 << 30, 1 << 30),
+                                 (1 << 20, 1 << 22, 1 << 22), (1, 1, 1)):
+                    n = g.gqa_attn_decode_diff_default_splits(B, T, H, Hk, S, d)
+                    assert 1 <= n <= max(2 * 152, -(-S // 128))
+                    for w in (-M - 1, -1, 0, M):
+                        assert 1 <= g.gqa_attn_prefill_diff_default_parts(B, T, S, H, Hk, w) <= 8
+    assert g.gqa_attn_prefill_diff_default_parts(M, M, M, 32767, 1, -1) == 1
+
+
 def test_helpers_refuse_cpu_tensors():
     k = torch.zeros(1, 8, 2, 64, dtype=torch.bfloat16)
     lens, lam = torch.ones(1, dtype=torch.int32), torch.ones(1)
