@@ -137,7 +137,7 @@ def test_decode_of_clusters_on_nearly_every_sm(d, page):
 @pytest.mark.parametrize("d,split", [(32, False), (64, True), (128, False)])
 def test_many_prompts_of_one_tile(d, split):
     # (a CTA takes one item of one tile after another: ten rounds)
-    c = Case([100 - b % 7 for b in range(48)], 40, 32, 8, d, split, norm=True, lam="token", seed=d)
+    c = Case([100 - b % 7 for b in range(80)], 40, 32, 8, d, split, norm=True, lam="token", seed=d)
     a = c.prefill()
     o, l, tol, tol_l = c.expect()
     c.compare(*a, (o, l.transpose(0, 2, 1), tol, tol_l.transpose(0, 2, 1)))
