@@ -468,22 +468,30 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
 template <int D, int HOLD>
 cudaError_t launch(const KvAppendParams& p, int sms, int width, cudaStream_t stream) {
   constexpr bool FP8 = HOLD > 0;
-  // Tokens to a CTA: enough CTAs for four on every SM, then as many tokens as share the
-  // set-up, but of few rows (half of a round to a token or less) no more than one round
-  // takes.  Few tokens: their rows are divided among CTAs.  E4M3: whole waves of the two or
-  // three CTAs that an SM holds; the same CTA turns the queries and then takes the keys and
-  // values, whose copies travel meanwhile, and only where CTAs are few do those go to CTAs of
-  // their own (32 / 8 heads of 128: 1000 tokens 5.1 us, 13.3 with four CTAs to an SM and the
-  // keys and values always apart; 32K 120 and 130, 95% of the copy rate with 64 query heads).
+  // Tokens to a CTA.  bf16: of few rows (half of a round to a token or less) as many as leave
+  // one wave of four CTAs to an SM, but no more than one round takes (20 / 5 heads of 64:
+  // 1000 tokens 3.2 us, 4.3 with a second wave of 392 CTAs; 4096 6.3 and 7.7); of many rows
+  // at least four CTAs to an SM, then as many tokens as share the set-up.  E4M3: whole
+  // waves of the two or three CTAs that an SM holds; the same CTA turns the queries and
+  // then takes the keys and values, whose copies travel meanwhile, and only where CTAs are
+  // few do those go to CTAs of their own (32 / 8 heads of 128: 1000 tokens 5.1 us, 13.3 with
+  // four CTAs to an SM and the keys and values always apart; 32K 120 and 130, 95% of the copy
+  // rate with 64 query heads).  Few tokens: their rows are divided among CTAs.
   const long long tokens = (long long)p.B * p.T;
   const int rows = (p.q ? p.H_q : 0) + (FP8 ? 0 : 2 * p.H_kv);
   const int pieces = rows * (D / 16);  // of a token in the list
-  const long long ctas = (HOLD == 0 ? 4 : HOLD == 1 ? 3 : 2) * (long long)sms;
-  const long long slots = ctas * ((tokens + ctas * kMaxTok - 1) / (ctas * kMaxTok));  // of whole waves
-  long long tok_per = FP8 ? (tokens + slots - 1) / slots : tokens / ctas;
-  if (!FP8 && pieces <= kUnroll * kThreads / 2)
-    tok_per = std::min(tok_per, (long long)kUnroll * kThreads / pieces);
-  tok_per = std::max(1LL, std::min(tok_per, (long long)kMaxTok));
+  const bool light = !FP8 && pieces <= kUnroll * kThreads / 2;
+  const long long ctas = (!FP8 ? 4 : HOLD == 1 ? 3 : 2) * (long long)sms;
+  long long tok_per;
+  if (FP8) {
+    const long long slots = ctas * ((tokens + ctas * kMaxTok - 1) / (ctas * kMaxTok));
+    tok_per = (tokens + slots - 1) / slots;
+  } else if (light) {
+    tok_per = std::min((tokens + ctas - 1) / ctas, (long long)kUnroll * kThreads / pieces);
+  } else {
+    tok_per = std::max(1LL, tokens / ctas);
+  }
+  tok_per = std::min(tok_per, (long long)kMaxTok);
   const long long x = (tokens + tok_per - 1) / tok_per;
   if (x > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int passes = (pieces + kThreads - 1) / kThreads;
