@@ -709,21 +709,24 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
     if (pieces > 0) return 2 * ((pieces + B - 1) / B);
     // One CTA on an SM: no more than fill them once (4 sequences of 8K, 8 KV heads, 32 rows:
     // 45 us in five splits, 26 in four), from 16 on a multiple of eight (32 rows, 8 KV heads,
-    // in 16 splits / 19: 8K tokens 10.9 / 11.8 us, 32K 23.7 / 24.1), and at least two tiles each.
+    // in 16 splits / 19: 8K tokens 10.9 / 11.8 us, 32K 23.7 / 24.1), and of four tiles or more
+    // no more than one for each (64 rows, 900 tokens in 8 / 4: 9.0 / 10.0; 200 in 2 / 1: 9.5 / 8.8).
     long long fill = num_sms_current_device() / ((long long)B * H_kv);
     if (fill >= 16) fill -= fill % 8;
     const long long tiles = ((long long)S_max + 127) / 128;
-    return (int)std::max(1LL, std::min(fill, (tiles + 1) / 2));
+    return (int)std::max(1LL, std::min(fill, tiles < 4 ? (tiles + 1) / 2 : tiles));
   }
   // Up to 1024 tokens one launch, which is a cluster of CTAs where the grid leaves room, and up
   // to 2048 if it leaves room for eight CTAs (8 KV heads of 128, 2K tokens: 6.6 us, 5.6 in 16
-  // splits, but a second launch takes the host 2.5 us).
+  // splits, but a second launch takes the host 2.5 us).  More than 32 rows are no clusters:
+  // up to 384 (900 tokens, 8 heads of 64, 64 rows: 12.0 us, 6.6 in eight splits).
   const long long sms = num_sms_current_device();
   const long long groups =
       std::min((long long)B * H_kv, 1LL << 40) * (rows <= 16 ? 1 : (rows + 31) / 32);
   const int pieces = diff_pieces(B, H_kv, rows, S_max);
   if (pieces > 0 && S_max > 1024) return 2 * ((pieces + B - 1) / B);
-  if (S_max <= 1024 || (S_max <= 2048 && rows <= 32 && groups * 8 <= sms)) return 1;
+  if (S_max <= (rows > 32 ? 384 : 1024) || (S_max <= 2048 && rows <= 32 && groups * 8 <= sms))
+    return 1;
   // One sequence: a CTA to an SM, or somewhat fewer, a multiple of eight (8 KV heads of 128 in 16
   // splits / 19: 4K tokens 6.2 us / 6.8, 8K 8.3 / 9.4, 32K 22.5-23.1 / 23.1-23.4; 4 of 64 in
   // 32 / 38: 4K 4.3 / 5.4, 32K 9.4 / 10.3, 64K 16.0 / 15.9).  Small heads do not fill HBM with
@@ -731,13 +734,15 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
   // rounds (8 heads in 16 / 32: of 64, 8K 6.6 / 5.9, 64K 28.9 / 22.2; of 32, 64K 24.1 /
   // 16.9).  Several: two (one and a half of more than 16 rows of 64, which have an
   // SM to themselves; three of up to 16 of d = 32), since sequences are seldom equally long
-  // and two fill it better: 2 x 4K-30K tokens, 8 KV heads of 128, 35 us in 9 splits, 28 in 18 (all of 30K 39
-  // and 39); 8 x 8K, 4 of 64, 21.7 in four, 13.9 in eight; 32 x 0.5K-2.5K, 5 of 32, 14.4 in
-  // one, 12.5 in two; 26 x 5K-9K, one of 32, 42 rows, 28.6 in two, 19.2 in five.  Splits of 128 to 8192 tokens.
+  // and two fill it better: 2 x 4K-30K tokens, 8 KV heads of 128, 35 us in 9 splits, 28 in 18
+  // (all of 30K 39 and 39); 8 x 8K, 4 of 64, 21.7 in four, 13.9 in eight; 32 x 0.5K-2.5K, 5 of
+  // 32, 14.4 in one, 12.5 in two; 26 x 5K-9K, one of 32, 42 rows, 28.6 in two, 19.2 in five.
+  // (Short ones, up to 1024 tokens of more than 32 rows: a CTA to an SM.)  Splits of 128 to
+  // 8192 tokens.
   long long n = sms / groups;
-  if (B > 1)
+  if (B > 1 && S_max > 1024)
     n = (rows > 16 ? (d == 32 ? 4 : 3) : d == 32 && S_max >= 1536 ? 6 : 4) * sms / (2 * groups);
-  else if (rows <= 16 && d < 128)
+  else if (B == 1 && rows <= 16 && d < 128)
     n = std::max(n, std::min(32LL, 2 * sms / groups));
   if (B == 1 && n >= 16) n -= n % 8;
   n = std::min(n, ((long long)S_max + 127) / 128);
