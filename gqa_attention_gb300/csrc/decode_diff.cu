@@ -173,8 +173,8 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
     int L_hint;
     asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(L_hint) : "l"(p.seq_lens + b));
     const int i = lane / subs, sub = lane % subs;
-    const int tk = split * chunk + i * kTile + sub * box;
-    if (i < p.prefetch_tiles && tk < min(min(p.S_max, L_hint), split * chunk + chunk)) {
+    const int ahead = i * kTile + sub * box, tk = split * chunk + ahead;
+    if (i < p.prefetch_tiles && ahead < chunk && tk < min(p.S_max, L_hint)) {
       int row = b * p.S_max + tk;
       bool ok = true;
       if constexpr (PAGED) {

@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int i = lane / nb, sub = lane % nb;
     int L_hint;
     asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(L_hint) : "l"(p.seq_lens + b));
-    const int tk = split * chunk + i * kTcKeys + sub * h;
-    if (i < p.prefetch_tiles && tk < min(min(p.S_max, L_hint), split * chunk + chunk)) {
+    const int ahead = i * kTcKeys + sub * h, tk = split * chunk + ahead;
+    if (i < p.prefetch_tiles && ahead < chunk && tk < min(p.S_max, L_hint)) {
       int row = b * p.S_max + tk;
       bool ok = true;
       if constexpr (PAGED) {
@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int L = p.seq_lens[b];
   const bool bad = L < p.T_q || L > p.S_max;  // (L >= T_q >= 1 otherwise)
   const int t0 = split * chunk;
-  const int t_end = bad || none ? 0 : min(t0 + chunk, L);
+  // (t0 + chunk may pass 2^31 for a sequence's last piece)
+  const int t_end = bad || none ? 0 : t0 + min(chunk, L - t0);
   const int n = t_end > t0 ? (t_end - t0 + kTcKeys - 1) / kTcKeys : 0;
   __syncthreads();
   tc_fence_after();

@@ -1,0 +1,46 @@
+"""Differential attention on the GPU at the limits of its arguments: the longest sequences, key rows
+that are not finite, default splits of large batches."""
+import pytest
+import torch
+
+import diff_ref as ref
+import gqa_attention_gb300 as g
+from test_diff_gpu import Case
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from gqa_attention_gb300 import build
+
+    build.build()
+    g.load()
+    yield
+    assert g.gqa_last_device_error() == g.GQA_OK
+
+
+def test_cut_batch_of_the_longest_sequences():
+    """Two sequences of up to 2^31 - 2^16 tokens in pages of 65536, all but the last of each the
+    same page: its keys are far from every query, and only the last 130 tokens have a weight.  The
+    last piece of the longer one ends past 2^31, were it a whole one."""
+    page, H, T, d, n = 65536, 8, 2, 128, 130
+    lens = [0x7fff0000, 0x60000000]
+    c = Case([n, n], T, H, 1, d, lam="token", seed=1)
+    c.q[..., 0] = c.q[..., 0].abs() + 1
+    k = torch.zeros(3, page, 1, d, dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros_like(k)
+    k[..., 0] = -30000.0  # (a score below -2600: its weight is 0 in fp32)
+    for b in range(2):
+        k[1 + b, -n:], v[1 + b, -n:] = c.k[b], c.v[b]
+    table = torch.zeros(2, lens[0] // page, dtype=torch.int32, device=DEV)
+    for b, L in enumerate(lens):
+        table[b, L // page - 1] = 1 + b
+    want = c.expect()
+    for n_split in (None, 152):
+        out, lse = g.decode_diff(c.q.to(DEV), k, v, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                 c.lam.to(DEV), block_table=table, n_split=n_split)
+        c.compare(out, lse, want, n_split)
