@@ -377,6 +377,30 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
       mma_bf16_16816(sacc[0], qa[kk], b00, b01);
       mma_bf16_16816(sacc[1], qa[kk], b10, b11);
     }
+    if (pp.diff.split_keys) {
+      // A key's half that is not finite makes NaN of the other map's zeros: then the product of
+      // each half for itself, of which a row takes its own.  (20 sequences of 1K to 2.5K, 6 KV
+      // heads of 64, 64 rows: 31.8 us without the check, 32.9 with it, 34.9 with the two products
+      // always, which took 33.3 to 35.7 with shared keys, too.)
+      const float sum = ((sacc[0][0] + sacc[0][1]) + (sacc[0][2] + sacc[0][3])) +
+                        ((sacc[1][0] + sacc[1][1]) + (sacc[1][2] + sacc[1][3]));
+      if (__any_sync(0xffffffffu, isnan(sum))) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int kk = half * (D / 32); kk < (half + 1) * (D / 32); ++kk) {
+            uint32_t b00, b01, b10, b11;
+            ldsm_x4(kbase + Lay::offset(k_row, kk * 2 + k_chk), b00, b01, b10, b11);
+            mma_bf16_16816(x[0], qa[kk], b00, b01);
+            mma_bf16_16816(x[1], qa[kk], b10, b11);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((g & 1) == half) sacc[e / 4][e % 4] = x[e / 4][e % 4];
+        }
+      }
+    }
     const bool partial = tok0 + 16 > lim_lo;
     float x0[4], x1[4];  // rows g and g + 8, tokens tok0 + 8 nt + 2 t + c
 #pragma unroll

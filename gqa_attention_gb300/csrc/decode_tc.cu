@@ -44,8 +44,9 @@
 // Differential attention (DIFF; decode_diff.cu says what it is): the rows are the maps of
 // the heads, two neighbours each.  With several splits only the merge differs; with one
 // the two lanes of a head exchange halves of their columns in the epilogue.  DIFF = 2, split
-// keys: both half-tiles of Q get all half rows from TMA, and the softmax warps then zero
-// the rows that are the other map's.  Batches of several sequences are cut by their
+// keys: the tile of Q is 64 wide, row r being its map's half of a query row, and S takes the
+// products with the first half of the keys into the even lanes and with the second half
+// into the odd ones.  Batches of several sequences are cut by their
 // lengths (decode_cut.cuh), and a row of V among the last T_q tokens that holds an
 // infinity or NaN reaches the queries that see it and no others.  4 sequences of 2K to 16K, 4
 // tokens of 8 maps each, 8 KV heads, pages of 64: 27 us with the merge, 4.9 TB/s.
@@ -80,6 +81,19 @@ __host__ __device__ __forceinline__ const DecodeParams& base_params(const Decode
 __host__ __device__ __forceinline__ const DecodeParams& base_params(const DecodeDiffParams& p) {
   return p.dec;
 }
+// D[tmem] (+)= A[smem] * B[smem] as tc_mma_ss, without the lanes of D whose bit in `skip` is set,
+// the same 32 bits for each 32 lanes: what those hold stays.
+__device__ __forceinline__ void tc_mma_ss_lanes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate, uint32_t skip) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(skip)
+      : "memory");
+}
+
 template <int DIFF>
 using TcParamsOf = std::conditional_t<DIFF != 0, DecodeDiffParams, DecodeParams>;
 
@@ -99,9 +113,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ int bad_page;
-  // differential: Q's zeros are in place; per column of V, the first of the last T_q tokens
-  // that holds an infinity or NaN there
-  __shared__ __align__(8) uint64_t q_ready;
+  // differential: per column of V, the first of the last T_q tokens that holds an infinity or
+  // NaN there
   __shared__ int odd_from[DIFF ? 128 : 1], odd_seen;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -146,10 +159,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(smem_u32(&p_ready[x]), 4);
     }
     mbar_init(smem_u32(&pv_done), 1);
-    if (DIFF) {
-      mbar_init(smem_u32(&q_ready), 4);
-      odd_seen = 0;
-    }
+    if (DIFF) odd_seen = 0;
     abort_flag = 0;
     bad_page = 0;
     fence_barrier_init();
@@ -308,11 +318,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tma_prefetch_map(&tm_q);
       tma_prefetch_map(&tm_k);
       tma_prefetch_map(&tm_v);
-      mbar_arrive_expect_tx(qb, static_cast<uint32_t>(rows) * 256u);
-      for (int dh = 0; dh < 2; ++dh) {
-        if constexpr (DIFF == 2)  // all half rows, in the order of the maps, to both half-tiles
-          tma_load_4d(sb + kOffQ + dh * kHalfB, &tm_q, qb, 0, 0, kv * (G / 2), b * p.T_q);
-        else
+      mbar_arrive_expect_tx(qb, static_cast<uint32_t>(rows) * (DIFF == 2 ? 128u : 256u));
+      if constexpr (DIFF == 2) {  // all half rows, in the order of the maps
+        tma_load_4d(sb + kOffQ, &tm_q, qb, 0, 0, kv * (G / 2), b * p.T_q);
+      } else {
+        for (int dh = 0; dh < 2; ++dh)
           tma_load_3d(sb + kOffQ + dh * kHalfB, &tm_q, qb, dh * 64, kv * G, b * p.T_q);
       }
     }
@@ -407,8 +417,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const uint32_t off = (kk >> 2) * kHalfB + (kk & 3) * 32;
-        tc_mma_ss(tmem + 128 * x, smem_desc_sw128(sb + kOffQ + off, 16, 1024),
-                  smem_desc_sw128(kb + off, 16, 1024), idS, kk > 0);
+        if constexpr (DIFF == 2)
+          tc_mma_ss_lanes(tmem + 128 * x, smem_desc_sw128(sb + kOffQ + (kk & 3) * 32, 16, 1024),
+                          smem_desc_sw128(kb + off, 16, 1024), idS, (kk & 3) > 0,
+                          kk < 4 ? 0xaaaaaaaau : 0x55555555u);
+        else
+          tc_mma_ss(tmem + 128 * x, smem_desc_sw128(sb + kOffQ + off, 16, 1024),
+                    smem_desc_sw128(kb + off, 16, 1024), idS, kk > 0);
       }
     };
     auto issue_pv = [&](int x, int slot, bool acc) {  // O (+)= P_x V, P_x in tensor memory
@@ -429,8 +444,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc_commit(smem_u32(&v_empty[j % kTcSlots]));
       return true;
     };
-    bool ok = wait_all(DIFF == 2 ? &q_ready : &q_full, 0);
-    if (DIFF == 2) tc_fence_after();
+    bool ok = wait_all(&q_full, 0);
     // Tensor-pipe order S_0, S_1, P_0 V_0, S_2, P_1 V_1, ...: S_{j+1} runs while
     // the softmax works on S_j.  S_j overwrites P_{j-2}, whose P V was issued
     // before it (the MMAs of one thread execute in issue order).
@@ -466,18 +480,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int lim_lo = min(t_end, L - p.T_q + 1);
     float m_ref = -INFINITY, l = 0.f;
     bool alive = true;
-    if constexpr (DIFF == 2) {  // row r is map r & 1: zero in the other half's columns
-      alive = wait_all(&q_full, 0);
-      if (alive) {
-        const uint32_t at = sb + kOffQ + ((r & 1) ? 0u : kHalfB) + r * 128;
-#pragma unroll
-        for (int c16 = 0; c16 < 8; ++c16) st_shared_v4(at + c16 * 16, 0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&q_ready));
-      }
-    }
-    for (int j = 0; alive && j < n; ++j) {
+    for (int j = 0; j < n; ++j) {
       const int x = j & 1;
       const uint32_t tS = tmem + lane_base + 128 * x;
       if (!wait_all(&s_full[x], (j >> 1) & 1)) {

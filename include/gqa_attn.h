@@ -675,7 +675,7 @@ gqa_status gqa_kv_append_paged_fp8(const void* q, const void* k_new, const void*
  * their lengths, into at most n_split splits of a sequence (a sequence's splits, and so
  * the rounding of its outputs, then depend on the other lengths too).  A row of V that a
  * query does not see never reaches it, whatever it holds (one that it sees: an infinity may
- * come out as NaN); with split keys, infinities and NaN of a key row count for both maps.
+ * come out as NaN); with split keys a map sees its own half of a key row alone.
  * Deterministic. */
 gqa_status gqa_attn_decode_diff(const void* q, const void* k_cache, const void* v_cache,
                                 const int32_t* seq_lens, const float* lam, int64_t lam_stride_b,

@@ -44,3 +44,40 @@ def test_cut_batch_of_the_longest_sequences():
         out, lse = g.decode_diff(c.q.to(DEV), k, v, torch.tensor(lens, dtype=torch.int32, device=DEV),
                                  c.lam.to(DEV), block_table=table, n_split=n_split)
         c.compare(out, lse, want, n_split)
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("T,H,Hk,d,n_split", [
+    (1, 3, 3, 64, 1), (1, 8, 2, 128, 2), (2, 8, 1, 128, 1), (3, 5, 1, 32, 3), (8, 4, 1, 64, 1),
+    (8, 8, 2, 128, 2), (5, 3, 1, 128, 1),
+])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_split_keys_see_their_own_half_of_a_key(T, H, Hk, d, n_split, prefill):
+    """NaN or an infinity in one half of a key row reaches that half's map alone; where its score
+    is minus infinity, it is as a key of no weight."""
+    half = d // 2
+    for u in (0, 1):
+        c = Case([70, 200], T, H, Hk, d, True, S=200, seed=d + T + u)
+        at = u * half + 3
+        c.q[..., at] = -1.0 - c.q[..., at].abs()
+        run = (lambda: c.prefill(n_part=n_split)) if prefill else (lambda: c.decode(n_split=n_split))
+
+        def maps(x):  # lse, [B, T, H, map]
+            x = x.transpose(1, 2) if prefill else x
+            return x.reshape(2, T, H, 2)
+
+        c.k[:, 5, :, at] = 1e5  # a score below -3000 in map u: its weight is 0 in fp32
+        out, lse = run()
+        assert torch.isfinite(out.float()).all()
+        c.k[:, 5, :, at] = float("inf")
+        far, far_lse = run()
+        assert same(far, out) and torch.equal(far_lse, lse)
+        c.k[:, 5, :, u * half:(u + 1) * half] = float("nan")
+        bad, bad_lse = run()
+        assert bad.isnan().all() and maps(bad_lse)[..., u].isnan().all()
+        assert torch.equal(maps(bad_lse)[..., 1 - u], maps(lse)[..., 1 - u])
+        torch.cuda.synchronize()
+        assert g.gqa_last_device_error() == g.GQA_OK
