@@ -108,6 +108,8 @@ bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 // tile (used above 16 rows).
 constexpr int kMaxMultiRows = 64;
 constexpr int kMaxMultiRowsTc = 128;
+// Splits of a sequence in differential decode, at most.
+constexpr int kMaxDiffSplits = 65535;
 // Token rows of a cache, at most, where a last tile may reach past them in 32 bits.
 constexpr long long kMaxCacheRows = 0x7fff0000LL;
 bool multi_uses_tc(int T_q, int G, int d) { return d == 128 && T_q * G > 16; }
@@ -506,7 +508,8 @@ gqa_status run_decode_diff(const void* q, const void* k, const void* v, const in
   // (rows and tokens stay below 2^31 with the last tile's overhang)
   if (rows < 1 || rows > kMaxCacheRows || S_max < 1 || S_max > kMaxCacheRows)
     return GQA_ERR_INVALID_ARG;
-  if (T_q < 1 || T_q > 64 || T_q > S_max || n_split > 65535) return GQA_ERR_INVALID_ARG;
+  if (T_q < 1 || T_q > 64 || T_q > S_max || n_split > kMaxDiffSplits)
+    return GQA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !aligned(lse, 8)) return GQA_ERR_INVALID_ARG;
   if (head_dim_ok(d) && T_q * (2 * H / H_kv) > kMaxMultiRows) return GQA_ERR_UNSUPPORTED;
   // More than 16 rows of d = 128: one tensor-core tile of 128 keys.
@@ -738,7 +741,7 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
   // (all of 30K 39 and 39); 8 x 8K, 4 of 64, 21.7 in four, 13.9 in eight; 32 x 0.5K-2.5K, 5 of
   // 32, 14.4 in one, 12.5 in two; 26 x 5K-9K, one of 32, 42 rows, 28.6 in two, 19.2 in five.
   // (Short ones, up to 1024 tokens of more than 32 rows: a CTA to an SM.)  Splits of 128 to
-  // 8192 tokens.
+  // 8192 tokens, or as many as the call takes.
   long long n = sms / groups;
   if (B > 1 && S_max > 1024)
     n = (rows > 16 ? (d == 32 ? 4 : 3) : d == 32 && S_max >= 1536 ? 6 : 4) * sms / (2 * groups);
@@ -746,7 +749,8 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
     n = std::max(n, std::min(32LL, 2 * sms / groups));
   if (B == 1 && n >= 16) n -= n % 8;
   n = std::min(n, ((long long)S_max + 127) / 128);
-  return (int)std::max({1LL, n, ((long long)S_max + 8191) / 8192});
+  n = std::max({1LL, n, ((long long)S_max + 8191) / 8192});
+  return (int)std::min<long long>(n, kMaxDiffSplits);
 }
 
 gqa_status gqa_attn_decode_diff(const void* q, const void* k_cache, const void* v_cache,

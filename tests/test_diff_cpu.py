@@ -185,6 +185,21 @@ def test_helpers_refuse_cpu_tensors():
         g.decode_diff(None, k, k, lens, lam)
 
 
+def test_default_splits_of_long_sequences_are_taken_by_the_call():
+    # (d = 16, of no kernel, is looked at after the splits)
+    for S in (1 << 29, 536862720, 536862721, 1 << 30, 0x7fff0000):
+        for T, H, d in ((1, 1, 64), (8, 4, 64), (8, 4, 128)):
+            for B in (1, 3, 100):
+                n = g.gqa_attn_decode_diff_default_splits(B, T, H, 1, S, d)
+                assert 1 <= n <= 65535
+                tile = 128 if d == 128 and T * 2 * H > 16 else 64
+                chunk = -(-(-(-S // n)) // tile) * tile
+                assert n * chunk < 2 ** 31
+                if B * S <= 0x7fff0000:
+                    assert _decode(False, B=B, T_q=T, H=H, H_kv=1, S_max=S, d=16, n_split=n,
+                                   ws=FAKE) == UNSUP
+
+
 # -------------------------------------------------------- the 64-bit forms --
 def test_turning_keeps_lengths_and_relative_angles():
     rng = np.random.default_rng(0)

@@ -81,3 +81,18 @@ def test_split_keys_see_their_own_half_of_a_key(T, H, Hk, d, n_split, prefill):
         assert torch.equal(maps(bad_lse)[..., 1 - u], maps(lse)[..., 1 - u])
         torch.cuda.synchronize()
         assert g.gqa_last_device_error() == g.GQA_OK
+
+
+@pytest.mark.parametrize("d,T", [(64, 1), (128, 2)])
+def test_default_splits_of_the_widest_table(d, T):
+    # short sequences behind a table of 2^31 - 2^16 tokens: nearly all of the default splits are empty
+    page, H = 65536, 8
+    c = Case([700], T, H, 1, d, lam="head", seed=d)
+    k = torch.full((2, page, 1, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    v = k.clone()
+    k[1, :700], v[1, :700] = c.k[0], c.v[0]
+    table = torch.full((1, 32767), -1, dtype=torch.int32, device=DEV)
+    table[0, 0] = 1
+    q, lam = c.q.to(DEV), c.lam.to(DEV)
+    out, lse = g.decode_diff(q, k, v, c.dev_lens(), lam, block_table=table)
+    c.compare(out, lse, c.expect())
