@@ -714,10 +714,21 @@ int gqa_attn_decode_diff_default_splits(int B, int T_q, int H, int H_kv, int S_m
     // 45 us in five splits, 26 in four), from 16 on a multiple of eight (32 rows, 8 KV heads,
     // in 16 splits / 19: 8K tokens 10.9 / 11.8 us, 32K 23.7 / 24.1), and of four tiles or more
     // no more than one for each (64 rows, 900 tokens in 8 / 4: 9.0 / 10.0; 200 in 2 / 1: 9.5 / 8.8).
-    long long fill = num_sms_current_device() / ((long long)B * H_kv);
+    const long long sms = num_sms_current_device();
+    long long fill = sms / ((long long)B * H_kv);
     if (fill >= 16) fill -= fill % 8;
     const long long tiles = ((long long)S_max + 127) / 128;
-    return (int)std::max(1LL, std::min(fill, tiles < 4 ? (tiles + 1) / 2 : tiles));
+    long long n = std::min(fill, tiles < 4 ? (tiles + 1) / 2 : tiles);
+    // Several sequences that are not cut, there being too many: splits of up to 8192 tokens, but
+    // no more than eight CTAs to an SM, or one CTA walks through the longest sequence after
+    // the others are done (32 rows, 8 KV heads, in one split / so: 10 sequences of 1K to 64K 595
+    // / 222 us, 16 592 / 390, 24 649 / 527; 10 of 1K to 16K 152 / 81, 16 152 / 94; 20 of 1K to 32K, 4
+    // heads, 299 / 140).  It costs equally long ones that fill one wave (10 of 16K 153 / 167, 16
+    // 155 / 171; 24, more than a wave, 325 / 259), and short ones behind a wide table, whose
+    // splits are empty (0.5K to 1K of 64K: 10 sequences 15.5 / 22.7, 24 29.7 / 36.5).
+    if (B > 1)
+      n = std::max(n, std::min(((long long)S_max + 8191) / 8192, 8 * sms / ((long long)B * H_kv)));
+    return (int)std::max(1LL, n);
   }
   // Up to 1024 tokens one launch, which is a cluster of CTAs where the grid leaves room, and up
   // to 2048 if it leaves room for eight CTAs (8 KV heads of 128, 2K tokens: 6.6 us, 5.6 in 16

@@ -200,6 +200,23 @@ def test_default_splits_of_long_sequences_are_taken_by_the_call():
                                    ws=FAKE) == UNSUP
 
 
+@pytest.mark.parametrize("T,H_of,d", [(1, 4, 128), (4, 4, 128), (8, 4, 64), (1, 1, 32), (2, 8, 128)])
+def test_default_splits_share_out_long_sequences(T, H_of, d):
+    # A split has at most 8192 tokens, or one sequence's splits fill the SMs, or several sequences'
+    # (those that are cut by their lengths, and the many that are not: eight CTAs to an SM).  On
+    # mma.sync 32 rows are a CTA.
+    sms = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 148
+    rows = 2 * T * H_of
+    groups = 1 if d == 128 or rows <= 16 else -(-rows // 32)
+    for Hk in (1, 2, 3, 4, 5, 8):
+        for B in range(1, 129):
+            for S in (8192, 8193, 16384, 65536, 1 << 20):
+                n = g.gqa_attn_decode_diff_default_splits(B, T, H_of * Hk, Hk, S, d)
+                fills = (2 * n * Hk > sms if B == 1 else (n + 1) * B * Hk > 8 * sms
+                         or (B <= 96 and n * B * Hk * groups >= sms))
+                assert n * 8192 >= S or fills, (Hk, B, S, n)
+
+
 # -------------------------------------------------------- the 64-bit forms --
 def test_turning_keeps_lengths_and_relative_angles():
     rng = np.random.default_rng(0)
