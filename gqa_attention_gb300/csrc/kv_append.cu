@@ -5,9 +5,10 @@
 //   (x cos a - y sin a, x sin a + y cos a),  a = p f.
 // The product p f in fp32 would be off by p f 2^-24 (0.008 radians at 128K); instead the
 // frequency is held as turns, f / 2 pi modulo 1, in 64 bits of fixed point: the
-// integer product with p, modulo 2^64, is the angle's fraction of a turn, off by p 2^-54
-// turns at most (the division by 2 pi is in fp64).  Its upper 32 bits become
-// an fp32 angle in half turns for sincospif.
+// integer product with p, modulo 2^64, is the angle's fraction of a turn.  The division by
+// 2 pi is in fp64, constant and product rounded to 2^-53 of themselves, so the angle is
+// off by |p f| 2^-52 radians, and the fixed point adds |p| 2^-65 turns.  Its upper 32
+// bits become an fp32 angle in half turns for sincospif.
 //
 // A CTA takes some tokens: their rows in the cache (lengths, pages) and the sines and
 // cosines of every pair go to shared memory once and serve all heads.  A thread then
@@ -38,11 +39,13 @@ __device__ __forceinline__ void copy_async_16(uint4* dst, const void* src) {
                : "memory");
 }
 
-// 2^64 f / 2 pi modulo 2^64.
+// 2^64 f / 2 pi modulo 2^64.  (The sign is taken in integers: 1 - t would round to 2^-54,
+// 2^-20 radians at position 2^31.)
 __device__ __forceinline__ uint64_t turns_of(float f) {
-  double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / 2 pi
+  double t = fabs(static_cast<double>(f)) * 0.15915494309189533577;  // 1 / 2 pi
   t -= floor(t);
-  return __double2ull_rn(t * 18446744073709551616.0);
+  const uint64_t turns = __double2ull_rn(t * 18446744073709551616.0);
+  return f < 0.f ? 0 - turns : turns;
 }
 
 // Two fp32 values to two E4M3 codes (lo in the low byte), to nearest even; NaN stays NaN.

@@ -202,6 +202,32 @@ def test_far_and_negative_positions():
         s.check()
 
 
+def test_frequencies_of_many_turns_at_far_positions():
+    # (|p f| up to 2.6e8, below 2^28)
+    pos = torch.tensor([[1, 1000, 131071, 2600000, 2599999, -2600000, -1, 0]], dtype=torch.int32)
+    for inter in (False, True):
+        s = Step(1, 8, 2, 1, 128, 128, inter, positions=pos, lens=[8], seed=3)
+        s.freqs = 6.5 + 93.5 * torch.rand(64, generator=s.gen)
+        s.freqs[0], s.freqs[1], s.freqs[2] = 100.0, -100.0, 6.2831855
+        s.run()
+        s.check()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_small_negative_frequencies_at_the_farthest_position(inter):
+    # p f is next to odd quarters of a turn, so that a cosine of 1e-6 shows the angle's error
+    pos = torch.tensor([[2 ** 31 - 1, -(2 ** 31), 0, 1]], dtype=torch.int32)
+    s = Step(1, 4, 1, 1, 16, 16, inter, positions=pos, lens=[4])
+    f = [float.fromhex("-0x1.858eb8p-26"), float.fromhex("-0x1.3a28cap-26")]
+    s.freqs = torch.tensor([*f, *(-x for x in f), *f, *f])
+    x = torch.zeros(1, 4, 1, 16, dtype=torch.bfloat16)
+    x[..., slice(0, 16, 2) if inter else slice(0, 8)] = 1.0
+    s.q, s.k, s.v = x, x, x
+    s.dev_rows = [t.to(DEV) for t in (x, x, x)]
+    s.run()
+    s.check()
+
+
 def test_far_place_in_a_long_sequence():
     # the position is the token's place: 2M tokens into a paged sequence, a small pool behind it
     nb, page = 1 << 15, 64
