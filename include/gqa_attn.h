@@ -656,27 +656,33 @@ gqa_status gqa_kv_append_paged_fp8(const void* q, const void* k_new, const void*
  *                h * lam_stride_h elements (strides >= 0; 0 shares a value)
  *   norm_weight  device fp32 [d], or NULL (ones); needs norm_eps >= 0
  *   norm_eps     finite; negative: no norm.  O's squares are summed in fp32: keep |O| below
- *                2^60, and norm_eps above 0 where all of O may be 0.
+ *                2^60, and norm_eps above 0 where all of O may be 0.  The weights of both maps
+ *                enter P V in bf16, as in the other calls (2^-8 of each): where the maps
+ *                nearly cancel, the norm divides that by a small root mean square, and
+ *                the relative error has no bound.
  *   out          device bf16 [B, T_q, H, d]
  * The cache has no more than 2^31 - 2^16 token rows.  The maps' query rows are rows of
  * the grouped-query kernels: K and V are read once for both.
  *
  * Decode of the last T_q positions of each sequence: query t of sequence b is at
  * L - T_q + t, L = seq_lens[b], and sees keys 0 .. L - T_q + t.  Cache, pages,
- * lengths, splits (gqa_attn_decode_split_chunk) and workspace are those of
- * gqa_attn_decode() / gqa_attn_decode_paged() for B * T_q sequences of 2 H query heads
+ * lengths and workspace are those of gqa_attn_decode() / gqa_attn_decode_paged() for
+ * B * T_q sequences of 2 H query heads
  * (gqa_attn_decode_workspace_bytes(B * T_q, 2 * H, d, n_split) bytes, 256-byte aligned);
  * a second launch merges several splits, no gqa_attn_decode_combine() follows.
  * lse: device fp32 [B, T_q, 2 H], of map u of head h at 2h + u - 1, 8-byte aligned.
  * 1 <= T_q <= 64, 2 H / H_kv <= 16 and T_q * 2 H / H_kv <= 64 (GQA_ERR_UNSUPPORTED
- * above), n_split <= 65535 and n_split splits' keys below 2^31.  With d = 128 and more than 16
- * rows (T_q * 2 H / H_kv) all rows form one tensor-core tile, splits are of 128-key
- * multiples, and batches of several sequences that fill the GPU are cut on the device by
- * their lengths, into at most n_split splits of a sequence (a sequence's splits, and so
- * the rounding of its outputs, then depend on the other lengths too).  A row of V that a
- * query does not see never reaches it, whatever it holds (one that it sees: an infinity may
- * come out as NaN); with split keys a map sees its own half of a key row alone.
- * Deterministic. */
+ * above), n_split <= 65535 and n_split splits' keys below 2^31.
+ * With n_split > 1, 2 to 96 sequences whose cache (B * S_max tokens) is long enough to fill the
+ * GPU may be cut on the device by their lengths, with every d and any number of rows
+ * (T_q * 2 H / H_kv): n_split is then the most splits of a sequence, and a sequence's splits,
+ * and so the rounding of its outputs, depend on the other lengths too.  Other batches' splits
+ * are even: those of gqa_attn_decode_split_chunk, or of 128-key multiples with d = 128 and
+ * more than 16 rows.  With n_split = 1 up to eight CTAs may share a sequence's keys (evenly,
+ * by S_max) and merge them in the same launch.
+ * A row of V that a query does not see never reaches it, whatever it holds (one that it sees:
+ * an infinity may come out as NaN); with split keys a map sees its own half of a key row
+ * alone.  Deterministic. */
 gqa_status gqa_attn_decode_diff(const void* q, const void* k_cache, const void* v_cache,
                                 const int32_t* seq_lens, const float* lam, int64_t lam_stride_b,
                                 int64_t lam_stride_t, int64_t lam_stride_h, int B, int T_q,
