@@ -20,7 +20,7 @@ struct Piece {
 constexpr int kMaxCut = 96;  // sequences
 __device__ __noinline__ Piece find_piece(int t0, int t1, int t2, int B, int n_split, int pieces,
                                          int index, int lane) {
-  const int total = t0 + t1 + t2;  // (each below 2^24)
+  const int total = t0 + t1 + t2;  // (each at most 2^25: 2^31 tokens in tiles of 64)
   const long long all = static_cast<long long>(__reduce_add_sync(0xffffffffu, total >> 12)) * 4096 +
                         __reduce_add_sync(0xffffffffu, total & 4095);
   const int most = max(1, __reduce_max_sync(0xffffffffu, max(max(t0, t1), t2)));

@@ -22,7 +22,7 @@
 // Bound by HBM up to 16 rows: 8 sequences of 1K to 64K, 8 KV heads of 128, 125 us, 6.8
 // TB/s; one of 32K 22.4 us, 6.0 TB/s, of which about 4.5 are the start and the merge's
 // launch.  Short sequences are a chain of latencies: 1024 tokens of 2 KV heads of 32,
-// 3.5 us.  From 17 rows on, without the tensor-core tile of decode_tc.cu, by mma.sync and the
+// 3.4 us.  From 17 rows on, without the tensor-core tile of decode_tc.cu, by mma.sync and the
 // softmax (20 sequences of 2.5K, 6 KV heads of 64, 64 rows: 36 us, floor 10.5).
 #include <type_traits>
 
@@ -59,7 +59,7 @@ __device__ __forceinline__ float4 diff_row(const DiffParams& p, float4 a, float4
 
 // Stages of a CTA that has an SM to itself, and of one that shares it.  (d = 64 and 32: 96 and
 // 48 KB, two and three CTAs of one row group on an SM.  Registers for a third and a
-// fourth slowed every CTA down: the tiny decode 3.4 -> 4.2 us, 8 x 8K of 64 in eight splits
+// fourth slowed every CTA down: 1024 tokens by 0.8 us, 8 x 8K of 64 in eight splits
 // 13.9 -> 15.5.  Two row groups: 96 registers for a second CTA slow each down, too (5 sequences
 // of up to 5K, 30 rows, d = 64: 10.5 -> 12.7 us), but pay where there are more KV heads and
 // sequences than SMs (60 x 1K, 5 KV heads, 64 rows: 52 -> 37; 40 x 2.5K, 5 of 32, 24 rows
@@ -424,6 +424,7 @@ __global__ void __launch_bounds__((kGroupWarps * NRG + kProducers) * 32,
         o[n][3] *= a1;
       }
     }
+    // (the weights in bf16, 2^-8 of each, as mma takes them with V; their sums are fp32)
     const uint32_t pa[4] = {pack_bf16x2(p0[0], p0[1]), pack_bf16x2(p1[0], p1[1]),
                             pack_bf16x2(p0[2], p0[3]), pack_bf16x2(p1[2], p1[3])};
     // O += P V with V's elements under the masks; of the accumulators, rows g and g + 8

@@ -404,13 +404,13 @@ __global__ void __launch_bounds__(kThreads, HOLD == 2 ? 2 : HOLD == 0 && EARLY ?
       copy_tile(tile + kRing * n_teams, stage);
       stage = stage == kRing - 1 ? 0 : stage + 1;
       amax = __uint_as_float(unit_max(__float_as_uint(amax)));
-              auto widest_finite = [&](float (&v)[8]) {
+      auto widest_finite = [&](float (&v)[8]) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  v[j] = isfinite(v[j]) ? v[j] : NAN;  // (an infinity would be clamped to 448)
-                  amax = fmaxf(amax, fabsf(v[j]));
-                }
-              };
+        for (int j = 0; j < 8; ++j) {
+          v[j] = isfinite(v[j]) ? v[j] : NAN;  // (an infinity would be clamped to 448)
+          amax = fmaxf(amax, fabsf(v[j]));
+        }
+      };
       // Rare: the maximum again, of what is finite.  (Lanes of one warp go together.)
       const bool infinite = amax > 3.4028235e38f;
       if (__any_sync(0xffffffffu, infinite)) {

@@ -244,11 +244,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __shared__ int abort_flag;
   // every role derives each item's key range from seq_lens[b]: read it once
   __shared__ int lens_sm[GENERAL ? lens_kept(DIFF) : 1];
-  // differential: 1 / l, which the two threads of a row tell each other, per quarter of rows
-  // the barrier that says it is there,
+  // differential: 1 / l of each map, which the two threads of a row tell each other; for
+  // each quarter of the rows the barrier that says it is there; and the norm's weight
   __shared__ float row_inv[DIFF ? 2 : 1][DIFF ? 128 : 1];
   __shared__ __align__(8) uint64_t inv_ready[2][DIFF ? 4 : 1];
-  __shared__ __align__(16) float weight_sm[DIFF ? DP : 1];  // and the norm's weight
+  __shared__ __align__(16) float weight_sm[DIFF ? DP : 1];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
